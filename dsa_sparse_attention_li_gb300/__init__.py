@@ -12,6 +12,7 @@ Functions (same names as the C entry points, without the ``dsa_`` prefix):
     sfa_prefill(...)         -> same
     sfa_workspace_bytes(...) -> int
     page_bytes(dtype, rows, dim), page_table_validate(...), cache_write(...)
+    cache_write_quant(...), cache_read(...): rows into, and out of, the quantised caches
 """
 from __future__ import annotations
 
@@ -29,11 +30,13 @@ HOOKS_LIB_PATH = os.path.join(_PKG, "libdsa_testhooks.so")
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA, DSA_ERR_DEVICE_CHECK, DSA_ERR_TIMEOUT = range(6)
 DSA_BF16, DSA_FP8_E4M3, DSA_MXFP8_E4M3 = 0, 1, 2
+ROW_BF16, ROW_FP8, ROW_MXFP8, ROW_LATENT_FP8 = range(4)
+_ELEM = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 SYMBOLS = ["dsa_status_string", "dsa_last_error", "dsa_abi_version", "dsa_li_workspace_bytes", "dsa_li_topk",
            "dsa_sfa_workspace_bytes", "dsa_sfa_decode", "dsa_sfa_prefill",
            "dsa_sfa_decode_static", "dsa_page_bytes", "dsa_page_table_validate",
-           "dsa_cache_write", "dsa_prolog_workspace_bytes", "dsa_indexer_prolog", "dsa_topk_merge"]
+           "dsa_cache_write", "dsa_cache_write_quant", "dsa_cache_read", "dsa_prolog_workspace_bytes", "dsa_indexer_prolog", "dsa_topk_merge"]
 
 # Capacity of the library's fixed scratch array used by dsa_sfa_decode_static.
 SFA_STATIC_SCRATCH_BYTES = 20 * 1024 * 1024
@@ -77,6 +80,13 @@ class SfaArgs(ctypes.Structure):
             "q", "kv_pool", "page_table", "seq_lens", "q_start", "idx", "out", "lse", "status",
             "workspace")] + [("workspace_bytes", ctypes.c_size_t), ("kv_dtype", ctypes.c_int),
                              ("row_splits", ctypes.c_int)]
+
+
+class CacheRowsArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "n_rows", "dim", "B", "page_size", "max_pages", "num_pages", "format", "elem")] + [
+        ("row_stride", ctypes.c_longlong)] + [(n, ctypes.c_void_p) for n in (
+            "rows", "pool", "scale_pool", "sf_pool", "page_table", "seq", "pos", "status")]
 
 
 _lib = None
@@ -142,6 +152,9 @@ def _configure(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.dsa_cache_write.argtypes = [P, P, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                     P, ctypes.c_int, ctypes.c_int, P, P, P, P, ctypes.c_int, P, P]
     lib.dsa_cache_write.restype = ctypes.c_int
+    for f in (lib.dsa_cache_write_quant, lib.dsa_cache_read):
+        f.argtypes = [ctypes.POINTER(CacheRowsArgs), P]
+        f.restype = ctypes.c_int
     return lib
 
 
@@ -354,6 +367,102 @@ def cache_write(pool, page_table, seq, pos, rows, *, scale_pool=None, row_scales
                                page_table.shape[0], _ptr(seq), _ptr(pos), _ptr(rows),
                                _ptr(row_scales), rows.shape[0], _ptr(status), _stream(stream))
     _check(code, "dsa_cache_write")
+
+
+def _on(device, **tensors):
+    """Every tensor given lives on `device`, the current CUDA device.  The library's launches go to
+    the current device, so a tensor of another one would be read across, or not at all."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device (got %s)" % device)
+    if device.index != torch.cuda.current_device():
+        raise ValueError("tensors are on %s, the current device is cuda:%d"
+                         % (device, torch.cuda.current_device()))
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+
+
+def _typed(name, t, dtype, shape=None):
+    """`t` has the type, and where given the shape, that the C struct takes for granted."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s (got %s)" % (name, dtype, t.dtype))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+
+
+def cache_rows_args(pool, page_table, seq, pos, rows, *, scale_pool=None, sf_pool=None, status=None):
+    """Fill the C argument struct of dsa_cache_write_quant and dsa_cache_read (tensors must outlive
+    the call).  The cache's format follows from its tensors: a uint8 pool holds FP8 latent rows,
+    an e4m3 pool per-row FP8 (scale_pool) or MXFP8 (sf_pool), a bf16 pool plain rows."""
+    if pool.dim() != 3 or rows.dim() != 2:
+        raise ValueError("pool is [num_pages, page_size, width], rows is [n, dim]")
+    num_pages, page_size, width = pool.shape
+    n, dim = rows.shape
+    if rows.dtype not in _ELEM:
+        raise ValueError("rows must be bf16, fp16 or fp32 (got %s)" % rows.dtype)
+    if pool.dtype == torch.uint8:
+        if width != 608:
+            raise ValueError("rows of an FP8 latent cache have 608 bytes (got %d)" % width)
+        fmt, want = ROW_LATENT_FP8, 576
+    elif pool.dtype == torch.float8_e4m3fn:
+        if (scale_pool is None) == (sf_pool is None):
+            raise ValueError("an e4m3 cache has either scale_pool (FP8) or sf_pool (MXFP8)")
+        fmt, want = (ROW_FP8 if sf_pool is None else ROW_MXFP8), width
+    elif pool.dtype == torch.bfloat16:
+        fmt, want = ROW_BF16, width
+    else:
+        raise ValueError("pool must be uint8 (FP8 latent rows), e4m3 or bf16 (got %s)" % pool.dtype)
+    if fmt in (ROW_LATENT_FP8, ROW_BF16) and (scale_pool is not None or sf_pool is not None):
+        raise ValueError("only an e4m3 cache has scale_pool or sf_pool")
+    if dim != want:
+        raise ValueError("rows have %d columns, the cache's have %d" % (dim, want))
+    if n > 1 and rows.stride(0) < dim or dim > 1 and rows.stride(1) != 1:
+        raise ValueError("the columns of rows must be adjacent, and its rows apart")
+    _typed("page_table", page_table, torch.int32)
+    _typed("seq", seq, torch.int32, (n,))
+    _typed("pos", pos, torch.int32, (n,))
+    _typed("scale_pool", scale_pool, torch.float32, (num_pages, page_size))
+    _typed("sf_pool", sf_pool, torch.uint8, (num_pages, page_size, dim // 32))
+    _typed("status", status, torch.int32)
+    a = CacheRowsArgs()
+    a.n_rows, a.dim, a.B, a.page_size = n, dim, page_table.shape[0], page_size
+    a.max_pages, a.num_pages, a.format, a.elem = page_table.shape[1], num_pages, fmt, _ELEM[rows.dtype]
+    a.row_stride = rows.stride(0) if n > 1 else dim
+    a.rows, a.pool, a.scale_pool, a.sf_pool = rows.data_ptr(), _ptr(pool), _ptr(scale_pool), _ptr(sf_pool)
+    a.page_table, a.seq, a.pos, a.status = _ptr(page_table), _ptr(seq), _ptr(pos), _ptr(status)
+    return a
+
+
+def cache_write_quant(pool, page_table, seq, pos, rows, *, scale_pool=None, sf_pool=None,
+                      status=None, stream=None) -> None:
+    """Quantise rows [n, dim] (bf16, fp16 or fp32; rows may be strided, their columns adjacent) into
+    the cache at (seq[i], pos[i]): FP8 latent rows (uint8 pool [num_pages, page_size, 608], dim
+    576), per-row FP8 (e4m3 pool with scale_pool) or MXFP8 (e4m3 pool with sf_pool) key rows."""
+    lib = load()
+    a = cache_rows_args(pool, page_table, seq, pos, rows, scale_pool=scale_pool, sf_pool=sf_pool,
+                        status=status)
+    _on(pool.device, page_table=page_table, seq=seq, pos=pos, rows=rows, scale_pool=scale_pool,
+        sf_pool=sf_pool, status=status)
+    _check(lib.dsa_cache_write_quant(ctypes.byref(a), _stream(stream)), "dsa_cache_write_quant")
+
+
+def cache_read(pool, page_table, seq, pos, *, out=None, dtype=torch.bfloat16, scale_pool=None,
+               sf_pool=None, status=None, stream=None):
+    """The cache rows at (seq[i], pos[i]) as values [n, dim]: into ``out`` (bf16, fp16 or fp32; its
+    rows may be strided), or a new tensor of ``dtype``.  Takes the formats of cache_write_quant
+    and bf16 caches.  A row out of range reads as zeros and sets ``status``."""
+    lib = load()
+    if out is None:
+        out = torch.empty((seq.shape[0], 576 if pool.dtype == torch.uint8 else pool.shape[-1]),
+                          dtype=dtype, device=pool.device)
+    a = cache_rows_args(pool, page_table, seq, pos, out, scale_pool=scale_pool, sf_pool=sf_pool,
+                        status=status)
+    _on(pool.device, page_table=page_table, seq=seq, pos=pos, out=out, scale_pool=scale_pool,
+        sf_pool=sf_pool, status=status)
+    _check(lib.dsa_cache_read(ctypes.byref(a), _stream(stream)), "dsa_cache_read")
+    return out
 
 
 def topk_merge(cand_idx, cand_score, shard_offset, K, *, out_idx=None, out_cnt=None, stream=None):

@@ -306,6 +306,55 @@ dsa_status dsa_cache_write(void* pool, float* scale_pool, int num_pages, int pag
   return s;
 }
 
+static dsa_status cache_rows(const dsa_cache_rows_args* a, bool write, dsa_stream_t stream) {
+  g_last_error.clear();
+  const std::string name = write ? "cache_write_quant" : "cache_read";
+  if (!a) return fail(DSA_ERR_INVALID_ARG, name + ": args is NULL");
+  if (a->n_rows < 0 || a->dim <= 0 || a->B <= 0 || a->page_size <= 0 || a->max_pages <= 0 ||
+      a->num_pages <= 0)
+    return fail(DSA_ERR_INVALID_ARG, name + ": non-positive size");
+  if (a->elem != DSA_ELEM_BF16 && a->elem != DSA_ELEM_FP16 && a->elem != DSA_ELEM_FP32)
+    return fail(DSA_ERR_INVALID_ARG, name + ": unknown element type of rows");
+  switch (a->format) {
+    case DSA_ROW_BF16:
+      if (write) return fail(DSA_ERR_UNSUPPORTED, name + ": a bf16 cache is written by dsa_cache_write");
+      if (a->dim % 8) return fail(DSA_ERR_UNSUPPORTED, name + ": dim must be a multiple of 8");
+      break;
+    case DSA_ROW_FP8:
+    case DSA_ROW_MXFP8:
+      if (a->dim != 32 && a->dim != 64 && a->dim != 128 && a->dim != 256)
+        return fail(DSA_ERR_UNSUPPORTED, name + ": dim must be 32, 64, 128 or 256");
+      break;
+    case DSA_ROW_LATENT_FP8:
+      if (a->dim != 576) return fail(DSA_ERR_UNSUPPORTED, name + ": latent rows have 576 columns");
+      break;
+    default:
+      return fail(DSA_ERR_INVALID_ARG, name + ": unknown cache format");
+  }
+  if (a->row_stride < a->dim) return fail(DSA_ERR_INVALID_ARG, name + ": row_stride below dim");
+  if (a->row_stride % (a->elem == DSA_ELEM_FP32 ? 4 : 8))
+    return fail(DSA_ERR_UNSUPPORTED, name + ": rows must start 16-byte aligned");
+  if (a->n_rows == 0) return DSA_OK;
+  if (!a->rows || !a->pool || !a->page_table || !a->seq || !a->pos)
+    return fail(DSA_ERR_INVALID_ARG, name + ": null device pointer");
+  if ((a->format == DSA_ROW_FP8 && !a->scale_pool) || (a->format == DSA_ROW_MXFP8 && !a->sf_pool))
+    return fail(DSA_ERR_INVALID_ARG, name + ": FP8 needs scale_pool, MXFP8 needs sf_pool");
+  if (!aligned16(a->rows) || !aligned16(a->pool))
+    return fail(DSA_ERR_INVALID_ARG, name + ": rows and pool must be 16-byte aligned");
+  std::string err;
+  const dsa_status s = dsa::launch_cache_rows(*a, write, reinterpret_cast<cudaStream_t>(stream), err);
+  if (s != DSA_OK) g_last_error = err;
+  return s;
+}
+
+dsa_status dsa_cache_write_quant(const dsa_cache_rows_args* a, dsa_stream_t stream) {
+  return cache_rows(a, true, stream);
+}
+
+dsa_status dsa_cache_read(const dsa_cache_rows_args* a, dsa_stream_t stream) {
+  return cache_rows(a, false, stream);
+}
+
 #ifdef DSA_TEST_HOOKS
 // Test build only (libdsa_testhooks.so; include/dsa_testhooks.h).
 void dsa_test_inject_stall(int kernel) { dsa::g_test_stall = kernel; }

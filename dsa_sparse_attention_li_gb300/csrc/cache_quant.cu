@@ -1,0 +1,306 @@
+// cache_quant.cu -- rows of activations into the quantised paged caches, and cache rows back out.
+//
+// "Inference Optimization for Kimi K3.1 Pro ...", section 4 (the latent cache in FP8 with one
+// scale per token and 128-column tile; the index keys in FP8 with group scales): the formats that
+// dsa_li_topk, dsa_sfa_* and dsa_mla_decode read.
+//
+// Quantisation of a group of columns with largest finite magnitude a:
+//   FP8:    s = fp32(a / 448), 1 for a = 0, at least 2^-126;   c_i = e4m3(x_i / s)
+//   MXFP8:  e = max(floor(log2 a) - 8, -127), 0 for a = 0;     c_i = e4m3(x_i 2^-e)
+// e4m3() rounds to nearest even and saturates at 448.  x_i / s is not rounded before e4m3(): a
+// quotient rounded to fp32 first can land exactly on the border between two codes.  The fast
+// path multiplies by 1/s and keeps a code only if the products 2^-21 below and above round to the
+// same one (the product is within 2^-22 of the quotient); the few others, about one element in
+// 2^16, compare |x| with border * s in 64 bits, where that product is exact.
+//
+// Both kernels move each byte once and are bound by HBM.  The unit of work of a warp is 256
+// columns, eight a lane (16- or 32-byte accesses), so a group is a segment of 4 to 32 lanes and its
+// maximum a few shuffles.  A latent row is 2.25 units: the 64-column tails of four rows share one,
+// else a third of the lanes would idle.  A warp takes one unit: its row loads are issued before
+// the dependent page-table lookup, and the other warps of the SM hide both.
+#include "dsa_internal.h"
+#include "ptx.cuh"
+
+namespace dsa {
+namespace cq {
+
+constexpr int kThreads = 256;
+constexpr int kLatent = 576;
+constexpr int kLatentRow = 608;   // 576 codes, 5 fp32 scales, 12 zero bytes
+
+struct Params {
+  int n_rows, dim, B, page_size, max_pages, num_pages;
+  long long row_stride;  // elements
+  long long units;
+  uint8_t* rows;
+  uint8_t* pool;
+  float* scale_pool;
+  uint8_t* sf_pool;
+  const int* page_table;
+  const int* seq;
+  const int* pos;
+  int* status;
+};
+
+// The row and the first column of a lane's eight columns in unit u; row < 0: none.
+struct Place {
+  int row, col;
+};
+
+template <int F>
+DSA_DEV Place place(const Params& p, long long u, int lane) {
+  const int per = p.dim >> 3;               // lanes of a row
+  long long row;
+  int col;
+  if constexpr (F == DSA_ROW_LATENT_FP8) {
+    const long long blk = u / 9;            // four rows are nine units
+    const int k = (int)(u - blk * 9);
+    row = blk * 4 + (k < 8 ? k >> 1 : lane >> 3);
+    col = k < 8 ? (k & 1) * 256 + lane * 8 : 512 + (lane & 7) * 8;
+  } else if constexpr (F == DSA_ROW_BF16) {  // any multiple of eight columns
+    const long long c = u * 32 + lane;
+    row = c / per;
+    col = (int)(c - row * per) * 8;
+  } else {                                  // 4, 8, 16 or 32 lanes a row
+    row = u * (32 / per) + lane / per;
+    col = (lane & (per - 1)) * 8;
+  }
+  return {row < p.n_rows ? (int)row : -1, col};
+}
+
+// Physical cache row of row r, or -1 (reported) when the sequence, position or page is out of range.
+DSA_DEV long long cache_row(const Params& p, int r) {
+  const int b = p.seq[r], j = p.pos[r];
+  if (b >= 0 && b < p.B && j >= 0) {
+    const int slot = j / p.page_size;
+    if (slot < p.max_pages) {
+      const int pg = p.page_table[(long long)b * p.max_pages + slot];
+      if (pg >= 0 && pg < p.num_pages) return (long long)pg * p.page_size + (j - slot * p.page_size);
+    }
+  }
+  report(p.status, kStatusDeviceCheck);
+  return -1;
+}
+
+template <int E>
+DSA_DEV void load8(const uint8_t* base, long long at, float* x) {
+  if constexpr (E == DSA_ELEM_FP32) {
+    const float4* s = reinterpret_cast<const float4*>(base + at * 4);
+    const float4 a = __ldcs(s), b = __ldcs(s + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  } else {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(base + at * 2));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (E == DSA_ELEM_BF16) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
+    }
+  }
+}
+
+template <int E>
+DSA_DEV void store8(uint8_t* base, long long at, const float* y) {
+  if constexpr (E == DSA_ELEM_FP32) {
+    float4* d = reinterpret_cast<float4*>(base + at * 4);
+    d[0] = make_float4(y[0], y[1], y[2], y[3]);
+    d[1] = make_float4(y[4], y[5], y[6], y[7]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (E == DSA_ELEM_BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&v);
+      } else {
+        const __half2 v = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    }
+    *reinterpret_cast<uint4*>(base + at * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+DSA_DEV uint32_t e4m3x2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
+DSA_DEV float e4m3_value(uint32_t code) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3);
+  return __half2float(*reinterpret_cast<const __half*>(&h));
+}
+
+// The code of x / s between its neighbours `lo` (toward zero) and `hi`, which differ by one.
+__device__ __noinline__ uint32_t settle(float x, float s, uint32_t lo, uint32_t hi) {
+  const float border = 0.5f * (fabsf(e4m3_value(lo & 0x7f)) + fabsf(e4m3_value(hi & 0x7f)));
+  const double d = fabs((double)x) - (double)border * (double)s;  // the product has at most 29 bits
+  if (d > 0.0) return hi;
+  if (d < 0.0) return lo;
+  return (hi & 1u) ? lo : hi;
+}
+
+// Eight columns with scale s -> eight codes.
+DSA_DEV uint2 quantise8(const float* x, float s) {
+  const float inv = __frcp_rn(s);
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = x[2 * i] * inv, b = x[2 * i + 1] * inv;
+    constexpr float kDown = 1.f - 0x1p-21f, kUp = 1.f + 0x1p-21f;
+    uint32_t lo = e4m3x2(a * kDown, b * kDown);
+    const uint32_t hi = e4m3x2(a * kUp, b * kUp);
+    if (lo != hi) {
+      const uint32_t c0 = (lo & 0xff) == (hi & 0xff) ? (lo & 0xff) : settle(x[2 * i], s, lo & 0xff, hi & 0xff);
+      const uint32_t c1 = (lo >> 8) == (hi >> 8) ? (lo >> 8) : settle(x[2 * i + 1], s, lo >> 8, hi >> 8);
+      lo = c0 | (c1 << 8);
+    }
+    c[i] = lo;
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+template <int F, int E>
+__global__ void __launch_bounds__(kThreads) write_kernel(const Params p) {
+  const long long u = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (u >= p.units) return;
+  const Place w = place<F>(p, u, lane);
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = 0.f;
+  long long dst = -1;
+  if (w.row >= 0) {
+    load8<E>(p.rows, (long long)w.row * p.row_stride + w.col, x);
+    dst = cache_row(p, w.row);
+  }
+  // the group's largest finite magnitude: a NaN or an infinity does not cost its neighbours
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float m = fabsf(x[i]);
+    a = fmaxf(a, m < INFINITY ? m : 0.f);
+  }
+  const int lanes = F == DSA_ROW_MXFP8 ? 4 : F == DSA_ROW_FP8 ? p.dim >> 3 : w.col >= 512 ? 8 : 16;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float m = __shfl_xor_sync(0xffffffffu, a, o);
+    if (o < lanes) a = fmaxf(a, m);
+  }
+  if (dst < 0) return;
+  if constexpr (F == DSA_ROW_MXFP8) {
+    const int e = a > 0.f ? max((int)(__float_as_uint(a) >> 23) - 127 - 8, -127) : 0;
+    // 2^-e with e in [-127, 119]: exact, and so is the product wherever e4m3 can tell
+    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
+    *reinterpret_cast<uint2*>(p.pool + dst * p.dim + w.col) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    if ((lane & 3) == 0) p.sf_pool[dst * (p.dim >> 5) + (w.col >> 5)] = (uint8_t)(e + 127);
+  } else {
+    const float s = a > 0.f ? fmaxf(__fdiv_rn(a, 448.f), 0x1p-126f) : 1.f;
+    const uint2 c = quantise8(x, s);
+    if constexpr (F == DSA_ROW_FP8) {
+      *reinterpret_cast<uint2*>(p.pool + dst * p.dim + w.col) = c;
+      if (w.col == 0) p.scale_pool[dst] = s;
+    } else {
+      uint8_t* row = p.pool + dst * kLatentRow;
+      *reinterpret_cast<uint2*>(row + w.col) = c;
+      if ((w.col & 127) == 0) *reinterpret_cast<float*>(row + kLatent + (w.col >> 7) * 4) = s;
+      if (w.col >= 552) *reinterpret_cast<uint32_t*>(row + kLatent + 20 + (w.col - 552) / 2) = 0u;
+    }
+  }
+}
+
+template <int F, int E>
+__global__ void __launch_bounds__(kThreads) read_kernel(const Params p) {
+  const long long u = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (u >= p.units) return;
+  const Place w = place<F>(p, u, lane);
+  if (w.row < 0) return;
+  const long long src = cache_row(p, w.row);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = 0.f;
+  if (src >= 0) {
+    if constexpr (F == DSA_ROW_BF16) {
+      load8<DSA_ELEM_BF16>(p.pool, src * p.dim + w.col, y);
+    } else {
+      const uint8_t* row = p.pool + src * (F == DSA_ROW_LATENT_FP8 ? kLatentRow : p.dim);
+      const uint2 c = __ldcs(reinterpret_cast<const uint2*>(row + w.col));
+      float s;
+      if constexpr (F == DSA_ROW_LATENT_FP8) {
+        s = *reinterpret_cast<const float*>(row + kLatent + (w.col >> 7) * 4);
+      } else if constexpr (F == DSA_ROW_FP8) {
+        s = p.scale_pool[src];
+      } else {
+        const uint32_t e = p.sf_pool[src * (p.dim >> 5) + (w.col >> 5)];
+        s = e == 255u ? __uint_as_float(0x7fffffffu)      // not a valid scale: NaN
+                      : e == 0u ? 0x1p-127f : __uint_as_float(e << 23);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t two = ((i < 2 ? c.x : c.y) >> ((i & 1) * 16)) & 0xffffu;
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        y[2 * i] = f.x * s;
+        y[2 * i + 1] = f.y * s;
+      }
+    }
+  }
+  store8<E>(p.rows, (long long)w.row * p.row_stride + w.col, y);
+}
+
+}  // namespace cq
+
+dsa_status launch_cache_rows(const dsa_cache_rows_args& a, bool write, cudaStream_t stream,
+                             std::string& err) {
+  using namespace cq;
+  Params p;
+  p.n_rows = a.n_rows;
+  p.dim = a.dim;
+  p.B = a.B;
+  p.page_size = a.page_size;
+  p.max_pages = a.max_pages;
+  p.num_pages = a.num_pages;
+  p.row_stride = a.row_stride;
+  p.rows = reinterpret_cast<uint8_t*>(a.rows);
+  p.pool = reinterpret_cast<uint8_t*>(a.pool);
+  p.scale_pool = a.scale_pool;
+  p.sf_pool = a.sf_pool;
+  p.page_table = a.page_table;
+  p.seq = a.seq;
+  p.pos = a.pos;
+  p.status = a.status;
+  p.units = a.format == DSA_ROW_LATENT_FP8 ? ((long long)a.n_rows + 3) / 4 * 9
+                                           : ((long long)a.n_rows * a.dim + 255) / 256;
+  const long long blocks = (p.units + kThreads / 32 - 1) / (kThreads / 32);
+  if (blocks > 0x7fffffffLL) {
+    err = "cache rows: too many rows for one launch";
+    return DSA_ERR_UNSUPPORTED;
+  }
+  using Kernel = void (*)(Params);
+  static const Kernel kWrite[3][3] = {
+      {write_kernel<DSA_ROW_FP8, 0>, write_kernel<DSA_ROW_FP8, 1>, write_kernel<DSA_ROW_FP8, 2>},
+      {write_kernel<DSA_ROW_MXFP8, 0>, write_kernel<DSA_ROW_MXFP8, 1>, write_kernel<DSA_ROW_MXFP8, 2>},
+      {write_kernel<DSA_ROW_LATENT_FP8, 0>, write_kernel<DSA_ROW_LATENT_FP8, 1>, write_kernel<DSA_ROW_LATENT_FP8, 2>}};
+  static const Kernel kRead[4][3] = {
+      {read_kernel<DSA_ROW_BF16, 0>, read_kernel<DSA_ROW_BF16, 1>, read_kernel<DSA_ROW_BF16, 2>},
+      {read_kernel<DSA_ROW_FP8, 0>, read_kernel<DSA_ROW_FP8, 1>, read_kernel<DSA_ROW_FP8, 2>},
+      {read_kernel<DSA_ROW_MXFP8, 0>, read_kernel<DSA_ROW_MXFP8, 1>, read_kernel<DSA_ROW_MXFP8, 2>},
+      {read_kernel<DSA_ROW_LATENT_FP8, 0>, read_kernel<DSA_ROW_LATENT_FP8, 1>, read_kernel<DSA_ROW_LATENT_FP8, 2>}};
+  const Kernel k = write ? kWrite[a.format - 1][a.elem] : kRead[a.format][a.elem];
+  k<<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, write ? "cache_write_quant: launch" : "cache_read: launch", err);
+  return DSA_OK;
+}
+
+}  // namespace dsa

@@ -41,6 +41,8 @@ dsa_status launch_cache_write(void* pool, float* scale_pool, int num_pages, int 
                               const int32_t* seq, const int32_t* pos, const void* rows,
                               const float* row_scales, int n_rows, int32_t* status,
                               cudaStream_t stream, std::string& err);
+dsa_status launch_cache_rows(const dsa_cache_rows_args& a, bool write, cudaStream_t stream,
+                             std::string& err);
 
 // 2-D tiled TMA descriptor over a row-major [outer][inner] array (inner contiguous).
 bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,

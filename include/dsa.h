@@ -361,6 +361,59 @@ dsa_status dsa_cache_write(void* pool, float* scale_pool, int num_pages, int pag
                            const float* row_scales, int n_rows, int32_t* status,
                            dsa_stream_t stream);
 
+/*
+ * Rows of activations into a quantised paged cache (dsa_cache_write_quant), and cache rows back
+ * out (dsa_cache_read): "Inference Optimization for Kimi K3.1 Pro", section 4, the latent cache
+ * in FP8 with one scale per token and 128-column tile and the index keys in FP8 with group
+ * scales, in the layouts that dsa_li_topk, dsa_sfa_* and dsa_mla_decode read.  Row r goes to, or
+ * comes from, physical row page_table[seq[r]][pos[r] / page_size] * page_size + pos[r] % page_size.
+ *
+ *   DSA_ROW_LATENT_FP8  pool [num_pages][page_size][608 bytes]: 576 e4m3 codes, one fp32 scale per
+ *                       128 columns (5; the last covers 64), 12 bytes that a write sets to zero
+ *   DSA_ROW_FP8         pool e4m3 [num_pages][page_size][dim], scale_pool fp32 [num_pages][page_size]
+ *   DSA_ROW_MXFP8       pool e4m3 [num_pages][page_size][dim], sf_pool E8M0 [...][dim / 32]
+ *   DSA_ROW_BF16        pool bf16 [num_pages][page_size][dim]; read only (dsa_cache_write writes it)
+ *
+ * Write: with a the largest finite magnitude of a group of columns (the scale's columns),
+ *   FP8:   s = fp32(a / 448), 1 when a = 0 and at least 2^-126; code = e4m3(x / s)
+ *   MXFP8: e = max(floor(log2 a) - 8, -127), 0 when a = 0;      code = e4m3(x * 2^-e), sf = e + 127
+ * e4m3() rounds to nearest even, saturates at 448 (infinities too) and keeps a NaN; x / s is not
+ * rounded before it.  Read: y = rows' type(fp32(code * scale)), to nearest even (to bf16: the
+ * operand that the attention over an FP8 latent cache forms); an E8M0 byte of 255 gives NaN.
+ *
+ * A row whose seq, pos or page id is out of range sets DSA_ERR_DEVICE_CHECK; a write skips it, a
+ * read fills it with zeros.  Two rows of one write to the same place leave either one's codes and
+ * scales, possibly mixed.  A read may name a place any number of times.
+ *
+ * Supported: dim 576 (LATENT_FP8); 32, 64, 128, 256 (FP8, MXFP8); any multiple of 8 (BF16).  rows
+ * and pool 16-byte aligned, row_stride * element size a multiple of 16, row_stride >= dim.
+ */
+typedef enum { DSA_ROW_BF16 = 0, DSA_ROW_FP8 = 1, DSA_ROW_MXFP8 = 2, DSA_ROW_LATENT_FP8 = 3 } dsa_row_format;
+typedef enum { DSA_ELEM_BF16 = 0, DSA_ELEM_FP16 = 1, DSA_ELEM_FP32 = 2 } dsa_elem;
+
+typedef struct {
+  int n_rows;
+  int dim;               /* columns of a row                                               */
+  int B;                 /* sequences (rows of page_table)                                 */
+  int page_size;         /* cache rows per page (any)                                      */
+  int max_pages;         /* row stride of page_table                                       */
+  int num_pages;         /* pages in pool                                                  */
+  dsa_row_format format; /* of the cache                                                   */
+  dsa_elem elem;         /* type of rows                                                   */
+  long long row_stride;  /* elements from one row of rows to the next                      */
+  void* rows;            /* [n_rows][dim]: read by dsa_cache_write_quant, written by dsa_cache_read */
+  void* pool;
+  float* scale_pool;     /* FP8 only                                                       */
+  uint8_t* sf_pool;      /* MXFP8 only                                                     */
+  const int32_t* page_table; /* [B][max_pages]                                             */
+  const int32_t* seq;    /* [n_rows]                                                       */
+  const int32_t* pos;    /* [n_rows]                                                       */
+  int32_t* status;       /* device int32 error word, or NULL                               */
+} dsa_cache_rows_args;
+
+dsa_status dsa_cache_write_quant(const dsa_cache_rows_args* args, dsa_stream_t stream);
+dsa_status dsa_cache_read(const dsa_cache_rows_args* args, dsa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
