@@ -11,6 +11,8 @@ Functions (same names as the C entry points, without the ``dsa_`` prefix):
     sfa_decode(...)          -> (out [n_q, H, 512] bf16, lse [n_q, H] fp32)
     sfa_prefill(...)         -> same
     sfa_workspace_bytes(...) -> int
+    mla_decode(...)          -> (out [n_q, H, 512] bf16, lse [n_q, H] fp32)   dense, absorbed form
+    mla_prefill(...)         -> (out [n_q, H, 128] bf16, lse [n_q, H] fp32)   dense, expanded form
     page_bytes(dtype, rows, dim), page_table_validate(...), cache_write(...)
     cache_write_quant(...), cache_read(...): rows into, and out of, the quantised caches
 """
@@ -35,7 +37,8 @@ _ELEM = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 SYMBOLS = ["dsa_status_string", "dsa_last_error", "dsa_abi_version", "dsa_li_workspace_bytes", "dsa_li_topk",
            "dsa_sfa_workspace_bytes", "dsa_sfa_decode", "dsa_sfa_prefill",
-           "dsa_sfa_decode_static", "dsa_page_bytes", "dsa_page_table_validate",
+           "dsa_sfa_decode_static", "dsa_mla_decode_workspace_bytes", "dsa_mla_decode", "dsa_mla_prefill",
+           "dsa_page_bytes", "dsa_page_table_validate",
            "dsa_cache_write", "dsa_cache_write_quant", "dsa_cache_read", "dsa_prolog_workspace_bytes", "dsa_indexer_prolog", "dsa_topk_merge"]
 
 # Capacity of the library's fixed scratch array used by dsa_sfa_decode_static.
@@ -80,6 +83,21 @@ class SfaArgs(ctypes.Structure):
             "q", "kv_pool", "page_table", "seq_lens", "q_start", "idx", "out", "lse", "status",
             "workspace")] + [("workspace_bytes", ctypes.c_size_t), ("kv_dtype", ctypes.c_int),
                              ("row_splits", ctypes.c_int)]
+
+
+class MlaDecodeArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "B", "n_q", "H", "d_qk", "d_v", "page_size", "max_pages", "num_pages", "max_q_per_seq")] + [
+        ("softmax_scale", ctypes.c_float), ("kv_dtype", ctypes.c_int)] + [(n, ctypes.c_void_p) for n in (
+            "q", "kv_pool", "page_table", "seq_lens", "q_start", "out", "lse", "status", "workspace")] + [
+        ("workspace_bytes", ctypes.c_size_t)]
+
+
+class MlaPrefillArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "B", "n_q", "n_kv", "H", "d_nope", "d_rope", "d_v", "max_q_per_seq")] + [
+        ("softmax_scale", ctypes.c_float), ("k_rope_stride", ctypes.c_longlong)] + [
+        (n, ctypes.c_void_p) for n in ("q", "kv", "k_rope", "q_start", "kv_start", "out", "lse", "status")]
 
 
 class CacheRowsArgs(ctypes.Structure):
@@ -152,6 +170,12 @@ def _configure(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.dsa_cache_write.argtypes = [P, P, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                     P, ctypes.c_int, ctypes.c_int, P, P, P, P, ctypes.c_int, P, P]
     lib.dsa_cache_write.restype = ctypes.c_int
+    lib.dsa_mla_decode_workspace_bytes.argtypes = [ctypes.POINTER(MlaDecodeArgs)]
+    lib.dsa_mla_decode_workspace_bytes.restype = ctypes.c_size_t
+    lib.dsa_mla_decode.argtypes = [ctypes.POINTER(MlaDecodeArgs), P]
+    lib.dsa_mla_decode.restype = ctypes.c_int
+    lib.dsa_mla_prefill.argtypes = [ctypes.POINTER(MlaPrefillArgs), P]
+    lib.dsa_mla_prefill.restype = ctypes.c_int
     for f in (lib.dsa_cache_write_quant, lib.dsa_cache_read):
         f.argtypes = [ctypes.POINTER(CacheRowsArgs), P]
         f.restype = ctypes.c_int
@@ -181,7 +205,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the raw handle: building a Stream object for it takes 3 us
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -374,11 +399,12 @@ def _on(device, **tensors):
     the current device, so a tensor of another one would be read across, or not at all."""
     if device.type != "cuda":
         raise ValueError("tensors must be on a CUDA device (got %s)" % device)
-    if device.index != torch.cuda.current_device():
+    index = device.index
+    if index != torch.cuda.current_device():
         raise ValueError("tensors are on %s, the current device is cuda:%d"
                          % (device, torch.cuda.current_device()))
     for name, t in tensors.items():
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != index:
             raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
 
 
@@ -463,6 +489,115 @@ def cache_read(pool, page_table, seq, pos, *, out=None, dtype=torch.bfloat16, sc
         sf_pool=sf_pool, status=status)
     _check(lib.dsa_cache_read(ctypes.byref(a), _stream(stream)), "dsa_cache_read")
     return out
+
+
+def mla_decode_workspace_bytes(n_q: int, H: int, max_q_per_seq: int) -> int:
+    """Scratch bytes dsa_mla_decode needs for a batch of this shape (any batch and lengths)."""
+    a = MlaDecodeArgs()
+    a.B = a.max_pages = a.num_pages = 1
+    a.n_q, a.H, a.max_q_per_seq = int(n_q), int(H), int(max_q_per_seq)
+    return int(load().dsa_mla_decode_workspace_bytes(ctypes.byref(a)))
+
+
+def _host_max_q(q_start, max_q_per_seq, n_q):
+    """The host's bound of a sequence's tokens (reading device tensors would synchronise)."""
+    if max_q_per_seq is None:
+        if q_start.is_cuda:
+            raise ValueError("max_q_per_seq is required with device tensors (reading it back "
+                             "would synchronise the stream)")
+        max_q_per_seq = int((q_start[1:] - q_start[:-1]).max())
+    return max(1, min(int(max_q_per_seq), n_q))
+
+
+def mla_decode(q, kv_pool, page_table, seq_lens, q_start, *, softmax_scale, max_q_per_seq=None, out=None,
+               lse=None, status=None, workspace=None, stream=None):
+    """Dense latent attention, absorbed form: every query token attends to all positions it sees of
+    the paged latent cache (bf16 [num_pages, 64, 576], or FP8 rows uint8 [num_pages, 64, 608]).
+    Returns (out [n_q, H, 512] bf16, lse [n_q, H] fp32).  ``max_q_per_seq`` bounds the tokens of a
+    sequence; ``workspace`` (mla_decode_workspace_bytes) is allocated here unless given."""
+    lib = load()
+    if q.dim() != 3 or q.shape[2] != 576:
+        raise ValueError("q must have shape [n_q, H, 576] (got %s)" % (tuple(q.shape),))
+    n_q, H, _ = q.shape
+    B = seq_lens.shape[0]
+    fp8 = kv_pool.dtype == torch.uint8
+    if kv_pool.dim() != 3 or kv_pool.shape[2] != (608 if fp8 else 576):
+        raise ValueError("kv_pool must have shape [num_pages, page_size, 576] (bf16) or [.., 608] (uint8)")
+    _typed("q", q, torch.bfloat16)
+    if not fp8:
+        _typed("kv_pool", kv_pool, torch.bfloat16)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must have one row per sequence")
+    _typed("page_table", page_table, torch.int32)
+    _typed("seq_lens", seq_lens, torch.int32, (B,))
+    _typed("q_start", q_start, torch.int32, (B + 1,))
+    _typed("out", out, torch.bfloat16, (n_q, H, 512))
+    _typed("lse", lse, torch.float32, (n_q, H))
+    _typed("status", status, torch.int32)
+    max_q_per_seq = _host_max_q(q_start, max_q_per_seq, n_q)
+    device = q.device
+    _on(device, kv_pool=kv_pool, page_table=page_table, seq_lens=seq_lens, q_start=q_start, out=out,
+        lse=lse, status=status, workspace=workspace)
+    if out is None:
+        out = torch.empty((n_q, H, 512), dtype=torch.bfloat16, device=device)
+    if lse is None:
+        lse = torch.empty((n_q, H), dtype=torch.float32, device=device)
+    a = MlaDecodeArgs()
+    a.B, a.n_q, a.H, a.d_qk, a.d_v = B, n_q, H, 576, 512
+    a.page_size, a.max_pages, a.num_pages = kv_pool.shape[1], page_table.shape[1], kv_pool.shape[0]
+    a.max_q_per_seq, a.softmax_scale = max_q_per_seq, float(softmax_scale)
+    a.kv_dtype = DSA_FP8_E4M3 if fp8 else DSA_BF16
+    if workspace is None and n_q:
+        nbytes = lib.dsa_mla_decode_workspace_bytes(ctypes.byref(a))
+        if nbytes:
+            workspace = torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    a.q, a.kv_pool, a.page_table = _ptr(q), _ptr(kv_pool), _ptr(page_table)
+    a.seq_lens, a.q_start, a.out, a.lse, a.status = (_ptr(seq_lens), _ptr(q_start), _ptr(out), _ptr(lse),
+                                                     _ptr(status))
+    if workspace is not None:
+        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+    _check(lib.dsa_mla_decode(ctypes.byref(a), _stream(stream)), "dsa_mla_decode")
+    return out, lse
+
+
+def mla_prefill(q, kv, k_rope, q_start, kv_start, *, softmax_scale, max_q_per_seq=None, out=None, lse=None,
+                status=None, stream=None):
+    """Dense latent attention, expanded form: q [n_q, H, 192] against every head's keys and values
+    kv [n_kv, H, 256] (128 key columns, 128 value columns: the up-projection's output) and the
+    shared rope keys k_rope [n_kv, 64], which may be a strided view of the latent rows.  The
+    tokens of a sequence are its last positions.  Returns (out [n_q, H, 128] bf16, lse [n_q, H])."""
+    lib = load()
+    if q.dim() != 3 or q.shape[2] != 192:
+        raise ValueError("q must have shape [n_q, H, 192] (got %s)" % (tuple(q.shape),))
+    n_q, H, _ = q.shape
+    n_kv = kv.shape[0]
+    B = q_start.shape[0] - 1
+    _typed("q", q, torch.bfloat16)
+    _typed("kv", kv, torch.bfloat16, (n_kv, H, 256))
+    _typed("k_rope", k_rope, torch.bfloat16, (n_kv, 64))
+    _typed("q_start", q_start, torch.int32)
+    _typed("kv_start", kv_start, torch.int32, (B + 1,))
+    _typed("out", out, torch.bfloat16, (n_q, H, 128))
+    _typed("lse", lse, torch.float32, (n_q, H))
+    _typed("status", status, torch.int32)
+    if n_kv > 1 and k_rope.stride(0) < 64 or n_kv > 0 and k_rope.stride(1) != 1:
+        raise ValueError("the columns of k_rope must be adjacent, and its rows apart")
+    max_q_per_seq = _host_max_q(q_start, max_q_per_seq, n_q)
+    device = q.device
+    _on(device, kv=kv, k_rope=k_rope, q_start=q_start, kv_start=kv_start, out=out, lse=lse, status=status)
+    if out is None:
+        out = torch.empty((n_q, H, 128), dtype=torch.bfloat16, device=device)
+    if lse is None:
+        lse = torch.empty((n_q, H), dtype=torch.float32, device=device)
+    a = MlaPrefillArgs()
+    a.B, a.n_q, a.n_kv, a.H, a.d_nope, a.d_rope, a.d_v = B, n_q, n_kv, H, 128, 64, 128
+    a.max_q_per_seq, a.softmax_scale = max_q_per_seq, float(softmax_scale)
+    a.k_rope_stride = k_rope.stride(0) if n_kv > 1 else 64
+    a.q, a.kv, a.k_rope = _ptr(q), _ptr(kv), k_rope.data_ptr()
+    a.q_start, a.kv_start, a.out, a.lse, a.status = (_ptr(q_start), _ptr(kv_start), _ptr(out), _ptr(lse),
+                                                     _ptr(status))
+    _check(lib.dsa_mla_prefill(ctypes.byref(a), _stream(stream)), "dsa_mla_prefill")
+    return out, lse
 
 
 def topk_merge(cand_idx, cand_score, shard_offset, K, *, out_idx=None, out_cnt=None, stream=None):

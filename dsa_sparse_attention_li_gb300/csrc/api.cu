@@ -226,6 +226,73 @@ dsa_status dsa_sfa_prefill(const dsa_sfa_args* a, dsa_stream_t stream) {
   return sfa_common(a, true, stream);
 }
 
+static dsa_status mla_decode_check(const dsa_mla_decode_args* a, bool pointers) {
+  if (!a) return fail(DSA_ERR_INVALID_ARG, "mla_decode: args is NULL");
+  if (a->B <= 0 || a->n_q < 0 || a->H <= 0 || a->max_pages <= 0 || a->num_pages <= 0 || a->max_q_per_seq <= 0)
+    return fail(DSA_ERR_INVALID_ARG, "mla_decode: non-positive size");
+  if (a->H > 128) return fail(DSA_ERR_UNSUPPORTED, "mla_decode: H > 128");
+  if (!pointers) return DSA_OK;  // sizes only (workspace query)
+  if (!(a->softmax_scale > 0.f) || a->softmax_scale > 3.0e38f)
+    return fail(DSA_ERR_INVALID_ARG, "mla_decode: softmax_scale must be positive and finite");
+  if (a->d_qk != 576 || a->d_v != 512) return fail(DSA_ERR_UNSUPPORTED, "mla_decode: d_qk must be 576 and d_v 512");
+  if (a->page_size != 64) return fail(DSA_ERR_UNSUPPORTED, "mla_decode: page_size must be 64");
+  if (a->kv_dtype != DSA_BF16 && a->kv_dtype != DSA_FP8_E4M3)
+    return fail(DSA_ERR_UNSUPPORTED, "mla_decode: kv_dtype must be BF16 or FP8_E4M3");
+  if ((long long)a->max_pages * 64 > 0x7fffffffLL || (long long)a->num_pages * 64 > 0x7fffffffLL ||
+      (long long)a->n_q * a->H > 0x7fffffffLL)
+    return fail(DSA_ERR_UNSUPPORTED, "mla_decode: positions, cache rows and query rows must number below 2^31");
+  if (a->n_q == 0) return DSA_OK;
+  if (!a->q || !a->kv_pool || !a->page_table || !a->seq_lens || !a->q_start || !a->out)
+    return fail(DSA_ERR_INVALID_ARG, "mla_decode: null device pointer");
+  if (!aligned16(a->q) || !aligned16(a->kv_pool) || !aligned16(a->out))
+    return fail(DSA_ERR_INVALID_ARG, "mla_decode: q, kv_pool, out must be 16-byte aligned");
+  if (a->workspace != nullptr && (reinterpret_cast<uintptr_t>(a->workspace) & 255u) != 0)
+    return fail(DSA_ERR_INVALID_ARG, "mla_decode: workspace must be 256-byte aligned");
+  const size_t need = dsa::mla_decode_workspace_bytes(*a);
+  if (need > 0 && (a->workspace == nullptr || a->workspace_bytes < need))
+    return fail(DSA_ERR_INVALID_ARG, "mla_decode: workspace of " + std::to_string(need) + " bytes required (got " +
+                                         std::to_string(a->workspace ? a->workspace_bytes : 0) + ")");
+  return DSA_OK;
+}
+
+size_t dsa_mla_decode_workspace_bytes(const dsa_mla_decode_args* a) {
+  if (mla_decode_check(a, false) != DSA_OK || a->n_q == 0) return 0;
+  return dsa::mla_decode_workspace_bytes(*a);
+}
+
+dsa_status dsa_mla_decode(const dsa_mla_decode_args* a, dsa_stream_t stream) {
+  g_last_error.clear();
+  const dsa_status c = mla_decode_check(a, true);
+  if (c != DSA_OK || a->n_q == 0) return c;
+  std::string err;
+  const dsa_status s = dsa::launch_mla_decode(*a, reinterpret_cast<cudaStream_t>(stream), err);
+  if (s != DSA_OK) g_last_error = err;
+  return s;
+}
+
+dsa_status dsa_mla_prefill(const dsa_mla_prefill_args* a, dsa_stream_t stream) {
+  g_last_error.clear();
+  if (!a) return fail(DSA_ERR_INVALID_ARG, "mla_prefill: args is NULL");
+  if (a->B <= 0 || a->n_q < 0 || a->n_kv < 0 || a->H <= 0 || a->max_q_per_seq <= 0)
+    return fail(DSA_ERR_INVALID_ARG, "mla_prefill: non-positive size");
+  if (!(a->softmax_scale > 0.f) || a->softmax_scale > 3.0e38f)
+    return fail(DSA_ERR_INVALID_ARG, "mla_prefill: softmax_scale must be positive and finite");
+  if (a->d_nope != 128 || a->d_rope != 64 || a->d_v != 128)
+    return fail(DSA_ERR_UNSUPPORTED, "mla_prefill: d_nope must be 128, d_rope 64 and d_v 128");
+  if (a->H > 1024) return fail(DSA_ERR_UNSUPPORTED, "mla_prefill: H > 1024");
+  if (a->k_rope_stride < a->d_rope) return fail(DSA_ERR_INVALID_ARG, "mla_prefill: k_rope_stride below d_rope");
+  if (a->k_rope_stride % 8) return fail(DSA_ERR_UNSUPPORTED, "mla_prefill: k_rope rows must start 16-byte aligned");
+  if (a->n_q == 0) return DSA_OK;
+  if (!a->q || (a->n_kv > 0 && (!a->kv || !a->k_rope)) || !a->q_start || !a->kv_start || !a->out)
+    return fail(DSA_ERR_INVALID_ARG, "mla_prefill: null device pointer");
+  if (!aligned16(a->q) || !aligned16(a->kv) || !aligned16(a->k_rope) || !aligned16(a->out))
+    return fail(DSA_ERR_INVALID_ARG, "mla_prefill: q, kv, k_rope, out must be 16-byte aligned");
+  std::string err;
+  const dsa_status s = dsa::launch_mla_prefill(*a, reinterpret_cast<cudaStream_t>(stream), err);
+  if (s != DSA_OK) g_last_error = err;
+  return s;
+}
+
 dsa_status dsa_topk_merge(const dsa_topk_merge_args* a, dsa_stream_t stream) {
   g_last_error.clear();
   if (!a) return fail(DSA_ERR_INVALID_ARG, "topk_merge: null args");

@@ -43,6 +43,9 @@ dsa_status launch_cache_write(void* pool, float* scale_pool, int num_pages, int 
                               cudaStream_t stream, std::string& err);
 dsa_status launch_cache_rows(const dsa_cache_rows_args& a, bool write, cudaStream_t stream,
                              std::string& err);
+dsa_status launch_mla_decode(const dsa_mla_decode_args& a, cudaStream_t stream, std::string& err);
+size_t mla_decode_workspace_bytes(const dsa_mla_decode_args& a);
+dsa_status launch_mla_prefill(const dsa_mla_prefill_args& a, cudaStream_t stream, std::string& err);
 
 // 2-D tiled TMA descriptor over a row-major [outer][inner] array (inner contiguous).
 bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,

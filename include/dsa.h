@@ -226,6 +226,101 @@ dsa_status dsa_sfa_prefill(const dsa_sfa_args* args, dsa_stream_t stream);
 dsa_status dsa_sfa_decode_static(const dsa_sfa_args* args, dsa_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------ */
+/* Dense latent attention                                                                      */
+/* ------------------------------------------------------------------------------------------ */
+
+/*
+ * Attention over every position a token sees, absorbed form: dsa_sfa_decode without the selection,
+ * for contexts up to top-K, for layers without an indexer and for draft layers.  For query token t
+ * (at position p = seq_lens[b] - n_b + i of sequence b) and head h, over j = 0 .. p:
+ *   z_j = softmax_scale * q[t][h][0:d_qk] . kv[j][0:d_qk]
+ *   out[t][h][:] = sum_j exp(z_j - m) kv[j][0:d_v] / sum_j exp(z_j - m),   m = max_j z_j
+ *   lse[t][h]    = m + ln(sum_j exp(z_j - m))
+ * q is the query with the keys' up-projection absorbed; the value is the leading d_v columns of
+ * the latent row.  A token that sees nothing (p < 0) gets out = 0 and lse = -inf.
+ *
+ * A value that a token does not see never reaches its output, whatever it holds: cache rows past
+ * a sequence's length may hold NaN or infinities, and so may the rows of a sequence's later tokens.
+ * A NaN that a token does see makes its whole output row NaN or leaves NaN in the columns it is in.
+ * Rows of out and lse of tokens that no sequence owns (before q_start[0], from q_start[B] on) are
+ * left as they were.  A length below 0 or above max_pages * page_size, a page id outside
+ * [0, num_pages), and a q_start that decreases or leaves [0, n_q] set DSA_ERR_DEVICE_CHECK; the
+ * length is clamped, the page's positions are skipped, the sequence is skipped.
+ *
+ * Workspace: dsa_mla_decode_workspace_bytes() bytes, no initial value; a call leaves nothing in it
+ * that a later call needs.  Calls that may overlap on the GPU need one each.
+ *
+ * Supported: page_size 64; d_qk 576; d_v 512; 1 <= H <= 128; bf16 q/out; latent cache bf16 or FP8
+ * (608-byte rows, as for dsa_sfa_decode); any lengths that the page table covers; any number of
+ * tokens per sequence.  max_q_per_seq (at least 1) is the host's bound of q_start[b+1]-q_start[b];
+ * it sizes the groups of tokens that share a pass over the cache, and more tokens than it says
+ * only take more passes.
+ */
+typedef struct {
+  int B, n_q;
+  int H;              /* query heads                                                     */
+  int d_qk, d_v;      /* 576, 512                                                        */
+  int page_size, max_pages, num_pages;
+  int max_q_per_seq;
+  float softmax_scale;
+  dsa_dtype kv_dtype;        /* DSA_BF16 (rows of 576 bf16) or DSA_FP8_E4M3 (608-byte rows) */
+  const void* q;             /* [n_q][H][d_qk] bf16                                      */
+  const void* kv_pool;       /* [num_pages][page_size][576 bf16 | 608 bytes]             */
+  const int32_t* page_table; /* [B][max_pages]                                           */
+  const int32_t* seq_lens;   /* [B] positions, new tokens included                       */
+  const int32_t* q_start;    /* [B+1]                                                    */
+  void* out;                 /* [n_q][H][d_v] bf16                                       */
+  float* lse;                /* [n_q][H] fp32, or NULL                                   */
+  int32_t* status;           /* device int32 error word, or NULL                         */
+  void* workspace;           /* device scratch, 256-B aligned                            */
+  size_t workspace_bytes;
+} dsa_mla_decode_args;
+
+/* Scratch that dsa_mla_decode needs for these arguments (only n_q, H and max_q_per_seq are read;
+ * host only, it reads the current device's SM count and launches nothing). */
+size_t dsa_mla_decode_workspace_bytes(const dsa_mla_decode_args* args);
+dsa_status dsa_mla_decode(const dsa_mla_decode_args* args, dsa_stream_t stream);
+
+/*
+ * The same attention in its expanded form, for many new tokens: every head has its own keys and
+ * values, the up-projection of the latent rows (a matrix product on the rows that dsa_cache_read
+ * returns), and all heads share one rope key.  Keys and values are packed over sequences:
+ * those of sequence b are kv_start[b] .. kv_start[b+1]-1, n_kv_b of them, and its n_b query
+ * tokens are the last n_b positions, so token i sees j = 0 .. n_kv_b - n_b + i of them:
+ *   z_j = softmax_scale * (q[t][h][0:128] . kv[j][h][0:128] + q[t][h][128:192] . k_rope[j])
+ *   out[t][h][:] = softmax(z) . kv[:][h][128:256],   lse[t][h] = ln sum_j exp(z_j)
+ * With q_absorbed = [W_uk[h]^T q_nope | q_rope], dsa_mla_decode followed by W_uv gives the same
+ * output up to rounding.  A token that sees nothing gets out = 0 and lse = -inf; tokens that no
+ * sequence owns keep their rows.  Keys and values of other sequences, and of later tokens, never
+ * reach a token's output, whatever they hold; a NaN or infinity among the values that a token
+ * does see may make its whole output row NaN.  A q_start or kv_start that decreases or leaves its array, and more tokens in a
+ * sequence than max_q_per_seq, set DSA_ERR_DEVICE_CHECK; that sequence, or its further tokens,
+ * are skipped.
+ *
+ * Supported: d_nope 128, d_rope 64, d_v 128; 1 <= H <= 1024; bf16; q, kv, k_rope and out 16-byte
+ * aligned, k_rope_stride a multiple of 8.
+ */
+typedef struct {
+  int B, n_q, n_kv;
+  int H;
+  int d_nope, d_rope, d_v;   /* 128, 64, 128                                             */
+  int max_q_per_seq;         /* host-known upper bound of q_start[b+1]-q_start[b]        */
+  float softmax_scale;
+  long long k_rope_stride;   /* elements from one row of k_rope to the next (576: a view of the
+                                latent rows' last columns)                               */
+  const void* q;             /* [n_q][H][192] bf16                                       */
+  const void* kv;            /* [n_kv][H][256] bf16: 128 key columns, then 128 value columns */
+  const void* k_rope;        /* [n_kv][64] bf16                                          */
+  const int32_t* q_start;    /* [B+1]                                                    */
+  const int32_t* kv_start;   /* [B+1]                                                    */
+  void* out;                 /* [n_q][H][128] bf16                                       */
+  float* lse;                /* [n_q][H] fp32, or NULL                                   */
+  int32_t* status;           /* device int32 error word, or NULL                         */
+} dsa_mla_prefill_args;
+
+dsa_status dsa_mla_prefill(const dsa_mla_prefill_args* args, dsa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
 /* Context-parallel top-K merge                                                                */
 /* ------------------------------------------------------------------------------------------ */
 
