@@ -238,7 +238,7 @@ static dsa_status mla_decode_check(const dsa_mla_decode_args* a, bool pointers) 
   if (a->page_size != 64) return fail(DSA_ERR_UNSUPPORTED, "mla_decode: page_size must be 64");
   if (a->kv_dtype != DSA_BF16 && a->kv_dtype != DSA_FP8_E4M3)
     return fail(DSA_ERR_UNSUPPORTED, "mla_decode: kv_dtype must be BF16 or FP8_E4M3");
-  if ((long long)a->max_pages * 64 > 0x7fffffffLL || (long long)a->num_pages * 64 > 0x7fffffffLL ||
+  if ((long long)a->max_pages * 64 > 0x7ffffe00LL || (long long)a->num_pages * 64 > 0x7fffffffLL ||
       (long long)a->n_q * a->H > 0x7fffffffLL)
     return fail(DSA_ERR_UNSUPPORTED, "mla_decode: positions, cache rows and query rows must number below 2^31");
   if (a->n_q == 0) return DSA_OK;

@@ -1,18 +1,62 @@
 // mla_decode.cu -- dense latent attention over the paged cache, absorbed form.
 //
-// One warp per (token, head): 18 of the 576 columns a lane, online softmax over the positions.
+//   z_j = scale q.kv_j (576 columns),  out = sum_j softmax(z)_j kv_j[0:512],  j up to the token's own
+//   position; flash attention with a running maximum and sum, the 64-token page as unit of the cache.
+//
+// Rows.  The T tokens of a sequence that share a pass over its cache, T = min(128 / H, tokens), give
+// T * H <= 128 query rows: the M = 128 of one two-CTA MMA (cta_group::2), 64 rows a CTA.  O is then
+// 64 x 512 fp32 a CTA, which in the two-CTA layout (two lanes a row) is 256 of the 512 TMEM columns,
+// so each CTA owns whole rows: no score, maximum or weight ever crosses the pair (dsa_sfa_decode,
+// whose O is split by columns, exchanges all three).
+//
+// Tiles of two pages.  Q.K^T has N = 128: CTA r supplies the 64 rows of page r (all 576 columns).
+// P.V has N = 256 twice: CTA r supplies value columns [256 r, 256 r + 256) of both pages, 64-column
+// blocks as MN-major operands.  The two uses need different halves of the tile, so a CTA loads its
+// page and the other page's value half, and its own page's value half again (the operands of both
+// CTAs must lie at the same offsets): 139 KB a tile and CTA against 74 KB that are distinct, from L2.
+//
+// Shared memory has room for one tile beside Q, so both operands are recycled in blocks: a K block
+// (64 columns, 8 KB) is reloaded for the next tile as soon as its four MMAs are done, a V slot (64
+// rows x 128 columns) likewise; the pages three tiles ahead are prefetched into L2 meanwhile.
+//
+// Work split.  Every group of T tokens counts ceil(length / 128) units of work; the units of all
+// groups form one line, cut into one equal range per CTA pair (whole wave, any mix of lengths).  A
+// group cut by a range border leaves normalised fp32 rows and their log-sum-exp in the workspace (at
+// most two such pieces a pair), and a second kernel joins the pieces in order.
+//
+// Bound: HBM for one token a sequence (1152 B and 278,528 FLOP a position at H = 128: 242 FLOP/B),
+// the tensor pipe for more.  A tile's 36 + 16 MMAs take 36 * 49 + 16 * 64 = 2,800 cycles.
+#include <algorithm>
+
 #include "dsa_internal.h"
 #include "ptx.cuh"
 
 namespace dsa {
 namespace mlad {
 
-constexpr int kWarps = 8;
+// Warps 0-3 softmax, 4 MMA (even CTA), 5 Q and K loads, 6 V loads; with an FP8 cache 5 loads Q, 8-11
+// convert K and 12-15 convert V.
+template <bool KV8>
+constexpr int kThreads = KV8 ? 512 : 256;
+constexpr int kKv8Row = 608;    // 576 e4m3 codes, 5 fp32 scales, 12 unused bytes
+constexpr int kTile = 128;      // positions a tile
+constexpr int kDqk = 576;
+constexpr int kDv = 512;
+constexpr int kKBlocks = 9;     // 64-column blocks of K (and of Q)
+constexpr int kKGroups = 3;     // a barrier, and a reload, per three blocks
+constexpr int kVPages = 2;      // V: a barrier, and a reload, per page of this CTA's 256 value columns
+constexpr int kBlockBytes = 64 * 128;   // 64 rows x 64 bf16
+constexpr int kKGroupBytes = 3 * kBlockBytes;
+constexpr int kVHalfBytes = 2 * kBlockBytes;   // 128 columns of a page
+constexpr int kVPageBytes = 2 * kVHalfBytes;
+constexpr int kPrefetch = 3;    // tiles
+constexpr float kRescaleLog2 = 8.0f;
+constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 
 struct Params {
-  int B, n_q, H, max_pages, num_pages;
+  int B, n_q, H, T, max_pages, num_pages;
+  int pairs;
   float scale_log2;
-  const __nv_bfloat16* q;
   const uint8_t* kv;
   const int* page_table;
   const int* seq_lens;
@@ -20,88 +64,881 @@ struct Params {
   __nv_bfloat16* out;
   float* lse;
   int* status;
+  float* ws_o;     // [pairs][2][rows][512]
+  float* ws_lse;   // [pairs][2][rows], log2
+  int4* ws_join;   // [pairs] {first token, rows, first piece's slot, pieces} of the group that a
+                   // pair's first unit continues; pieces 0: none, or another pair joins it
+  int ws_rows;
+};
+
+struct Layout {
+  static constexpr int q = 0;
+  static constexpr int k = q + kKBlocks * kBlockBytes;
+  static constexpr int v = k + kKBlocks * kBlockBytes;
+  static constexpr int p = v + kVPages * kVPageBytes;
+  static constexpr int ctl = p + 2 * kBlockBytes;
+  static constexpr int total = ctl + 2048;
+};
+
+struct Ctl {
+  uint64_t q_full, q_empty;
+  uint64_t k_full[kKGroups], k_empty[kKGroups];
+  uint64_t v_full[kVPages], v_empty[kVPages];
+  uint64_t s_full[2], s_free[2];
+  uint64_t p_full, pv_done, o_free, edge;
+  uint32_t tmem_base;
+  int abort;
+  int start_b;
+  int bad_pages;
+  int piece[2];   // tiles of a piece
+  long long start_at, part[16];
+  float x[128];
+};
+static_assert(sizeof(Ctl) <= 2048, "control block");
+
+DSA_DEV float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A shared-memory matrix descriptor moved by a constant (the address field cannot carry: every operand
+// lies below 256 KiB).
+DSA_DEV uint64_t desc_at(uint64_t d, int bytes) {
+  uint32_t lo = (uint32_t)d, hi = (uint32_t)(d >> 32);
+  lo += (uint32_t)(bytes >> 4);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+// The same value, newly made: what is computed from it is not kept in registers over a loop (the MMA
+// warp's 104 descriptor words cost the other warps their registers).
+DSA_DEV uint32_t fresh(uint32_t x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
+
+DSA_DEV uint32_t pack_bf16(float a, float b) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// Two bf16 with what is not finite set to zero.
+DSA_DEV uint32_t finite_bf16x2(uint32_t e) {
+  if ((e & 0x7f80u) == 0x7f80u) e &= 0xffff0000u;
+  if ((e & 0x7f800000u) == 0x7f800000u) e &= 0xffffu;
+  return e;
+}
+
+// 16 e4m3 codes times their scale as bf16 (fp32 product, both roundings to nearest even): the operand
+// that an element of an FP8 latent row stands for.
+DSA_DEV void dequant16(uint4 c, float s, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t two = i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu;
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    o[i] = pack_bf16(f.x * s, f.y * s);
+  }
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// Bounded wait of a whole warp, which is converged again after it.
+DSA_DEV void warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  mbar_wait_fast(bar, parity, abort, status);
+  __syncwarp();
+}
+
+// A sequence's tokens and length, checked: n = 0 where q_start is out of order.
+struct Seq {
+  int s0, n, len;
+};
+DSA_DEV Seq sequence(const Params& p, int b, bool tell) {
+  Seq s = {0, 0, 0};
+  if (b < p.B) {
+    const int s0 = p.q_start[b], s1 = p.q_start[b + 1], len = p.seq_lens[b];
+    const int most = p.max_pages * 64;
+    s.s0 = s0;
+    s.len = max(0, min(len, most));
+    const bool ok = s0 >= 0 && s1 >= s0 && s1 <= p.n_q;
+    s.n = ok ? s1 - s0 : 0;
+    if (tell && (!ok || (s.n > 0 && (len < 0 || len > most)))) report(p.status, kStatusDeviceCheck);
+  }
+  return s;
+}
+DSA_DEV int unit_count(const Seq& s) { return max(1, (s.len + kTile - 1) / kTile); }
+DSA_DEV long long units(const Params& p, const Seq& s) {
+  return (long long)((s.n + p.T - 1) / p.T) * unit_count(s);
+}
+
+// One pair's share of the line of units, group by group.  Every warp walks it on its own.
+struct Walk {
+  int b, g;             // sequence, token group
+  long long at;         // line position of the group's first unit
+  long long pos, end;   // the rest of the pair's range
+  Seq s;
+  // the current piece: tiles [tile0, tile1) of the group's `tiles`
+  int tile0, tile1, tiles, t0, rows, seen_first, seen_last;
+  bool first;
+
+  DSA_DEV void set(const Params& p) {
+    const int i0 = g * p.T, n = min(p.T, s.n - i0);
+    t0 = s.s0 + i0;
+    rows = n * p.H;
+    seen_first = s.len - s.n + i0 + 1;   // positions that the group's first and last token see
+    seen_last = seen_first + n - 1;
+    tiles = max(1, (seen_last + kTile - 1) / kTile);
+    const long long u = unit_count(s);
+    const long long stop = at + u < end ? at + u : end;
+    tile0 = (int)(pos - at);
+    tile1 = min((int)(stop - at), tiles);
+  }
+  // Next piece with any tile in it; false at the end of the range.
+  DSA_DEV bool next(const Params& p, int lane) {
+    while (true) {
+      const long long u = unit_count(s);
+      pos = at + u;
+      first = false;
+      if (pos >= end) return false;
+      at = pos;
+      ++g;
+      if ((long long)g * p.T >= s.n) {
+        g = 0;
+        while (true) {  // the next sequence with tokens (there is one: the range goes on)
+          const Seq c = sequence(p, b + 1 + lane, false);
+          const uint32_t some = __ballot_sync(0xffffffffu, c.n > 0);
+          if (some == 0) {
+            b += 32;
+            if (b >= p.B) return false;
+            continue;
+          }
+          const int l = __ffs((int)some) - 1;
+          b += 1 + l;
+          s.s0 = __shfl_sync(0xffffffffu, c.s0, l);
+          s.n = __shfl_sync(0xffffffffu, c.n, l);
+          s.len = __shfl_sync(0xffffffffu, c.len, l);
+          break;
+        }
+      }
+      set(p);
+      if (tile0 < tile1) return true;
+    }
+  }
+  DSA_DEV bool whole() const { return tile0 == 0 && tile1 == tiles; }
 };
 
 template <bool KV8>
-__global__ void __launch_bounds__(kWarps * 32) mla_decode_kernel(const Params p) {
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < p.B; i += kWarps * 32)
-      if (p.q_start[i] < 0 || p.q_start[i + 1] < p.q_start[i] || p.q_start[i + 1] > p.n_q)
-        report(p.status, kStatusDeviceCheck);
-  const int t = (int)(w / p.H);
-  if (t >= p.n_q) return;
-  int lo = 0, hi = p.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.q_start[mid] <= t) lo = mid; else hi = mid - 1;
-  }
-  const int b = lo, s0 = p.q_start[b], s1 = p.q_start[b + 1];
-  if (s0 < 0 || s1 > p.n_q || t < s0 || t >= s1) return;
-  int len = p.seq_lens[b];
-  if (len < 0 || len > p.max_pages * 64) {
-    if (lane == 0) report(p.status, kStatusDeviceCheck);
-    len = max(0, min(len, p.max_pages * 64));
-  }
-  const int seen = len - (s1 - s0) + (t - s0) + 1;
-  float q[18], o[16], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < 18; ++i) q[i] = __bfloat162float(p.q[w * 576 + i * 32 + lane]);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) o[i] = 0.f;
-  for (int j = 0; j < seen; ++j) {
-    const int pg = p.page_table[(long long)b * p.max_pages + (j >> 6)];
-    if (pg < 0 || pg >= p.num_pages) {
-      if (lane == 0) report(p.status, kStatusDeviceCheck);
-      continue;
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
+    mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
+                      const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + Layout::ctl);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1;
+  volatile int* abort = &ctl->abort;
+  constexpr int kThr = kThreads<KV8>;
+  constexpr uint32_t kFills = KV8 ? 8 : 1;   // arrivals that fill a K group or V page: the
+                                             // converting warps of both CTAs, or one expect_tx
+  if (tid == 0) {
+    mbar_init(&ctl->q_full, 1);
+    mbar_init(&ctl->q_empty, 1);
+    for (int i = 0; i < kKGroups; ++i) {
+      mbar_init(&ctl->k_full[i], kFills);
+      mbar_init(&ctl->k_empty[i], 1);
     }
-    const long long row = (long long)pg * 64 + (j & 63);
-    float k[18], z = 0.f;
+    for (int i = 0; i < kVPages; ++i) {
+      mbar_init(&ctl->v_full[i], kFills);
+      mbar_init(&ctl->v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->s_full[i], 1);
+      mbar_init(&ctl->s_free[i], 8);   // four softmax warps of either CTA
+    }
+    mbar_init(&ctl->p_full, 8);
+    mbar_init(&ctl->pv_done, 1);
+    mbar_init(&ctl->o_free, 8);
+    mbar_init(&ctl->edge, 1);
+    ctl->abort = 0;
+    ctl->bad_pages = 0;
+    fence_barrier_init();
+  }
+  if (warp == 4) {
+    tmem_alloc2(&ctl->tmem_base, kTmemCols);
+    tmem_relinquish2();
+  }
+  if (warp == 5 && lane == 0) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_kv);
+  }
+  griddep_wait();  // nothing above reads global memory
+
+  // ---------------- this pair's range of the line of units
+  long long mine = 0;
+  for (int b = tid; b < p.B; b += kThr) mine += units(p, sequence(p, b, blockIdx.x == 0));
 #pragma unroll
-    for (int i = 0; i < 18; ++i) {
-      if constexpr (KV8) {
-        const uint8_t* r = p.kv + row * 608;
-        const __half_raw h = __nv_cvt_fp8_to_halfraw(r[i * 32 + lane], __NV_E4M3);
-        const float s = reinterpret_cast<const float*>(r + 576)[i >> 2];
-        k[i] = __bfloat162float(__float2bfloat16_rn(__half2float(*reinterpret_cast<const __half*>(&h)) * s));
-      } else {
-        k[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.kv)[row * 576 + i * 32 + lane]);
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) ctl->part[warp] = mine;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kThr / 32; ++w) total += ctl->part[w];
+  const long long share = max(1LL, (total + p.pairs - 1) / p.pairs);
+  Walk w0;
+  w0.pos = share * pair;
+  w0.end = min(total, w0.pos + share);
+  const bool any = w0.pos < total;
+  if (any) {
+    long long before = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThr) {
+      const long long u = units(p, sequence(p, b0 + tid, false));
+      long long incl = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
       }
-      z += q[i] * k[i];
+      __syncthreads();
+      if (lane == 31) ctl->part[warp] = incl;
+      __syncthreads();
+      long long base = before, all = 0;
+#pragma unroll
+      for (int w = 0; w < kThr / 32; ++w) {
+        if (w < warp) base += ctl->part[w];
+        all += ctl->part[w];
+      }
+      const long long lo = base + incl - u;
+      if (lo <= w0.pos && w0.pos < lo + u) {
+        ctl->start_b = b0 + tid;
+        ctl->start_at = lo;
+      }
+      before += all;
+      if (before > w0.pos) break;
     }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-    z *= p.scale_log2;
-    const float m2 = fmaxf(m, z);
-    const float a = m == m2 ? 1.f : exp2f(m - m2), e = exp2f(z - m2);
-    m = m2;
-    l = l * a + e;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = o[i] * a + e * k[i];
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // barriers and tensor memory of both CTAs are ready
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
+  bool have = false;
+  if (any) {
+    w0.b = ctl->start_b;
+    w0.s = sequence(p, w0.b, false);
+    const long long u = unit_count(w0.s);
+    w0.g = (int)((w0.pos - ctl->start_at) / u);
+    w0.at = ctl->start_at + w0.g * u;
+    w0.first = true;
+    w0.set(p);
+    have = w0.tile0 < w0.tile1 || w0.next(p, lane);
+  }
+  Walk w = w0;
+  if (warp == 5) {
+    // ---------------- Q and K loads, and the L2 prefetch
+    const uint32_t q_full = map_cluster(&ctl->q_full, 0), k_full = map_cluster(&ctl->k_full[0], 0);
+    const int oob = p.num_pages * 64;
+    uint32_t it = 0, seg = 0;
+    bool ok = true;
+    for (; have && ok; have = w.next(p, lane), ++seg) {
+      if (lane == 0) {
+        ok = seg == 0 || mbar_wait(&ctl->q_empty, (seg - 1) & 1u, abort, p.status);
+        if (ok) {
+          if (rank == 0) {
+            ctl->piece[seg & 1u] = w.tile1 - w.tile0;
+            mbar_arrive_expect_tx(&ctl->q_full, 2 * kKBlocks * kBlockBytes);
+          }
+          for (int c = 0; c < kKBlocks; ++c)
+            tma_load_2d_pair(smem + Layout::q + c * kBlockBytes, &tm_q, q_full, c * 64,
+                             w.t0 * p.H + (int)rank * 64);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if constexpr (KV8) continue;
+      const int* pt = p.page_table + (size_t)w.b * p.max_pages;
+      const int pages = (max(w.seen_last, 0) + 63) >> 6;
+      auto window = [&](int tile) {  // this CTA's page of tile + lane, -1: none
+        const int i = 2 * (tile + lane) + (int)rank;
+        if (tile + lane >= w.tile1 || i >= pages) return -1;
+        const int pg = pt[i];
+        return pg < p.num_pages ? pg : -1;
+      };
+      auto warm = [&](int pg) {
+        if (pg >= 0 && lane == 0) prefetch_l2_bulk(p.kv + (size_t)pg * 64 * (kDqk * 2), 64 * kDqk * 2);
+      };
+      int cur = window(w.tile0), nxt = window(w.tile0 + 32);
+      for (int i = w.tile0; i < w.tile1 && ok; ++i, ++it) {
+        const int j = (i - w.tile0) & 31;
+        if (j == 0 && i > w.tile0) {
+          cur = nxt;
+          nxt = window(i + 32);
+        }
+        const int pg = __shfl_sync(0xffffffffu, cur, j);
+        if (i == w.tile0)
+          for (int d = 1; d < kPrefetch; ++d) warm(__shfl_sync(0xffffffffu, cur, d));
+        const int ja = j + kPrefetch;
+        const int far = ja < 32 ? __shfl_sync(0xffffffffu, cur, ja) : __shfl_sync(0xffffffffu, nxt, ja - 32);
+        if (lane == 0) {
+          const int y = pg < 0 ? oob : pg * 64;
+          for (int c = 0; c < kKGroups && ok; ++c) {
+            ok = it == 0 || mbar_wait_fast(&ctl->k_empty[c], (it - 1) & 1u, abort, p.status);
+            if (!ok) break;
+            if (rank == 0) mbar_arrive_expect_tx(&ctl->k_full[c], 2 * kKGroupBytes);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) p.out[w * 512 + i * 32 + lane] = __float2bfloat16_rn(o[i] * inv);
-  if (lane == 0 && p.lse) p.lse[w] = l == 0.f ? -INFINITY : m * 0.69314718055994531f + logf(l);
+            for (int u = 0; u < 3; ++u)
+              tma_load_2d_pair(smem + Layout::k + (3 * c + u) * kBlockBytes, &tm_kv, k_full + c * 8, (3 * c + u) * 64, y);
+          }
+        }
+        warm(far);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      }
+    }
+    if (lane == 0 && rank == 0 && ok) {
+      ok = seg == 0 || mbar_wait(&ctl->q_empty, (seg - 1) & 1u, abort, p.status);
+      ctl->piece[seg & 1u] = 0;
+      if (ok) mbar_arrive(&ctl->q_full);
+    }
+    __syncwarp();
+  } else if (!KV8 && warp == 6) {
+    // ---------------- V loads: this CTA's 256 value columns of both pages
+    const uint32_t v_full = map_cluster(&ctl->v_full[0], 0);
+    const int oob = p.num_pages * 64;
+    uint32_t it = 0;
+    bool ok = true;
+    for (; have && ok; have = w.next(p, lane)) {
+      const int* pt = p.page_table + (size_t)w.b * p.max_pages;
+      const int pages = (max(w.seen_last, 0) + 63) >> 6;
+      int ids = -1;
+      for (int i = w.tile0; i < w.tile1 && ok; ++i, ++it) {
+        const int j = (i - w.tile0) & 15;
+        if (j == 0) {  // both pages of 16 tiles
+          const int page = 2 * i + lane;
+          ids = page < pages ? pt[page] : -1;
+          if (ids >= p.num_pages) ids = -1;
+        }
+        const int pg0 = __shfl_sync(0xffffffffu, ids, 2 * j), pg1 = __shfl_sync(0xffffffffu, ids, 2 * j + 1);
+        if (lane == 0) {
+          // a tile that some row does not see to its end: the softmax warps clean it first
+          const bool edge = (i + 1) * kTile > w.seen_first;
+          for (int s = 0; s < kVPages && ok; ++s) {
+            ok = it == 0 || mbar_wait_fast(&ctl->v_empty[s], (it - 1) & 1u, abort, p.status);
+            if (!ok) break;
+            const int pg = s == 0 ? pg0 : pg1, y = pg < 0 ? oob : pg * 64;
+            uint8_t* dst = smem + Layout::v + s * kVPageBytes;
+            if (edge) {
+              // (page 0 is free: the previous tile's weights were complete, and with them its
+              // phase of this barrier)
+              if (s == 0) mbar_arrive_expect_tx(&ctl->edge, kVPages * kVPageBytes);
+              if (rank == 0) mbar_arrive(&ctl->v_full[s]);
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                tma_load_2d(dst + u * kBlockBytes, &tm_kv, &ctl->edge, (int)rank * 256 + u * 64, y);
+            } else {
+              if (rank == 0) mbar_arrive_expect_tx(&ctl->v_full[s], 2 * kVPageBytes);
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                tma_load_2d_pair(dst + u * kBlockBytes, &tm_kv, v_full + s * 8, (int)rank * 256 + u * 64, y);
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      }
+    }
+  } else if (KV8 && warp >= 8) {
+    // ---------------- FP8 cache: warps 8-11 convert this CTA's page into K (all 576 columns), warps
+    // 12-15 both pages' value columns of this CTA into V.  A warp has 16 rows of a page; four lanes
+    // share a row, a lane takes every fourth 16-code chunk of it (two passes of eight rows), so the
+    // 16-byte stores into the 128-byte-swizzled blocks meet no bank conflict.  The codes of the next
+    // part are loaded before the wait for its slot.
+    const bool is_k = warp < 12;
+    const int r0 = (warp & 3) * 16 + (lane >> 2), q4 = lane & 3;
+    constexpr int kParts = 3;                   // K groups; V has two parts, one a page
+    const uint32_t full = is_k ? map_cluster(&ctl->k_full[0], 0) : map_cluster(&ctl->v_full[0], 0);
+    uint64_t* empty = is_k ? &ctl->k_empty[0] : &ctl->v_empty[0];
+    const int parts = is_k ? kParts : kVPages;
+    const int chunks = is_k ? 3 : 4;            // a lane's chunks of a row in a part
+    uint32_t it = 0;
+    for (; have; have = w.next(p, lane)) {
+      const int* pt = p.page_table + (size_t)w.b * p.max_pages;
+      const int pages = (max(w.seen_last, 0) + 63) >> 6;
+      // row `pass` of a part: its codes and scales, and whether it exists
+      uint4 code[2][4];
+      float scale[2][2];
+      int page_id = -1, first_chunk = 0;
+      auto fetch = [&](int i, int part) {
+        const int page = 2 * i + (is_k ? (int)rank : part);
+        first_chunk = is_k ? part * 12 : (int)rank * 16;
+        if (!is_k || part == 0) {
+          page_id = page < pages ? pt[page] : -1;
+          if (page_id >= p.num_pages) page_id = -1;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint8_t* row = p.kv + ((size_t)max(page_id, 0) * 64 + r0 + 8 * x) * kKv8Row;
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (u < chunks) code[x][u] = *reinterpret_cast<const uint4*>(row + (first_chunk + q4 + 4 * u) * 16);
+          // a part spans two scales
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            scale[x][u] = *reinterpret_cast<const float*>(row + kDqk + min((first_chunk >> 3) + u, 4) * 4);
+        }
+      };
+      fetch(w.tile0, 0);
+      for (int i = w.tile0; i < w.tile1; ++i, ++it) {
+        if (warp == 8) {  // this CTA's page of a later tile into L2
+          const int page = 2 * (i + kPrefetch) + (int)rank;
+          const int pg = i + kPrefetch < w.tile1 && page < pages ? pt[page] : -1;
+          if (pg >= 0 && pg < p.num_pages && lane == 0)
+            prefetch_l2_bulk(p.kv + (size_t)pg * 64 * kKv8Row, 64 * kKv8Row);
+        }
+#pragma unroll 1
+        for (int part = 0; part < parts; ++part) {
+          if (it > 0) warp_wait(&empty[part], (it - 1) & 1u, abort, p.status);
+          const bool edge = !is_k && (i + 1) * kTile > w.seen_first;
+          uint8_t* dst = smem + (is_k ? Layout::k + part * kKGroupBytes : Layout::v + part * kVPageBytes);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int r = r0 + 8 * x;
+            const int pos = i * kTile + part * 64 + r;   // (of V)
+            const bool none = !is_k && (page_id < 0 || (edge && pos >= w.seen_last));
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (u < chunks) {
+                const int ch = q4 + 4 * u;               // chunk of the part: 16 columns
+                const int si = ((first_chunk + ch) >> 3) - (first_chunk >> 3);
+                uint4 lo, hi;
+                dequant16(code[x][u], si == 0 ? scale[x][0] : scale[x][1], lo, hi);
+                if (none) {
+                  lo = hi = make_uint4(0u, 0u, 0u, 0u);
+                } else if (edge && pos >= w.seen_first) {
+                  lo = make_uint4(finite_bf16x2(lo.x), finite_bf16x2(lo.y), finite_bf16x2(lo.z), finite_bf16x2(lo.w));
+                  hi = make_uint4(finite_bf16x2(hi.x), finite_bf16x2(hi.y), finite_bf16x2(hi.z), finite_bf16x2(hi.w));
+                }
+                uint8_t* at = dst + (ch >> 2) * kBlockBytes + r * 128;
+                *reinterpret_cast<uint4*>(at + ((((ch & 3) * 2) ^ (r & 7)) << 4)) = lo;
+                *reinterpret_cast<uint4*>(at + ((((ch & 3) * 2 + 1) ^ (r & 7)) << 4)) = hi;
+              }
+          }
+          const bool last = part + 1 == parts;
+          if (!last || i + 1 < w.tile1) fetch(last ? i + 1 : i, last ? 0 : part + 1);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_pair(full + part * 8);
+        }
+        if (__any_sync(0xffffffffu, *abort)) break;
+      }
+      if (__any_sync(0xffffffffu, *abort)) break;
+    }
+  } else if (warp == 4 && rank == 0) {
+    // ---------------- MMA issue, for both CTAs
+    constexpr uint32_t idesc_qk = idesc_bf16(128, kTile);
+    constexpr uint32_t idesc_pv = idesc_bf16(128, 256, /*b_mn_major=*/true);
+    const uint32_t q_at = smem_u32(smem + Layout::q), k_at = smem_u32(smem + Layout::k),
+                   v_at = smem_u32(smem + Layout::v), p_at = smem_u32(smem + Layout::p);
+    // The whole warp walks the tiles and one lane issues, in the order Q.K^T of tile i + 1, P.V of tile i: the softmax of a tile runs under
+    // the next tile's Q.K^T.  Fully unrolled, with operand offsets that are constants: an issue loop
+    // with integer work around each instruction ran at a third of the tensor pipe's rate.  The K
+    // loads say how many tiles each piece has (0: the end) when they arm its Q barrier.
+    {
+      const uint32_t me = elect_one();
+      auto qk = [&](uint32_t n) {
+        if (n >= 2) warp_wait(&ctl->s_free[n & 1u], ((n >> 1) - 1) & 1u, abort, p.status);
+        const uint32_t d = tmem + kColS + (n & 1u) * 64u;
+        const uint64_t qd = sdesc_sw128(fresh(q_at), 16, 1024), kd = sdesc_sw128(fresh(k_at), 16, 1024);
+#pragma unroll
+        for (int c = 0; c < kKGroups; ++c) {
+          warp_wait(&ctl->k_full[c], n & 1u, abort, p.status);
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 12; ++kk) {
+            const int at = c * kKGroupBytes + (kk >> 2) * kBlockBytes + (kk & 3) * 32;
+            mma2_f16_ss(d, desc_at(qd, at), desc_at(kd, at), idesc_qk, (c > 0 || kk > 0) ? 1u : 0u, me);
+          }
+          mma2_commit_both(&ctl->k_empty[c], me);
+        }
+        mma2_commit_both(&ctl->s_full[n & 1u], me);
+      };
+      auto pv = [&](uint32_t n, bool first) {
+        warp_wait(&ctl->p_full, n & 1u, abort, p.status);
+        const uint64_t pd = sdesc_sw128(fresh(p_at), 16, 1024), vd = sdesc_sw128(fresh(v_at), kBlockBytes, 1024);
+#pragma unroll
+        for (int v = 0; v < kVPages; ++v) {
+          warp_wait(&ctl->v_full[v], n & 1u, abort, p.status);
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              mma2_f16_ss(tmem + kColO + (uint32_t)(h * 128), desc_at(pd, v * kBlockBytes + kk * 32),
+                          desc_at(vd, v * kVPageBytes + h * kVHalfBytes + kk * 2048), idesc_pv,
+                          (v > 0 || kk > 0) ? 1u : first ? 0u : 1u, me);
+          mma2_commit_both(&ctl->v_empty[v], me);
+        }
+        mma2_commit_both(&ctl->pv_done, me);
+      };
+      // after a wait that gave up, the rest runs on whatever is there: nothing of it is kept
+      uint32_t n = 0;       // tiles whose Q.K^T is issued; their P.V runs one behind
+      bool behind_first = false;
+      for (uint32_t seg = 0;; ++seg) {
+        warp_wait(&ctl->q_full, seg & 1u, abort, p.status);
+        const int tiles = __shfl_sync(0xffffffffu, ctl->piece[seg & 1u], 0);
+        if (tiles == 0 || __any_sync(0xffffffffu, *abort)) break;
+#pragma unroll 1
+        for (int i = 0; i < tiles; ++i, ++n) {
+          if (__any_sync(0xffffffffu, *abort)) break;
+          qk(n);
+          if (i + 1 == tiles) mma2_commit_both(&ctl->q_empty, me);
+          if (n > 0) pv(n - 1, behind_first);
+          // O is the previous piece's until its rows have been read
+          if (i == 0 && seg > 0) warp_wait(&ctl->o_free, (seg - 1) & 1u, abort, p.status);
+          behind_first = i == 0;
+        }
+      }
+      if (n > 0) pv(n - 1, behind_first);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ---------------- softmax: lane l of the CTA's 128 is row l & 63, page l >> 6 of a tile
+    const int row = tid & 63, half = tid >> 6;
+    const int mrow = (int)rank * 64 + row;           // row of the group
+    const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t s_free = map_cluster(&ctl->s_free[0], 0), p_full = map_cluster(&ctl->p_full, 0),
+                   o_free = map_cluster(&ctl->o_free, 0);
+    uint8_t* p_row = smem + Layout::p + half * kBlockBytes + row * 128;
+    uint32_t it = 0, edges = 0;
+    int nseg = 0;
+    bool ok = true;
+    for (; have && ok; have = w.next(p, lane), ++nseg) {
+      const bool active = mrow < w.rows;
+      const bool busy = __any_sync(0xffffffffu, active);
+      // (rows that are no one's count as seeing everything: no masking, and nothing of them is kept)
+      const int seen = active ? w.seen_first + mrow / p.H : 0x7fffffff;
+      // pages that do not exist are masked: look for them once
+      {
+        const int* pt = p.page_table + (size_t)w.b * p.max_pages;
+        const int pages = min((max(w.seen_last, 0) + 63) >> 6, 2 * w.tile1);
+        int bad = 0;
+        for (int i = 2 * w.tile0 + tid; i < pages; i += 128) {
+          const int pg = pt[i];
+          bad |= pg < 0 || pg >= p.num_pages;
+        }
+        if (bad) {
+          report(p.status, kStatusDeviceCheck);
+          ctl->bad_pages = nseg + 1;
+        }
+      }
+      named_barrier(1, 128);
+      const bool check_pages = ctl->bad_pages == nseg + 1;
+      float m_ref = -INFINITY, l = 0.f;
+      for (int i = w.tile0; i < w.tile1; ++i, ++it) {
+        const uint32_t buf = it & 1u;
+        warp_wait(&ctl->s_full[buf], (it >> 1) & 1u, abort, p.status);
+        tc_fence_after();
+        uint32_t sr[64];
+        tmem_ld_x32(lane_addr + kColS + buf * 64u, sr);
+        tmem_ld_x32(lane_addr + kColS + buf * 64u + 32u, sr + 32);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_relaxed(s_free + buf * 8);
+        const int pos0 = i * kTile + half * 64;
+        int keep = min(64, seen - pos0);  // visible columns of ours
+        if (check_pages && keep > 0) {
+          const int pg = p.page_table[(size_t)w.b * p.max_pages + (pos0 >> 6)];
+          if (pg < 0 || pg >= p.num_pages) keep = 0;
+        }
+        float mx = -INFINITY;
+        if (__all_sync(0xffffffffu, keep == 64)) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) mx = fmaxf(mx, __uint_as_float(sr[c]));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            if (c >= keep) sr[c] = 0xff800000u;
+            mx = fmaxf(mx, __uint_as_float(sr[c]));
+          }
+        }
+        mx *= p.scale_log2;
+        // one vote a tile; a warp whose wait gave up brings all to the second one, where they leave
+        if (!named_barrier_and(2, 128, !*abort && !(active && mx > m_ref + kRescaleLog2))) {
+          // some row's maximum has outgrown its reference: every row takes its true maximum
+          ctl->x[tid] = mx;
+          ok = named_barrier_and(1, 128, !*abort);
+          if (!ok) break;
+          const float m_new = fmaxf(m_ref, fmaxf(mx, ctl->x[tid ^ 64]));
+          const float alpha = m_new == m_ref ? 1.f : fast_exp2(m_ref - m_new);
+          m_ref = m_new;
+          l *= alpha;
+          if (i > w.tile0) {
+            warp_wait(&ctl->pv_done, (it - 1) & 1u, abort, p.status);
+            tc_fence_after();
+            if (busy) {
+#pragma unroll 1
+              for (int cc = 0; cc < 16; ++cc) {
+                uint32_t o[16];
+                tmem_ld_x16(lane_addr + kColO + (uint32_t)(cc * 16), o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                tmem_st_x16(lane_addr + kColO + (uint32_t)(cc * 16), o);
+              }
+              tmem_st_wait();
+            }
+            tc_fence_before();
+          }
+        }
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+        if (busy) {
+          float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const float a = fast_exp2(fmaf(__uint_as_float(sr[c]), p.scale_log2, -m_use));
+            const float b = fast_exp2(fmaf(__uint_as_float(sr[c + 1]), p.scale_log2, -m_use));
+            sum0 += a;
+            sum1 += b;
+            sr[c >> 1] = pack_bf16(a, b);  // P.V takes bf16 weights: 2^-8 relative each, unbiased
+          }
+          l += sum0 + sum1;
+        }
+        // P is free once the previous tile's P.V has read it
+        if (it > 0) warp_wait(&ctl->pv_done, (it - 1) & 1u, abort, p.status);
+        if (busy) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(p_row + ((c ^ (row & 7)) << 4)) =
+                make_uint4(sr[4 * c], sr[4 * c + 1], sr[4 * c + 2], sr[4 * c + 3]);
+        }
+        if (!KV8 && (i + 1) * kTile > w.seen_first) {
+          // value rows that some row of the group does not see: a weight of 0 times what they hold
+          // must be 0.  Past every token's end they become 0; among the tokens' own rows only what
+          // is not finite does (the rows that see it get their NaN from the scores, whose keys are
+          // the same columns).
+          warp_wait(&ctl->edge, edges & 1u, abort, p.status);
+          ++edges;
+          const int r0 = max(0, w.seen_first - i * kTile);
+          for (int c = r0 * 32 + tid; c < kTile * 32; c += 128) {
+            const int r = c >> 5, ch = c & 31;  // tile row; 16-byte chunk of our 256 columns
+            uint4* at = reinterpret_cast<uint4*>(smem + Layout::v + (r >> 6) * kVPageBytes + (ch >> 3) * kBlockBytes +
+                                                 (r & 63) * 128 +
+                                                 (((ch & 7) ^ (r & 7)) << 4));
+            if (i * kTile + r >= w.seen_last) {
+              *at = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+              uint4 v = *at;
+              uint32_t* e = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) e[k] = finite_bf16x2(e[k]);
+              *at = v;
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_pair(p_full);
+      }
+      // ---------------- the piece's rows: O is complete once its last P.V is
+      if (!ok) break;
+      warp_wait(&ctl->pv_done, (it - 1) & 1u, abort, p.status);
+      ctl->x[tid] = l;
+      ok = named_barrier_and(1, 128, !*abort);
+      if (!ok) break;
+      tc_fence_after();
+      const float l_all = ctl->x[row] + ctl->x[row + 64];
+      const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
+      const float lse2 = l_all == 0.f ? -INFINITY : m_ref + log2f(l_all);
+      const bool whole = w.whole();
+      const size_t slot = (size_t)pair * 2 + (w.first ? 0 : 1);
+      if (busy) {
+        const size_t grow = (size_t)w.t0 * p.H + mrow;
+        __nv_bfloat16* o_out = p.out + grow * kDv + half * 256;
+        float* o_ws = p.ws_o + (slot * p.ws_rows + mrow) * kDv + half * 256;
+#pragma unroll 1
+        for (int cc = 0; cc < 8; ++cc) {
+          uint32_t o[32];
+          tmem_ld_x32(lane_addr + kColO + (uint32_t)(cc * 32), o);
+          tmem_ld_wait();
+          if (active) {
+            if (whole) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t e[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  e[q] = pack_bf16(__uint_as_float(o[8 * k + 2 * q]) * inv, __uint_as_float(o[8 * k + 2 * q + 1]) * inv);
+                reinterpret_cast<uint4*>(o_out + cc * 32)[k] = make_uint4(e[0], e[1], e[2], e[3]);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                reinterpret_cast<float4*>(o_ws + cc * 32)[k] =
+                    make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
+                                __uint_as_float(o[4 * k + 2]) * inv, __uint_as_float(o[4 * k + 3]) * inv);
+            }
+          }
+        }
+        if (active && half == 0) {
+          if (!whole)
+            p.ws_lse[slot * p.ws_rows + mrow] = lse2;
+          else if (p.lse)
+            p.lse[grow] = lse2 * 0.69314718055994531f;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote_relaxed(o_free);
+    }
+  }
+  // A range that starts inside a group, the first to do so, names the group's pieces for the join.
+  if (rank == 0 && tid == 0) {
+    int4 j = make_int4(0, 0, 0, 0);
+    if (any) {
+      const Seq s = sequence(p, ctl->start_b, false);
+      const long long u = unit_count(s), pos = share * pair;
+      const int g = (int)((pos - ctl->start_at) / u);
+      const long long at = ctl->start_at + g * u;
+      const int i0 = g * p.T, n = min(p.T, s.n - i0);
+      const int seen_last = s.len - s.n + i0 + n;
+      const long long tiles = max(1, (seen_last + kTile - 1) / kTile);
+      if (pos > at && pos < at + tiles && pos - share <= at) {
+        const long long p0 = at / share, p1 = (at + tiles - 1) / share;
+        j = make_int4(s.s0 + i0, n * p.H, (int)(p0 * 2 + (p0 * share == at ? 0 : 1)), (int)(p1 - p0 + 1));
+      }
+    }
+    p.ws_join[pair] = j;
+  }
+  if (ctl->abort) {  // copies may still be in flight: give them time to land
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 2000000u) {
+    }
+  }
+  griddep_launch_dependents();
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 4) tmem_dealloc2(tmem, kTmemCols);
+}
+
+// Joins the pieces of the groups that a range border cuts: blockIdx.y is the pair whose range starts
+// inside the group, a block takes four rows, a thread four columns of each.
+__global__ void __launch_bounds__(128) mla_join_kernel(const Params p) {
+  griddep_wait();
+  const int4 j = p.ws_join[blockIdx.y];
+  const int parts = j.w;
+  if (parts == 0) return;
+#pragma unroll 1
+  for (int r = blockIdx.x * 4; r < min(j.y, (int)blockIdx.x * 4 + 4); ++r) {
+    float m = -INFINITY;
+    bool nan = false;
+    // piece 0 lies in slot j.z, the following ones each at the start of the next pair's range
+    auto slot = [&](int k) { return k == 0 ? (size_t)j.z : ((size_t)(j.z >> 1) + k) * 2; };
+    for (int k = 0; k < parts; ++k) {
+      const float x = p.ws_lse[slot(k) * p.ws_rows + r];
+      nan |= x != x;
+      m = fmaxf(m, x);
+    }
+    if (nan) m = __uint_as_float(0x7fffffffu);
+    const float m_use = m == -INFINITY ? 0.f : m;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int k = 0; k < parts; ++k) {
+      const float wgt = exp2f(p.ws_lse[slot(k) * p.ws_rows + r] - m_use);
+      const float4 x = reinterpret_cast<const float4*>(p.ws_o + (slot(k) * p.ws_rows + r) * kDv)[threadIdx.x];
+      sum += wgt;
+      o.x = fmaf(wgt, x.x, o.x);
+      o.y = fmaf(wgt, x.y, o.y);
+      o.z = fmaf(wgt, x.z, o.z);
+      o.w = fmaf(wgt, x.w, o.w);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const size_t grow = (size_t)j.x * p.H + r;
+    reinterpret_cast<uint2*>(p.out + grow * kDv)[threadIdx.x] =
+        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    if (threadIdx.x == 0 && p.lse)
+      p.lse[grow] = sum == 0.f ? -INFINITY : (m_use + log2f(sum)) * 0.69314718055994531f;
+  }
+}
+
+// Tokens of a group, and the rows of a piece in the workspace.
+static int group_tokens(const dsa_mla_decode_args& a) {
+  return std::max(1, std::min({128 / a.H, a.max_q_per_seq, a.n_q}));
+}
+
+static int pair_count() {
+  DeviceInfo dev;
+  std::string err;
+  return (device_info(dev, err) ? dev.sm_count : 152) / 2;
 }
 
 }  // namespace mlad
 
-size_t mla_decode_workspace_bytes(const dsa_mla_decode_args&) { return 0; }
+size_t mla_decode_workspace_bytes(const dsa_mla_decode_args& a) {
+  using namespace mlad;
+  const size_t pieces = (size_t)pair_count() * 2, rows = (size_t)group_tokens(a) * a.H;
+  size_t bytes = pieces * rows * kDv * 4;
+  bytes += (pieces * rows * 4 + 255) / 256 * 256;
+  return bytes + ((size_t)pair_count() * sizeof(int4) + 255) / 256 * 256;
+}
 
 dsa_status launch_mla_decode(const dsa_mla_decode_args& a, cudaStream_t stream, std::string& err) {
   using namespace mlad;
-  Params p = {a.B, a.n_q, a.H, a.max_pages, a.num_pages, a.softmax_scale * 1.4426950408889634f,
-              (const __nv_bfloat16*)a.q, (const uint8_t*)a.kv_pool, a.page_table, a.seq_lens, a.q_start,
-              (__nv_bfloat16*)a.out, a.lse, a.status};
-  const unsigned blocks = (unsigned)(((long long)a.n_q * a.H + kWarps - 1) / kWarps);
-  if (a.kv_dtype == DSA_FP8_E4M3)
-    mla_decode_kernel<true><<<blocks, kWarps * 32, 0, stream>>>(p);
-  else
-    mla_decode_kernel<false><<<blocks, kWarps * 32, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const bool kv8 = a.kv_dtype == DSA_FP8_E4M3;
+  Params p;
+  p.B = a.B;
+  p.n_q = a.n_q;
+  p.H = a.H;
+  p.T = group_tokens(a);
+  p.max_pages = a.max_pages;
+  p.num_pages = a.num_pages;
+  p.pairs = pair_count();
+  p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
+  p.kv = reinterpret_cast<const uint8_t*>(a.kv_pool);
+  p.page_table = a.page_table;
+  p.seq_lens = a.seq_lens;
+  p.q_start = a.q_start;
+  p.out = reinterpret_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse;
+  p.status = a.status;
+  p.ws_rows = p.T * p.H;
+  const size_t pieces = (size_t)p.pairs * 2;
+  uint8_t* ws = reinterpret_cast<uint8_t*>(a.workspace);
+  p.ws_o = reinterpret_cast<float*>(ws);
+  ws += pieces * p.ws_rows * kDv * 4;
+  p.ws_lse = reinterpret_cast<float*>(ws);
+  ws += (pieces * p.ws_rows * 4 + 255) / 256 * 256;
+  p.ws_join = reinterpret_cast<int4*>(ws);
+
+  CUtensorMap tm_q, tm_kv;
+  if (!encode_tmap_2d(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, kDqk, (uint64_t)a.n_q * a.H, kDqk * 2, 64, 64,
+                      CU_TENSOR_MAP_SWIZZLE_128B, err) ||
+      // (an FP8 cache is read with plain loads: its map is never used, any valid one will do)
+      !encode_tmap_2d(&tm_kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv_pool, kDqk, (uint64_t)(kv8 ? 1 : a.num_pages * 64), kDqk * 2,
+                      64, 64, CU_TENSOR_MAP_SWIZZLE_128B, err))
+    return DSA_ERR_CUDA;
+  const int smem = Layout::total + 1024;
+  auto kern = kv8 ? mla_decode_kernel<true> : mla_decode_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "mla_decode: set shared memory size", err);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * p.pairs));
+  cfg.blockDim = dim3(kv8 ? kThreads<true> : kThreads<false>);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, tm_q, tm_kv, p);
   if (e != cudaSuccess) return cuda_fail(e, "mla_decode: launch", err);
+  cfg.gridDim = dim3((unsigned)((p.ws_rows + 3) / 4), (unsigned)p.pairs);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  e = cudaLaunchKernelEx(&cfg, mla_join_kernel, p);
+  if (e != cudaSuccess) return cuda_fail(e, "mla_decode: launch of the join", err);
   return DSA_OK;
 }
 

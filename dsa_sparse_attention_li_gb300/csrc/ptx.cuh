@@ -182,6 +182,16 @@ DSA_DEV bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int*
   }
 }
 
+// As mbar_wait, kept out of line, for waits whose phase has usually completed: a test (17 cycles
+// against 51 of a try_wait) stands before the call.
+static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                                   int* status) {
+  return mbar_wait(bar, parity, abort, status);
+}
+DSA_DEV bool mbar_wait_fast(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  return mbar_test(bar, parity) || mbar_wait_slow(bar, parity, abort, status);
+}
+
 // Bounded wait that does not give up when the CTA has aborted: for draining asynchronous copies
 // that were issued and will complete (their bytes exist) before their destination is reused or
 // the CTA exits.
@@ -440,6 +450,67 @@ DSA_DEV void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
 }
 
 DSA_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ---------------------------------------------------------------- two-CTA tcgen05 (cta_group::2)
+//
+// The CTA pair of a cluster (ranks 2i, 2i + 1) as one MMA unit: the even CTA issues, each CTA
+// holds its half of A's rows and of B's rows (columns of D) at the same shared-memory offset, and
+// its half of D's rows in its own tensor memory.  With M = 128 a CTA has 64 rows of D: lane l < 64
+// holds columns 0 .. N/2 - 1 of row l, lane 64 + l columns N/2 .. N - 1 of the same row (checked
+// with integer operands for N = 32 .. 256, K-major and MN-major B).  Measured, issued back to back:
+// 49 cycles an instruction for N <= 128, 64 for N = 256.
+
+DSA_DEV void tmem_alloc2(uint32_t* result_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(result_smem)),
+               "r"(ncols)
+               : "memory");
+}
+DSA_DEV void tmem_relinquish2() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+DSA_DEV void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+// These two are executed by a whole converged warp and act in the lane whose `issuer` is not 0 (one,
+// always the same): with no divergent branch around them their operands stay in uniform registers,
+// which the instruction reads (behind an `if (lane == 0)` each MMA took about 90 cycles to issue).
+DSA_DEV void mma2_f16_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                         uint32_t accumulate, uint32_t issuer) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(issuer)
+      : "memory");
+}
+// Arrive once on `bar` of both CTAs of the pair (same offset) when every MMA issued so far by this
+// thread has completed.
+DSA_DEV void mma2_commit_both(uint64_t* bar, uint32_t issuer) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
+      " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3), "r"(issuer)
+      : "memory");
+}
+// 2-D tiled load into this CTA's shared memory that completes bytes on an mbarrier of either CTA of
+// the pair (shared::cluster address).
+DSA_DEV void tma_load_2d_pair(void* dst, const CUtensorMap* m, uint32_t bar_cluster, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(x), "r"(y)
+      : "memory");
+}
+// Arrive on an mbarrier of either CTA of the pair for data that the tensor cores read from this
+// CTA's own shared memory (or tensor memory): this thread's fences toward the async proxy have
+// ordered it already, so the arrival releases at CTA scope only.  A release at cluster scope waits
+// for every earlier access of the thread to be performed cluster-wide (measured: 2,000 cycles).
+DSA_DEV void mbar_arrive_pair(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
+               : "memory");
+}
 
 // ---------------------------------------------------------------- cluster
 
