@@ -86,6 +86,7 @@ struct Ctl {
   uint64_t v_full[kVPages], v_empty[kVPages];
   uint64_t s_full[2], s_free[2];
   uint64_t p_full, pv_done, o_free, edge;
+  uint64_t written[kKGroups + kVPages];   // FP8: a part is in shared memory (four warps)
   uint32_t tmem_base;
   int abort;
   int start_b;
@@ -129,21 +130,60 @@ DSA_DEV uint32_t finite_bf16x2(uint32_t e) {
   return e;
 }
 
+// Two fp32 products with one factor (a packed multiplication: one instruction for both).
+DSA_DEV float2 mul2(float2 a, float s) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mul.rn.f32x2 z, x, y;\n"
+      " mov.b64 {%0, %1}, z;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(s));
+  return d;
+}
+
 // 16 e4m3 codes times their scale as bf16 (fp32 product, both roundings to nearest even): the operand
 // that an element of an FP8 latent row stands for.
-DSA_DEV void dequant16(uint4 c, float s, uint4& lo, uint4& hi) {
+DSA_DEV void dequant16(const uint4& c, float s, uint4& lo, uint4& hi) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   uint32_t o[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t two = i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu;
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    o[i] = pack_bf16(f.x * s, f.y * s);
+    const float2 f = mul2(__half22float2(*reinterpret_cast<const __half2*>(&h)), s);
+    o[i] = pack_bf16(f.x, f.y);
   }
   lo = make_uint4(o[0], o[1], o[2], o[3]);
   hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
+
+// A lane's N chunks of 16 codes of one FP8 row in one part of a tile, and the row's two scales there;
+// chunks from `split` on have the second.
+template <int N>
+struct RowPart {
+  uint4 code[N];
+  float s0, s1;
+
+  DSA_DEV void fetch(const uint8_t* row, int first, int q4) {
+#pragma unroll
+    for (int u = 0; u < N; ++u) code[u] = *reinterpret_cast<const uint4*>(row + (first + q4 + 4 * u) * 16);
+    const float* s = reinterpret_cast<const float*>(row + kDqk) + (first >> 3);
+    s0 = s[0];
+    s1 = s[1];
+  }
+  // Into the row's line of N 64-column blocks: chunk q4 + 4 u is pieces 2 q4 and 2 q4 + 1 of block u.
+  template <class Clean>
+  DSA_DEV void store(uint8_t* line, uint32_t piece0, uint32_t piece1, int split, Clean clean) const {
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      uint4 lo, hi;
+      dequant16(code[u], u >= split ? s1 : s0, lo, hi);
+      clean(lo);
+      clean(hi);
+      *reinterpret_cast<uint4*>(line + u * kBlockBytes + piece0) = lo;
+      *reinterpret_cast<uint4*>(line + u * kBlockBytes + piece1) = hi;
+    }
+  }
+};
 
 // Bounded wait of a whole warp, which is converged again after it.
 DSA_DEV void warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
@@ -241,8 +281,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
   const int pair = blockIdx.x >> 1;
   volatile int* abort = &ctl->abort;
   constexpr int kThr = kThreads<KV8>;
-  constexpr uint32_t kFills = KV8 ? 8 : 1;   // arrivals that fill a K group or V page: the
-                                             // converting warps of both CTAs, or one expect_tx
+  constexpr uint32_t kFills = KV8 ? 2 : 1;   // arrivals that fill a K group or V page: one a CTA, or
+                                             // one expect_tx
   if (tid == 0) {
     mbar_init(&ctl->q_full, 1);
     mbar_init(&ctl->q_empty, 1);
@@ -262,6 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
     mbar_init(&ctl->pv_done, 1);
     mbar_init(&ctl->o_free, 8);
     mbar_init(&ctl->edge, 1);
+    for (int i = 0; i < kKGroups + kVPages; ++i) mbar_init(&ctl->written[i], 4);
     ctl->abort = 0;
     ctl->bad_pages = 0;
     fence_barrier_init();
@@ -447,89 +488,116 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
       }
     }
   } else if (KV8 && warp >= 8) {
-    // ---------------- FP8 cache: warps 8-11 convert this CTA's page into K (all 576 columns), warps
-    // 12-15 both pages' value columns of this CTA into V.  A warp has 16 rows of a page; four lanes
-    // share a row, a lane takes every fourth 16-code chunk of it (two passes of eight rows), so the
-    // 16-byte stores into the 128-byte-swizzled blocks meet no bank conflict.  The codes of the next
-    // part are loaded before the wait for its slot.
-    const bool is_k = warp < 12;
-    const int r0 = (warp & 3) * 16 + (lane >> 2), q4 = lane & 3;
-    constexpr int kParts = 3;                   // K groups; V has two parts, one a page
-    const uint32_t full = is_k ? map_cluster(&ctl->k_full[0], 0) : map_cluster(&ctl->v_full[0], 0);
-    uint64_t* empty = is_k ? &ctl->k_empty[0] : &ctl->v_empty[0];
-    const int parts = is_k ? kParts : kVPages;
-    const int chunks = is_k ? 3 : 4;            // a lane's chunks of a row in a part
+    // ---------------- FP8 cache: warps 8-11 convert this CTA's page into K (all 576 columns, three
+    // parts a tile), warps 12-15 both pages' value columns of this CTA into V (two parts).  A warp has
+    // 16 rows of a page; four lanes share a row, a lane takes every fourth 16-code chunk of it (two
+    // passes of eight rows), so the 16-byte stores into the 128-byte-swizzled blocks meet no bank
+    // conflict.  A part's registers are loaded for the next tile as soon as they are stored.
+    const int r = (warp & 3) * 16 + (lane >> 2), q4 = lane & 3;
+    // Warps 6 and 7 pass the news on: they order the part toward the tensor core's (async) proxy
+    // and tell the issuing CTA.  That fence waits for the thread's outstanding loads too, which would
+    // cost these warps an L2 latency a part.
+    uint64_t* written = &ctl->written[warp < 12 ? 0 : kKGroups];
+    auto filled = [&](int part) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&written[part]);
+    };
+    const uint32_t piece0 = (uint32_t)(((q4 * 2) ^ (r & 7)) << 4), piece1 = (uint32_t)(((q4 * 2 + 1) ^ (r & 7)) << 4);
     uint32_t it = 0;
     for (; have; have = w.next(p, lane)) {
       const int* pt = p.page_table + (size_t)w.b * p.max_pages;
-      const int pages = (max(w.seen_last, 0) + 63) >> 6;
-      // row `pass` of a part: its codes and scales, and whether it exists
-      uint4 code[2][4];
-      float scale[2][2];
-      int page_id = -1, first_chunk = 0;
-      auto fetch = [&](int i, int part) {
-        const int page = 2 * i + (is_k ? (int)rank : part);
-        first_chunk = is_k ? part * 12 : (int)rank * 16;
-        if (!is_k || part == 0) {
-          page_id = page < pages ? pt[page] : -1;
-          if (page_id >= p.num_pages) page_id = -1;
+      const int pages = min((max(w.seen_last, 0) + 63) >> 6, 2 * w.tile1);
+      // page ids, 32 at a time (a load whose value is wanted at once would stall a tile); -1: none
+      // (never read: page 0 stands in for it)
+      int ids = -1, base = -0x7fffffff;
+      auto id = [&](int page) {
+        if (page >= base + 32) {
+          base = page & ~31;
+          ids = base + lane < pages ? pt[base + lane] : -1;
+          if (ids >= p.num_pages) ids = -1;
         }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint8_t* row = p.kv + ((size_t)max(page_id, 0) * 64 + r0 + 8 * x) * kKv8Row;
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (u < chunks) code[x][u] = *reinterpret_cast<const uint4*>(row + (first_chunk + q4 + 4 * u) * 16);
-          // a part spans two scales
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            scale[x][u] = *reinterpret_cast<const float*>(row + kDqk + min((first_chunk >> 3) + u, 4) * 4);
-        }
+        return __shfl_sync(0xffffffffu, ids, page & 31);
       };
-      fetch(w.tile0, 0);
-      for (int i = w.tile0; i < w.tile1; ++i, ++it) {
-        if (warp == 8) {  // this CTA's page of a later tile into L2
-          const int page = 2 * (i + kPrefetch) + (int)rank;
-          const int pg = i + kPrefetch < w.tile1 && page < pages ? pt[page] : -1;
-          if (pg >= 0 && pg < p.num_pages && lane == 0)
-            prefetch_l2_bulk(p.kv + (size_t)pg * 64 * kKv8Row, 64 * kKv8Row);
-        }
-#pragma unroll 1
-        for (int part = 0; part < parts; ++part) {
-          if (it > 0) warp_wait(&empty[part], (it - 1) & 1u, abort, p.status);
-          const bool edge = !is_k && (i + 1) * kTile > w.seen_first;
-          uint8_t* dst = smem + (is_k ? Layout::k + part * kKGroupBytes : Layout::v + part * kVPageBytes);
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int r = r0 + 8 * x;
-            const int pos = i * kTile + part * 64 + r;   // (of V)
-            const bool none = !is_k && (page_id < 0 || (edge && pos >= w.seen_last));
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              if (u < chunks) {
-                const int ch = q4 + 4 * u;               // chunk of the part: 16 columns
-                const int si = ((first_chunk + ch) >> 3) - (first_chunk >> 3);
-                uint4 lo, hi;
-                dequant16(code[x][u], si == 0 ? scale[x][0] : scale[x][1], lo, hi);
-                if (none) {
-                  lo = hi = make_uint4(0u, 0u, 0u, 0u);
-                } else if (edge && pos >= w.seen_first) {
-                  lo = make_uint4(finite_bf16x2(lo.x), finite_bf16x2(lo.y), finite_bf16x2(lo.z), finite_bf16x2(lo.w));
-                  hi = make_uint4(finite_bf16x2(hi.x), finite_bf16x2(hi.y), finite_bf16x2(hi.z), finite_bf16x2(hi.w));
-                }
-                uint8_t* at = dst + (ch >> 2) * kBlockBytes + r * 128;
-                *reinterpret_cast<uint4*>(at + ((((ch & 3) * 2) ^ (r & 7)) << 4)) = lo;
-                *reinterpret_cast<uint4*>(at + ((((ch & 3) * 2 + 1) ^ (r & 7)) << 4)) = hi;
-              }
+      auto row = [&](int pg) { return p.kv + ((size_t)max(pg, 0) * 64 + r) * kKv8Row; };
+      if (warp < 12) {
+        const int mine = (int)rank;
+        RowPart<3> a, b;
+        const uint8_t* at = row(id(2 * w.tile0 + mine));
+        a.fetch(at, 0, q4);
+        b.fetch(at + 8 * kKv8Row, 0, q4);
+        auto as_is = [](uint4&) {};
+        int far = -1;
+        for (int i = w.tile0; i < w.tile1; ++i, ++it) {
+          const uint8_t* next = row(id(2 * i + 2 + mine));
+          if (warp == 8) {  // a later tile's page into L2, its id loaded a tile ahead
+            if (far >= 0 && far < p.num_pages && lane == 0)
+              prefetch_l2_bulk(p.kv + (size_t)far * 64 * kKv8Row, 64 * kKv8Row);
+            const int page = 2 * (i + kPrefetch + 1) + mine;
+            far = page < pages ? pt[page] : -1;
           }
-          const bool last = part + 1 == parts;
-          if (!last || i + 1 < w.tile1) fetch(last ? i + 1 : i, last ? 0 : part + 1);
+#pragma unroll 1
+          for (int part = 0; part < kKGroups; ++part) {
+            if (it > 0) warp_wait(&ctl->k_empty[part], (it - 1) & 1u, abort, p.status);
+            uint8_t* line = smem + Layout::k + part * kKGroupBytes + r * 128;
+            const int split = part == 1 ? 1 : 2, first = part == 2 ? 0 : part * 12 + 12;
+            if (part == 2) at = next;
+            a.store(line, piece0, piece1, split, as_is);
+            a.fetch(at, first, q4);
+            b.store(line + 8 * 128, piece0, piece1, split, as_is);
+            b.fetch(at + 8 * kKv8Row, first, q4);
+            filled(part);
+          }
+          if (__any_sync(0xffffffffu, *abort)) break;
+        }
+      } else {
+        const int first = (int)rank * 16;
+        int pg = id(2 * w.tile0);
+        RowPart<4> a, b;
+        a.fetch(row(pg), first, q4);
+        b.fetch(row(pg) + 8 * kKv8Row, first, q4);
+        for (int i = w.tile0; i < w.tile1; ++i, ++it) {
+#pragma unroll 1
+          for (int part = 0; part < kVPages; ++part) {
+            const int next = id(2 * i + part + 1);
+            // rows that no token sees, or that are not there, become zeros; of those that only some
+            // see, what is not finite does (see the softmax warps)
+            const bool edge = (i + 1) * kTile > w.seen_first || pg < 0;
+            const int pos = i * kTile + part * 64 + r;
+            auto clean = [&](int x) {
+              return [=](uint4& v) {
+                if (!edge) return;
+                if (pg < 0 || pos + x >= w.seen_last)
+                  v = make_uint4(0u, 0u, 0u, 0u);
+                else if (pos + x >= w.seen_first)
+                  v = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w));
+              };
+            };
+            if (it > 0) warp_wait(&ctl->v_empty[part], (it - 1) & 1u, abort, p.status);
+            uint8_t* line = smem + Layout::v + part * kVPageBytes + r * 128;
+            a.store(line, piece0, piece1, 2, clean(0));
+            a.fetch(row(next), first, q4);
+            b.store(line + 8 * 128, piece0, piece1, 2, clean(8));
+            b.fetch(row(next) + 8 * kKv8Row, first, q4);
+            filled(part);
+            pg = next;
+          }
+          if (__any_sync(0xffffffffu, *abort)) break;
+        }
+      }
+      if (__any_sync(0xffffffffu, *abort)) break;
+    }
+  } else if (KV8 && (warp == 6 || warp == 7)) {
+    const int parts = warp == 6 ? kKGroups : kVPages;
+    uint64_t* written = &ctl->written[warp == 6 ? 0 : kKGroups];
+    const uint32_t full = warp == 6 ? map_cluster(&ctl->k_full[0], 0) : map_cluster(&ctl->v_full[0], 0);
+    uint32_t it = 0;
+    for (; have; have = w.next(p, lane)) {
+      for (int i = w.tile0; i < w.tile1; ++i, ++it)
+        for (int part = 0; part < parts; ++part) {
+          warp_wait(&written[part], it & 1u, abort, p.status);
           fence_proxy_async_smem();
-          __syncwarp();
           if (lane == 0) mbar_arrive_pair(full + part * 8);
         }
-        if (__any_sync(0xffffffffu, *abort)) break;
-      }
       if (__any_sync(0xffffffffu, *abort)) break;
     }
   } else if (warp == 4 && rank == 0) {
@@ -823,43 +891,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
 }
 
 // Joins the pieces of the groups that a range border cuts: blockIdx.y is the pair whose range starts
-// inside the group, a block takes four rows, a thread four columns of each.
-__global__ void __launch_bounds__(128) mla_join_kernel(const Params p) {
+// inside the group, a block takes one row, a thread four columns of every second piece, eight loads
+// in flight.  The pieces' order in the sums is fixed.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) mla_join_kernel(const Params p) {
+  __shared__ float wgt[512];
+  __shared__ float4 half[128];
+  __shared__ float red[2];
   griddep_wait();
   const int4 j = p.ws_join[blockIdx.y];
-  const int parts = j.w;
-  if (parts == 0) return;
-#pragma unroll 1
-  for (int r = blockIdx.x * 4; r < min(j.y, (int)blockIdx.x * 4 + 4); ++r) {
+  const int parts = j.w, r = blockIdx.x, tid = threadIdx.x;
+  if (r >= j.y || parts == 0) return;
+  // piece 0 lies in slot j.z, the following ones each at the start of the next pair's range
+  auto slot = [&](int k) { return k == 0 ? (size_t)j.z : ((size_t)(j.z >> 1) + k) * 2; };
+  if (tid < 32) {
     float m = -INFINITY;
     bool nan = false;
-    // piece 0 lies in slot j.z, the following ones each at the start of the next pair's range
-    auto slot = [&](int k) { return k == 0 ? (size_t)j.z : ((size_t)(j.z >> 1) + k) * 2; };
-    for (int k = 0; k < parts; ++k) {
+    for (int k = tid; k < parts; k += 32) {
       const float x = p.ws_lse[slot(k) * p.ws_rows + r];
+      wgt[k] = x;
       nan |= x != x;
       m = fmaxf(m, x);
     }
-    if (nan) m = __uint_as_float(0x7fffffffu);
-    const float m_use = m == -INFINITY ? 0.f : m;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (__any_sync(0xffffffffu, nan)) m = __uint_as_float(0x7fffffffu);
+    if (m == -INFINITY) m = 0.f;
     float sum = 0.f;
-    for (int k = 0; k < parts; ++k) {
-      const float wgt = exp2f(p.ws_lse[slot(k) * p.ws_rows + r] - m_use);
-      const float4 x = reinterpret_cast<const float4*>(p.ws_o + (slot(k) * p.ws_rows + r) * kDv)[threadIdx.x];
-      sum += wgt;
-      o.x = fmaf(wgt, x.x, o.x);
-      o.y = fmaf(wgt, x.y, o.y);
-      o.z = fmaf(wgt, x.z, o.z);
-      o.w = fmaf(wgt, x.w, o.w);
+    for (int k = tid; k < parts; k += 32) {
+      const float e = exp2f(wgt[k] - m);
+      wgt[k] = e;
+      sum += e;
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const size_t grow = (size_t)j.x * p.H + r;
-    reinterpret_cast<uint2*>(p.out + grow * kDv)[threadIdx.x] =
-        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    if (threadIdx.x == 0 && p.lse)
-      p.lse[grow] = sum == 0.f ? -INFINITY : (m_use + log2f(sum)) * 0.69314718055994531f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (tid == 0) {
+      red[0] = m;
+      red[1] = sum;
+    }
   }
+  __syncthreads();
+  const int col = tid & 127, which = tid >> 7;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int k = which; k < parts; k += 2) {
+    const float e = wgt[k];
+    const float4 x = __ldcs(reinterpret_cast<const float4*>(p.ws_o + (slot(k) * p.ws_rows + r) * kDv) + col);
+    o.x = fmaf(e, x.x, o.x);
+    o.y = fmaf(e, x.y, o.y);
+    o.z = fmaf(e, x.z, o.z);
+    o.w = fmaf(e, x.w, o.w);
+  }
+  if (which == 1) half[col] = o;
+  __syncthreads();
+  if (which == 1) return;
+  const float4 x = half[col];
+  const float m = red[0], sum = red[1], inv = sum == 0.f ? 0.f : 1.f / sum;
+  const size_t grow = (size_t)j.x * p.H + r;
+  reinterpret_cast<uint2*>(p.out + grow * kDv)[col] =
+      make_uint2(pack_bf16((o.x + x.x) * inv, (o.y + x.y) * inv), pack_bf16((o.z + x.z) * inv, (o.w + x.w) * inv));
+  if (tid == 0 && p.lse) p.lse[grow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
 }
 
 // Tokens of a group, and the rows of a piece in the workspace.
@@ -870,7 +961,7 @@ static int group_tokens(const dsa_mla_decode_args& a) {
 static int pair_count() {
   DeviceInfo dev;
   std::string err;
-  return (device_info(dev, err) ? dev.sm_count : 152) / 2;
+  return std::min(256, (device_info(dev, err) ? dev.sm_count : 152) / 2);
 }
 
 }  // namespace mlad
@@ -934,8 +1025,8 @@ dsa_status launch_mla_decode(const dsa_mla_decode_args& a, cudaStream_t stream, 
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, tm_q, tm_kv, p);
   if (e != cudaSuccess) return cuda_fail(e, "mla_decode: launch", err);
-  cfg.gridDim = dim3((unsigned)((p.ws_rows + 3) / 4), (unsigned)p.pairs);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3((unsigned)p.ws_rows, (unsigned)p.pairs);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, mla_join_kernel, p);
   if (e != cudaSuccess) return cuda_fail(e, "mla_decode: launch of the join", err);
