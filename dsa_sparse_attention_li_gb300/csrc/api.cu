@@ -63,9 +63,9 @@ bool device_info(DeviceInfo& info, std::string& err) {
   return true;
 }
 
-bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner,
-                    uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner,
-                    uint32_t box_outer, CUtensorMapSwizzle swizzle, std::string& err) {
+static bool encode_tmap(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint32_t rank,
+                        const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                        CUtensorMapSwizzle swizzle, std::string& err) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -80,11 +80,8 @@ bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* bas
     err = "cuTensorMapEncodeTiled is not available from the driver";
     return false;
   }
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {row_stride_bytes};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, dtype, rank, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
@@ -92,6 +89,24 @@ bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* bas
     return false;
   }
   return true;
+}
+
+bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner,
+                    uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner,
+                    uint32_t box_outer, CUtensorMapSwizzle swizzle, std::string& err) {
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {row_stride_bytes};
+  cuuint32_t box[2] = {box_inner, box_outer};
+  return encode_tmap(map, dtype, base, 2, dims, strides, box, swizzle, err);
+}
+
+bool encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const uint64_t dims[3],
+                    const uint64_t strides[2], const uint32_t box[3], CUtensorMapSwizzle swizzle,
+                    std::string& err) {
+  cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
+  cuuint64_t s[2] = {strides[0], strides[1]};
+  cuuint32_t b[3] = {box[0], box[1], box[2]};
+  return encode_tmap(map, dtype, base, 3, d, s, b, swizzle, err);
 }
 
 }  // namespace dsa

@@ -51,6 +51,10 @@ dsa_status launch_mla_prefill(const dsa_mla_prefill_args& a, cudaStream_t stream
 bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
                     uint64_t inner, uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner,
                     uint32_t box_outer, CUtensorMapSwizzle swizzle, std::string& err);
+// 3-D, innermost dimension first; strides in bytes of the second and third.
+bool encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const uint64_t dims[3],
+                    const uint64_t strides[2], const uint32_t box[3], CUtensorMapSwizzle swizzle,
+                    std::string& err);
 
 #ifdef DSA_TEST_HOOKS
 // Test build only: which kernel's first CTA makes one of its waits wait on a barrier that nothing

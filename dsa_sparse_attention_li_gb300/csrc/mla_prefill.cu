@@ -1,21 +1,43 @@
-// mla_prefill.cu -- dense latent attention, expanded form.
+// mla_prefill.cu -- dense latent attention, expanded form: causal flash attention over packed
+// sequences with 192-column queries and keys (128 of the head's own, 64 of the rope key that all
+// heads share) and 128-column values.
 //
-// One warp per (token, head): online softmax over the keys the token sees.
+// A CTA takes 256 consecutive tokens of one sequence and head as two row tiles A and B of 128, and
+// walks the keys in tiles of 128.  The tensor pipe works on one row tile while the softmax of the
+// other runs:
+//   ... P_A(j).V(j) -> O_A,  Q_A.K(j+1)^T -> S_A,  P_B(j).V(j) -> O_B,  Q_B.K(j+1)^T -> S_B ...
+// TMEM: S_A, S_B, O_A, O_B, 128 columns each; P (bf16) takes the place of the first half of its S,
+// as the A operand of P.V.  A softmax thread owns a row: no exchange, the maximum and the sum stay
+// in registers; O is rescaled only when a row's maximum outgrows its reference by 2^8 (per warp).
+// P is handed over in two halves, so that P.V starts under the second half's exponentials.
+//
+// Shared memory: Q (96 KB) and a ring of eight 16-KB blocks: a key tile is three (64 columns each), a
+// value tile two (64 keys each), in the order K0 K1 V0 K2 V1 ...; any three of those in a row fit,
+// so load n waits for the release of load n - 3.
+//
+// Bound: the tensor pipe, 2 * (12 + 8) MMAs of 64 cycles a key tile and CTA = 2,560 cycles for 21
+// MFLOP; the keys and values come from L2, which the CTAs of a head share (heads in groups of 16,
+// the longest token blocks of a group first).
+#include <algorithm>
+
 #include "dsa_internal.h"
 #include "ptx.cuh"
 
 namespace dsa {
 namespace mlap {
 
-constexpr int kWarps = 8;
+constexpr int kThreads = 384;   // warps 0-3 softmax of A, 4-7 of B, 8 MMA, 9 loads
+constexpr int kRows = 128, kKeys = 128, kTokens = 2 * kRows;
+constexpr int kDqk = 192, kDv = 128;
+constexpr int kBlock = 16384;   // 128 keys x 64 columns, or 64 keys x 128 columns
+constexpr int kBlocks = 8;
+constexpr int kHeadGroup = 16;
+constexpr float kRescaleLog2 = 8.0f;
+constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;  // A, then B 128 columns on
 
 struct Params {
-  int B, n_q, n_kv, H, max_q;
+  int B, n_q, n_kv, H, max_q, blocks;
   float scale_log2;
-  long long rope_stride;
-  const __nv_bfloat16* q;
-  const __nv_bfloat16* kv;
-  const __nv_bfloat16* rope;
   const int* q_start;
   const int* kv_start;
   __nv_bfloat16* out;
@@ -23,64 +45,403 @@ struct Params {
   int* status;
 };
 
-__global__ void __launch_bounds__(kWarps * 32) mla_prefill_kernel(const Params p) {
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < p.B; i += kWarps * 32)
-      if (p.q_start[i] < 0 || p.q_start[i + 1] < p.q_start[i] || p.q_start[i + 1] > p.n_q)
-        report(p.status, kStatusDeviceCheck);
-  const int t = (int)(w / p.H), h = (int)(w % p.H);
-  if (t >= p.n_q) return;
-  int lo = 0, hi = p.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.q_start[mid] <= t) lo = mid; else hi = mid - 1;
+struct Layout {
+  static constexpr int q = 0;                       // [A, B][3 blocks of 64 columns][128 rows]
+  static constexpr int ring = q + 6 * kBlock;
+  static constexpr int ctl = ring + kBlocks * kBlock;
+  static constexpr int total = ctl + 2048;
+};
+
+struct Ctl {
+  uint64_t q_full, full[3], empty[3];
+  uint64_t s_full[2], p_full[2][2], pv_done[2];
+  uint32_t tmem_base;
+  int abort;
+  int any_bad[2];            // j + 1 if edge tile j has value rows that are not finite
+  uint8_t bad[2][kKeys];     // those rows (by j & 1: the row tiles may be a key tile apart)
+};
+static_assert(sizeof(Ctl) <= 2048, "control block");
+
+DSA_DEV float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+DSA_DEV uint32_t pack_bf16(float a, float b) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+DSA_DEV uint64_t desc_at(uint64_t d, int bytes) {
+  uint32_t lo = (uint32_t)d, hi = (uint32_t)(d >> 32);
+  lo += (uint32_t)(bytes >> 4);
+  return ((uint64_t)hi << 32) | lo;
+}
+DSA_DEV void warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  mbar_wait_fast(bar, parity, abort, status);
+  __syncwarp();
+}
+
+// First ring block of load n (K0 K1 V0 K2 V1 K3 ...): the first two are three blocks each, then two
+// and three in turn.
+DSA_DEV int k_load(int j) { return j < 2 ? j : 2 * j - 1; }
+DSA_DEV int v_load(int j) { return 2 * j + 2; }
+DSA_DEV int k_block(int j) { return j < 2 ? 3 * j : 5 * j - 2; }
+DSA_DEV int v_block(int j) { return 5 * j + 6; }
+
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_r,
+                       const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + Layout::ctl);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  volatile int* abort = &ctl->abort;
+
+  // (sequence, head group, token block from the last, head of the group)
+  int idx = blockIdx.x;
+  const int per_seq = p.blocks * p.H;
+  const int b = idx / per_seq;
+  idx -= b * per_seq;
+  const int group = idx / (p.blocks * kHeadGroup);
+  const int heads = min(kHeadGroup, p.H - group * kHeadGroup);
+  idx -= group * p.blocks * kHeadGroup;
+  const int h = group * kHeadGroup + idx % heads;
+  const int blk = p.blocks - 1 - idx / heads;
+
+  griddep_wait();
+  const int s0 = p.q_start[b], s1 = p.q_start[b + 1], k0 = p.kv_start[b], k1 = p.kv_start[b + 1];
+  const bool fine = s0 >= 0 && s1 >= s0 && s1 <= p.n_q && k0 >= 0 && k1 >= k0 && k1 <= p.n_kv;
+  if (tid == 0 && blk == 0 && h == 0 && (!fine || s1 - s0 > p.max_q)) report(p.status, kStatusDeviceCheck);
+  const int t0 = blk * kTokens;           // of the sequence
+  if (!fine || t0 >= s1 - s0) return;
+  const int n_tok = s1 - s0, n_key = k1 - k0;
+  const int seen0 = n_key - n_tok + t0 + 1;   // keys that the block's first token sees (may be < 1)
+  const int rows_a = min(kRows, n_tok - t0), rows_b = max(0, min(kRows, n_tok - t0 - kRows));
+  const int na = max(1, (seen0 + rows_a - 1 + kKeys - 1) / kKeys);
+  const int nb = rows_b > 0 ? max(1, (seen0 + kRows + rows_b - 1 + kKeys - 1) / kKeys) : 0;
+  const int tiles = max(na, nb);
+
+  if (tid == 0) {
+    mbar_init(&ctl->q_full, 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->s_full[i], 1);
+      mbar_init(&ctl->p_full[i][0], 4);
+      mbar_init(&ctl->p_full[i][1], 4);
+      mbar_init(&ctl->pv_done[i], 1);
+    }
+    ctl->abort = 0;
+    ctl->any_bad[0] = ctl->any_bad[1] = 0;
+    fence_barrier_init();
   }
-  const int b = lo, s0 = p.q_start[b], s1 = p.q_start[b + 1];
-  if (s0 < 0 || s1 > p.n_q || t < s0 || t >= s1) return;
-  const int k0 = p.kv_start[b], k1 = p.kv_start[b + 1];
-  if (k0 < 0 || k1 < k0 || k1 > p.n_kv || t - s0 >= p.max_q) {
-    if (lane == 0) report(p.status, kStatusDeviceCheck);
-    return;
+  if (warp == 8) {
+    tmem_alloc(&ctl->tmem_base, kTmemCols);
+    tmem_relinquish();
   }
-  const int seen = k1 - k0 - (s1 - s0) + (t - s0) + 1;
-  float q[6], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
+
+  if (warp == 9) {
+    // ---------------- loads
+    if (lane == 0) {
+      const int parts = nb > 0 ? 2 : 1;
+      mbar_arrive_expect_tx(&ctl->q_full, parts * 3 * kBlock);
+      for (int c = 0; c < parts * 3; ++c)
+        tma_load_3d(smem + Layout::q + c * kBlock, &tm_q, &ctl->q_full, (c % 3) * 64, h, s0 + t0 + (c / 3) * kRows);
+      bool ok = true;
+      auto slot = [&](int block) { return smem + Layout::ring + (block & (kBlocks - 1)) * kBlock; };
+      auto arm = [&](int n, int bytes) {
+        ok = ok && (n < 3 || mbar_wait_fast(&ctl->empty[n % 3], (uint32_t)(n / 3 - 1) & 1u, abort, p.status));
+        if (ok) mbar_arrive_expect_tx(&ctl->full[n % 3], bytes);
+        return ok;
+      };
+      auto load_k = [&](int j) {
+        const int n = k_load(j), at = k_block(j), key = k0 + j * kKeys;
+        if (!arm(n, 3 * kBlock)) return;
+        tma_load_3d(slot(at), &tm_k, &ctl->full[n % 3], 0, h, key);
+        tma_load_3d(slot(at + 1), &tm_k, &ctl->full[n % 3], 64, h, key);
+        tma_load_2d(slot(at + 2), &tm_r, &ctl->full[n % 3], 0, key);
+      };
+      auto load_v = [&](int j) {
+        const int n = v_load(j), at = v_block(j), key = k0 + j * kKeys;
+        if (!arm(n, 2 * kBlock)) return;
+        for (int u = 0; u < 4; ++u)
+          tma_load_3d(slot(at + (u >> 1)) + (u & 1) * (kBlock / 2), &tm_v, &ctl->full[n % 3], 128 + (u & 1) * 64, h,
+                      key + (u >> 1) * 64);
+      };
+      load_k(0);
+      // (load numbers count a second key tile even when there is none)
+      if (tiles > 1) load_k(1);
+      for (int j = 0; j < tiles && ok; ++j) {
+        load_v(j);
+        if (j + 2 < tiles) load_k(j + 2);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // ---------------- MMA issue: the whole warp walks, one lane issues
+    constexpr uint32_t idesc_qk = idesc_bf16(kRows, kKeys);
+    constexpr uint32_t idesc_pv = idesc_bf16(kRows, kDv, /*b_mn_major=*/true);
+    const uint64_t qd = sdesc_sw128(smem_u32(smem + Layout::q), 16, 1024);
+    const uint64_t kd = sdesc_sw128(smem_u32(smem + Layout::ring), 16, 1024);
+    const uint64_t vd = sdesc_sw128(smem_u32(smem + Layout::ring), kBlock / 2, 1024);
+    const uint32_t me = elect_one();
+    auto wait_load = [&](int n) {
+      warp_wait(&ctl->full[n % 3], (uint32_t)(n / 3) & 1u, abort, p.status);
+      tc_fence_after();
+    };
+    auto qk = [&](int x, int j) {
+      const uint64_t a = desc_at(qd, x * 3 * kBlock);
 #pragma unroll
-  for (int i = 0; i < 6; ++i) q[i] = __bfloat162float(p.q[w * 192 + i * 32 + lane]);
-  for (int j = k0; j < k0 + seen; ++j) {
-    const __nv_bfloat16* row = p.kv + ((long long)j * p.H + h) * 256;
-    float z = 0.f;
+      for (int c = 0; c < 3; ++c) {
+        const uint64_t k = desc_at(kd, ((k_block(j) + c) & (kBlocks - 1)) * kBlock);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) z += q[i] * __bfloat162float(row[i * 32 + lane]);
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f16_ss_by(tmem + kColS + x * 128, desc_at(a, c * kBlock + kk * 32), desc_at(k, kk * 32), idesc_qk,
+                        (c > 0 || kk > 0) ? 1u : 0u, me);
+      }
+      mma_commit_by(&ctl->s_full[x], me);
+    };
+    auto pv = [&](int x, int j) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) z += q[4 + i] * __bfloat162float(p.rope[j * p.rope_stride + i * 32 + lane]);
+      for (int c = 0; c < 2; ++c) {
+        warp_wait(&ctl->p_full[x][c], (uint32_t)j & 1u, abort, p.status);
+        tc_fence_after();
+        const uint64_t v = desc_at(vd, ((v_block(j) + c) & (kBlocks - 1)) * kBlock);
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-    z *= p.scale_log2;
-    const float m2 = fmaxf(m, z);
-    const float a = m == m2 ? 1.f : exp2f(m - m2), e = exp2f(z - m2);
-    m = m2;
-    l = l * a + e;
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f16_ts_by(tmem + kColO + x * 128, tmem + kColS + x * 128 + c * 32 + kk * 8, desc_at(v, kk * 2048),
+                        idesc_pv, (c > 0 || kk > 0) ? 1u : j > 0 ? 1u : 0u, me);
+      }
+      mma_commit_by(&ctl->pv_done[x], me);
+    };
+    warp_wait(&ctl->q_full, 0, abort, p.status);
+    wait_load(k_load(0));
+    qk(0, 0);
+    if (nb > 0) qk(1, 0);
+    mma_commit_by(&ctl->empty[0], me);
+#pragma unroll 1
+    for (int j = 0; j < tiles; ++j) {
+      if (__any_sync(0xffffffffu, *abort)) break;
+      const bool more = j + 1 < tiles;
+      wait_load(v_load(j));
+      if (j < na) pv(0, j);
+      if (more) wait_load(k_load(j + 1));
+      if (j + 1 < na) qk(0, j + 1);
+      if (j < nb) pv(1, j);
+      mma_commit_by(&ctl->empty[v_load(j) % 3], me);
+      if (j + 1 < nb) qk(1, j + 1);
+      if (more) mma_commit_by(&ctl->empty[k_load(j + 1) % 3], me);
+    }
+  } else if (warp < 8) {
+    // ---------------- softmax of row tile x: a thread is a row
+    const int x = warp >> 2;
+    const int row = tid & 127;
+    const int n = x == 0 ? na : nb;
+    const int rows = x == 0 ? rows_a : rows_b;
+    // rows past the block's tokens count as seeing everything: no masking, nothing of them is kept
+    const int seen = row < rows ? seen0 + x * kRows + row : 0x7fffffff;
+    const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_at = lane_addr + kColS + x * 128, o_at = lane_addr + kColO + x * 128;
+    float m_ref = -INFINITY, l = 0.f;
+    for (int j = 0; j < n; ++j) {
+      // A tile that some token of the block does not see to its end.  What it does not see must not
+      // reach it, and a weight of 0 times NaN would: value rows past the sequence become zeros, and in
+      // the others what is not finite, whose tokens then get their NaN through the score.
+      const bool edge = (j + 1) * kKeys > seen0;
+      bool bad_tile = false;
+      if (edge) {
+        const bool both = j < na && j < nb;
+        const int nl = v_load(j);
+        warp_wait(&ctl->full[nl % 3], (uint32_t)(nl / 3) & 1u, abort, p.status);
+        const int w = both ? warp : warp & 3, nw = both ? 8 : 4;
+        bool any = false;
+        for (int r2 = w * 2; r2 < kKeys; r2 += nw * 2) {  // two rows at a time, 16 lanes each
+          const int r = r2 + (lane >> 4), ch = lane & 15;
+          uint4* at = reinterpret_cast<uint4*>(smem + Layout::ring + ((v_block(j) + (r >> 6)) & (kBlocks - 1)) * kBlock +
+                                               (ch >> 3) * (kBlock / 2) + (r & 63) * 128 + (((ch & 7) ^ (r & 7)) << 4));
+          const bool none = j * kKeys + r >= n_key;
+          uint4 v = *at;
+          uint32_t* e = reinterpret_cast<uint32_t*>(&v);
+          bool hit = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = o[i] * a + e * __bfloat162float(row[128 + i * 32 + lane]);
+          for (int k = 0; k < 4; ++k) {
+            if ((e[k] & 0x7f80u) == 0x7f80u || none) hit = true, e[k] &= 0xffff0000u;
+            if ((e[k] & 0x7f800000u) == 0x7f800000u || none) hit = true, e[k] &= 0xffffu;
+          }
+          if (hit) *at = v;
+          const uint32_t votes = __ballot_sync(0xffffffffu, hit && !none);
+          if (ch == 0) ctl->bad[j & 1][r] = (votes >> (lane & 16)) & 0xffffu ? 1 : 0;
+          any |= votes != 0u;
+        }
+        if (any && lane == 0) ctl->any_bad[j & 1] = j + 1;
+        fence_proxy_async_smem();
+        if (both)
+          named_barrier(3, 256);
+        else
+          named_barrier(1 + x, 128);
+        bad_tile = *(volatile int*)&ctl->any_bad[j & 1] == j + 1;
+      }
+      warp_wait(&ctl->s_full[x], (uint32_t)j & 1u, abort, p.status);
+      tc_fence_after();
+      uint32_t s[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld_x32(s_at + c * 32, s + c * 32);
+      tmem_ld_wait();
+      const int keep = seen - j * kKeys;  // the first keys of the tile that are seen
+      if (!__all_sync(0xffffffffu, keep >= kKeys)) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c >= keep) s[c] = 0xff800000u;
+        if (bad_tile) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c < keep && ctl->bad[j & 1][c]) s[c] = 0x7fffffffu;
+        }
+      } else if (bad_tile) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (ctl->bad[j & 1][c]) s[c] = 0x7fffffffu;
+      }
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < 128; ++c) m4[c & 3] = fmaxf(m4[c & 3], __uint_as_float(s[c]));
+      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+      if (__any_sync(0xffffffffu, row < rows && mx > m_ref + kRescaleLog2)) {
+        const float m_new = fmaxf(m_ref, mx);
+        const float alpha = m_new == m_ref ? 1.f : fast_exp2(m_ref - m_new);
+        m_ref = m_new;
+        l *= alpha;
+        if (j > 0) {
+          warp_wait(&ctl->pv_done[x], (uint32_t)(j - 1) & 1u, abort, p.status);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            tmem_ld_x16(o_at + c * 16, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st_x16(o_at + c * 16, o);
+          }
+          tmem_st_wait();
+        }
+      }
+      const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+      float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int c = half * 64; c < half * 64 + 64; c += 2) {
+          const float a = fast_exp2(fmaf(__uint_as_float(s[c]), p.scale_log2, -m_use));
+          const float e = fast_exp2(fmaf(__uint_as_float(s[c + 1]), p.scale_log2, -m_use));
+          sum0 += a;
+          sum1 += e;
+          s[c >> 1] = pack_bf16(a, e);  // P.V takes bf16 weights: 2^-8 relative each, unbiased
+        }
+        tmem_st_x16(s_at + half * 32, s + half * 32);
+        tmem_st_x16(s_at + half * 32 + 16, s + half * 32 + 16);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->p_full[x][half]);
+      }
+      l += sum0 + sum1;  // (after an abort the waits return at once: no warp leaves a barrier short)
+    }
+    // ---------------- rows out
+    if (n > 0 && rows > 0) {
+      warp_wait(&ctl->pv_done[x], (uint32_t)(n - 1) & 1u, abort, p.status);
+      tc_fence_after();
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const size_t at = (size_t)(s0 + t0 + x * kRows + row) * p.H + h;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        tmem_ld_x32(o_at + c * 32, o);
+        tmem_ld_wait();
+        if (row < rows) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t e[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              e[q] = pack_bf16(__uint_as_float(o[8 * k + 2 * q]) * inv, __uint_as_float(o[8 * k + 2 * q + 1]) * inv);
+            reinterpret_cast<uint4*>(p.out + at * kDv + c * 32)[k] = make_uint4(e[0], e[1], e[2], e[3]);
+          }
+        }
+      }
+      if (row < rows && p.lse) p.lse[at] = l == 0.f ? -INFINITY : m_ref * 0.69314718055994531f + logf(l);
+    }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) p.out[w * 128 + i * 32 + lane] = __float2bfloat16_rn(o[i] * inv);
-  if (lane == 0 && p.lse) p.lse[w] = l == 0.f ? -INFINITY : m * 0.69314718055994531f + logf(l);
+  if (ctl->abort) {  // copies may still be in flight: give them time to land
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 2000000u) {
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) tmem_dealloc(tmem, kTmemCols);
 }
 
 }  // namespace mlap
 
 dsa_status launch_mla_prefill(const dsa_mla_prefill_args& a, cudaStream_t stream, std::string& err) {
   using namespace mlap;
-  Params p = {a.B, a.n_q, a.n_kv, a.H, a.max_q_per_seq, a.softmax_scale * 1.4426950408889634f, a.k_rope_stride,
-              (const __nv_bfloat16*)a.q, (const __nv_bfloat16*)a.kv, (const __nv_bfloat16*)a.k_rope, a.q_start,
-              a.kv_start, (__nv_bfloat16*)a.out, a.lse, a.status};
-  const long long blocks = ((long long)a.n_q * a.H + kWarps - 1) / kWarps;
-  mla_prefill_kernel<<<(unsigned)blocks, kWarps * 32, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  Params p;
+  p.B = a.B;
+  p.n_q = a.n_q;
+  p.n_kv = a.n_kv;
+  p.H = a.H;
+  p.max_q = std::min(a.max_q_per_seq, a.n_q);
+  p.blocks = (p.max_q + kTokens - 1) / kTokens;
+  p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
+  p.q_start = a.q_start;
+  p.kv_start = a.kv_start;
+  p.out = reinterpret_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse;
+  p.status = a.status;
+  const long long grid = (long long)a.B * p.blocks * a.H;
+  if (grid > 0x7fffffffLL) {
+    err = "mla_prefill: sequences * token blocks * heads must number below 2^31";
+    return DSA_ERR_UNSUPPORTED;
+  }
+  // without any keys nothing is seen: any valid memory stands in for them
+  const bool none = a.n_kv == 0;
+  const uint64_t H = (uint64_t)a.H, keys = none ? 1 : (uint64_t)a.n_kv;
+  const void* kv = none ? a.q : a.kv;
+  const void* rope = none ? a.q : a.k_rope;
+  const uint64_t qdims[3] = {kDqk, H, (uint64_t)a.n_q}, qstr[2] = {kDqk * 2, H * kDqk * 2};
+  const uint64_t kvdims[3] = {none ? 192u : 256u, none ? 1 : H, keys}, kvstr[2] = {512, H * 512};
+  const uint32_t box128[3] = {64, 1, 128}, box64[3] = {64, 1, 64};
+  CUtensorMap tm_q, tm_k, tm_v, tm_r;
+  const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  if (!encode_tmap_3d(&tm_q, bf, a.q, qdims, qstr, box128, sw, err) ||
+      !encode_tmap_3d(&tm_k, bf, kv, kvdims, kvstr, box128, sw, err) ||
+      !encode_tmap_3d(&tm_v, bf, kv, kvdims, kvstr, box64, sw, err) ||
+      !encode_tmap_2d(&tm_r, bf, rope, 64, keys, none ? 128 : (uint64_t)a.k_rope_stride * 2, 64, 128, sw, err))
+    return DSA_ERR_CUDA;
+  const int smem = Layout::total + 1024;
+  cudaError_t e = cudaFuncSetAttribute(mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "mla_prefill: set shared memory size", err);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, mla_prefill_kernel, tm_q, tm_k, tm_v, tm_r, p);
   if (e != cudaSuccess) return cuda_fail(e, "mla_prefill: launch", err);
   return DSA_OK;
 }

@@ -186,6 +186,7 @@ DSA_DEV bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int*
 // against 51 of a try_wait) stands before the call.
 static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort,
                                                    int* status) {
+  if (*abort) return false;
   return mbar_wait(bar, parity, abort, status);
 }
 DSA_DEV bool mbar_wait_fast(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
@@ -234,6 +235,14 @@ DSA_DEV void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, 
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+
+DSA_DEV void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
 
@@ -450,6 +459,33 @@ DSA_DEV void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
 }
 
 DSA_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The one-CTA forms for a whole converged warp: they act in the lane whose `issuer` is not 0 (one,
+// always the same), so that their operands stay in uniform registers (see the two-CTA forms).
+DSA_DEV void mma_f16_ss_by(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                           uint32_t accumulate, uint32_t issuer) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(issuer)
+      : "memory");
+}
+DSA_DEV void mma_f16_ts_by(uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                           uint32_t accumulate, uint32_t issuer) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(issuer)
+      : "memory");
+}
+DSA_DEV void mma_commit_by(uint64_t* bar, uint32_t issuer) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          smem_u32(bar)),
+      "r"(issuer)
+      : "memory");
+}
 
 // ---------------------------------------------------------------- two-CTA tcgen05 (cta_group::2)
 //
