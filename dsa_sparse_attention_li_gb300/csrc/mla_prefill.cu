@@ -12,8 +12,9 @@
 // P is handed over in two halves, so that P.V starts under the second half's exponentials.
 //
 // Shared memory: Q (96 KB) and a ring of eight 16-KB blocks: a key tile is three (64 columns each), a
-// value tile two (64 keys each), in the order K0 K1 V0 K2 V1 ...; any three of those in a row fit,
-// so load n waits for the release of load n - 3.
+// value tile two (64 keys each), in the order K0 V0 K1 V1 ...  V(j) then loads a whole step ahead of
+// its use, and K(j+1) from the release of V(j-1) on, which leaves it half a step (with K(j+1) before
+// V(j) the tensor pipe waited 1,500 of 4,400 cycles a step for V).
 //
 // Bound: the tensor pipe, 2 * (12 + 8) MMAs of 64 cycles a key tile and CTA = 2,560 cycles for 21
 // MFLOP; the keys and values come from L2, which the CTAs of a head share (heads in groups of 16,
@@ -53,7 +54,7 @@ struct Layout {
 };
 
 struct Ctl {
-  uint64_t q_full, full[3], empty[3];
+  uint64_t q_full, full[kBlocks], empty[kBlocks];
   uint64_t s_full[2], p_full[2][2], pv_done[2];
   uint32_t tmem_base;
   int abort;
@@ -81,12 +82,10 @@ DSA_DEV void warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int*
   __syncwarp();
 }
 
-// First ring block of load n (K0 K1 V0 K2 V1 K3 ...): the first two are three blocks each, then two
-// and three in turn.
-DSA_DEV int k_load(int j) { return j < 2 ? j : 2 * j - 1; }
-DSA_DEV int v_load(int j) { return 2 * j + 2; }
-DSA_DEV int k_block(int j) { return j < 2 ? 3 * j : 5 * j - 2; }
-DSA_DEV int v_block(int j) { return 5 * j + 6; }
+// Position in the line of blocks of a key tile's first block, and of a value tile's; block i lies in
+// slot i % 8, in its (i / 8)th use.
+DSA_DEV uint32_t k_block(int j) { return 5u * j; }
+DSA_DEV uint32_t v_block(int j) { return 5u * j + 3u; }
 
 __global__ void __launch_bounds__(kThreads, 1)
     mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -124,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     mbar_init(&ctl->q_full, 1);
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < kBlocks; ++i) {
       mbar_init(&ctl->full[i], 1);
       mbar_init(&ctl->empty[i], 1);
     }
@@ -154,33 +153,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive_expect_tx(&ctl->q_full, parts * 3 * kBlock);
       for (int c = 0; c < parts * 3; ++c)
         tma_load_3d(smem + Layout::q + c * kBlock, &tm_q, &ctl->q_full, (c % 3) * 64, h, s0 + t0 + (c / 3) * kRows);
-      bool ok = true;
-      auto slot = [&](int block) { return smem + Layout::ring + (block & (kBlocks - 1)) * kBlock; };
-      auto arm = [&](int n, int bytes) {
-        ok = ok && (n < 3 || mbar_wait_fast(&ctl->empty[n % 3], (uint32_t)(n / 3 - 1) & 1u, abort, p.status));
-        if (ok) mbar_arrive_expect_tx(&ctl->full[n % 3], bytes);
-        return ok;
+      // block i may take its slot once block i - 8 is used up
+      auto arm = [&](uint32_t i) {
+        const uint32_t c = i % kBlocks;
+        if (i >= kBlocks) mbar_wait_fast(&ctl->empty[c], (i / kBlocks - 1) & 1u, abort, p.status);
+        mbar_arrive_expect_tx(&ctl->full[c], kBlock);
+        return smem + Layout::ring + c * kBlock;
       };
-      auto load_k = [&](int j) {
-        const int n = k_load(j), at = k_block(j), key = k0 + j * kKeys;
-        if (!arm(n, 3 * kBlock)) return;
-        tma_load_3d(slot(at), &tm_k, &ctl->full[n % 3], 0, h, key);
-        tma_load_3d(slot(at + 1), &tm_k, &ctl->full[n % 3], 64, h, key);
-        tma_load_2d(slot(at + 2), &tm_r, &ctl->full[n % 3], 0, key);
-      };
-      auto load_v = [&](int j) {
-        const int n = v_load(j), at = v_block(j), key = k0 + j * kKeys;
-        if (!arm(n, 2 * kBlock)) return;
-        for (int u = 0; u < 4; ++u)
-          tma_load_3d(slot(at + (u >> 1)) + (u & 1) * (kBlock / 2), &tm_v, &ctl->full[n % 3], 128 + (u & 1) * 64, h,
-                      key + (u >> 1) * 64);
-      };
-      load_k(0);
-      // (load numbers count a second key tile even when there is none)
-      if (tiles > 1) load_k(1);
-      for (int j = 0; j < tiles && ok; ++j) {
-        load_v(j);
-        if (j + 2 < tiles) load_k(j + 2);
+      for (int j = 0; j < tiles && !*abort; ++j) {
+        const int key = k0 + j * kKeys;
+        for (int c = 0; c < 3; ++c) {
+          const uint32_t i = k_block(j) + c;
+          uint8_t* dst = arm(i);
+          if (c < 2)
+            tma_load_3d(dst, &tm_k, &ctl->full[i % kBlocks], c * 64, h, key);
+          else
+            tma_load_2d(dst, &tm_r, &ctl->full[i % kBlocks], 0, key);
+        }
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t i = v_block(j) + c;
+          uint8_t* dst = arm(i);
+          for (int u = 0; u < 2; ++u)
+            tma_load_3d(dst + u * (kBlock / 2), &tm_v, &ctl->full[i % kBlocks], 128 + u * 64, h, key + c * 64);
+        }
       }
     }
     __syncwarp();
@@ -192,52 +187,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t kd = sdesc_sw128(smem_u32(smem + Layout::ring), 16, 1024);
     const uint64_t vd = sdesc_sw128(smem_u32(smem + Layout::ring), kBlock / 2, 1024);
     const uint32_t me = elect_one();
-    auto wait_load = [&](int n) {
-      warp_wait(&ctl->full[n % 3], (uint32_t)(n / 3) & 1u, abort, p.status);
+    auto wait_block = [&](uint32_t i) {
+      warp_wait(&ctl->full[i % kBlocks], (i / kBlocks) & 1u, abort, p.status);
       tc_fence_after();
     };
-    auto qk = [&](int x, int j) {
+    // Q_x . K(j)^T; the first row tile to use a key tile waits for it, the last one releases it
+    auto qk = [&](int x, int j, bool wait, bool release) {
       const uint64_t a = desc_at(qd, x * 3 * kBlock);
 #pragma unroll
       for (int c = 0; c < 3; ++c) {
-        const uint64_t k = desc_at(kd, ((k_block(j) + c) & (kBlocks - 1)) * kBlock);
+        const uint32_t i = k_block(j) + c;
+        if (wait) wait_block(i);
+        const uint64_t k = desc_at(kd, (i % kBlocks) * kBlock);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           mma_f16_ss_by(tmem + kColS + x * 128, desc_at(a, c * kBlock + kk * 32), desc_at(k, kk * 32), idesc_qk,
                         (c > 0 || kk > 0) ? 1u : 0u, me);
+        if (release) mma_commit_by(&ctl->empty[i % kBlocks], me);
       }
       mma_commit_by(&ctl->s_full[x], me);
     };
-    auto pv = [&](int x, int j) {
+    auto pv = [&](int x, int j, bool wait, bool release) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
+        const uint32_t i = v_block(j) + c;
+        if (wait) wait_block(i);
         warp_wait(&ctl->p_full[x][c], (uint32_t)j & 1u, abort, p.status);
         tc_fence_after();
-        const uint64_t v = desc_at(vd, ((v_block(j) + c) & (kBlocks - 1)) * kBlock);
+        const uint64_t v = desc_at(vd, (i % kBlocks) * kBlock);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           mma_f16_ts_by(tmem + kColO + x * 128, tmem + kColS + x * 128 + c * 32 + kk * 8, desc_at(v, kk * 2048),
                         idesc_pv, (c > 0 || kk > 0) ? 1u : j > 0 ? 1u : 0u, me);
+        if (release) mma_commit_by(&ctl->empty[i % kBlocks], me);
       }
       mma_commit_by(&ctl->pv_done[x], me);
     };
     warp_wait(&ctl->q_full, 0, abort, p.status);
-    wait_load(k_load(0));
-    qk(0, 0);
-    if (nb > 0) qk(1, 0);
-    mma_commit_by(&ctl->empty[0], me);
+    qk(0, 0, true, nb == 0);
+    if (nb > 0) qk(1, 0, false, true);
 #pragma unroll 1
     for (int j = 0; j < tiles; ++j) {
       if (__any_sync(0xffffffffu, *abort)) break;
-      const bool more = j + 1 < tiles;
-      wait_load(v_load(j));
-      if (j < na) pv(0, j);
-      if (more) wait_load(k_load(j + 1));
-      if (j + 1 < na) qk(0, j + 1);
-      if (j < nb) pv(1, j);
-      mma_commit_by(&ctl->empty[v_load(j) % 3], me);
-      if (j + 1 < nb) qk(1, j + 1);
-      if (more) mma_commit_by(&ctl->empty[k_load(j + 1) % 3], me);
+      if (j < na) pv(0, j, true, j >= nb);
+      if (j + 1 < na) qk(0, j + 1, true, j + 1 >= nb);
+      if (j < nb) pv(1, j, j >= na, true);
+      if (j + 1 < nb) qk(1, j + 1, j + 1 >= na, true);
     }
   } else if (warp < 8) {
     // ---------------- softmax of row tile x: a thread is a row
@@ -258,13 +253,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool bad_tile = false;
       if (edge) {
         const bool both = j < na && j < nb;
-        const int nl = v_load(j);
-        warp_wait(&ctl->full[nl % 3], (uint32_t)(nl / 3) & 1u, abort, p.status);
+        for (uint32_t i = v_block(j); i < v_block(j) + 2; ++i)
+          warp_wait(&ctl->full[i % kBlocks], (i / kBlocks) & 1u, abort, p.status);
         const int w = both ? warp : warp & 3, nw = both ? 8 : 4;
         bool any = false;
         for (int r2 = w * 2; r2 < kKeys; r2 += nw * 2) {  // two rows at a time, 16 lanes each
           const int r = r2 + (lane >> 4), ch = lane & 15;
-          uint4* at = reinterpret_cast<uint4*>(smem + Layout::ring + ((v_block(j) + (r >> 6)) & (kBlocks - 1)) * kBlock +
+          uint4* at = reinterpret_cast<uint4*>(smem + Layout::ring + (v_block(j) + (r >> 6)) % kBlocks * kBlock +
                                                (ch >> 3) * (kBlock / 2) + (r & 63) * 128 + (((ch & 7) ^ (r & 7)) << 4));
           const bool none = j * kKeys + r >= n_key;
           uint4 v = *at;
