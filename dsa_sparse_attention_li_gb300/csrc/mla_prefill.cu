@@ -306,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 128; ++c) m4[c & 3] = fmaxf(m4[c & 3], __uint_as_float(s[c]));
+      for (int c = 0; c < 128; c += 2)
+        m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
       const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
       if (__any_sync(0xffffffffu, row < rows && mx > m_ref + kRescaleLog2)) {
         const float m_new = fmaxf(m_ref, mx);
@@ -329,16 +330,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-      float sum0 = 0.f, sum1 = 0.f;
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
 #pragma unroll
         for (int c = half * 64; c < half * 64 + 64; c += 2) {
-          const float a = fast_exp2(fmaf(__uint_as_float(s[c]), p.scale_log2, -m_use));
-          const float e = fast_exp2(fmaf(__uint_as_float(s[c + 1]), p.scale_log2, -m_use));
-          sum0 += a;
-          sum1 += e;
-          s[c >> 1] = pack_bf16(a, e);  // P.V takes bf16 weights: 2^-8 relative each, unbiased
+          float2 e = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), p.scale_log2, -m_use);
+          e.x = fast_exp2(e.x);
+          e.y = fast_exp2(e.y);
+          sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], e);
+          s[c >> 1] = pack_bf16(e.x, e.y);  // P.V takes bf16 weights: 2^-8 relative each, unbiased
         }
         tmem_st_x16(s_at + half * 32, s + half * 32);
         tmem_st_x16(s_at + half * 32 + 16, s + half * 32 + 16);
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->p_full[x][half]);
       }
-      l += sum0 + sum1;  // (after an abort the waits return at once: no warp leaves a barrier short)
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);  // (after an abort the waits return at once: no warp leaves a barrier short)
     }
     // ---------------- rows out
     if (n > 0 && rows > 0) {

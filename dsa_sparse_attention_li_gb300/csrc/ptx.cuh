@@ -616,6 +616,30 @@ DSA_DEV uint4 ld_cluster_v4(uint32_t addr) {
 
 // ---------------------------------------------------------------- misc
 
+// Largest of three (a NaN loses), one instruction.
+DSA_DEV float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// a * s + t on two values, and the sum of two pairs: one packed instruction each.
+DSA_DEV float2 fma2(float2 a, float s, float t) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mov.b64 z, {%5, %5};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(s), "f"(t));
+  return d;
+}
+DSA_DEV float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 x, x, y;\n"
+      " mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 // Order-preserving map of an fp32 score to uint32 (larger score -> larger key); -0.0 and +0.0
 // map to the same key.  Key 0 is reserved for "not a candidate" (no finite score maps there).
 DSA_DEV uint32_t score_key(float s) {
