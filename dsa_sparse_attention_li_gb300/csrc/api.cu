@@ -300,8 +300,8 @@ dsa_status dsa_mla_prefill(const dsa_mla_prefill_args* a, dsa_stream_t stream) {
   if (a->n_q == 0) return DSA_OK;
   if (!a->q || (a->n_kv > 0 && (!a->kv || !a->k_rope)) || !a->q_start || !a->kv_start || !a->out)
     return fail(DSA_ERR_INVALID_ARG, "mla_prefill: null device pointer");
-  if (!aligned16(a->q) || !aligned16(a->kv) || !aligned16(a->k_rope) || !aligned16(a->out))
-    return fail(DSA_ERR_INVALID_ARG, "mla_prefill: q, kv, k_rope, out must be 16-byte aligned");
+  if (!aligned16(a->q) || !aligned16(a->kv) || !aligned16(a->k_rope) || (reinterpret_cast<uintptr_t>(a->out) & 31u))
+    return fail(DSA_ERR_INVALID_ARG, "mla_prefill: q, kv, k_rope must be 16-byte aligned, out 32-byte aligned");
   std::string err;
   const dsa_status s = dsa::launch_mla_prefill(*a, reinterpret_cast<cudaStream_t>(stream), err);
   if (s != DSA_OK) g_last_error = err;

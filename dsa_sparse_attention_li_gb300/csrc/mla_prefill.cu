@@ -16,6 +16,10 @@
 // its use, and K(j+1) from the release of V(j-1) on, which leaves it half a step (with K(j+1) before
 // V(j) the tensor pipe waited 1,500 of 4,400 cycles a step for V).
 //
+// Items (token block, head) are the grid's blocks; a CTA asks for another block that has not started
+// (cluster launch control) while it works on one, so that the next item's loads and first products
+// run under the last softmax and the epilogue of the one before.
+//
 // Bound: the tensor pipe, 2 * (12 + 8) MMAs of 64 cycles a key tile and CTA = 2,560 cycles for 21
 // MFLOP; the keys and values come from L2, which the CTAs of a head share (heads in groups of 16,
 // the longest token blocks of a group first).
@@ -27,7 +31,7 @@
 namespace dsa {
 namespace mlap {
 
-constexpr int kThreads = 384;   // warps 0-3 softmax of A, 4-7 of B, 8 MMA, 9 loads
+constexpr int kThreads = 384;   // warps 0-3 softmax of A, 4-7 of B, 8 MMA, 9 loads, 10-11 edge tiles
 constexpr int kRows = 128, kKeys = 128, kTokens = 2 * kRows;
 constexpr int kDqk = 192, kDv = 128;
 constexpr int kBlock = 16384;   // 128 keys x 64 columns, or 64 keys x 128 columns
@@ -53,13 +57,27 @@ struct Layout {
   static constexpr int total = ctl + 2048;
 };
 
+// What the warps know of an item.
+struct Item {
+  int h, tok, key, n_key;   // head; first token and first key row; keys of the sequence
+  int seen0;                // keys that the block's first token sees (may be < 1)
+  int rows_a, rows_b, na, nb;   // tokens and key tiles of A and B
+  int tiles;                // max(na, nb); 0: no further item
+  int edge0;                // tiles from here on are edge tiles: some token does not see all of it
+};
+
 struct Ctl {
-  uint64_t q_full, full[kBlocks], empty[kBlocks];
+  uint64_t q_full, q_empty, full[kBlocks], empty[kBlocks];
   uint64_t s_full[2], p_full[2][2], pv_done[2];
+  uint64_t edge[2][2];       // values of an edge tile (by its count & 1), half, have landed
+  uint64_t item_full[2], item_empty[2], answer_full;
+  alignas(16) uint8_t answer[16];
+  Item item[2];
   uint32_t tmem_base;
   int abort;
-  int any_bad[2];            // j + 1 if edge tile j has value rows that are not finite
-  uint8_t bad[2][kKeys];     // those rows (by j & 1: the row tiles may be a key tile apart)
+  uint32_t any_bad[2][2];    // t + 1 if a half of edge tile t (of all the CTA's tiles) has value rows
+                             // that are not finite
+  alignas(4) uint8_t bad[2][kKeys];   // those rows (by t & 1)
 };
 static_assert(sizeof(Ctl) <= 2048, "control block");
 
@@ -72,6 +90,12 @@ DSA_DEV uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&v);
 }
+// Two bf16 with what is not finite set to zero.
+DSA_DEV uint32_t finite_bf16x2(uint32_t e) {
+  if ((e & 0x7f80u) == 0x7f80u) e &= 0xffff0000u;
+  if ((e & 0x7f800000u) == 0x7f800000u) e &= 0xffffu;
+  return e;
+}
 DSA_DEV uint64_t desc_at(uint64_t d, int bytes) {
   uint32_t lo = (uint32_t)d, hi = (uint32_t)(d >> 32);
   lo += (uint32_t)(bytes >> 4);
@@ -82,10 +106,70 @@ DSA_DEV void warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int*
   __syncwarp();
 }
 
-// Position in the line of blocks of a key tile's first block, and of a value tile's; block i lies in
-// slot i % 8, in its (i / 8)th use.
-DSA_DEV uint32_t k_block(int j) { return 5u * j; }
-DSA_DEV uint32_t v_block(int j) { return 5u * j + 3u; }
+// Position of a key tile's first block, and of a value tile's, in the line of blocks that the ring
+// carries (`at`: the item's first); block i lies in slot i % 8, in its (i / 8)th use.
+DSA_DEV uint32_t k_block(uint32_t at, int j) { return at + 5u * j; }
+DSA_DEV uint32_t v_block(uint32_t at, int j) { return at + 5u * j + 3u; }
+
+// The line of all sequences' token blocks, one sequence after the other, of which p.blocks is the
+// host's bound; the loading warp looks items up in it.  Lane i holds sequence b0 + i.
+struct Line {
+  int s0, s1, k0, k1, first, count;   // its ranges, and its blocks in the line
+
+  // Sequences b0 .. b0 + 31, which the line reaches at `before`; returns where they end.
+  DSA_DEV int chunk(const Params& p, int b0, int before, int lane, bool tell) {
+    const int b = b0 + lane;
+    s0 = s1 = k0 = k1 = 0;
+    if (b < p.B) {
+      s0 = p.q_start[b];
+      s1 = p.q_start[b + 1];
+      k0 = p.kv_start[b];
+      k1 = p.kv_start[b + 1];
+    }
+    const bool fine = s0 >= 0 && s1 >= s0 && s1 <= p.n_q && k0 >= 0 && k1 >= k0 && k1 <= p.n_kv;
+    if (tell && (!fine || s1 - s0 > p.max_q)) report(p.status, kStatusDeviceCheck);
+    count = fine ? (s1 - s0 + kTokens - 1) / kTokens : 0;
+    int upto = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    first = before + upto - count;
+    return before + __shfl_sync(0xffffffffu, upto, 31);
+  }
+  // Grid block i: by head group, then token blocks from the line's last to its first, then heads.
+  DSA_DEV bool find(const Params& p, int i, int lane, Item& w) {
+    const int group = i / (p.blocks * kHeadGroup);
+    const int heads = min(kHeadGroup, p.H - group * kHeadGroup);
+    i -= group * p.blocks * kHeadGroup;
+    w.h = group * kHeadGroup + i % heads;
+    const int want = p.blocks - 1 - i / heads;
+    uint32_t hit = __ballot_sync(0xffffffffu, want >= first && want < first + count);
+    if (hit == 0 && p.B > 32) {  // more sequences than lanes: look from the start
+      int at = 0;
+      for (int b0 = 0; b0 < p.B && hit == 0; b0 += 32) {
+        at = chunk(p, b0, at, lane, false);
+        hit = __ballot_sync(0xffffffffu, want >= first && want < first + count);
+      }
+    }
+    if (hit == 0) return false;  // the line is shorter than its bound
+    const int l = __ffs((int)hit) - 1;
+    const int t0 = (want - __shfl_sync(0xffffffffu, first, l)) * kTokens;
+    const int q0 = __shfl_sync(0xffffffffu, s0, l), n_tok = __shfl_sync(0xffffffffu, s1, l) - q0;
+    w.key = __shfl_sync(0xffffffffu, k0, l);
+    w.n_key = __shfl_sync(0xffffffffu, k1, l) - w.key;
+    w.tok = q0 + t0;
+    w.seen0 = w.n_key - n_tok + t0 + 1;
+    w.rows_a = min(kRows, n_tok - t0);
+    w.rows_b = max(0, min(kRows, n_tok - t0 - kRows));
+    w.na = max(1, (w.seen0 + w.rows_a - 1 + kKeys - 1) / kKeys);
+    w.nb = w.rows_b > 0 ? max(1, (w.seen0 + kRows + w.rows_b - 1 + kKeys - 1) / kKeys) : 0;
+    w.tiles = max(w.na, w.nb);
+    w.edge0 = min(max(w.seen0, 0) / kKeys, w.tiles);
+    return true;
+  }
+};
 
 __global__ void __launch_bounds__(kThreads, 1)
     mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -97,32 +181,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   volatile int* abort = &ctl->abort;
 
-  // (sequence, head group, token block from the last, head of the group)
-  int idx = blockIdx.x;
-  const int per_seq = p.blocks * p.H;
-  const int b = idx / per_seq;
-  idx -= b * per_seq;
-  const int group = idx / (p.blocks * kHeadGroup);
-  const int heads = min(kHeadGroup, p.H - group * kHeadGroup);
-  idx -= group * p.blocks * kHeadGroup;
-  const int h = group * kHeadGroup + idx % heads;
-  const int blk = p.blocks - 1 - idx / heads;
-
-  griddep_wait();
-  const int s0 = p.q_start[b], s1 = p.q_start[b + 1], k0 = p.kv_start[b], k1 = p.kv_start[b + 1];
-  const bool fine = s0 >= 0 && s1 >= s0 && s1 <= p.n_q && k0 >= 0 && k1 >= k0 && k1 <= p.n_kv;
-  if (tid == 0 && blk == 0 && h == 0 && (!fine || s1 - s0 > p.max_q)) report(p.status, kStatusDeviceCheck);
-  const int t0 = blk * kTokens;           // of the sequence
-  if (!fine || t0 >= s1 - s0) return;
-  const int n_tok = s1 - s0, n_key = k1 - k0;
-  const int seen0 = n_key - n_tok + t0 + 1;   // keys that the block's first token sees (may be < 1)
-  const int rows_a = min(kRows, n_tok - t0), rows_b = max(0, min(kRows, n_tok - t0 - kRows));
-  const int na = max(1, (seen0 + rows_a - 1 + kKeys - 1) / kKeys);
-  const int nb = rows_b > 0 ? max(1, (seen0 + kRows + rows_b - 1 + kKeys - 1) / kKeys) : 0;
-  const int tiles = max(na, nb);
-
   if (tid == 0) {
     mbar_init(&ctl->q_full, 1);
+    mbar_init(&ctl->q_empty, 1);
+    mbar_init(&ctl->answer_full, 1);
     for (int i = 0; i < kBlocks; ++i) {
       mbar_init(&ctl->full[i], 1);
       mbar_init(&ctl->empty[i], 1);
@@ -132,9 +194,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->p_full[i][0], 4);
       mbar_init(&ctl->p_full[i][1], 4);
       mbar_init(&ctl->pv_done[i], 1);
+      mbar_init(&ctl->item_full[i], 1);
+      mbar_init(&ctl->item_empty[i], 11);  // all warps but this one
+      mbar_init(&ctl->edge[i][0], 1);
+      mbar_init(&ctl->edge[i][1], 1);
     }
     ctl->abort = 0;
-    ctl->any_bad[0] = ctl->any_bad[1] = 0;
+    for (int i = 0; i < 4; ++i) ctl->any_bad[i >> 1][i & 1] = 0u;
     fence_barrier_init();
   }
   if (warp == 8) {
@@ -145,40 +211,141 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
+  griddep_wait();  // nothing above reads global memory
+  uint32_t at = 0;   // the item's first ring block; at / 5 is its first tile of the CTA's
 
   if (warp == 9) {
-    // ---------------- loads
-    if (lane == 0) {
-      const int parts = nb > 0 ? 2 : 1;
+    // ---------------- items and loads
+    uint32_t edges = 0;   // edge tiles so far
+    auto load = [&](const Item& w, uint32_t item) {
+      const int parts = w.nb > 0 ? 2 : 1;
+      if (item > 0) mbar_wait_fast(&ctl->q_empty, (item - 1) & 1u, abort, p.status);
       mbar_arrive_expect_tx(&ctl->q_full, parts * 3 * kBlock);
       for (int c = 0; c < parts * 3; ++c)
-        tma_load_3d(smem + Layout::q + c * kBlock, &tm_q, &ctl->q_full, (c % 3) * 64, h, s0 + t0 + (c / 3) * kRows);
+        tma_load_3d(smem + Layout::q + c * kBlock, &tm_q, &ctl->q_full, (c % 3) * 64, w.h, w.tok + (c / 3) * kRows);
       // block i may take its slot once block i - 8 is used up
-      auto arm = [&](uint32_t i) {
+      auto arm = [&](uint32_t i, uint64_t* bar) {
         const uint32_t c = i % kBlocks;
         if (i >= kBlocks) mbar_wait_fast(&ctl->empty[c], (i / kBlocks - 1) & 1u, abort, p.status);
-        mbar_arrive_expect_tx(&ctl->full[c], kBlock);
+        mbar_arrive_expect_tx(bar, kBlock);
         return smem + Layout::ring + c * kBlock;
       };
-      for (int j = 0; j < tiles && !*abort; ++j) {
-        const int key = k0 + j * kKeys;
+      for (int j = 0; j < w.tiles && !*abort; ++j) {
+        const int key = w.key + j * kKeys;
         for (int c = 0; c < 3; ++c) {
-          const uint32_t i = k_block(j) + c;
-          uint8_t* dst = arm(i);
+          const uint32_t i = k_block(at, j) + c;
+          uint64_t* bar = &ctl->full[i % kBlocks];
+          uint8_t* dst = arm(i, bar);
           if (c < 2)
-            tma_load_3d(dst, &tm_k, &ctl->full[i % kBlocks], c * 64, h, key);
+            tma_load_3d(dst, &tm_k, bar, c * 64, w.h, key);
           else
-            tma_load_2d(dst, &tm_r, &ctl->full[i % kBlocks], 0, key);
+            tma_load_2d(dst, &tm_r, bar, 0, key);
         }
         for (int c = 0; c < 2; ++c) {
-          const uint32_t i = v_block(j) + c;
-          uint8_t* dst = arm(i);
+          const uint32_t i = v_block(at, j) + c;
+          uint64_t* bar = j < w.edge0 ? &ctl->full[i % kBlocks] : &ctl->edge[edges & 1u][c];
+          uint8_t* dst = arm(i, bar);
           for (int u = 0; u < 2; ++u)
-            tma_load_3d(dst + u * (kBlock / 2), &tm_v, &ctl->full[i % kBlocks], 128 + u * 64, h, key + c * 64);
+            tma_load_3d(dst + u * (kBlock / 2), &tm_v, bar, 128 + u * 64, w.h, key + c * 64);
         }
+        if (j >= w.edge0) ++edges;
       }
+    };
+    Line line;
+    const bool tell = blockIdx.x == 0;   // this CTA looks at every sequence
+    if (tell)
+      for (int b0 = 32, end = line.chunk(p, 0, 0, lane, true); b0 < p.B; b0 += 32)
+        end = line.chunk(p, b0, end, lane, true);
+    if (!tell || p.B > 32) line.chunk(p, 0, 0, lane, false);
+    uint32_t item = 0;
+    // room for item number `item` in its slot, two items back
+    auto room = [&] {
+      if (item > 1) mbar_wait_fast(&ctl->item_empty[item & 1u], ((item >> 1) - 1) & 1u, abort, p.status);
+      __syncwarp();
+    };
+    int index = (int)blockIdx.x;
+    for (uint32_t asked = 0; index >= 0; ++asked) {
+      if (lane == 0) {  // the next index is on its way while this item's loads are issued
+        mbar_arrive_expect_tx(&ctl->answer_full, 16);
+        clc_try_cancel(ctl->answer, &ctl->answer_full);
+      }
+      Item w;
+      if (line.find(p, index, lane, w)) {
+        room();
+        if (lane == 0) {
+          ctl->item[item & 1u] = w;
+          mbar_arrive(&ctl->item_full[item & 1u]);
+          load(w, item);
+        }
+        __syncwarp();
+        at += 5u * w.tiles;
+        ++item;
+      }
+      warp_wait(&ctl->answer_full, asked & 1u, abort, p.status);
+      index = __shfl_sync(0xffffffffu, *abort ? -1 : clc_block(ctl->answer), 0);
+      // (the next answer is written through the async proxy, after these reads)
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
+    room();
+    if (lane == 0) {
+      ctl->item[item & 1u].tiles = 0;
+      mbar_arrive(&ctl->item_full[item & 1u]);
     }
     __syncwarp();
+  } else if (warp >= 10) {
+    // ---------------- edge tiles: half c of the values of a tile that some token of the block does not
+    // see to its end.  What a token does not see must not reach it, and a weight of 0 times NaN would:
+    // value rows past the sequence become zeros, and in the others what is not finite, whose tokens
+    // then get their NaN through the score.
+    const int c = warp - 10;
+    uint32_t edges = 0;
+    for (uint32_t item = 0;; ++item) {
+      warp_wait(&ctl->item_full[item & 1u], (item >> 1) & 1u, abort, p.status);
+      const Item& w = ctl->item[item & 1u];
+      const int tiles = w.tiles, edge0 = w.edge0, n_key = w.n_key;
+      if (tiles == 0 || __any_sync(0xffffffffu, *abort)) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->item_empty[item & 1u]);
+      for (int j = edge0; j < tiles; ++j, ++edges) {
+        warp_wait(&ctl->edge[edges & 1u][c], (edges >> 1) & 1u, abort, p.status);
+        const uint32_t t = at / 5u + j, slot = (v_block(at, j) + c) % kBlocks;
+        const int rows = min(max(n_key - j * kKeys - c * 64, 0), 64);   // of the sequence
+        uint8_t* half = smem + Layout::ring + slot * kBlock;
+        auto piece = [&](int r, int ch) {   // 16 bytes of row r
+          return reinterpret_cast<uint4*>(half + (ch >> 3) * (kBlock / 2) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+        };
+        // is anything not finite?  (an exponent of all ones is the only one that a 1 carries out of)
+        uint32_t odd = 0;
+#pragma unroll 8
+        for (int r2 = 0; r2 < 64; r2 += 2) {  // two rows at a time, 16 lanes each
+          const int r = r2 + (lane >> 4);
+          const uint4 v = *piece(r, lane & 15);
+          const uint32_t o = ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
+                             ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
+          if (r < rows) odd |= o;
+        }
+        const bool any = __any_sync(0xffffffffu, (odd & 0x80008000u) != 0u);
+        if (lane < 16) reinterpret_cast<uint32_t*>(ctl->bad[t & 1u] + c * 64)[lane] = 0u;
+        __syncwarp();
+        for (int r2 = any ? 0 : rows & ~1; r2 < 64; r2 += 2) {
+          const int r = r2 + (lane >> 4), ch = lane & 15;
+          uint4 v = *piece(r, ch);
+          const uint4 was = v;
+          v = r < rows ? make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w))
+                       : make_uint4(0u, 0u, 0u, 0u);
+          *piece(r, ch) = v;
+          const uint32_t votes = __ballot_sync(
+              0xffffffffu, r < rows && (v.x != was.x || v.y != was.y || v.z != was.z || v.w != was.w));
+          if (ch == 0 && ((votes >> (lane & 16)) & 0xffffu)) ctl->bad[t & 1u][c * 64 + r] = 1;
+        }
+        if (any && lane == 0) ctl->any_bad[t & 1u][c] = t + 1u;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->full[slot]);
+      }
+      at += 5u * tiles;
+    }
   } else if (warp == 8) {
     // ---------------- MMA issue: the whole warp walks, one lane issues
     constexpr uint32_t idesc_qk = idesc_bf16(kRows, kKeys);
@@ -192,11 +359,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
     };
     // Q_x . K(j)^T; the first row tile to use a key tile waits for it, the last one releases it
+    uint32_t done[2] = {0, 0};   // tiles that row tile x had in earlier items
     auto qk = [&](int x, int j, bool wait, bool release) {
       const uint64_t a = desc_at(qd, x * 3 * kBlock);
 #pragma unroll
       for (int c = 0; c < 3; ++c) {
-        const uint32_t i = k_block(j) + c;
+        const uint32_t i = k_block(at, j) + c;
         if (wait) wait_block(i);
         const uint64_t k = desc_at(kd, (i % kBlocks) * kBlock);
 #pragma unroll
@@ -210,9 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto pv = [&](int x, int j, bool wait, bool release) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const uint32_t i = v_block(j) + c;
+        const uint32_t i = v_block(at, j) + c;
         if (wait) wait_block(i);
-        warp_wait(&ctl->p_full[x][c], (uint32_t)j & 1u, abort, p.status);
+        warp_wait(&ctl->p_full[x][c], (done[x] + j) & 1u, abort, p.status);
         tc_fence_after();
         const uint64_t v = desc_at(vd, (i % kBlocks) * kBlock);
 #pragma unroll
@@ -223,156 +391,150 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mma_commit_by(&ctl->pv_done[x], me);
     };
-    warp_wait(&ctl->q_full, 0, abort, p.status);
-    qk(0, 0, true, nb == 0);
-    if (nb > 0) qk(1, 0, false, true);
+    // (a row tile's first products of an item may overwrite S, whose weights the last P.V has read by
+    // then, and O, which its softmax warps have read before they hand over new weights)
+    for (uint32_t item = 0;; ++item) {
+      warp_wait(&ctl->item_full[item & 1u], (item >> 1) & 1u, abort, p.status);
+      const Item& w = ctl->item[item & 1u];
+      const int na = __shfl_sync(0xffffffffu, w.na, 0), nb = __shfl_sync(0xffffffffu, w.nb, 0),
+                tiles = __shfl_sync(0xffffffffu, w.tiles, 0);
+      if (tiles == 0 || __any_sync(0xffffffffu, *abort)) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->item_empty[item & 1u]);
+      warp_wait(&ctl->q_full, item & 1u, abort, p.status);
+      qk(0, 0, true, nb == 0);
+      if (nb > 0) qk(1, 0, false, true);
 #pragma unroll 1
-    for (int j = 0; j < tiles; ++j) {
-      if (__any_sync(0xffffffffu, *abort)) break;
-      if (j < na) pv(0, j, true, j >= nb);
-      if (j + 1 < na) qk(0, j + 1, true, j + 1 >= nb);
-      if (j < nb) pv(1, j, j >= na, true);
-      if (j + 1 < nb) qk(1, j + 1, j + 1 >= na, true);
+      for (int j = 0; j < tiles; ++j) {
+        if (__any_sync(0xffffffffu, *abort)) break;
+        if (j + 1 == tiles) mma_commit_by(&ctl->q_empty, me);  // every product with Q is issued
+        if (j < na) pv(0, j, true, j >= nb);
+        if (j + 1 < na) qk(0, j + 1, true, j + 1 >= nb);
+        if (j < nb) pv(1, j, j >= na, true);
+        if (j + 1 < nb) qk(1, j + 1, j + 1 >= na, true);
+      }
+      done[0] += na;
+      done[1] += nb;
+      at += 5u * tiles;
     }
   } else if (warp < 8) {
     // ---------------- softmax of row tile x: a thread is a row
     const int x = warp >> 2;
     const int row = tid & 127;
-    const int n = x == 0 ? na : nb;
-    const int rows = x == 0 ? rows_a : rows_b;
-    // rows past the block's tokens count as seeing everything: no masking, nothing of them is kept
-    const int seen = row < rows ? seen0 + x * kRows + row : 0x7fffffff;
     const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_at = lane_addr + kColS + x * 128, o_at = lane_addr + kColO + x * 128;
-    float m_ref = -INFINITY, l = 0.f;
-    for (int j = 0; j < n; ++j) {
-      // A tile that some token of the block does not see to its end.  What it does not see must not
-      // reach it, and a weight of 0 times NaN would: value rows past the sequence become zeros, and in
-      // the others what is not finite, whose tokens then get their NaN through the score.
-      const bool edge = (j + 1) * kKeys > seen0;
-      bool bad_tile = false;
-      if (edge) {
-        const bool both = j < na && j < nb;
-        for (uint32_t i = v_block(j); i < v_block(j) + 2; ++i)
-          warp_wait(&ctl->full[i % kBlocks], (i / kBlocks) & 1u, abort, p.status);
-        const int w = both ? warp : warp & 3, nw = both ? 8 : 4;
-        bool any = false;
-        for (int r2 = w * 2; r2 < kKeys; r2 += nw * 2) {  // two rows at a time, 16 lanes each
-          const int r = r2 + (lane >> 4), ch = lane & 15;
-          uint4* at = reinterpret_cast<uint4*>(smem + Layout::ring + (v_block(j) + (r >> 6)) % kBlocks * kBlock +
-                                               (ch >> 3) * (kBlock / 2) + (r & 63) * 128 + (((ch & 7) ^ (r & 7)) << 4));
-          const bool none = j * kKeys + r >= n_key;
-          uint4 v = *at;
-          uint32_t* e = reinterpret_cast<uint32_t*>(&v);
-          bool hit = false;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if ((e[k] & 0x7f80u) == 0x7f80u || none) hit = true, e[k] &= 0xffff0000u;
-            if ((e[k] & 0x7f800000u) == 0x7f800000u || none) hit = true, e[k] &= 0xffffu;
-          }
-          if (hit) *at = v;
-          const uint32_t votes = __ballot_sync(0xffffffffu, hit && !none);
-          if (ch == 0) ctl->bad[j & 1][r] = (votes >> (lane & 16)) & 0xffffu ? 1 : 0;
-          any |= votes != 0u;
+    uint32_t done = 0;   // tiles of earlier items
+    for (uint32_t item = 0;; ++item) {
+      warp_wait(&ctl->item_full[item & 1u], (item >> 1) & 1u, abort, p.status);
+      const volatile Item& w = ctl->item[item & 1u];
+      if (w.tiles == 0 || __any_sync(0xffffffffu, *abort)) break;
+      const int n = x == 0 ? w.na : w.nb, rows = x == 0 ? w.rows_a : w.rows_b;
+      // rows past the block's tokens count as seeing everything: no masking, nothing of them is kept
+      const int seen = row < rows ? w.seen0 + x * kRows + row : 0x7fffffff;
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j) {
+        warp_wait(&ctl->s_full[x], (done + j) & 1u, abort, p.status);
+        bool bad_tile = false;
+        const uint32_t t = at / 5u + j;
+        if (j >= w.edge0) {
+          // (after the scores: the slots' previous uses, of K(j-1), are over by then, so that the parity
+          // of this wait means this use)
+          for (uint32_t i = v_block(at, j); i < v_block(at, j) + 2; ++i)
+            warp_wait(&ctl->full[i % kBlocks], (i / kBlocks) & 1u, abort, p.status);
+          const volatile uint32_t* any = ctl->any_bad[t & 1u];
+          bad_tile = any[0] == t + 1u || any[1] == t + 1u;
         }
-        if (any && lane == 0) ctl->any_bad[j & 1] = j + 1;
-        fence_proxy_async_smem();
-        if (both)
-          named_barrier(3, 256);
-        else
-          named_barrier(1 + x, 128);
-        bad_tile = *(volatile int*)&ctl->any_bad[j & 1] == j + 1;
-      }
-      warp_wait(&ctl->s_full[x], (uint32_t)j & 1u, abort, p.status);
-      tc_fence_after();
-      uint32_t s[128];
+        tc_fence_after();
+        uint32_t s[128];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld_x32(s_at + c * 32, s + c * 32);
-      tmem_ld_wait();
-      const int keep = seen - j * kKeys;  // the first keys of the tile that are seen
-      if (!__all_sync(0xffffffffu, keep >= kKeys)) {
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c >= keep) s[c] = 0xff800000u;
-        if (bad_tile) {
+        for (int c = 0; c < 4; ++c) tmem_ld_x32(s_at + c * 32, s + c * 32);
+        tmem_ld_wait();
+        const int keep = seen - j * kKeys;  // the first keys of the tile that are seen
+        if (!__all_sync(0xffffffffu, keep >= kKeys)) {
 #pragma unroll
           for (int c = 0; c < 128; ++c)
-            if (c < keep && ctl->bad[j & 1][c]) s[c] = 0x7fffffffu;
-        }
-      } else if (bad_tile) {
+            if (c >= keep) s[c] = 0xff800000u;
+          if (bad_tile) {
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (ctl->bad[j & 1][c]) s[c] = 0x7fffffffu;
-      }
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < 128; c += 2)
-        m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
-      if (__any_sync(0xffffffffu, row < rows && mx > m_ref + kRescaleLog2)) {
-        const float m_new = fmaxf(m_ref, mx);
-        const float alpha = m_new == m_ref ? 1.f : fast_exp2(m_ref - m_new);
-        m_ref = m_new;
-        l *= alpha;
-        if (j > 0) {
-          warp_wait(&ctl->pv_done[x], (uint32_t)(j - 1) & 1u, abort, p.status);
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t o[16];
-            tmem_ld_x16(o_at + c * 16, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-            tmem_st_x16(o_at + c * 16, o);
+            for (int c = 0; c < 128; ++c)
+              if (c < keep && ctl->bad[t & 1u][c]) s[c] = 0x7fffffffu;
           }
+        } else if (bad_tile) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (ctl->bad[t & 1u][c]) s[c] = 0x7fffffffu;
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 128; c += 2)
+          m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+        if (__any_sync(0xffffffffu, row < rows && mx > m_ref + kRescaleLog2)) {
+          const float m_new = fmaxf(m_ref, mx);
+          const float alpha = m_new == m_ref ? 1.f : fast_exp2(m_ref - m_new);
+          m_ref = m_new;
+          l *= alpha;
+          if (j > 0) {
+            warp_wait(&ctl->pv_done[x], (done + j - 1) & 1u, abort, p.status);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[16];
+              tmem_ld_x16(o_at + c * 16, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              tmem_st_x16(o_at + c * 16, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int c = half * 64; c < half * 64 + 64; c += 2) {
+            float2 e = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), p.scale_log2, -m_use);
+            e.x = fast_exp2(e.x);
+            e.y = fast_exp2(e.y);
+            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], e);
+            s[c >> 1] = pack_bf16(e.x, e.y);  // P.V takes bf16 weights: 2^-8 relative each, unbiased
+          }
+          tmem_st_x16(s_at + half * 32, s + half * 32);
+          tmem_st_x16(s_at + half * 32 + 16, s + half * 32 + 16);
           tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->p_full[x][half]);
         }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
-      const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-#pragma unroll
-        for (int c = half * 64; c < half * 64 + 64; c += 2) {
-          float2 e = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), p.scale_log2, -m_use);
-          e.x = fast_exp2(e.x);
-          e.y = fast_exp2(e.y);
-          sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], e);
-          s[c >> 1] = pack_bf16(e.x, e.y);  // P.V takes bf16 weights: 2^-8 relative each, unbiased
-        }
-        tmem_st_x16(s_at + half * 32, s + half * 32);
-        tmem_st_x16(s_at + half * 32 + 16, s + half * 32 + 16);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->p_full[x][half]);
-      }
-      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);  // (after an abort the waits return at once: no warp leaves a barrier short)
-    }
-    // ---------------- rows out
-    if (n > 0 && rows > 0) {
-      warp_wait(&ctl->pv_done[x], (uint32_t)(n - 1) & 1u, abort, p.status);
-      tc_fence_after();
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const size_t at = (size_t)(s0 + t0 + x * kRows + row) * p.H + h;
+      // ---------------- rows out
+      done += n;
+      if (n > 0) {
+        warp_wait(&ctl->pv_done[x], (done - 1) & 1u, abort, p.status);
+        tc_fence_after();
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const size_t to = (size_t)(w.tok + x * kRows + row) * p.H + w.h;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
-        tmem_ld_x32(o_at + c * 32, o);
-        tmem_ld_wait();
-        if (row < rows) {
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tmem_ld_x32(o_at + c * 32, o);
+          tmem_ld_wait();
+          if (row < rows) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t e[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              e[q] = pack_bf16(__uint_as_float(o[8 * k + 2 * q]) * inv, __uint_as_float(o[8 * k + 2 * q + 1]) * inv);
-            reinterpret_cast<uint4*>(p.out + at * kDv + c * 32)[k] = make_uint4(e[0], e[1], e[2], e[3]);
+            for (int k = 0; k < 16; ++k)
+              o[k] = pack_bf16(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+            st_global_v8(p.out + to * kDv + c * 32, o);
+            st_global_v8(p.out + to * kDv + c * 32 + 16, o + 8);
           }
         }
+        if (row < rows && p.lse) p.lse[to] = l == 0.f ? -INFINITY : m_ref * 0.69314718055994531f + logf(l);
       }
-      if (row < rows && p.lse) p.lse[at] = l == 0.f ? -INFINITY : m_ref * 0.69314718055994531f + logf(l);
+      at += 5u * w.tiles;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->item_empty[item & 1u]);
     }
   }
   if (ctl->abort) {  // copies may still be in flight: give them time to land
@@ -395,19 +557,20 @@ dsa_status launch_mla_prefill(const dsa_mla_prefill_args& a, cudaStream_t stream
   p.n_q = a.n_q;
   p.n_kv = a.n_kv;
   p.H = a.H;
-  p.max_q = std::min(a.max_q_per_seq, a.n_q);
-  p.blocks = (p.max_q + kTokens - 1) / kTokens;
+  p.max_q = a.max_q_per_seq;
   p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
   p.q_start = a.q_start;
   p.kv_start = a.kv_start;
   p.out = reinterpret_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;
   p.status = a.status;
-  const long long grid = (long long)a.B * p.blocks * a.H;
-  if (grid > 0x7fffffffLL) {
-    err = "mla_prefill: sequences * token blocks * heads must number below 2^31";
+  // every sequence has at most one block that is not full
+  const long long blocks = (long long)a.n_q / kTokens + a.B, grid = blocks * a.H;
+  if (grid > 0x7fff0000LL) {
+    err = "mla_prefill: token blocks * heads must number below 2^31";
     return DSA_ERR_UNSUPPORTED;
   }
+  p.blocks = (int)blocks;
   // without any keys nothing is seen: any valid memory stands in for them
   const bool none = a.n_kv == 0;
   const uint64_t H = (uint64_t)a.H, keys = none ? 1 : (uint64_t)a.n_kv;

@@ -614,7 +614,40 @@ DSA_DEV uint4 ld_cluster_v4(uint32_t addr) {
   return v;
 }
 
+// ---------------------------------------------------------------- cluster launch control
+
+// Ask for a block of this grid that has not started: its index, or that there is none, arrives as 16
+// bytes in shared memory, counted on `bar`.  The grid's remaining blocks go to whoever asks first.  Not
+// to be asked again after the answer that there is none.
+DSA_DEV void clc_try_cancel(void* response, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(response)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// The x index of the block in an answer, or -1: none.
+DSA_DEV int clc_block(const void* response) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n .reg .b128 r;\n .reg .pred p;\n ld.shared.b128 r, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n"
+      " selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}\n"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(response))
+      : "memory");
+  return ok ? (int)x : -1;
+}
+
 // ---------------------------------------------------------------- misc
+
+// 32 bytes to global memory, a full sector (32-byte aligned).
+DSA_DEV void st_global_v8(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 
 // Largest of three (a NaN loses), one instruction.
 DSA_DEV float max3(float a, float b, float c) {

@@ -293,12 +293,12 @@ dsa_status dsa_mla_decode(const dsa_mla_decode_args* args, dsa_stream_t stream);
  * output up to rounding.  A token that sees nothing gets out = 0 and lse = -inf; tokens that no
  * sequence owns keep their rows.  Keys and values of other sequences, and of later tokens, never
  * reach a token's output, whatever they hold; a NaN or infinity among the values that a token
- * does see may make its whole output row NaN.  A q_start or kv_start that decreases or leaves its array, and more tokens in a
- * sequence than max_q_per_seq, set DSA_ERR_DEVICE_CHECK; that sequence, or its further tokens,
- * are skipped.
+ * does see may make its whole output row NaN.  A q_start or kv_start that decreases or leaves its
+ * array sets DSA_ERR_DEVICE_CHECK, and the sequence is skipped; so do more tokens in a sequence
+ * than max_q_per_seq, which are computed all the same.
  *
- * Supported: d_nope 128, d_rope 64, d_v 128; 1 <= H <= 1024; bf16; q, kv, k_rope and out 16-byte
- * aligned, k_rope_stride a multiple of 8.
+ * Supported: d_nope 128, d_rope 64, d_v 128; 1 <= H <= 1024; bf16; q, kv and k_rope 16-byte aligned,
+ * out 32-byte aligned, k_rope_stride a multiple of 8.
  */
 typedef struct {
   int B, n_q, n_kv;
