@@ -67,7 +67,7 @@ struct Item {
 };
 
 struct Ctl {
-  uint64_t q_full, q_empty, full[kBlocks], empty[kBlocks];
+  uint64_t q_full[2], q_empty[2], full[kBlocks], empty[kBlocks];
   uint64_t s_full[2], p_full[2][2], pv_done[2];
   uint64_t edge[2][2];       // values of an edge tile (by its count & 1), half, have landed
   uint64_t item_full[2], item_empty[2], answer_full;
@@ -138,24 +138,38 @@ struct Line {
     first = before + upto - count;
     return before + __shfl_sync(0xffffffffu, upto, 31);
   }
-  // Grid block i: by head group, then token blocks from the line's last to its first, then heads.
+  // Grid block i: by head group, then token blocks by their place in their sequence, the last first
+  // (the longest; with more than 32 sequences: from the line's end), then heads.
   DSA_DEV bool find(const Params& p, int i, int lane, Item& w) {
     const int group = i / (p.blocks * kHeadGroup);
     const int heads = min(kHeadGroup, p.H - group * kHeadGroup);
     i -= group * p.blocks * kHeadGroup;
     w.h = group * kHeadGroup + i % heads;
-    const int want = p.blocks - 1 - i / heads;
-    uint32_t hit = __ballot_sync(0xffffffffu, want >= first && want < first + count);
-    if (hit == 0 && p.B > 32) {  // more sequences than lanes: look from the start
-      int at = 0;
-      for (int b0 = 0; b0 < p.B && hit == 0; b0 += 32) {
+    int rank = i / heads, l = -1, block = 0;
+    if (p.B <= 32) {
+      for (int k = __reduce_max_sync(0xffffffffu, count) - 1; k >= 0; --k) {
+        const uint32_t have = __ballot_sync(0xffffffffu, count > k);
+        if (rank < __popc(have)) {  // its (rank + 1)th sequence
+          l = __ffs((int)__ballot_sync(0xffffffffu, count > k && __popc(have & ((1u << lane) - 1u)) == rank)) - 1;
+          block = k;
+          break;
+        }
+        rank -= __popc(have);
+      }
+    } else {
+      const int want = p.blocks - 1 - rank;
+      uint32_t hit = 0;
+      for (int b0 = 0, at = 0; b0 < p.B && hit == 0; b0 += 32) {
         at = chunk(p, b0, at, lane, false);
         hit = __ballot_sync(0xffffffffu, want >= first && want < first + count);
       }
+      if (hit != 0) {
+        l = __ffs((int)hit) - 1;
+        block = want - __shfl_sync(0xffffffffu, first, l);
+      }
     }
-    if (hit == 0) return false;  // the line is shorter than its bound
-    const int l = __ffs((int)hit) - 1;
-    const int t0 = (want - __shfl_sync(0xffffffffu, first, l)) * kTokens;
+    if (l < 0) return false;  // the line is shorter than its bound
+    const int t0 = block * kTokens;
     const int q0 = __shfl_sync(0xffffffffu, s0, l), n_tok = __shfl_sync(0xffffffffu, s1, l) - q0;
     w.key = __shfl_sync(0xffffffffu, k0, l);
     w.n_key = __shfl_sync(0xffffffffu, k1, l) - w.key;
@@ -182,14 +196,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &ctl->abort;
 
   if (tid == 0) {
-    mbar_init(&ctl->q_full, 1);
-    mbar_init(&ctl->q_empty, 1);
     mbar_init(&ctl->answer_full, 1);
     for (int i = 0; i < kBlocks; ++i) {
       mbar_init(&ctl->full[i], 1);
       mbar_init(&ctl->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->q_full[i], 1);
+      mbar_init(&ctl->q_empty[i], 1);
       mbar_init(&ctl->s_full[i], 1);
       mbar_init(&ctl->p_full[i][0], 4);
       mbar_init(&ctl->p_full[i][1], 4);
@@ -216,13 +230,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 9) {
     // ---------------- items and loads
-    uint32_t edges = 0;   // edge tiles so far
-    auto load = [&](const Item& w, uint32_t item) {
-      const int parts = w.nb > 0 ? 2 : 1;
-      if (item > 0) mbar_wait_fast(&ctl->q_empty, (item - 1) & 1u, abort, p.status);
-      mbar_arrive_expect_tx(&ctl->q_full, parts * 3 * kBlock);
-      for (int c = 0; c < parts * 3; ++c)
-        tma_load_3d(smem + Layout::q + c * kBlock, &tm_q, &ctl->q_full, (c % 3) * 64, w.h, w.tok + (c / 3) * kRows);
+    uint32_t edges = 0, loads_a = 0, loads_b = 0;   // edge tiles, and loads of A's and B's queries, so far
+    auto load = [&](const Item& w) {
+      // (A's last product with its queries is half a step or more before B's, whose new queries are
+      // waited for after the first keys and values)
+      auto load_q = [&](int x, uint32_t& loads) {
+        if (loads > 0) mbar_wait_fast(&ctl->q_empty[x], (loads - 1) & 1u, abort, p.status);
+        ++loads;
+        mbar_arrive_expect_tx(&ctl->q_full[x], 3 * kBlock);
+        for (int c = 0; c < 3; ++c)
+          tma_load_3d(smem + Layout::q + (x * 3 + c) * kBlock, &tm_q, &ctl->q_full[x], c * 64, w.h, w.tok + x * kRows);
+      };
+      load_q(0, loads_a);
       // block i may take its slot once block i - 8 is used up
       auto arm = [&](uint32_t i, uint64_t* bar) {
         const uint32_t c = i % kBlocks;
@@ -249,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(dst + u * (kBlock / 2), &tm_v, bar, 128 + u * 64, w.h, key + c * 64);
         }
         if (j >= w.edge0) ++edges;
+        if (j == 0 && w.nb > 0) load_q(1, loads_b);
       }
     };
     Line line;
@@ -256,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tell)
       for (int b0 = 32, end = line.chunk(p, 0, 0, lane, true); b0 < p.B; b0 += 32)
         end = line.chunk(p, b0, end, lane, true);
-    if (!tell || p.B > 32) line.chunk(p, 0, 0, lane, false);
+    if (!tell) line.chunk(p, 0, 0, lane, false);
     uint32_t item = 0;
     // room for item number `item` in its slot, two items back
     auto room = [&] {
@@ -275,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           ctl->item[item & 1u] = w;
           mbar_arrive(&ctl->item_full[item & 1u]);
-          load(w, item);
+          load(w);
         }
         __syncwarp();
         at += 5u * w.tiles;
@@ -359,8 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
     };
     // Q_x . K(j)^T; the first row tile to use a key tile waits for it, the last one releases it
-    uint32_t done[2] = {0, 0};   // tiles that row tile x had in earlier items
-    auto qk = [&](int x, int j, bool wait, bool release) {
+    uint32_t done[2] = {0, 0}, with_b = 0;   // tiles that row tile x had in earlier items; items with a B
+    auto qk = [&](int x, int j, bool wait, bool release, bool last) {
       const uint64_t a = desc_at(qd, x * 3 * kBlock);
 #pragma unroll
       for (int c = 0; c < 3; ++c) {
@@ -374,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (release) mma_commit_by(&ctl->empty[i % kBlocks], me);
       }
       mma_commit_by(&ctl->s_full[x], me);
+      if (last) mma_commit_by(&ctl->q_empty[x], me);
     };
     auto pv = [&](int x, int j, bool wait, bool release) {
 #pragma unroll
@@ -401,17 +422,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tiles == 0 || __any_sync(0xffffffffu, *abort)) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->item_empty[item & 1u]);
-      warp_wait(&ctl->q_full, item & 1u, abort, p.status);
-      qk(0, 0, true, nb == 0);
-      if (nb > 0) qk(1, 0, false, true);
+      warp_wait(&ctl->q_full[0], item & 1u, abort, p.status);
+      qk(0, 0, true, nb == 0, na == 1);
+      if (nb > 0) {
+        warp_wait(&ctl->q_full[1], with_b & 1u, abort, p.status);
+        ++with_b;
+        qk(1, 0, false, true, nb == 1);
+      }
 #pragma unroll 1
       for (int j = 0; j < tiles; ++j) {
         if (__any_sync(0xffffffffu, *abort)) break;
-        if (j + 1 == tiles) mma_commit_by(&ctl->q_empty, me);  // every product with Q is issued
         if (j < na) pv(0, j, true, j >= nb);
-        if (j + 1 < na) qk(0, j + 1, true, j + 1 >= nb);
+        if (j + 1 < na) qk(0, j + 1, true, j + 1 >= nb, j + 2 == na);
         if (j < nb) pv(1, j, j >= na, true);
-        if (j + 1 < nb) qk(1, j + 1, j + 1 >= na, true);
+        if (j + 1 < nb) qk(1, j + 1, j + 1 >= na, true, j + 2 == nb);
       }
       done[0] += na;
       done[1] += nb;
