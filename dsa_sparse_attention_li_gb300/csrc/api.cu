@@ -259,8 +259,8 @@ static dsa_status mla_decode_check(const dsa_mla_decode_args* a, bool pointers) 
   if (a->n_q == 0) return DSA_OK;
   if (!a->q || !a->kv_pool || !a->page_table || !a->seq_lens || !a->q_start || !a->out)
     return fail(DSA_ERR_INVALID_ARG, "mla_decode: null device pointer");
-  if (!aligned16(a->q) || !aligned16(a->kv_pool) || !aligned16(a->out))
-    return fail(DSA_ERR_INVALID_ARG, "mla_decode: q, kv_pool, out must be 16-byte aligned");
+  if (!aligned16(a->q) || !aligned16(a->kv_pool) || (reinterpret_cast<uintptr_t>(a->out) & 31u))
+    return fail(DSA_ERR_INVALID_ARG, "mla_decode: q and kv_pool must be 16-byte aligned, out 32-byte aligned");
   if (a->workspace != nullptr && (reinterpret_cast<uintptr_t>(a->workspace) & 255u) != 0)
     return fail(DSA_ERR_INVALID_ARG, "mla_decode: workspace must be 256-byte aligned");
   const size_t need = dsa::mla_decode_workspace_bytes(*a);

@@ -417,8 +417,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
           nxt = window(i + 32);
         }
         const int pg = __shfl_sync(0xffffffffu, cur, j);
-        if (i == w.tile0)
-          for (int d = 1; d < kPrefetch; ++d) warm(__shfl_sync(0xffffffffu, cur, d));
         const int ja = j + kPrefetch;
         const int far = ja < 32 ? __shfl_sync(0xffffffffu, cur, ja) : __shfl_sync(0xffffffffu, nxt, ja - 32);
         if (lane == 0) {
@@ -432,6 +430,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
               tma_load_2d_pair(smem + Layout::k + (3 * c + u) * kBlockBytes, &tm_kv, k_full + c * 8, (3 * c + u) * 64, y);
           }
         }
+        if (i == w.tile0)  // (after the first tile's loads, which are waited for)
+          for (int d = 1; d < kPrefetch; ++d) warm(__shfl_sync(0xffffffffu, cur, d));
         warm(far);
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
@@ -829,21 +829,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
           tmem_ld_x32(lane_addr + kColO + (uint32_t)(cc * 32), o);
           tmem_ld_wait();
           if (active) {
+            // 32 bytes a store: with 16-byte ones (half a sector each) a piece took 5 us to leave
             if (whole) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uint32_t e[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  e[q] = pack_bf16(__uint_as_float(o[8 * k + 2 * q]) * inv, __uint_as_float(o[8 * k + 2 * q + 1]) * inv);
-                reinterpret_cast<uint4*>(o_out + cc * 32)[k] = make_uint4(e[0], e[1], e[2], e[3]);
-              }
+              for (int k = 0; k < 16; ++k)
+                o[k] = pack_bf16(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+              st_global_v8(o_out + cc * 32, o);
+              st_global_v8(o_out + cc * 32 + 16, o + 8);
             } else {
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                reinterpret_cast<float4*>(o_ws + cc * 32)[k] =
-                    make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
-                                __uint_as_float(o[4 * k + 2]) * inv, __uint_as_float(o[4 * k + 3]) * inv);
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * inv);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) st_global_v8(o_ws + cc * 32 + 8 * k, o + 8 * k);
             }
           }
         }
@@ -890,67 +887,164 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
   if (warp == 4) tmem_dealloc2(tmem, kTmemCols);
 }
 
-// Joins the pieces of the groups that a range border cuts: blockIdx.y is the pair whose range starts
-// inside the group, a block takes one row, a thread four columns of every second piece, eight loads
-// in flight.  The pieces' order in the sums is fixed.
-constexpr int kJoinThreads = 256;
-__global__ void __launch_bounds__(kJoinThreads) mla_join_kernel(const Params p) {
-  __shared__ float wgt[512];
-  __shared__ float4 half[128];
-  __shared__ float red[2];
-  griddep_wait();
-  const int4 j = p.ws_join[blockIdx.y];
-  const int parts = j.w, r = blockIdx.x, tid = threadIdx.x;
-  if (r >= j.y || parts == 0) return;
+// Joins the pieces of the groups that a range border cuts.  A warp does a row of a group of up to four
+// pieces, or 128 columns of one of up to 16; a block does 128 columns of one of more, its warp g adding
+// up pieces g, g + 8, ....  The sums are added in a fixed order.  The blocks share all groups' work: a
+// block for every row that there might be (9,728) took 5 us to launch, and one for every row there is
+// 12 us for a group of 74 pieces.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinRow = 4, kJoinFew = 16;
+constexpr int kJoinChunks = kDv / 128, kJoinBlocksPerSm = 4, kMostPairs = 256;
+// (offsets into the workspace fit 32 bits: 2 * kMostPairs pieces of at most 128 rows)
+
+DSA_DEV void add_to(float4& o, float e, const float4& x) {
+  o.x = fmaf(e, x.x, o.x);
+  o.y = fmaf(e, x.y, o.y);
+  o.z = fmaf(e, x.z, o.z);
+  o.w = fmaf(e, x.w, o.w);
+}
+
+// Weights of the pieces whose log-sum-exps (log2) start in slot z, relative to the largest: into wgt,
+// by a whole warp; returns the reference (NaN if a piece is, 0 if nothing was seen) and their sum.
+// (Out of line: inlined twice it cost the join half of its registers.)
+__device__ __noinline__ float2 join_weights(const float* lse, int z, int parts, int rows, float* wgt, int lane) {
+  float top = -INFINITY;
+  bool nan = false;
+#pragma unroll 1
+  for (int k = lane; k < parts; k += 32) {
+    const float v = lse[(k == 0 ? z : ((z >> 1) + k) * 2) * rows];
+    wgt[k] = v;
+    nan |= v != v;
+    top = fmaxf(top, v);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float m = __any_sync(0xffffffffu, nan) ? __uint_as_float(0x7fffffffu) : top == -INFINITY ? 0.f : top;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int k = lane; k < parts; k += 32) {
+    const float e = exp2f(wgt[k] - m);
+    wgt[k] = e;
+    sum += e;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  __syncwarp();
+  return make_float2(m, sum);
+}
+
+// The pieces of one row, C times four columns a lane (col4, col4 + 32, ...); wgt: the warp's weights.
+template <int C>
+struct Pieces {
+  static constexpr int kAtOnce = 8 / C;
+  const Params& p;
+  int4 j;
+  int r, col4, lane;
+  float* wgt;
+  float m, sum;      // reference of the weights (NaN if a piece has one), their sum
+  float4 o[C];
+
   // piece 0 lies in slot j.z, the following ones each at the start of the next pair's range
-  auto slot = [&](int k) { return k == 0 ? (size_t)j.z : ((size_t)(j.z >> 1) + k) * 2; };
-  if (tid < 32) {
-    float m = -INFINITY;
-    bool nan = false;
-    for (int k = tid; k < parts; k += 32) {
-      const float x = p.ws_lse[slot(k) * p.ws_rows + r];
-      wgt[k] = x;
-      nan |= x != x;
-      m = fmaxf(m, x);
-    }
+  DSA_DEV const float4* cols(int k) const {
+    const int slot = k == 0 ? j.z : ((j.z >> 1) + k) * 2;
+    return reinterpret_cast<const float4*>(p.ws_o) + ((slot * p.ws_rows + r) * (kDv / 4) + col4);
+  }
+  // o = weighted sum of pieces first, first + step, ...
+  DSA_DEV void add_up(int first, int step) {
+    // (on their way while the weights are worked out, without the registers that loads would take)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (__any_sync(0xffffffffu, nan)) m = __uint_as_float(0x7fffffffu);
-    if (m == -INFINITY) m = 0.f;
-    float sum = 0.f;
-    for (int k = tid; k < parts; k += 32) {
-      const float e = exp2f(wgt[k] - m);
-      wgt[k] = e;
-      sum += e;
-    }
+    for (int i = 0; i < kAtOnce; ++i)
+      if (first + i * step < j.w)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (tid == 0) {
-      red[0] = m;
-      red[1] = sum;
+        for (int c = 0; c < C; ++c) asm volatile("prefetch.global.L1 [%0];" ::"l"(cols(first + i * step) + c * 32));
+    const float2 w = join_weights(p.ws_lse + r, j.z, j.w, p.ws_rows, wgt, lane);
+    m = w.x;
+    sum = w.y;
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k0 = first; k0 < j.w; k0 += step * kAtOnce) {
+      float4 x[kAtOnce][C];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        if (k0 + i * step < j.w)
+#pragma unroll
+          for (int c = 0; c < C; ++c) x[i][c] = cols(k0 + i * step)[c * 32];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        if (k0 + i * step < j.w)
+#pragma unroll
+          for (int c = 0; c < C; ++c) add_to(o[c], wgt[k0 + i * step], x[i][c]);
+    }
+  }
+  DSA_DEV void finish() const {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const size_t grow = (size_t)j.x * p.H + r;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      reinterpret_cast<uint2*>(p.out + grow * kDv)[col4 + c * 32] =
+          make_uint2(pack_bf16(o[c].x * inv, o[c].y * inv), pack_bf16(o[c].z * inv, o[c].w * inv));
+    if (col4 == 0 && p.lse) p.lse[grow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+  }
+};
+
+__global__ void __launch_bounds__(kJoinThreads, 2) mla_join_kernel(const __grid_constant__ Params p) {
+  __shared__ float4 part[kJoinWarps][32];
+  __shared__ float wgt[kJoinWarps][kMostPairs];
+  __shared__ int4 groups[kMostPairs];
+  __shared__ int ends[kMostPairs];      // items of the groups up to and with each
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  griddep_wait();
+  if (warp == 0) {
+    int before = 0;
+#pragma unroll 1
+    for (int b = 0; b < p.pairs; b += 32) {
+      const int4 j = b + lane < p.pairs ? p.ws_join[b + lane] : make_int4(0, 0, 0, 0);
+      int n = j.w == 0 ? 0 : j.w <= kJoinRow ? j.y : j.y * kJoinChunks;
+      if (j.w <= kJoinFew) n = (n + kJoinWarps - 1) / kJoinWarps;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, n, o);
+        if (lane >= o) n += x;
+      }
+      groups[b + lane] = j;
+      ends[b + lane] = before + n;
+      before += __shfl_sync(0xffffffffu, n, 31);
     }
   }
   __syncthreads();
-  const int col = tid & 127, which = tid >> 7;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int k = which; k < parts; k += 2) {
-    const float e = wgt[k];
-    const float4 x = __ldcs(reinterpret_cast<const float4*>(p.ws_o + (slot(k) * p.ws_rows + r) * kDv) + col);
-    o.x = fmaf(e, x.x, o.x);
-    o.y = fmaf(e, x.y, o.y);
-    o.z = fmaf(e, x.z, o.z);
-    o.w = fmaf(e, x.w, o.w);
+  const int total = ends[p.pairs - 1];
+#pragma unroll 1
+  for (int item = blockIdx.x; item < total; item += gridDim.x) {
+    int lo = 0, hi = p.pairs - 1;
+    while (lo < hi) {  // the first group that ends beyond the item
+      const int mid = (lo + hi) >> 1;
+      if (ends[mid] > item) hi = mid; else lo = mid + 1;
+    }
+    const int4 j = groups[lo];
+    const int i = item - (lo > 0 ? ends[lo - 1] : 0);
+    if (j.w <= kJoinRow) {
+      Pieces<kJoinChunks> w = {p, j, i * kJoinWarps + warp, lane, lane, wgt[warp]};
+      if (w.r < j.y) {
+        w.add_up(0, 1);
+        w.finish();
+      }
+    } else {
+      const bool few = j.w <= kJoinFew;
+      const int u = few ? i * kJoinWarps + warp : i;
+      Pieces<1> w = {p, j, u / kJoinChunks, u % kJoinChunks * 32 + lane, lane, wgt[warp]};
+      if (w.r < j.y) w.add_up(few ? 0 : warp, few ? 1 : kJoinWarps);
+      if (!few) {
+        __syncthreads();   // the previous item's sums have been read
+        part[warp][lane] = w.o[0];
+        __syncthreads();
+        if (warp == 0)
+#pragma unroll
+          for (int g = 1; g < kJoinWarps; ++g) add_to(w.o[0], 1.f, part[g][lane]);
+      }
+      if (w.r < j.y && (few || warp == 0)) w.finish();
+    }
+    __syncwarp();
   }
-  if (which == 1) half[col] = o;
-  __syncthreads();
-  if (which == 1) return;
-  const float4 x = half[col];
-  const float m = red[0], sum = red[1], inv = sum == 0.f ? 0.f : 1.f / sum;
-  const size_t grow = (size_t)j.x * p.H + r;
-  reinterpret_cast<uint2*>(p.out + grow * kDv)[col] =
-      make_uint2(pack_bf16((o.x + x.x) * inv, (o.y + x.y) * inv), pack_bf16((o.z + x.z) * inv, (o.w + x.w) * inv));
-  if (tid == 0 && p.lse) p.lse[grow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
 }
 
 // Tokens of a group, and the rows of a piece in the workspace.
@@ -961,7 +1055,7 @@ static int group_tokens(const dsa_mla_decode_args& a) {
 static int pair_count() {
   DeviceInfo dev;
   std::string err;
-  return std::min(256, (device_info(dev, err) ? dev.sm_count : 152) / 2);
+  return std::min(kMostPairs, (device_info(dev, err) ? dev.sm_count : 152) / 2);
 }
 
 }  // namespace mlad
@@ -1025,7 +1119,9 @@ dsa_status launch_mla_decode(const dsa_mla_decode_args& a, cudaStream_t stream, 
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, tm_q, tm_kv, p);
   if (e != cudaSuccess) return cuda_fail(e, "mla_decode: launch", err);
-  cfg.gridDim = dim3((unsigned)p.ws_rows, (unsigned)p.pairs);
+  // at most one group a token, and one a border
+  const long long items = (long long)std::min(p.pairs, a.n_q) * p.ws_rows * kJoinChunks;
+  cfg.gridDim = dim3((unsigned)std::min<long long>(items, (long long)p.pairs * 2 * kJoinBlocksPerSm));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, mla_join_kernel, p);

@@ -254,7 +254,7 @@ dsa_status dsa_sfa_decode_static(const dsa_sfa_args* args, dsa_stream_t stream);
  * (608-byte rows, as for dsa_sfa_decode); any lengths that the page table covers; any number of
  * tokens per sequence.  max_q_per_seq (at least 1) is the host's bound of q_start[b+1]-q_start[b];
  * it sizes the groups of tokens that share a pass over the cache, and more tokens than it says
- * only take more passes.
+ * only take more passes.  q and kv_pool 16-byte aligned, out 32-byte aligned.
  */
 typedef struct {
   int B, n_q;
