@@ -9,15 +9,17 @@
 //   MXFP8:  e = max(floor(log2 a) - 8, -127), 0 for a = 0;     c_i = e4m3(x_i 2^-e)
 // e4m3() rounds to nearest even and saturates at 448.  x_i / s is not rounded before e4m3(): a
 // quotient rounded to fp32 first can land exactly on the border between two codes.  The fast
-// path multiplies by 1/s and keeps a code only if the products 2^-21 below and above round to the
-// same one (the product is within 2^-22 of the quotient); the few others, about one element in
-// 2^16, compare |x| with border * s in 64 bits, where that product is exact.
+// path multiplies by 1/s (1 - 2^-21) and 1/s (1 + 2^-21), between which the quotient lies, and keeps a
+// code on which both agree; the few others, about one element in 2^16, compare |x| with border * s in
+// 64 bits, where that product is exact.
 //
 // Both kernels move each byte once and are bound by HBM.  The unit of work of a warp is 256
 // columns, eight a lane (16- or 32-byte accesses), so a group is a segment of 4 to 32 lanes and its
 // maximum a few shuffles.  A latent row is 2.25 units: the 64-column tails of four rows share one,
-// else a third of the lanes would idle.  A warp takes one unit: its row loads are issued before
-// the dependent page-table lookup, and the other warps of the SM hide both.
+// else a third of the lanes would idle.  With many rows a warp takes four units at once, each step of
+// the chain seq, pos -> page table -> cache row issued for all of them before the next, beside the
+// loads of the rows: one unit a warp left the SM waiting for that chain (65,536 fp32 latent rows 47
+// us).  With few rows (less than a wave of warps) one unit a warp is the shorter chain.
 #include "dsa_internal.h"
 #include "ptx.cuh"
 
@@ -25,6 +27,7 @@ namespace dsa {
 namespace cq {
 
 constexpr int kThreads = 256;
+constexpr int kUnits = 4;         // units of a warp, with many rows
 constexpr int kLatent = 576;
 constexpr int kLatentRow = 608;   // 576 codes, 5 fp32 scales, 12 zero bytes
 
@@ -68,18 +71,28 @@ DSA_DEV Place place(const Params& p, long long u, int lane) {
   return {row < p.n_rows ? (int)row : -1, col};
 }
 
-// Physical cache row of row r, or -1 (reported) when the sequence, position or page is out of range.
-DSA_DEV long long cache_row(const Params& p, int r) {
-  const int b = p.seq[r], j = p.pos[r];
-  if (b >= 0 && b < p.B && j >= 0) {
-    const int slot = j / p.page_size;
-    if (slot < p.max_pages) {
-      const int pg = p.page_table[(long long)b * p.max_pages + slot];
-      if (pg >= 0 && pg < p.num_pages) return (long long)pg * p.page_size + (j - slot * p.page_size);
-    }
+// Physical cache rows of N rows (-1: none, or out of range, which is reported), the loads of all of
+// them in flight together.
+template <int N>
+DSA_DEV void cache_rows(const Params& p, const Place* w, long long* at) {
+  int b[N], j[N], slot[N], pg[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    b[i] = w[i].row >= 0 ? p.seq[w[i].row] : 0;
+    j[i] = w[i].row >= 0 ? p.pos[w[i].row] : 0;
   }
-  report(p.status, kStatusDeviceCheck);
-  return -1;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    slot[i] = j[i] / p.page_size;
+    const bool ok = w[i].row >= 0 && b[i] >= 0 && b[i] < p.B && j[i] >= 0 && slot[i] < p.max_pages;
+    pg[i] = ok ? p.page_table[(long long)b[i] * p.max_pages + slot[i]] : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const bool ok = pg[i] >= 0 && pg[i] < p.num_pages;
+    at[i] = ok ? (long long)pg[i] * p.page_size + (j[i] - slot[i] * p.page_size) : -1;
+    if (!ok && w[i].row >= 0) report(p.status, kStatusDeviceCheck);
+  }
 }
 
 template <int E>
@@ -148,48 +161,40 @@ __device__ __noinline__ uint32_t settle(float x, float s, uint32_t lo, uint32_t 
 
 // Eight columns with scale s -> eight codes.
 DSA_DEV uint2 quantise8(const float* x, float s) {
-  const float inv = __frcp_rn(s);
-  uint32_t c[4];
+  const float inv = __frcp_rn(s), down = inv * (1.f - 0x1p-21f), up = inv * (1.f + 0x1p-21f);
+  uint32_t lo[4], hi[4], differ = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = x[2 * i] * inv, b = x[2 * i + 1] * inv;
-    constexpr float kDown = 1.f - 0x1p-21f, kUp = 1.f + 0x1p-21f;
-    uint32_t lo = e4m3x2(a * kDown, b * kDown);
-    const uint32_t hi = e4m3x2(a * kUp, b * kUp);
-    if (lo != hi) {
-      const uint32_t c0 = (lo & 0xff) == (hi & 0xff) ? (lo & 0xff) : settle(x[2 * i], s, lo & 0xff, hi & 0xff);
-      const uint32_t c1 = (lo >> 8) == (hi >> 8) ? (lo >> 8) : settle(x[2 * i + 1], s, lo >> 8, hi >> 8);
-      lo = c0 | (c1 << 8);
-    }
-    c[i] = lo;
+    lo[i] = e4m3x2(x[2 * i] * down, x[2 * i + 1] * down);
+    hi[i] = e4m3x2(x[2 * i] * up, x[2 * i + 1] * up);
+    differ |= lo[i] ^ hi[i];
   }
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  if (differ) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t l0 = lo[i] & 0xff, h0 = hi[i] & 0xff, l1 = lo[i] >> 8, h1 = hi[i] >> 8;
+      lo[i] = (l0 == h0 ? l0 : settle(x[2 * i], s, l0, h0)) | ((l1 == h1 ? l1 : settle(x[2 * i + 1], s, l1, h1)) << 8);
+    }
+  }
+  return make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
 }
 
-template <int F, int E>
-__global__ void __launch_bounds__(kThreads) write_kernel(const Params p) {
-  const long long u = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (u >= p.units) return;
-  const Place w = place<F>(p, u, lane);
-  float x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = 0.f;
-  long long dst = -1;
-  if (w.row >= 0) {
-    load8<E>(p.rows, (long long)w.row * p.row_stride + w.col, x);
-    dst = cache_row(p, w.row);
-  }
-  // the group's largest finite magnitude: a NaN or an infinity does not cost its neighbours
+// Eight columns x of a row to cache row dst (< 0: nowhere).  The whole warp takes part.
+template <int F>
+DSA_DEV void write8(const Params& p, const Place& w, long long dst, const float* x, int lane) {
+  // the group's largest finite magnitude: a NaN (which every maximum loses) or an infinity does not
+  // cost its neighbours
   float a = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float m = fabsf(x[i]);
-    a = fmaxf(a, m < INFINITY ? m : 0.f);
+  for (int i = 0; i < 8; i += 2) a = max3(a, fabsf(x[i]), fabsf(x[i + 1]));
+  if (a == INFINITY) {
+    a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
   }
   const int lanes = F == DSA_ROW_MXFP8 ? 4 : F == DSA_ROW_FP8 ? p.dim >> 3 : w.col >= 512 ? 8 : 16;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+  for (int o = 1; o < (F == DSA_ROW_MXFP8 ? 4 : F == DSA_ROW_FP8 ? 32 : 16); o <<= 1) {
     const float m = __shfl_xor_sync(0xffffffffu, a, o);
     if (o < lanes) a = fmaxf(a, m);
   }
@@ -218,45 +223,104 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const Params p) {
   }
 }
 
-template <int F, int E>
-__global__ void __launch_bounds__(kThreads) read_kernel(const Params p) {
-  const long long u = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+template <int F, int E, int N>
+__global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ Params p) {
+  const long long u = ((long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * N;
   const int lane = threadIdx.x & 31;
-  if (u >= p.units) return;
-  const Place w = place<F>(p, u, lane);
-  if (w.row < 0) return;
-  const long long src = cache_row(p, w.row);
-  float y[8];
+  Place w[N];
+  float x[N][8];
+  long long dst[N];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = 0.f;
-  if (src >= 0) {
+  for (int n = 0; n < N; ++n) {
+    w[n] = place<F>(p, u + n, lane);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[n][i] = 0.f;
+    if (w[n].row >= 0) load8<E>(p.rows, (long long)w[n].row * p.row_stride + w[n].col, x[n]);
+  }
+  cache_rows<N>(p, w, dst);
+#pragma unroll
+  for (int n = 0; n < N; ++n) write8<F>(p, w[n], dst[n], x[n], lane);
+}
+
+// Eight columns of a cache row as they lie there, and their scale.
+struct Packed {
+  uint4 bits;
+  float scale;
+};
+
+template <int F, int E, int N>
+__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ Params p) {
+  const long long u = ((long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * N;
+  const int lane = threadIdx.x & 31;
+  Place w[N];
+  long long src[N];
+  Packed v[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) w[n] = place<F>(p, u + n, lane);
+  cache_rows<N>(p, w, src);
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    v[n].bits = make_uint4(0u, 0u, 0u, 0u);
+    v[n].scale = 0.f;
+    if (src[n] < 0) continue;
     if constexpr (F == DSA_ROW_BF16) {
-      load8<DSA_ELEM_BF16>(p.pool, src * p.dim + w.col, y);
+      v[n].bits = __ldcs(reinterpret_cast<const uint4*>(p.pool + (src[n] * p.dim + w[n].col) * 2));
     } else {
-      const uint8_t* row = p.pool + src * (F == DSA_ROW_LATENT_FP8 ? kLatentRow : p.dim);
-      const uint2 c = __ldcs(reinterpret_cast<const uint2*>(row + w.col));
-      float s;
+      const uint8_t* row = p.pool + src[n] * (F == DSA_ROW_LATENT_FP8 ? kLatentRow : p.dim);
+      const uint2 c = __ldcs(reinterpret_cast<const uint2*>(row + w[n].col));
+      v[n].bits.x = c.x;
+      v[n].bits.y = c.y;
       if constexpr (F == DSA_ROW_LATENT_FP8) {
-        s = *reinterpret_cast<const float*>(row + kLatent + (w.col >> 7) * 4);
+        v[n].scale = *reinterpret_cast<const float*>(row + kLatent + (w[n].col >> 7) * 4);
       } else if constexpr (F == DSA_ROW_FP8) {
-        s = p.scale_pool[src];
+        v[n].scale = p.scale_pool[src[n]];
       } else {
-        const uint32_t e = p.sf_pool[src * (p.dim >> 5) + (w.col >> 5)];
-        s = e == 255u ? __uint_as_float(0x7fffffffu)      // not a valid scale: NaN
-                      : e == 0u ? 0x1p-127f : __uint_as_float(e << 23);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t two = ((i < 2 ? c.x : c.y) >> ((i & 1) * 16)) & 0xffffu;
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        y[2 * i] = f.x * s;
-        y[2 * i + 1] = f.y * s;
+        const uint32_t e = p.sf_pool[src[n] * (p.dim >> 5) + (w[n].col >> 5)];
+        v[n].scale = e == 255u ? __uint_as_float(0x7fffffffu)      // not a valid scale: NaN
+                               : e == 0u ? 0x1p-127f : __uint_as_float(e << 23);
       }
     }
   }
-  store8<E>(p.rows, (long long)w.row * p.row_stride + w.col, y);
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    if (w[n].row < 0) continue;
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (F == DSA_ROW_BF16) {
+        const uint32_t e = i == 0 ? v[n].bits.x : i == 1 ? v[n].bits.y : i == 2 ? v[n].bits.z : v[n].bits.w;
+        y[2 * i] = __uint_as_float(e << 16);
+        y[2 * i + 1] = __uint_as_float(e & 0xffff0000u);
+      } else {
+        const uint32_t two = ((i < 2 ? v[n].bits.x : v[n].bits.y) >> ((i & 1) * 16)) & 0xffffu;
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        y[2 * i] = f.x * v[n].scale;
+        y[2 * i + 1] = f.y * v[n].scale;
+      }
+    }
+    store8<E>(p.rows, (long long)w[n].row * p.row_stride + w[n].col, y);
+  }
 }
+
+template <int N>
+struct Kernels {
+  using Kernel = void (*)(Params);
+  static Kernel get(bool write, int format, int elem) {
+    static const Kernel kWrite[3][3] = {
+        {write_kernel<DSA_ROW_FP8, 0, N>, write_kernel<DSA_ROW_FP8, 1, N>, write_kernel<DSA_ROW_FP8, 2, N>},
+        {write_kernel<DSA_ROW_MXFP8, 0, N>, write_kernel<DSA_ROW_MXFP8, 1, N>, write_kernel<DSA_ROW_MXFP8, 2, N>},
+        {write_kernel<DSA_ROW_LATENT_FP8, 0, N>, write_kernel<DSA_ROW_LATENT_FP8, 1, N>,
+         write_kernel<DSA_ROW_LATENT_FP8, 2, N>}};
+    static const Kernel kRead[4][3] = {
+        {read_kernel<DSA_ROW_BF16, 0, N>, read_kernel<DSA_ROW_BF16, 1, N>, read_kernel<DSA_ROW_BF16, 2, N>},
+        {read_kernel<DSA_ROW_FP8, 0, N>, read_kernel<DSA_ROW_FP8, 1, N>, read_kernel<DSA_ROW_FP8, 2, N>},
+        {read_kernel<DSA_ROW_MXFP8, 0, N>, read_kernel<DSA_ROW_MXFP8, 1, N>, read_kernel<DSA_ROW_MXFP8, 2, N>},
+        {read_kernel<DSA_ROW_LATENT_FP8, 0, N>, read_kernel<DSA_ROW_LATENT_FP8, 1, N>,
+         read_kernel<DSA_ROW_LATENT_FP8, 2, N>}};
+    return write ? kWrite[format - 1][elem] : kRead[format][elem];
+  }
+};
 
 }  // namespace cq
 
@@ -281,22 +345,16 @@ dsa_status launch_cache_rows(const dsa_cache_rows_args& a, bool write, cudaStrea
   p.status = a.status;
   p.units = a.format == DSA_ROW_LATENT_FP8 ? ((long long)a.n_rows + 3) / 4 * 9
                                            : ((long long)a.n_rows * a.dim + 255) / 256;
-  const long long blocks = (p.units + kThreads / 32 - 1) / (kThreads / 32);
+  DeviceInfo dev;
+  if (!device_info(dev, err)) return DSA_ERR_CUDA;
+  const bool many = p.units > (long long)dev.sm_count * 64;   // more than a wave of warps
+  const long long warps = many ? (p.units + kUnits - 1) / kUnits : p.units;
+  const long long blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7fffffffLL) {
     err = "cache rows: too many rows for one launch";
     return DSA_ERR_UNSUPPORTED;
   }
-  using Kernel = void (*)(Params);
-  static const Kernel kWrite[3][3] = {
-      {write_kernel<DSA_ROW_FP8, 0>, write_kernel<DSA_ROW_FP8, 1>, write_kernel<DSA_ROW_FP8, 2>},
-      {write_kernel<DSA_ROW_MXFP8, 0>, write_kernel<DSA_ROW_MXFP8, 1>, write_kernel<DSA_ROW_MXFP8, 2>},
-      {write_kernel<DSA_ROW_LATENT_FP8, 0>, write_kernel<DSA_ROW_LATENT_FP8, 1>, write_kernel<DSA_ROW_LATENT_FP8, 2>}};
-  static const Kernel kRead[4][3] = {
-      {read_kernel<DSA_ROW_BF16, 0>, read_kernel<DSA_ROW_BF16, 1>, read_kernel<DSA_ROW_BF16, 2>},
-      {read_kernel<DSA_ROW_FP8, 0>, read_kernel<DSA_ROW_FP8, 1>, read_kernel<DSA_ROW_FP8, 2>},
-      {read_kernel<DSA_ROW_MXFP8, 0>, read_kernel<DSA_ROW_MXFP8, 1>, read_kernel<DSA_ROW_MXFP8, 2>},
-      {read_kernel<DSA_ROW_LATENT_FP8, 0>, read_kernel<DSA_ROW_LATENT_FP8, 1>, read_kernel<DSA_ROW_LATENT_FP8, 2>}};
-  const Kernel k = write ? kWrite[a.format - 1][a.elem] : kRead[a.format][a.elem];
+  const auto k = many ? Kernels<kUnits>::get(write, a.format, a.elem) : Kernels<1>::get(write, a.format, a.elem);
   k<<<(unsigned)blocks, kThreads, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, write ? "cache_write_quant: launch" : "cache_read: launch", err);
