@@ -416,6 +416,8 @@ static dsa_status cache_rows(const dsa_cache_rows_args* a, bool write, dsa_strea
   if (a->row_stride < a->dim) return fail(DSA_ERR_INVALID_ARG, name + ": row_stride below dim");
   if (a->row_stride % (a->elem == DSA_ELEM_FP32 ? 4 : 8))
     return fail(DSA_ERR_UNSUPPORTED, name + ": rows must start 16-byte aligned");
+  if (a->row_stride > 0x7fffffffLL || (long long)a->num_pages * a->page_size > 0x7fffffffLL)
+    return fail(DSA_ERR_UNSUPPORTED, name + ": row_stride and the cache's rows must be below 2^31");
   if (a->n_rows == 0) return DSA_OK;
   if (!a->rows || !a->pool || !a->page_table || !a->seq || !a->pos)
     return fail(DSA_ERR_INVALID_ARG, name + ": null device pointer");

@@ -33,7 +33,9 @@ constexpr int kLatentRow = 608;   // 576 codes, 5 fp32 scales, 12 zero bytes
 
 struct Params {
   int n_rows, dim, B, page_size, max_pages, num_pages;
-  long long row_stride;  // elements
+  int row_stride;        // elements
+  uint32_t page_mul;     // j / page_size = j * page_mul >> page_shift for 0 <= j < 2^31
+  int page_shift;
   long long units;
   uint8_t* rows;
   uint8_t* pool;
@@ -74,7 +76,7 @@ DSA_DEV Place place(const Params& p, long long u, int lane) {
 // Physical cache rows of N rows (-1: none, or out of range, which is reported), the loads of all of
 // them in flight together.
 template <int N>
-DSA_DEV void cache_rows(const Params& p, const Place* w, long long* at) {
+DSA_DEV void cache_rows(const Params& p, const Place* w, int* at) {
   int b[N], j[N], slot[N], pg[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -83,14 +85,14 @@ DSA_DEV void cache_rows(const Params& p, const Place* w, long long* at) {
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    slot[i] = j[i] / p.page_size;
+    slot[i] = (int)(((unsigned long long)(uint32_t)j[i] * p.page_mul) >> p.page_shift);
     const bool ok = w[i].row >= 0 && b[i] >= 0 && b[i] < p.B && j[i] >= 0 && slot[i] < p.max_pages;
     pg[i] = ok ? p.page_table[(long long)b[i] * p.max_pages + slot[i]] : -1;
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const bool ok = pg[i] >= 0 && pg[i] < p.num_pages;
-    at[i] = ok ? (long long)pg[i] * p.page_size + (j[i] - slot[i] * p.page_size) : -1;
+    at[i] = ok ? pg[i] * p.page_size + (j[i] - slot[i] * p.page_size) : -1;
     if (!ok && w[i].row >= 0) report(p.status, kStatusDeviceCheck);
   }
 }
@@ -150,18 +152,22 @@ DSA_DEV float e4m3_value(uint32_t code) {
   return __half2float(*reinterpret_cast<const __half*>(&h));
 }
 
-// The code of x / s between its neighbours `lo` (toward zero) and `hi`, which differ by one.
-__device__ __noinline__ uint32_t settle(float x, float s, uint32_t lo, uint32_t hi) {
-  const float border = 0.5f * (fabsf(e4m3_value(lo & 0x7f)) + fabsf(e4m3_value(hi & 0x7f)));
-  const double d = fabs((double)x) - (double)border * (double)s;  // the product has at most 29 bits
-  if (d > 0.0) return hi;
-  if (d < 0.0) return lo;
-  return (hi & 1u) ? lo : hi;
+// The code of x / s between its neighbours `lo` (toward zero) and `hi`, which differ by one: by the sign
+// of |x| - border s, which one fused rounding keeps unless the scale is so small that it underflows.
+// (16-bit rows meet exact borders often, about one element in 2^10.)
+DSA_DEV uint32_t settle(float x, float s, uint32_t lo, uint32_t hi) {
+  const float border = 0.5f * (e4m3_value(lo & 0x7f) + e4m3_value(hi & 0x7f));
+  float d = fmaf(-border, s, fabsf(x));
+  if (s < 0x1p-100f) d = fmaf(-border, s * 0x1p60f, fabsf(x) * 0x1p60f);  // both products exact
+  const uint32_t even = (hi & 1u) ? lo : hi;
+  return d > 0.f ? hi : d < 0.f ? lo : even;
 }
 
 // Eight columns with scale s -> eight codes.
 DSA_DEV uint2 quantise8(const float* x, float s) {
-  const float inv = __frcp_rn(s), down = inv * (1.f - 0x1p-21f), up = inv * (1.f + 0x1p-21f);
+  float inv;   // within 2^-23; with the two roundings that follow, well inside 2^-21
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  const float down = inv * (1.f - 0x1p-21f), up = inv * (1.f + 0x1p-21f);
   uint32_t lo[4], hi[4], differ = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -181,7 +187,8 @@ DSA_DEV uint2 quantise8(const float* x, float s) {
 
 // Eight columns x of a row to cache row dst (< 0: nowhere).  The whole warp takes part.
 template <int F>
-DSA_DEV void write8(const Params& p, const Place& w, long long dst, const float* x, int lane) {
+DSA_DEV void write8(const Params& p, const Place& w, int row, const float* x, int lane) {
+  const long long dst = row;
   // the group's largest finite magnitude: a NaN (which every maximum loses) or an infinity does not
   // cost its neighbours
   float a = 0.f;
@@ -192,9 +199,11 @@ DSA_DEV void write8(const Params& p, const Place& w, long long dst, const float*
 #pragma unroll
     for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
   }
-  const int lanes = F == DSA_ROW_MXFP8 ? 4 : F == DSA_ROW_FP8 ? p.dim >> 3 : w.col >= 512 ? 8 : 16;
+  constexpr int kMost = F == DSA_ROW_MXFP8 ? 4 : F == DSA_ROW_FP8 ? 32 : 16;   // lanes of a group
+  const int lanes = F == DSA_ROW_FP8 ? p.dim >> 3 : F == DSA_ROW_LATENT_FP8 && w.col >= 512 ? 8 : kMost;
 #pragma unroll
-  for (int o = 1; o < (F == DSA_ROW_MXFP8 ? 4 : F == DSA_ROW_FP8 ? 32 : 16); o <<= 1) {
+  for (int o = 1; o < kMost; o <<= 1) {
+    if (F == DSA_ROW_FP8 && o >= lanes) break;   // (the same for the whole warp)
     const float m = __shfl_xor_sync(0xffffffffu, a, o);
     if (o < lanes) a = fmaxf(a, m);
   }
@@ -229,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
   const int lane = threadIdx.x & 31;
   Place w[N];
   float x[N][8];
-  long long dst[N];
+  int dst[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     w[n] = place<F>(p, u + n, lane);
@@ -253,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
   const long long u = ((long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * N;
   const int lane = threadIdx.x & 31;
   Place w[N];
-  long long src[N];
+  int src[N];
   Packed v[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) w[n] = place<F>(p, u + n, lane);
@@ -264,9 +273,9 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
     v[n].scale = 0.f;
     if (src[n] < 0) continue;
     if constexpr (F == DSA_ROW_BF16) {
-      v[n].bits = __ldcs(reinterpret_cast<const uint4*>(p.pool + (src[n] * p.dim + w[n].col) * 2));
+      v[n].bits = __ldcs(reinterpret_cast<const uint4*>(p.pool + ((long long)src[n] * p.dim + w[n].col) * 2));
     } else {
-      const uint8_t* row = p.pool + src[n] * (F == DSA_ROW_LATENT_FP8 ? kLatentRow : p.dim);
+      const uint8_t* row = p.pool + (long long)src[n] * (F == DSA_ROW_LATENT_FP8 ? kLatentRow : p.dim);
       const uint2 c = __ldcs(reinterpret_cast<const uint2*>(row + w[n].col));
       v[n].bits.x = c.x;
       v[n].bits.y = c.y;
@@ -275,7 +284,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
       } else if constexpr (F == DSA_ROW_FP8) {
         v[n].scale = p.scale_pool[src[n]];
       } else {
-        const uint32_t e = p.sf_pool[src[n] * (p.dim >> 5) + (w[n].col >> 5)];
+        const uint32_t e = p.sf_pool[(long long)src[n] * (p.dim >> 5) + (w[n].col >> 5)];
         v[n].scale = e == 255u ? __uint_as_float(0x7fffffffu)      // not a valid scale: NaN
                                : e == 0u ? 0x1p-127f : __uint_as_float(e << 23);
       }
@@ -334,7 +343,11 @@ dsa_status launch_cache_rows(const dsa_cache_rows_args& a, bool write, cudaStrea
   p.page_size = a.page_size;
   p.max_pages = a.max_pages;
   p.num_pages = a.num_pages;
-  p.row_stride = a.row_stride;
+  p.row_stride = (int)a.row_stride;
+  int shift = 0;   // 2^shift >= page_size
+  while ((1LL << shift) < a.page_size) ++shift;
+  p.page_shift = 31 + shift;
+  p.page_mul = (uint32_t)((((unsigned long long)1 << p.page_shift) + a.page_size - 1) / a.page_size);
   p.rows = reinterpret_cast<uint8_t*>(a.rows);
   p.pool = reinterpret_cast<uint8_t*>(a.pool);
   p.scale_pool = a.scale_pool;
