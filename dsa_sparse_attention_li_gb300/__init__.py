@@ -494,7 +494,6 @@ def cache_read(pool, page_table, seq, pos, *, out=None, dtype=torch.bfloat16, sc
 def mla_decode_workspace_bytes(n_q: int, H: int, max_q_per_seq: int) -> int:
     """Scratch bytes dsa_mla_decode needs for a batch of this shape (any batch and lengths)."""
     a = MlaDecodeArgs()
-    a.B = a.max_pages = a.num_pages = 1
     a.n_q, a.H, a.max_q_per_seq = int(n_q), int(H), int(max_q_per_seq)
     return int(load().dsa_mla_decode_workspace_bytes(ctypes.byref(a)))
 

@@ -241,13 +241,15 @@ dsa_status dsa_sfa_prefill(const dsa_sfa_args* a, dsa_stream_t stream) {
   return sfa_common(a, true, stream);
 }
 
-static dsa_status mla_decode_check(const dsa_mla_decode_args* a, bool pointers) {
+// A softmax scale and its product with log2(e) are positive and finite.
+static bool scale_ok(float s) { return s > 0.f && s <= 2.0e38f; }
+
+static dsa_status mla_decode_check(const dsa_mla_decode_args* a) {
   if (!a) return fail(DSA_ERR_INVALID_ARG, "mla_decode: args is NULL");
   if (a->B <= 0 || a->n_q < 0 || a->H <= 0 || a->max_pages <= 0 || a->num_pages <= 0 || a->max_q_per_seq <= 0)
     return fail(DSA_ERR_INVALID_ARG, "mla_decode: non-positive size");
   if (a->H > 128) return fail(DSA_ERR_UNSUPPORTED, "mla_decode: H > 128");
-  if (!pointers) return DSA_OK;  // sizes only (workspace query)
-  if (!(a->softmax_scale > 0.f) || a->softmax_scale > 3.0e38f)
+  if (!scale_ok(a->softmax_scale))
     return fail(DSA_ERR_INVALID_ARG, "mla_decode: softmax_scale must be positive and finite");
   if (a->d_qk != 576 || a->d_v != 512) return fail(DSA_ERR_UNSUPPORTED, "mla_decode: d_qk must be 576 and d_v 512");
   if (a->page_size != 64) return fail(DSA_ERR_UNSUPPORTED, "mla_decode: page_size must be 64");
@@ -271,13 +273,13 @@ static dsa_status mla_decode_check(const dsa_mla_decode_args* a, bool pointers) 
 }
 
 size_t dsa_mla_decode_workspace_bytes(const dsa_mla_decode_args* a) {
-  if (mla_decode_check(a, false) != DSA_OK || a->n_q == 0) return 0;
+  if (!a || a->n_q <= 0 || a->H <= 0 || a->H > 128 || a->max_q_per_seq <= 0) return 0;
   return dsa::mla_decode_workspace_bytes(*a);
 }
 
 dsa_status dsa_mla_decode(const dsa_mla_decode_args* a, dsa_stream_t stream) {
   g_last_error.clear();
-  const dsa_status c = mla_decode_check(a, true);
+  const dsa_status c = mla_decode_check(a);
   if (c != DSA_OK || a->n_q == 0) return c;
   std::string err;
   const dsa_status s = dsa::launch_mla_decode(*a, reinterpret_cast<cudaStream_t>(stream), err);
@@ -290,7 +292,7 @@ dsa_status dsa_mla_prefill(const dsa_mla_prefill_args* a, dsa_stream_t stream) {
   if (!a) return fail(DSA_ERR_INVALID_ARG, "mla_prefill: args is NULL");
   if (a->B <= 0 || a->n_q < 0 || a->n_kv < 0 || a->H <= 0 || a->max_q_per_seq <= 0)
     return fail(DSA_ERR_INVALID_ARG, "mla_prefill: non-positive size");
-  if (!(a->softmax_scale > 0.f) || a->softmax_scale > 3.0e38f)
+  if (!scale_ok(a->softmax_scale))
     return fail(DSA_ERR_INVALID_ARG, "mla_prefill: softmax_scale must be positive and finite");
   if (a->d_nope != 128 || a->d_rope != 64 || a->d_v != 128)
     return fail(DSA_ERR_UNSUPPORTED, "mla_prefill: d_nope must be 128, d_rope 64 and d_v 128");

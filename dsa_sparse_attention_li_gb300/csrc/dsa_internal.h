@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <string>
 
 #include "dsa.h"
@@ -58,7 +59,8 @@ bool encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* bas
 
 #ifdef DSA_TEST_HOOKS
 // Test build only: which kernel's first CTA makes one of its waits wait on a barrier that nothing
-// arrives on (0 none, 1 li_topk, 2 sparse attention); set by dsa_test_inject_stall().
+// arrives on (0 none, 1 li_topk, 2 sparse attention,
+// 3 mla_decode, 4 mla_prefill); set by dsa_test_inject_stall().
 extern int g_test_stall;
 #endif
 
@@ -74,6 +76,16 @@ struct DeviceInfo {
   int cc_major = 0, cc_minor = 0;
 };
 bool device_info(DeviceInfo& info, std::string& err);
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device; `done` is the kernel's own
+// record of the devices where that is so already (a runtime call of 1 us otherwise).
+inline cudaError_t allow_smem(const void* kernel, int bytes, int device, std::atomic<uint64_t>& done) {
+  const uint64_t bit = device >= 0 && device < 64 ? 1ull << device : 0;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 inline dsa_status cuda_fail(cudaError_t e, const char* what, std::string& err) {
   err = std::string(what) + ": " + cudaGetErrorString(e);

@@ -69,6 +69,9 @@ struct Params {
   int4* ws_join;   // [pairs] {first token, rows, first piece's slot, pieces} of the group that a
                    // pair's first unit continues; pieces 0: none, or another pair joins it
   int ws_rows;
+#ifdef DSA_TEST_HOOKS
+  int stall;       // test build: the first pair's MMA warp waits on a barrier nothing arrives on
+#endif
 };
 
 struct Layout {
@@ -87,6 +90,9 @@ struct Ctl {
   uint64_t s_full[2], s_free[2];
   uint64_t p_full, pv_done, o_free, edge;
   uint64_t written[kKGroups + kVPages];   // FP8: a part is in shared memory (four warps)
+#ifdef DSA_TEST_HOOKS
+  uint64_t never;      // test build: no thread ever arrives here
+#endif
   uint32_t tmem_base;
   int abort;
   int start_b;
@@ -303,6 +309,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
     mbar_init(&ctl->o_free, 8);
     mbar_init(&ctl->edge, 1);
     for (int i = 0; i < kKGroups + kVPages; ++i) mbar_init(&ctl->written[i], 4);
+#ifdef DSA_TEST_HOOKS
+    mbar_init(&ctl->never, 1);
+#endif
     ctl->abort = 0;
     ctl->bad_pages = 0;
     fence_barrier_init();
@@ -647,6 +656,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
         }
         mma2_commit_both(&ctl->pv_done, me);
       };
+#ifdef DSA_TEST_HOOKS
+      if (p.stall == 3 && blockIdx.x == 0) warp_wait(&ctl->never, 0, abort, p.status);
+#endif
       // after a wait that gave up, the rest runs on whatever is there: nothing of it is kept
       uint32_t n = 0;       // tiles whose Q.K^T is issued; their P.V runs one behind
       bool behind_first = false;
@@ -1088,6 +1100,9 @@ dsa_status launch_mla_decode(const dsa_mla_decode_args& a, cudaStream_t stream, 
   p.lse = a.lse;
   p.status = a.status;
   p.ws_rows = p.T * p.H;
+#ifdef DSA_TEST_HOOKS
+  p.stall = g_test_stall;
+#endif
   const size_t pieces = (size_t)p.pairs * 2;
   uint8_t* ws = reinterpret_cast<uint8_t*>(a.workspace);
   p.ws_o = reinterpret_cast<float*>(ws);
@@ -1105,7 +1120,10 @@ dsa_status launch_mla_decode(const dsa_mla_decode_args& a, cudaStream_t stream, 
     return DSA_ERR_CUDA;
   const int smem = Layout::total + 1024;
   auto kern = kv8 ? mla_decode_kernel<true> : mla_decode_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  DeviceInfo dev;
+  if (!device_info(dev, err)) return DSA_ERR_CUDA;
+  static std::atomic<uint64_t> done[2];
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, dev.device, done[kv8]);
   if (e != cudaSuccess) return cuda_fail(e, "mla_decode: set shared memory size", err);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

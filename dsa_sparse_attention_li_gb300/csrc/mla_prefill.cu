@@ -48,6 +48,9 @@ struct Params {
   __nv_bfloat16* out;
   float* lse;
   int* status;
+#ifdef DSA_TEST_HOOKS
+  int stall;       // test build: the first CTA's MMA warp waits on a barrier nothing arrives on
+#endif
 };
 
 struct Layout {
@@ -73,6 +76,9 @@ struct Ctl {
   uint64_t item_full[2], item_empty[2], answer_full;
   alignas(16) uint8_t answer[16];
   Item item[2];
+#ifdef DSA_TEST_HOOKS
+  uint64_t never;      // test build: no thread ever arrives here
+#endif
   uint32_t tmem_base;
   int abort;
   uint32_t any_bad[2][2];    // t + 1 if a half of edge tile t (of all the CTA's tiles) has value rows
@@ -213,6 +219,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->edge[i][0], 1);
       mbar_init(&ctl->edge[i][1], 1);
     }
+#ifdef DSA_TEST_HOOKS
+    mbar_init(&ctl->never, 1);
+#endif
     ctl->abort = 0;
     for (int i = 0; i < 4; ++i) ctl->any_bad[i >> 1][i & 1] = 0u;
     fence_barrier_init();
@@ -412,6 +421,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mma_commit_by(&ctl->pv_done[x], me);
     };
+#ifdef DSA_TEST_HOOKS
+    if (p.stall == 4 && blockIdx.x == 0) warp_wait(&ctl->never, 0, abort, p.status);
+#endif
     // (a row tile's first products of an item may overwrite S, whose weights the last P.V has read by
     // then, and O, which its softmax warps have read before they hand over new weights)
     for (uint32_t item = 0;; ++item) {
@@ -595,6 +607,9 @@ dsa_status launch_mla_prefill(const dsa_mla_prefill_args& a, cudaStream_t stream
     return DSA_ERR_UNSUPPORTED;
   }
   p.blocks = (int)blocks;
+#ifdef DSA_TEST_HOOKS
+  p.stall = g_test_stall;
+#endif
   // without any keys nothing is seen: any valid memory stands in for them
   const bool none = a.n_kv == 0;
   const uint64_t H = (uint64_t)a.H, keys = none ? 1 : (uint64_t)a.n_kv;
@@ -612,7 +627,10 @@ dsa_status launch_mla_prefill(const dsa_mla_prefill_args& a, cudaStream_t stream
       !encode_tmap_2d(&tm_r, bf, rope, 64, keys, none ? 128 : (uint64_t)a.k_rope_stride * 2, 64, 128, sw, err))
     return DSA_ERR_CUDA;
   const int smem = Layout::total + 1024;
-  cudaError_t e = cudaFuncSetAttribute(mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  DeviceInfo dev;
+  if (!device_info(dev, err)) return DSA_ERR_CUDA;
+  static std::atomic<uint64_t> done;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(mla_prefill_kernel), smem, dev.device, done);
   if (e != cudaSuccess) return cuda_fail(e, "mla_prefill: set shared memory size", err);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -6,10 +6,10 @@
  *
  * In the test build every bounded device-side wait gives up after 20 ms (1 s in the product).
  *
- * dsa_test_inject_stall(kernel): from the next launch on, the single MMA-issuing thread of the
- * first CTA of the chosen kernel (1: the indexer, dsa_li_topk; 2: sparse attention,
- * dsa_sfa_decode / dsa_sfa_prefill; 0: none) first waits on an mbarrier that no thread ever
- * arrives on.  That wait runs out, the CTA raises its abort flag, the kernel stores
+ * dsa_test_inject_stall(kernel): from the next launch on, the MMA-issuing thread (or its warp) of
+ * the first CTA of the chosen kernel (1: the indexer, dsa_li_topk; 2: sparse attention,
+ * dsa_sfa_decode / dsa_sfa_prefill; 3: dsa_mla_decode; 4: dsa_mla_prefill; 0: none) first waits on
+ * an mbarrier that no thread ever arrives on.  That wait runs out, the CTA raises its abort flag, the kernel stores
  * DSA_ERR_TIMEOUT into *status, the other roles of the CTA (and of its cluster) leave their
  * loops through their own bounded waits, every issued copy is drained, tensor memory is
  * freed, and the launch completes: the next call on the same context works.  The output of the

@@ -232,6 +232,41 @@ def test_decode_hidden_rows_may_hold_anything(cuda_lib, fp8):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_decode_on_two_streams_with_tokens_of_no_sequence(cuda_lib, fp8):
+    """Two calls at once, each with its workspace; the first sequence starts behind four query rows
+    that no sequence owns; both sequences share their first pages."""
+    cases = []
+    for seed in (1, 2):
+        c = make_decode([1500, 4000], [1, 2], 32, fp8, seed=seed, tail=0)
+        c["pt"][1, :8] = c["pt"][0, :8]
+        c["rows"][1] = torch.cat([c["rows"][0][:512], c["rows"][1][512:]])
+        lead = torch.full((4, 32, 576), math.nan, dtype=torch.bfloat16, device="cuda")
+        c["q"] = torch.cat([lead, c["q"]])
+        c["q_start"] += 4
+        cases.append(c)
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = []
+    torch.cuda.synchronize()
+    for c, s in zip(cases, streams):
+        out = torch.full((7, 32, 512), 5.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((7, 32), 6.0, device="cuda")
+        outs.append((out, lse))
+        for t in outs[-1]:
+            t.record_stream(s)
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            for _ in range(3):
+                dsa.mla_decode(c["q"], c["pool"], c["pt"], c["seq_lens"], c["q_start"], softmax_scale=SCALE,
+                               max_q_per_seq=2, out=out, lse=lse)
+    torch.cuda.synchronize()
+    for c, (out, lse) in zip(cases, outs):
+        assert torch.all(out[:4] == 5.0) and torch.all(lse[:4] == 6.0)
+        c["q"] = c["q"][4:]
+        verify_decode(c, out[4:], lse[4:])
+
+
+@pytest.mark.gpu
 def test_decode_reports_what_is_out_of_range(cuda_lib):
     c = make_decode([400, 200], [1, 1], 16, False, extra=0, tail=0)
     c["pt"][0, 2] = 10 ** 6
@@ -389,6 +424,58 @@ def test_prefill_reports_what_is_out_of_range(cuda_lib):
 
 
 @pytest.mark.gpu
+def test_prefill_many_sequences(cuda_lib):
+    """More sequences than a warp has lanes, empty ones among them, and tokens of no sequence."""
+    g = torch.Generator().manual_seed(4)
+    new = torch.randint(0, 300, (77,), generator=g).tolist()
+    new[::5] = [0] * len(new[::5])
+    keys = [n + k for n, k in zip(new, torch.randint(0, 200, (77,), generator=g).tolist())]
+    c = make_prefill(new, keys, 2, seed=77)
+    out, lse, status = run_prefill(c)
+    assert status == 0
+    verify_prefill(c, out, lse)
+    # without the first three sequences: their tokens are no one's
+    c["q_start"], c["kv_start"] = c["q_start"][3:].contiguous(), c["kv_start"][3:].contiguous()
+    rest, lse2, status = run_prefill(c)
+    n = sum(new[:3])
+    assert status == 0 and torch.all(rest[:n] == 5.0) and torch.equal(rest[n:], out[n:]) and torch.equal(lse2[n:], lse[n:])
+
+
+@pytest.mark.gpu
+def test_prefill_without_any_key(cuda_lib):
+    q = torch.randn((5, 3, 192), device="cuda").bfloat16()
+    kv = torch.empty((0, 3, 256), dtype=torch.bfloat16, device="cuda")
+    rope = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 2, 5], dtype=torch.int32, device="cuda")
+    out, lse = dsa.mla_prefill(q, kv, rope, at, torch.zeros_like(at), softmax_scale=SCALE, max_q_per_seq=3)
+    assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+
+
+@pytest.mark.gpu
+def test_prefill_captures_and_replays_with_other_lengths(cuda_lib):
+    c = make_prefill([300, 500, 40], [300, 700, 41], 20, tail=0)
+    first = run_prefill(c)
+    out, lse = torch.full_like(first[0], 5.0), torch.full_like(first[1], 6.0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        for _ in range(2):
+            dsa.mla_prefill(c["q"], c["kv"], c["rope"], c["q_start"], c["kv_start"], softmax_scale=SCALE,
+                            max_q_per_seq=840, out=out, lse=lse)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    # the ranges are read on the device
+    c["new"], c["keys"] = [100, 640, 100], [150, 800, 91]
+    for key, x in (("q_start", c["new"]), ("kv_start", c["keys"])):
+        c[key].copy_(torch.tensor([0] + list(torch.tensor(x).cumsum(0)), dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    verify_prefill(c, out, lse)
+
+
+@pytest.mark.gpu
 def test_prefill_offsets_beyond_32_bits(cuda_lib):
     """Keys and values, and query rows, past 2^31 elements of their arrays."""
     H, n = 128, 70000
@@ -479,6 +566,7 @@ def _decode_args(**over):
     ({"B": 0}, dsa.DSA_ERR_INVALID_ARG), ({"n_q": -1}, dsa.DSA_ERR_INVALID_ARG), ({"H": 0}, dsa.DSA_ERR_INVALID_ARG),
     ({"max_q_per_seq": 0}, dsa.DSA_ERR_INVALID_ARG), ({"softmax_scale": 0.0}, dsa.DSA_ERR_INVALID_ARG),
     ({"softmax_scale": float("nan")}, dsa.DSA_ERR_INVALID_ARG), ({"softmax_scale": float("inf")}, dsa.DSA_ERR_INVALID_ARG),
+    ({"softmax_scale": 3.0e38}, dsa.DSA_ERR_INVALID_ARG), ({"out": 4112}, dsa.DSA_ERR_INVALID_ARG),
     ({"H": 129}, dsa.DSA_ERR_UNSUPPORTED), ({"d_qk": 512}, dsa.DSA_ERR_UNSUPPORTED), ({"d_v": 576}, dsa.DSA_ERR_UNSUPPORTED),
     ({"page_size": 32}, dsa.DSA_ERR_UNSUPPORTED), ({"kv_dtype": dsa.DSA_MXFP8_E4M3}, dsa.DSA_ERR_UNSUPPORTED),
     ({"num_pages": 1 << 25}, dsa.DSA_ERR_UNSUPPORTED), ({"q_start": None}, dsa.DSA_ERR_INVALID_ARG),
