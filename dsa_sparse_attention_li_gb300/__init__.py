@@ -394,7 +394,16 @@ def cache_write(pool, page_table, seq, pos, rows, *, scale_pool=None, row_scales
     _check(code, "dsa_cache_write")
 
 
-def _on(device, **tensors):
+def _addr(t: Optional[torch.Tensor]):
+    """Device address of a contiguous tensor, for a pointer field (as _ptr, without its object)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to the DSA library must be contiguous")
+    return t.data_ptr()
+
+
+def _on(device, *tensors):
     """Every tensor given lives on `device`, the current CUDA device.  The library's launches go to
     the current device, so a tensor of another one would be read across, or not at all."""
     if device.type != "cuda":
@@ -403,9 +412,9 @@ def _on(device, **tensors):
     if index != torch.cuda.current_device():
         raise ValueError("tensors are on %s, the current device is cuda:%d"
                          % (device, torch.cuda.current_device()))
-    for name, t in tensors.items():
+    for t in tensors:
         if t is not None and t.get_device() != index:
-            raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+            raise ValueError("a tensor is on %s, the others are on %s" % (t.device, device))
 
 
 def _typed(name, t, dtype, shape=None):
@@ -456,8 +465,8 @@ def cache_rows_args(pool, page_table, seq, pos, rows, *, scale_pool=None, sf_poo
     a.n_rows, a.dim, a.B, a.page_size = n, dim, page_table.shape[0], page_size
     a.max_pages, a.num_pages, a.format, a.elem = page_table.shape[1], num_pages, fmt, _ELEM[rows.dtype]
     a.row_stride = rows.stride(0) if n > 1 else dim
-    a.rows, a.pool, a.scale_pool, a.sf_pool = rows.data_ptr(), _ptr(pool), _ptr(scale_pool), _ptr(sf_pool)
-    a.page_table, a.seq, a.pos, a.status = _ptr(page_table), _ptr(seq), _ptr(pos), _ptr(status)
+    a.rows, a.pool, a.scale_pool, a.sf_pool = rows.data_ptr(), _addr(pool), _addr(scale_pool), _addr(sf_pool)
+    a.page_table, a.seq, a.pos, a.status = _addr(page_table), _addr(seq), _addr(pos), _addr(status)
     return a
 
 
@@ -469,8 +478,7 @@ def cache_write_quant(pool, page_table, seq, pos, rows, *, scale_pool=None, sf_p
     lib = load()
     a = cache_rows_args(pool, page_table, seq, pos, rows, scale_pool=scale_pool, sf_pool=sf_pool,
                         status=status)
-    _on(pool.device, page_table=page_table, seq=seq, pos=pos, rows=rows, scale_pool=scale_pool,
-        sf_pool=sf_pool, status=status)
+    _on(pool.device, page_table, seq, pos, rows, scale_pool, sf_pool, status)
     _check(lib.dsa_cache_write_quant(ctypes.byref(a), _stream(stream)), "dsa_cache_write_quant")
 
 
@@ -485,8 +493,7 @@ def cache_read(pool, page_table, seq, pos, *, out=None, dtype=torch.bfloat16, sc
                           dtype=dtype, device=pool.device)
     a = cache_rows_args(pool, page_table, seq, pos, out, scale_pool=scale_pool, sf_pool=sf_pool,
                         status=status)
-    _on(pool.device, page_table=page_table, seq=seq, pos=pos, out=out, scale_pool=scale_pool,
-        sf_pool=sf_pool, status=status)
+    _on(pool.device, page_table, seq, pos, out, scale_pool, sf_pool, status)
     _check(lib.dsa_cache_read(ctypes.byref(a), _stream(stream)), "dsa_cache_read")
     return out
 
@@ -535,8 +542,7 @@ def mla_decode(q, kv_pool, page_table, seq_lens, q_start, *, softmax_scale, max_
     _typed("status", status, torch.int32)
     max_q_per_seq = _host_max_q(q_start, max_q_per_seq, n_q)
     device = q.device
-    _on(device, kv_pool=kv_pool, page_table=page_table, seq_lens=seq_lens, q_start=q_start, out=out,
-        lse=lse, status=status, workspace=workspace)
+    _on(device, kv_pool, page_table, seq_lens, q_start, out, lse, status, workspace)
     if out is None:
         out = torch.empty((n_q, H, 512), dtype=torch.bfloat16, device=device)
     if lse is None:
@@ -550,11 +556,11 @@ def mla_decode(q, kv_pool, page_table, seq_lens, q_start, *, softmax_scale, max_
         nbytes = lib.dsa_mla_decode_workspace_bytes(ctypes.byref(a))
         if nbytes:
             workspace = torch.empty((nbytes,), dtype=torch.uint8, device=device)
-    a.q, a.kv_pool, a.page_table = _ptr(q), _ptr(kv_pool), _ptr(page_table)
-    a.seq_lens, a.q_start, a.out, a.lse, a.status = (_ptr(seq_lens), _ptr(q_start), _ptr(out), _ptr(lse),
-                                                     _ptr(status))
+    a.q, a.kv_pool, a.page_table = _addr(q), _addr(kv_pool), _addr(page_table)
+    a.seq_lens, a.q_start, a.out, a.lse, a.status = (_addr(seq_lens), _addr(q_start), _addr(out), _addr(lse),
+                                                     _addr(status))
     if workspace is not None:
-        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+        a.workspace, a.workspace_bytes = _addr(workspace), workspace.numel() * workspace.element_size()
     _check(lib.dsa_mla_decode(ctypes.byref(a), _stream(stream)), "dsa_mla_decode")
     return out, lse
 
@@ -583,7 +589,7 @@ def mla_prefill(q, kv, k_rope, q_start, kv_start, *, softmax_scale, max_q_per_se
         raise ValueError("the columns of k_rope must be adjacent, and its rows apart")
     max_q_per_seq = _host_max_q(q_start, max_q_per_seq, n_q)
     device = q.device
-    _on(device, kv=kv, k_rope=k_rope, q_start=q_start, kv_start=kv_start, out=out, lse=lse, status=status)
+    _on(device, kv, k_rope, q_start, kv_start, out, lse, status)
     if out is None:
         out = torch.empty((n_q, H, 128), dtype=torch.bfloat16, device=device)
     if lse is None:
@@ -592,9 +598,9 @@ def mla_prefill(q, kv, k_rope, q_start, kv_start, *, softmax_scale, max_q_per_se
     a.B, a.n_q, a.n_kv, a.H, a.d_nope, a.d_rope, a.d_v = B, n_q, n_kv, H, 128, 64, 128
     a.max_q_per_seq, a.softmax_scale = max_q_per_seq, float(softmax_scale)
     a.k_rope_stride = k_rope.stride(0) if n_kv > 1 else 64
-    a.q, a.kv, a.k_rope = _ptr(q), _ptr(kv), k_rope.data_ptr()
-    a.q_start, a.kv_start, a.out, a.lse, a.status = (_ptr(q_start), _ptr(kv_start), _ptr(out), _ptr(lse),
-                                                     _ptr(status))
+    a.q, a.kv, a.k_rope = _addr(q), _addr(kv), k_rope.data_ptr()
+    a.q_start, a.kv_start, a.out, a.lse, a.status = (_addr(q_start), _addr(kv_start), _addr(out), _addr(lse),
+                                                     _addr(status))
     _check(lib.dsa_mla_prefill(ctypes.byref(a), _stream(stream)), "dsa_mla_prefill")
     return out, lse
 
