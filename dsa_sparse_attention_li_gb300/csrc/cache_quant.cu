@@ -27,7 +27,8 @@ namespace dsa {
 namespace cq {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 4;         // units of a warp, with many rows
+// units of a warp, with many rows
+constexpr int kWriteUnits = 2, kReadUnits = 4;
 constexpr int kLatent = 576;
 constexpr int kLatentRow = 608;   // 576 codes, 5 fp32 scales, 12 zero bytes
 
@@ -47,13 +48,33 @@ struct Params {
   int* status;
 };
 
-// The row and the first column of a lane's eight columns in unit u; row < 0: none.
+// The row and the first column of a lane's columns in unit u; row < 0: none.  A read takes eight of them, a
+// write these eight and the eight that follow `step` columns on, both of one group.
 struct Place {
-  int row, col;
+  int row, col, step;
 };
 
 template <int F>
-DSA_DEV Place place(const Params& p, long long u, int lane) {
+DSA_DEV Place place_write(const Params& p, long long u, int lane) {
+  long long row;
+  int col, step;
+  if constexpr (F == DSA_ROW_LATENT_FP8) {
+    const long long blk = u / 9;            // eight rows are nine units
+    const int k = (int)(u - blk * 9);
+    row = blk * 8 + (k < 8 ? k : lane >> 2);
+    col = k < 8 ? (lane >> 3) * 128 + (lane & 7) * 8 : 512 + (lane & 3) * 8;
+    step = k < 8 ? 64 : 32;
+  } else {                                  // 2, 4, 8 or 16 lanes a row
+    const int per = p.dim >> 4, l = lane & (per - 1);
+    row = u * (32 / per) + lane / per;
+    col = F == DSA_ROW_MXFP8 ? (l >> 1) * 32 + (l & 1) * 8 : l * 8;
+    step = F == DSA_ROW_MXFP8 ? 16 : p.dim >> 1;
+  }
+  return {row < p.n_rows ? (int)row : -1, col, step};
+}
+
+template <int F>
+DSA_DEV Place place_read(const Params& p, long long u, int lane) {
   const int per = p.dim >> 3;               // lanes of a row
   long long row;
   int col;
@@ -70,7 +91,7 @@ DSA_DEV Place place(const Params& p, long long u, int lane) {
     row = u * (32 / per) + lane / per;
     col = (lane & (per - 1)) * 8;
   }
-  return {row < p.n_rows ? (int)row : -1, col};
+  return {row < p.n_rows ? (int)row : -1, col, 0};
 }
 
 // Physical cache rows of N rows (-1: none, or out of range, which is reported), the loads of all of
@@ -143,6 +164,13 @@ DSA_DEV void store8(uint8_t* base, long long at, const float* y) {
   }
 }
 
+DSA_DEV float2 mul2(float a, float b, float s) {
+  float2 d;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mul.rn.f32x2 x, x, y;\n"
+      " mov.b64 {%0, %1}, x;\n}\n" : "=f"(d.x), "=f"(d.y) : "f"(a), "f"(b), "f"(s));
+  return d;
+}
+
 DSA_DEV uint32_t e4m3x2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
@@ -163,21 +191,21 @@ DSA_DEV uint32_t settle(float x, float s, uint32_t lo, uint32_t hi) {
   return d > 0.f ? hi : d < 0.f ? lo : even;
 }
 
-// Eight columns with scale s -> eight codes.
-DSA_DEV uint2 quantise8(const float* x, float s) {
-  float inv;   // within 2^-23; with the two roundings that follow, well inside 2^-21
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+// Eight columns with scale s, and inv about 1 / s -> eight codes.
+DSA_DEV uint2 quantise8(const float* x, float s, float inv) {
   const float down = inv * (1.f - 0x1p-21f), up = inv * (1.f + 0x1p-21f);
   uint32_t lo[4], hi[4], differ = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    lo[i] = e4m3x2(x[2 * i] * down, x[2 * i + 1] * down);
-    hi[i] = e4m3x2(x[2 * i] * up, x[2 * i + 1] * up);
+    const float2 l = mul2(x[2 * i], x[2 * i + 1], down), h = mul2(x[2 * i], x[2 * i + 1], up);
+    lo[i] = e4m3x2(l.x, l.y);
+    hi[i] = e4m3x2(h.x, h.y);
     differ |= lo[i] ^ hi[i];
   }
   if (differ) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      if (lo[i] == hi[i]) continue;
       const uint32_t l0 = lo[i] & 0xff, h0 = hi[i] & 0xff, l1 = lo[i] >> 8, h1 = hi[i] >> 8;
       lo[i] = (l0 == h0 ? l0 : settle(x[2 * i], s, l0, h0)) | ((l1 == h1 ? l1 : settle(x[2 * i + 1], s, l1, h1)) << 8);
     }
@@ -185,22 +213,22 @@ DSA_DEV uint2 quantise8(const float* x, float s) {
   return make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
 }
 
-// Eight columns x of a row to cache row dst (< 0: nowhere).  The whole warp takes part.
+// A lane's sixteen columns x of a row to cache row dst (< 0: nowhere).  The whole warp takes part.
 template <int F>
-DSA_DEV void write8(const Params& p, const Place& w, int row, const float* x, int lane) {
+DSA_DEV void write16(const Params& p, const Place& w, int row, const float* x) {
   const long long dst = row;
   // the group's largest finite magnitude: a NaN (which every maximum loses) or an infinity does not
   // cost its neighbours
   float a = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) a = max3(a, fabsf(x[i]), fabsf(x[i + 1]));
+  for (int i = 0; i < 16; i += 2) a = max3(a, fabsf(x[i]), fabsf(x[i + 1]));
   if (a == INFINITY) {
     a = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
+    for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
   }
-  constexpr int kMost = F == DSA_ROW_MXFP8 ? 4 : F == DSA_ROW_FP8 ? 32 : 16;   // lanes of a group
-  const int lanes = F == DSA_ROW_FP8 ? p.dim >> 3 : F == DSA_ROW_LATENT_FP8 && w.col >= 512 ? 8 : kMost;
+  constexpr int kMost = F == DSA_ROW_MXFP8 ? 2 : F == DSA_ROW_FP8 ? 16 : 8;   // lanes of a group
+  const int lanes = F == DSA_ROW_MXFP8 ? 2 : w.step >> 3;
 #pragma unroll
   for (int o = 1; o < kMost; o <<= 1) {
     if (F == DSA_ROW_FP8 && o >= lanes) break;   // (the same for the whole warp)
@@ -212,22 +240,25 @@ DSA_DEV void write8(const Params& p, const Place& w, int row, const float* x, in
     const int e = a > 0.f ? max((int)(__float_as_uint(a) >> 23) - 127 - 8, -127) : 0;
     // 2^-e with e in [-127, 119]: exact, and so is the product wherever e4m3 can tell
     const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-    uint32_t c[4];
+    uint32_t c[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
-    *reinterpret_cast<uint2*>(p.pool + dst * p.dim + w.col) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-    if ((lane & 3) == 0) p.sf_pool[dst * (p.dim >> 5) + (w.col >> 5)] = (uint8_t)(e + 127);
+    for (int i = 0; i < 8; ++i) c[i] = e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
+    uint8_t* d = p.pool + dst * p.dim + w.col;
+    *reinterpret_cast<uint2*>(d) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    *reinterpret_cast<uint2*>(d + w.step) = make_uint2(c[4] | (c[5] << 16), c[6] | (c[7] << 16));
+    if ((w.col & 31) == 0) p.sf_pool[dst * (p.dim >> 5) + (w.col >> 5)] = (uint8_t)(e + 127);
   } else {
     const float s = a > 0.f ? fmaxf(__fdiv_rn(a, 448.f), 0x1p-126f) : 1.f;
-    const uint2 c = quantise8(x, s);
+    float inv;   // within 2^-23; with the two roundings that follow, well inside 2^-21
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    uint8_t* d = p.pool + dst * (F == DSA_ROW_FP8 ? p.dim : kLatentRow);
+    *reinterpret_cast<uint2*>(d + w.col) = quantise8(x, s, inv);
+    *reinterpret_cast<uint2*>(d + w.col + w.step) = quantise8(x + 8, s, inv);
     if constexpr (F == DSA_ROW_FP8) {
-      *reinterpret_cast<uint2*>(p.pool + dst * p.dim + w.col) = c;
       if (w.col == 0) p.scale_pool[dst] = s;
     } else {
-      uint8_t* row = p.pool + dst * kLatentRow;
-      *reinterpret_cast<uint2*>(row + w.col) = c;
-      if ((w.col & 127) == 0) *reinterpret_cast<float*>(row + kLatent + (w.col >> 7) * 4) = s;
-      if (w.col >= 552) *reinterpret_cast<uint32_t*>(row + kLatent + 20 + (w.col - 552) / 2) = 0u;
+      if ((w.col & 127) == 0) *reinterpret_cast<float*>(d + kLatent + (w.col >> 7) * 4) = s;
+      if (w.col >= 520) *reinterpret_cast<uint32_t*>(d + kLatent + 20 + (w.col - 520) / 2) = 0u;
     }
   }
 }
@@ -237,18 +268,21 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
   const long long u = ((long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * N;
   const int lane = threadIdx.x & 31;
   Place w[N];
-  float x[N][8];
+  float x[N][16];
   int dst[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    w[n] = place<F>(p, u + n, lane);
+    w[n] = place_write<F>(p, u + n, lane);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[n][i] = 0.f;
-    if (w[n].row >= 0) load8<E>(p.rows, (long long)w[n].row * p.row_stride + w[n].col, x[n]);
+    for (int i = 0; i < 16; ++i) x[n][i] = 0.f;
+    if (w[n].row < 0) continue;
+    const long long at = (long long)w[n].row * p.row_stride + w[n].col;
+    load8<E>(p.rows, at, x[n]);
+    load8<E>(p.rows, at + w[n].step, x[n] + 8);
   }
   cache_rows<N>(p, w, dst);
 #pragma unroll
-  for (int n = 0; n < N; ++n) write8<F>(p, w[n], dst[n], x[n], lane);
+  for (int n = 0; n < N; ++n) write16<F>(p, w[n], dst[n], x[n]);
 }
 
 // Eight columns of a cache row as they lie there, and their scale.
@@ -265,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
   int src[N];
   Packed v[N];
 #pragma unroll
-  for (int n = 0; n < N; ++n) w[n] = place<F>(p, u + n, lane);
+  for (int n = 0; n < N; ++n) w[n] = place_read<F>(p, u + n, lane);
   cache_rows<N>(p, w, src);
 #pragma unroll
   for (int n = 0; n < N; ++n) {
@@ -312,21 +346,21 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
   }
 }
 
-template <int N>
+template <int W, int R>
 struct Kernels {
   using Kernel = void (*)(Params);
   static Kernel get(bool write, int format, int elem) {
     static const Kernel kWrite[3][3] = {
-        {write_kernel<DSA_ROW_FP8, 0, N>, write_kernel<DSA_ROW_FP8, 1, N>, write_kernel<DSA_ROW_FP8, 2, N>},
-        {write_kernel<DSA_ROW_MXFP8, 0, N>, write_kernel<DSA_ROW_MXFP8, 1, N>, write_kernel<DSA_ROW_MXFP8, 2, N>},
-        {write_kernel<DSA_ROW_LATENT_FP8, 0, N>, write_kernel<DSA_ROW_LATENT_FP8, 1, N>,
-         write_kernel<DSA_ROW_LATENT_FP8, 2, N>}};
+        {write_kernel<DSA_ROW_FP8, 0, W>, write_kernel<DSA_ROW_FP8, 1, W>, write_kernel<DSA_ROW_FP8, 2, W>},
+        {write_kernel<DSA_ROW_MXFP8, 0, W>, write_kernel<DSA_ROW_MXFP8, 1, W>, write_kernel<DSA_ROW_MXFP8, 2, W>},
+        {write_kernel<DSA_ROW_LATENT_FP8, 0, W>, write_kernel<DSA_ROW_LATENT_FP8, 1, W>,
+         write_kernel<DSA_ROW_LATENT_FP8, 2, W>}};
     static const Kernel kRead[4][3] = {
-        {read_kernel<DSA_ROW_BF16, 0, N>, read_kernel<DSA_ROW_BF16, 1, N>, read_kernel<DSA_ROW_BF16, 2, N>},
-        {read_kernel<DSA_ROW_FP8, 0, N>, read_kernel<DSA_ROW_FP8, 1, N>, read_kernel<DSA_ROW_FP8, 2, N>},
-        {read_kernel<DSA_ROW_MXFP8, 0, N>, read_kernel<DSA_ROW_MXFP8, 1, N>, read_kernel<DSA_ROW_MXFP8, 2, N>},
-        {read_kernel<DSA_ROW_LATENT_FP8, 0, N>, read_kernel<DSA_ROW_LATENT_FP8, 1, N>,
-         read_kernel<DSA_ROW_LATENT_FP8, 2, N>}};
+        {read_kernel<DSA_ROW_BF16, 0, R>, read_kernel<DSA_ROW_BF16, 1, R>, read_kernel<DSA_ROW_BF16, 2, R>},
+        {read_kernel<DSA_ROW_FP8, 0, R>, read_kernel<DSA_ROW_FP8, 1, R>, read_kernel<DSA_ROW_FP8, 2, R>},
+        {read_kernel<DSA_ROW_MXFP8, 0, R>, read_kernel<DSA_ROW_MXFP8, 1, R>, read_kernel<DSA_ROW_MXFP8, 2, R>},
+        {read_kernel<DSA_ROW_LATENT_FP8, 0, R>, read_kernel<DSA_ROW_LATENT_FP8, 1, R>,
+         read_kernel<DSA_ROW_LATENT_FP8, 2, R>}};
     return write ? kWrite[format - 1][elem] : kRead[format][elem];
   }
 };
@@ -356,18 +390,22 @@ dsa_status launch_cache_rows(const dsa_cache_rows_args& a, bool write, cudaStrea
   p.seq = a.seq;
   p.pos = a.pos;
   p.status = a.status;
-  p.units = a.format == DSA_ROW_LATENT_FP8 ? ((long long)a.n_rows + 3) / 4 * 9
-                                           : ((long long)a.n_rows * a.dim + 255) / 256;
+  // (a unit of a write is 512 columns, of a read 256)
+  const int latent_rows = write ? 8 : 4, cols = write ? 512 : 256;
+  p.units = a.format == DSA_ROW_LATENT_FP8 ? ((long long)a.n_rows + latent_rows - 1) / latent_rows * 9
+                                           : ((long long)a.n_rows * a.dim + cols - 1) / cols;
   DeviceInfo dev;
   if (!device_info(dev, err)) return DSA_ERR_CUDA;
   const bool many = p.units > (long long)dev.sm_count * 64;   // more than a wave of warps
-  const long long warps = many ? (p.units + kUnits - 1) / kUnits : p.units;
+  const int each = !many ? 1 : write ? kWriteUnits : kReadUnits;
+  const long long warps = (p.units + each - 1) / each;
   const long long blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7fffffffLL) {
     err = "cache rows: too many rows for one launch";
     return DSA_ERR_UNSUPPORTED;
   }
-  const auto k = many ? Kernels<kUnits>::get(write, a.format, a.elem) : Kernels<1>::get(write, a.format, a.elem);
+  const auto k = many ? Kernels<kWriteUnits, kReadUnits>::get(write, a.format, a.elem)
+                      : Kernels<1, 1>::get(write, a.format, a.elem);
   k<<<(unsigned)blocks, kThreads, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, write ? "cache_write_quant: launch" : "cache_read: launch", err);
