@@ -13,20 +13,29 @@
 // code on which both agree; the few others, about one element in 2^16, compare |x| with border * s in
 // 64 bits, where that product is exact.
 //
-// Both kernels move each byte once and are bound by HBM.  The unit of work of a warp is 256
-// columns, eight a lane (16- or 32-byte accesses), so a group is a segment of 4 to 32 lanes and its
-// maximum a few shuffles.  A latent row is 2.25 units: the 64-column tails of four rows share one,
-// else a third of the lanes would idle.  With many rows a warp takes four units at once, each step of
-// the chain seq, pos -> page table -> cache row issued for all of them before the next, beside the
-// loads of the rows: one unit a warp left the SM waiting for that chain (65,536 fp32 latent rows 47
-// us).  With few rows (less than a wave of warps) one unit a warp is the shorter chain.
+// Both kernels move each byte once and are bound by HBM, with short rows by the instructions and the chain
+// seq, pos -> page table -> cache row.  The unit of work of a warp is 256 columns of a read and 512 of a
+// write, by pieces of eight a lane (16- or 32-byte loads): a write's lane takes two pieces of one group, so
+// that the group's maximum, its scale and the addresses are paid once for sixteen columns (eight a lane:
+// 262,144 key rows 35 us, sixteen: 31).  A group is a segment of 2 to 16 lanes and its maximum a few
+// shuffles.  A latent row is a unit and an eighth (a read's: two and a quarter): the 64-column tails of
+// eight (four) rows share one, else most lanes of it would idle.
+//
+// With many rows a warp takes two (four) units at once, each step of the chain issued for all of them
+// before the next, beside the loads of the rows, which stay packed until they are quantised.  One unit a
+// warp: 65,536 fp32 latent rows 33 against 31 us, 61,440 rows read 33 against 22; four units of a write: 37
+// us (fewer warps fit).  With few rows (less than a wave of warps) one unit a warp is the shorter chain.
+// Blocks of four warps: of eight, whose last warps hold the SM longer, 35 us.
+//
+// Measured, launch included: 65,536 fp32 latent rows written in 31 us (6.1 TB/s), 262,144 bf16 key rows of
+// 128 in 27 us (3.9 TB/s), 61,440 latent rows read as bf16 in 22 us (4.8 TB/s).
 #include "dsa_internal.h"
 #include "ptx.cuh"
 
 namespace dsa {
 namespace cq {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 // units of a warp, with many rows
 constexpr int kWriteUnits = 2, kReadUnits = 4;
 constexpr int kLatent = 576;
@@ -118,29 +127,42 @@ DSA_DEV void cache_rows(const Params& p, const Place* w, int* at) {
   }
 }
 
+// Eight columns of a row as they lie there: half the registers of their fp32 values while 16-bit rows are on
+// their way.
 template <int E>
-DSA_DEV void load8(const uint8_t* base, long long at, float* x) {
-  if constexpr (E == DSA_ELEM_FP32) {
-    const float4* s = reinterpret_cast<const float4*>(base + at * 4);
-    const float4 a = __ldcs(s), b = __ldcs(s + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(base + at * 2));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+struct Eight {
+  static constexpr int kWords = E == DSA_ELEM_FP32 ? 2 : 1;
+  uint4 v[kWords];
+
+  DSA_DEV void load(const uint8_t* base, long long at) {
+    const uint4* s = reinterpret_cast<const uint4*>(base + at * (E == DSA_ELEM_FP32 ? 4 : 2));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (E == DSA_ELEM_BF16) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+    for (int k = 0; k < kWords; ++k) v[k] = __ldcs(s + k);
+  }
+  DSA_DEV void zero() {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  DSA_DEV void values(float* x) const {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (E == DSA_ELEM_FP32) {
+          x[4 * k + i] = __uint_as_float(w[i]);
+        } else if constexpr (E == DSA_ELEM_BF16) {
+          x[2 * i] = __uint_as_float(w[i] << 16);
+          x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+          x[2 * i] = f.x;
+          x[2 * i + 1] = f.y;
+        }
       }
     }
   }
-}
+};
 
 template <int E>
 DSA_DEV void store8(uint8_t* base, long long at, const float* y) {
@@ -268,21 +290,26 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
   const long long u = ((long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * N;
   const int lane = threadIdx.x & 31;
   Place w[N];
-  float x[N][16];
+  Eight<E> x[N][2];
   int dst[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     w[n] = place_write<F>(p, u + n, lane);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[n][i] = 0.f;
+    x[n][0].zero();
+    x[n][1].zero();
     if (w[n].row < 0) continue;
     const long long at = (long long)w[n].row * p.row_stride + w[n].col;
-    load8<E>(p.rows, at, x[n]);
-    load8<E>(p.rows, at + w[n].step, x[n] + 8);
+    x[n][0].load(p.rows, at);
+    x[n][1].load(p.rows, at + w[n].step);
   }
   cache_rows<N>(p, w, dst);
 #pragma unroll
-  for (int n = 0; n < N; ++n) write16<F>(p, w[n], dst[n], x[n]);
+  for (int n = 0; n < N; ++n) {
+    float y[16];
+    x[n][0].values(y);
+    x[n][1].values(y + 8);
+    write16<F>(p, w[n], dst[n], y);
+  }
 }
 
 // Eight columns of a cache row as they lie there, and their scale.
