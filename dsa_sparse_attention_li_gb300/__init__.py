@@ -394,6 +394,20 @@ def cache_write(pool, page_table, seq, pos, rows, *, scale_pool=None, row_scales
     _check(code, "dsa_cache_write")
 
 
+def _empty(stream, shape, dtype, device):
+    """A new tensor for a launch on `stream` (None: the current one), out of that stream's memory: out
+    of the current stream's, it could be one that this stream still works on, and a workspace
+    that is dropped after the launch could be handed out again before the kernels are done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError("the stream is one of %s, the tensors are on %s" % (stream.device, device))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _addr(t: Optional[torch.Tensor]):
     """Device address of a contiguous tensor, for a pointer field (as _ptr, without its object)."""
     if t is None:
@@ -489,8 +503,8 @@ def cache_read(pool, page_table, seq, pos, *, out=None, dtype=torch.bfloat16, sc
     and bf16 caches.  A row out of range reads as zeros and sets ``status``."""
     lib = load()
     if out is None:
-        out = torch.empty((seq.shape[0], 576 if pool.dtype == torch.uint8 else pool.shape[-1]),
-                          dtype=dtype, device=pool.device)
+        out = _empty(stream, (seq.shape[0], 576 if pool.dtype == torch.uint8 else pool.shape[-1]), dtype,
+                     pool.device)
     a = cache_rows_args(pool, page_table, seq, pos, out, scale_pool=scale_pool, sf_pool=sf_pool,
                         status=status)
     _on(pool.device, page_table, seq, pos, out, scale_pool, sf_pool, status)
@@ -544,9 +558,9 @@ def mla_decode(q, kv_pool, page_table, seq_lens, q_start, *, softmax_scale, max_
     device = q.device
     _on(device, kv_pool, page_table, seq_lens, q_start, out, lse, status, workspace)
     if out is None:
-        out = torch.empty((n_q, H, 512), dtype=torch.bfloat16, device=device)
+        out = _empty(stream, (n_q, H, 512), torch.bfloat16, device)
     if lse is None:
-        lse = torch.empty((n_q, H), dtype=torch.float32, device=device)
+        lse = _empty(stream, (n_q, H), torch.float32, device)
     a = MlaDecodeArgs()
     a.B, a.n_q, a.H, a.d_qk, a.d_v = B, n_q, H, 576, 512
     a.page_size, a.max_pages, a.num_pages = kv_pool.shape[1], page_table.shape[1], kv_pool.shape[0]
@@ -555,7 +569,7 @@ def mla_decode(q, kv_pool, page_table, seq_lens, q_start, *, softmax_scale, max_
     if workspace is None and n_q:
         nbytes = lib.dsa_mla_decode_workspace_bytes(ctypes.byref(a))
         if nbytes:
-            workspace = torch.empty((nbytes,), dtype=torch.uint8, device=device)
+            workspace = _empty(stream, (nbytes,), torch.uint8, device)
     a.q, a.kv_pool, a.page_table = _addr(q), _addr(kv_pool), _addr(page_table)
     a.seq_lens, a.q_start, a.out, a.lse, a.status = (_addr(seq_lens), _addr(q_start), _addr(out), _addr(lse),
                                                      _addr(status))
@@ -591,9 +605,9 @@ def mla_prefill(q, kv, k_rope, q_start, kv_start, *, softmax_scale, max_q_per_se
     device = q.device
     _on(device, kv, k_rope, q_start, kv_start, out, lse, status)
     if out is None:
-        out = torch.empty((n_q, H, 128), dtype=torch.bfloat16, device=device)
+        out = _empty(stream, (n_q, H, 128), torch.bfloat16, device)
     if lse is None:
-        lse = torch.empty((n_q, H), dtype=torch.float32, device=device)
+        lse = _empty(stream, (n_q, H), torch.float32, device)
     a = MlaPrefillArgs()
     a.B, a.n_q, a.n_kv, a.H, a.d_nope, a.d_rope, a.d_v = B, n_q, n_kv, H, 128, 64, 128
     a.max_q_per_seq, a.softmax_scale = max_q_per_seq, float(softmax_scale)

@@ -21,10 +21,11 @@
 // shuffles.  A latent row is a unit and an eighth (a read's: two and a quarter): the 64-column tails of
 // eight (four) rows share one, else most lanes of it would idle.
 //
-// With many rows a warp takes two (four) units at once, each step of the chain issued for all of them
-// before the next, beside the loads of the rows, which stay packed until they are quantised.  One unit a
-// warp: 65,536 fp32 latent rows 33 against 31 us, 61,440 rows read 33 against 22; four units of a write: 37
-// us (fewer warps fit).  With few rows (less than a wave of warps) one unit a warp is the shorter chain.
+// A warp takes two (four) units at once, each step of the chain issued for all of them before the next,
+// beside the loads of the rows, which stay packed until they are quantised.  One unit a warp: 65,536 fp32
+// latent rows 33 against 31 us, 61,440 rows read 29 against 22; four units of a write: 37 us (fewer warps
+// fit).  A write of less than a wave of warps takes one unit a warp, the shorter chain of instructions
+// (one latent row 6 us against 8, launch included; a read of 50 rows is 7 us either way).
 // Blocks of four warps: of eight, whose last warps hold the SM longer, 35 us.
 //
 // Measured, launch included: 65,536 fp32 latent rows written in 31 us (6.1 TB/s), 262,144 bf16 key rows of
@@ -36,7 +37,7 @@ namespace dsa {
 namespace cq {
 
 constexpr int kThreads = 128;
-// units of a warp, with many rows
+// units of a warp (a write's with many rows)
 constexpr int kWriteUnits = 2, kReadUnits = 4;
 constexpr int kLatent = 576;
 constexpr int kLatentRow = 608;   // 576 codes, 5 fp32 scales, 12 zero bytes
@@ -373,24 +374,28 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
   }
 }
 
-template <int W, int R>
-struct Kernels {
-  using Kernel = void (*)(Params);
-  static Kernel get(bool write, int format, int elem) {
-    static const Kernel kWrite[3][3] = {
-        {write_kernel<DSA_ROW_FP8, 0, W>, write_kernel<DSA_ROW_FP8, 1, W>, write_kernel<DSA_ROW_FP8, 2, W>},
-        {write_kernel<DSA_ROW_MXFP8, 0, W>, write_kernel<DSA_ROW_MXFP8, 1, W>, write_kernel<DSA_ROW_MXFP8, 2, W>},
-        {write_kernel<DSA_ROW_LATENT_FP8, 0, W>, write_kernel<DSA_ROW_LATENT_FP8, 1, W>,
-         write_kernel<DSA_ROW_LATENT_FP8, 2, W>}};
-    static const Kernel kRead[4][3] = {
-        {read_kernel<DSA_ROW_BF16, 0, R>, read_kernel<DSA_ROW_BF16, 1, R>, read_kernel<DSA_ROW_BF16, 2, R>},
-        {read_kernel<DSA_ROW_FP8, 0, R>, read_kernel<DSA_ROW_FP8, 1, R>, read_kernel<DSA_ROW_FP8, 2, R>},
-        {read_kernel<DSA_ROW_MXFP8, 0, R>, read_kernel<DSA_ROW_MXFP8, 1, R>, read_kernel<DSA_ROW_MXFP8, 2, R>},
-        {read_kernel<DSA_ROW_LATENT_FP8, 0, R>, read_kernel<DSA_ROW_LATENT_FP8, 1, R>,
-         read_kernel<DSA_ROW_LATENT_FP8, 2, R>}};
-    return write ? kWrite[format - 1][elem] : kRead[format][elem];
-  }
-};
+using Kernel = void (*)(Params);
+
+template <int N>
+Kernel write_variant(int format, int elem) {
+  static const Kernel k[3][3] = {
+      {write_kernel<DSA_ROW_FP8, 0, N>, write_kernel<DSA_ROW_FP8, 1, N>, write_kernel<DSA_ROW_FP8, 2, N>},
+      {write_kernel<DSA_ROW_MXFP8, 0, N>, write_kernel<DSA_ROW_MXFP8, 1, N>, write_kernel<DSA_ROW_MXFP8, 2, N>},
+      {write_kernel<DSA_ROW_LATENT_FP8, 0, N>, write_kernel<DSA_ROW_LATENT_FP8, 1, N>,
+       write_kernel<DSA_ROW_LATENT_FP8, 2, N>}};
+  return k[format - 1][elem];
+}
+
+template <int N>
+Kernel read_variant(int format, int elem) {
+  static const Kernel k[4][3] = {
+      {read_kernel<DSA_ROW_BF16, 0, N>, read_kernel<DSA_ROW_BF16, 1, N>, read_kernel<DSA_ROW_BF16, 2, N>},
+      {read_kernel<DSA_ROW_FP8, 0, N>, read_kernel<DSA_ROW_FP8, 1, N>, read_kernel<DSA_ROW_FP8, 2, N>},
+      {read_kernel<DSA_ROW_MXFP8, 0, N>, read_kernel<DSA_ROW_MXFP8, 1, N>, read_kernel<DSA_ROW_MXFP8, 2, N>},
+      {read_kernel<DSA_ROW_LATENT_FP8, 0, N>, read_kernel<DSA_ROW_LATENT_FP8, 1, N>,
+       read_kernel<DSA_ROW_LATENT_FP8, 2, N>}};
+  return k[format][elem];
+}
 
 }  // namespace cq
 
@@ -423,16 +428,16 @@ dsa_status launch_cache_rows(const dsa_cache_rows_args& a, bool write, cudaStrea
                                            : ((long long)a.n_rows * a.dim + cols - 1) / cols;
   DeviceInfo dev;
   if (!device_info(dev, err)) return DSA_ERR_CUDA;
-  const bool many = p.units > (long long)dev.sm_count * 64;   // more than a wave of warps
-  const int each = !many ? 1 : write ? kWriteUnits : kReadUnits;
+  const bool few = write && p.units <= (long long)dev.sm_count * 64;   // less than a wave of warps
+  const int each = few ? 1 : write ? kWriteUnits : kReadUnits;
   const long long warps = (p.units + each - 1) / each;
   const long long blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7fffffffLL) {
     err = "cache rows: too many rows for one launch";
     return DSA_ERR_UNSUPPORTED;
   }
-  const auto k = many ? Kernels<kWriteUnits, kReadUnits>::get(write, a.format, a.elem)
-                      : Kernels<1, 1>::get(write, a.format, a.elem);
+  const Kernel k = !write ? read_variant<kReadUnits>(a.format, a.elem)
+                   : few ? write_variant<1>(a.format, a.elem) : write_variant<kWriteUnits>(a.format, a.elem);
   k<<<(unsigned)blocks, kThreads, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, write ? "cache_write_quant: launch" : "cache_read: launch", err);

@@ -267,6 +267,38 @@ def test_decode_on_two_streams_with_tokens_of_no_sequence(cuda_lib, fp8):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("handle", [False, True], ids=["stream", "handle"])
+def test_stream_argument_while_the_current_stream_works_on(cuda_lib, handle):
+    """What a call allocates for another stream is that stream's memory: tensors that the current stream
+    makes and fills right after the call, while the launch still waits its turn, are not the call's
+    workspace or outputs."""
+    c, f = make_decode([9000, 100, 3333], [2, 1, 2], 64, False), make_prefill([200, 30], [500, 30], 4)
+    want = run_decode(c) + run_prefill(f)
+    rows = dsa.cache_read(c["pool"], c["pt"], torch.zeros(100, dtype=torch.int32, device="cuda"),
+                          torch.arange(100, dtype=torch.int32, device="cuda"))
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+    seq, pos = torch.zeros(100, dtype=torch.int32, device="cuda"), torch.arange(100, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    got = dsa.mla_decode(c["q"], c["pool"], c["pt"], c["seq_lens"], c["q_start"], softmax_scale=SCALE,
+                         max_q_per_seq=2, stream=stream)
+    got += dsa.mla_prefill(f["q"], f["kv"], f["rope"], f["q_start"], f["kv_start"], softmax_scale=SCALE,
+                           max_q_per_seq=200, stream=stream)
+    got += (dsa.cache_read(c["pool"], c["pt"], seq, pos, stream=stream),)
+    ws = dsa.mla_decode_workspace_bytes(c["q"].shape[0], 64, 2)
+    others = [torch.zeros(n, dtype=torch.uint8, device="cuda")
+              for n in [ws] + [t.numel() * t.element_size() for t in got] for _ in range(2)]
+    torch.cuda.synchronize()
+    n, m = sum(c["new"]), 230
+    assert torch.equal(got[0][:n], want[0][:n]) and torch.equal(got[1][:n], want[1][:n])
+    assert torch.equal(got[2][:m], want[3][:m]) and torch.equal(got[3][:m], want[4][:m])
+    assert torch.equal(got[4], rows)
+    assert all(not bool(t.any()) for t in others)
+
+
+@pytest.mark.gpu
 def test_decode_reports_what_is_out_of_range(cuda_lib):
     c = make_decode([400, 200], [1, 1], 16, False, extra=0, tail=0)
     c["pt"][0, 2] = 10 ** 6
@@ -619,6 +651,14 @@ def test_mla_prefill_host_validation(over, code):
 def test_struct_layouts():
     assert ctypes.sizeof(dsa.MlaDecodeArgs) == 11 * 4 + 4 + 9 * 8 + 8
     assert ctypes.sizeof(dsa.MlaPrefillArgs) == 9 * 4 + 4 + 8 + 8 * 8
+
+
+def test_bindings_refuse_a_stream_of_another_device():
+    class Stream:
+        cuda_stream, device = 0, torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="stream"):
+        dsa._empty(Stream(), (1,), torch.uint8, torch.device("cuda", 0))
 
 
 def test_bindings_refuse_what_does_not_fit():
