@@ -409,12 +409,22 @@ def _empty(stream, shape, dtype, device):
 
 
 def _addr(t: Optional[torch.Tensor]):
-    """Device address of a contiguous tensor, for a pointer field (as _ptr, without its object)."""
-    if t is None:
-        return None
-    if not t.is_contiguous():
-        raise ValueError("tensors passed to the DSA library must be contiguous")
-    return t.data_ptr()
+    """Device address of a checked tensor, for a pointer field."""
+    return None if t is None else t.data_ptr()
+
+
+def _fits(*specs):
+    """Each (name, tensor, type, shape) has the type, and where a shape is given the shape, that the C
+    struct takes for granted, and is contiguous; a tensor of None is left out.  (One loop for all of
+    a call's tensors: a helper for each check costs a small call 3 us.)"""
+    for name, t, dtype, shape in specs:
+        if t is None or (t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous()):
+            continue
+        if t.dtype is not dtype:
+            raise ValueError("%s must be %s (got %s)" % (name, dtype, t.dtype))
+        if shape is not None and t.shape != shape:
+            raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+        raise ValueError("%s must be contiguous" % name)
 
 
 def _on(device, *tensors):
@@ -429,16 +439,6 @@ def _on(device, *tensors):
     for t in tensors:
         if t is not None and t.get_device() != index:
             raise ValueError("a tensor is on %s, the others are on %s" % (t.device, device))
-
-
-def _typed(name, t, dtype, shape=None):
-    """`t` has the type, and where given the shape, that the C struct takes for granted."""
-    if t is None:
-        return
-    if t.dtype != dtype:
-        raise ValueError("%s must be %s (got %s)" % (name, dtype, t.dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
 
 
 def cache_rows_args(pool, page_table, seq, pos, rows, *, scale_pool=None, sf_pool=None, status=None):
@@ -469,12 +469,12 @@ def cache_rows_args(pool, page_table, seq, pos, rows, *, scale_pool=None, sf_poo
         raise ValueError("rows have %d columns, the cache's have %d" % (dim, want))
     if n > 1 and rows.stride(0) < dim or dim > 1 and rows.stride(1) != 1:
         raise ValueError("the columns of rows must be adjacent, and its rows apart")
-    _typed("page_table", page_table, torch.int32)
-    _typed("seq", seq, torch.int32, (n,))
-    _typed("pos", pos, torch.int32, (n,))
-    _typed("scale_pool", scale_pool, torch.float32, (num_pages, page_size))
-    _typed("sf_pool", sf_pool, torch.uint8, (num_pages, page_size, dim // 32))
-    _typed("status", status, torch.int32)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must have one row per sequence")
+    _fits(("pool", pool, pool.dtype, None), ("page_table", page_table, torch.int32, None),
+          ("seq", seq, torch.int32, (n,)), ("pos", pos, torch.int32, (n,)),
+          ("scale_pool", scale_pool, torch.float32, (num_pages, page_size)),
+          ("sf_pool", sf_pool, torch.uint8, (num_pages, page_size, dim // 32)), ("status", status, torch.int32, None))
     a = CacheRowsArgs()
     a.n_rows, a.dim, a.B, a.page_size = n, dim, page_table.shape[0], page_size
     a.max_pages, a.num_pages, a.format, a.elem = page_table.shape[1], num_pages, fmt, _ELEM[rows.dtype]
@@ -543,17 +543,14 @@ def mla_decode(q, kv_pool, page_table, seq_lens, q_start, *, softmax_scale, max_
     fp8 = kv_pool.dtype == torch.uint8
     if kv_pool.dim() != 3 or kv_pool.shape[2] != (608 if fp8 else 576):
         raise ValueError("kv_pool must have shape [num_pages, page_size, 576] (bf16) or [.., 608] (uint8)")
-    _typed("q", q, torch.bfloat16)
-    if not fp8:
-        _typed("kv_pool", kv_pool, torch.bfloat16)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must have one row per sequence")
-    _typed("page_table", page_table, torch.int32)
-    _typed("seq_lens", seq_lens, torch.int32, (B,))
-    _typed("q_start", q_start, torch.int32, (B + 1,))
-    _typed("out", out, torch.bfloat16, (n_q, H, 512))
-    _typed("lse", lse, torch.float32, (n_q, H))
-    _typed("status", status, torch.int32)
+    _fits(("q", q, torch.bfloat16, None), ("kv_pool", kv_pool, torch.uint8 if fp8 else torch.bfloat16, None),
+          ("page_table", page_table, torch.int32, None), ("seq_lens", seq_lens, torch.int32, (B,)),
+          ("q_start", q_start, torch.int32, (B + 1,)), ("out", out, torch.bfloat16, (n_q, H, 512)),
+          ("lse", lse, torch.float32, (n_q, H)), ("status", status, torch.int32, None))
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     max_q_per_seq = _host_max_q(q_start, max_q_per_seq, n_q)
     device = q.device
     _on(device, kv_pool, page_table, seq_lens, q_start, out, lse, status, workspace)
@@ -591,14 +588,12 @@ def mla_prefill(q, kv, k_rope, q_start, kv_start, *, softmax_scale, max_q_per_se
     n_q, H, _ = q.shape
     n_kv = kv.shape[0]
     B = q_start.shape[0] - 1
-    _typed("q", q, torch.bfloat16)
-    _typed("kv", kv, torch.bfloat16, (n_kv, H, 256))
-    _typed("k_rope", k_rope, torch.bfloat16, (n_kv, 64))
-    _typed("q_start", q_start, torch.int32)
-    _typed("kv_start", kv_start, torch.int32, (B + 1,))
-    _typed("out", out, torch.bfloat16, (n_q, H, 128))
-    _typed("lse", lse, torch.float32, (n_q, H))
-    _typed("status", status, torch.int32)
+    _fits(("q", q, torch.bfloat16, None), ("kv", kv, torch.bfloat16, (n_kv, H, 256)),
+          ("q_start", q_start, torch.int32, None), ("kv_start", kv_start, torch.int32, (B + 1,)),
+          ("out", out, torch.bfloat16, (n_q, H, 128)), ("lse", lse, torch.float32, (n_q, H)),
+          ("status", status, torch.int32, None))
+    if k_rope.dtype is not torch.bfloat16 or k_rope.shape != (n_kv, 64):
+        raise ValueError("k_rope must be bf16 of shape %s (got %s %s)" % ((n_kv, 64), k_rope.dtype, tuple(k_rope.shape)))
     if n_kv > 1 and k_rope.stride(0) < 64 or n_kv > 0 and k_rope.stride(1) != 1:
         raise ValueError("the columns of k_rope must be adjacent, and its rows apart")
     max_q_per_seq = _host_max_q(q_start, max_q_per_seq, n_q)
