@@ -13,23 +13,25 @@
 // code on which both agree; the few others, about one element in 2^16, compare |x| with border * s in
 // 64 bits, where that product is exact.
 //
-// Both kernels move each byte once and are bound by HBM, with short rows by the instructions and the chain
-// seq, pos -> page table -> cache row.  The unit of work of a warp is 256 columns of a read and 512 of a
-// write, by pieces of eight a lane (16- or 32-byte loads): a write's lane takes two pieces of one group, so
-// that the group's maximum, its scale and the addresses are paid once for sixteen columns (eight a lane:
-// 262,144 key rows 35 us, sixteen: 31).  A group is a segment of 2 to 16 lanes and its maximum a few
-// shuffles.  A latent row is a unit and an eighth (a read's: two and a quarter): the 64-column tails of
-// eight (four) rows share one, else most lanes of it would idle.
+// Both kernels move each byte once and are bound by HBM, with short rows by instruction issue (key rows: 70%
+// of the issue slots).  The unit of work of a warp is 512 columns, two pieces of eight a lane (16- or
+// 32-byte loads) out of one group, so that the group's maximum, its scale and the addresses are paid once
+// for sixteen columns (eight a lane: 262,144 key rows 35 us instead of 31, 61,440 rows read 22 instead of
+// 18).  A group is a segment of 2 to 16 lanes and its maximum a few shuffles.  A latent row is a unit and an
+// eighth: the 64-column tails of eight rows share one, else most lanes of it would idle.  (A bf16 row has
+// no groups and any width: units of 256 columns, four a warp.)
 //
-// A warp takes two (four) units at once, each step of the chain issued for all of them before the next,
-// beside the loads of the rows, which stay packed until they are quantised.  One unit a warp: 65,536 fp32
-// latent rows 33 against 31 us, 61,440 rows read 29 against 22; four units of a write: 37 us (fewer warps
-// fit).  A write of less than a wave of warps takes one unit a warp, the shorter chain of instructions
-// (one latent row 6 us against 8, launch included; a read of 50 rows is 7 us either way).
-// Blocks of four warps: of eight, whose last warps hold the SM longer, 35 us.
+// A warp takes two units at once, each step of the chain seq, pos -> page table -> cache row issued for both
+// before the next, beside the loads of the rows, which stay packed until they are quantised.  One unit a
+// warp: 65,536 fp32 latent rows 33 against 31 us, 61,440 rows read 20 against 18; four: 35 and 18.  A write
+// of less than a wave of warps takes one unit a warp, the shorter chain of instructions (one latent row 6
+// us against 8, launch included; a read of 50 rows is 7 us either way).  Blocks of four warps: of eight,
+// whose last warps hold the SM longer, 65,536 latent rows took 35 us.
 //
-// Measured, launch included: 65,536 fp32 latent rows written in 31 us (6.1 TB/s), 262,144 bf16 key rows of
-// 128 in 27 us (3.9 TB/s), 61,440 latent rows read as bf16 in 22 us (4.8 TB/s).
+// Measured, launch included: 65,536 fp32 latent rows written in 31 us (6.1 TB/s), 262,144 fp16 key rows of
+// 128 in 25 us (4.1 TB/s), 61,440 latent rows read as bf16 in 18 us (5.9 TB/s).
+#include <type_traits>
+
 #include "dsa_internal.h"
 #include "ptx.cuh"
 
@@ -37,8 +39,8 @@ namespace dsa {
 namespace cq {
 
 constexpr int kThreads = 128;
-// units of a warp (a write's with many rows)
-constexpr int kWriteUnits = 2, kReadUnits = 4;
+constexpr int kUnits = 2;         // of a warp (a write's with many rows)
+constexpr int kUnitsBf16 = 4;
 constexpr int kLatent = 576;
 constexpr int kLatentRow = 608;   // 576 codes, 5 fp32 scales, 12 zero bytes
 
@@ -58,50 +60,38 @@ struct Params {
   int* status;
 };
 
-// The row and the first column of a lane's columns in unit u; row < 0: none.  A read takes eight of them, a
-// write these eight and the eight that follow `step` columns on, both of one group.
+// The row and the first column of a lane's columns in unit u; row < 0: none.  They are eight, and of a quantised
+// format the eight that follow `step` columns on too, both of one group.
 struct Place {
   int row, col, step;
 };
 
+// (units of a quantised format number at most 9/8 of the rows; a bf16 row may have any width)
 template <int F>
-DSA_DEV Place place_write(const Params& p, long long u, int lane) {
-  long long row;
-  int col, step;
-  if constexpr (F == DSA_ROW_LATENT_FP8) {
-    const long long blk = u / 9;            // eight rows are nine units
-    const int k = (int)(u - blk * 9);
-    row = blk * 8 + (k < 8 ? k : lane >> 2);
-    col = k < 8 ? (lane >> 3) * 128 + (lane & 7) * 8 : 512 + (lane & 3) * 8;
-    step = k < 8 ? 64 : 32;
-  } else {                                  // 2, 4, 8 or 16 lanes a row
-    const int per = p.dim >> 4, l = lane & (per - 1);
-    row = u * (32 / per) + lane / per;
-    col = F == DSA_ROW_MXFP8 ? (l >> 1) * 32 + (l & 1) * 8 : l * 8;
-    step = F == DSA_ROW_MXFP8 ? 16 : p.dim >> 1;
-  }
-  return {row < p.n_rows ? (int)row : -1, col, step};
-}
+using Unit = std::conditional_t<F == DSA_ROW_BF16, unsigned long long, uint32_t>;
 
 template <int F>
-DSA_DEV Place place_read(const Params& p, long long u, int lane) {
-  const int per = p.dim >> 3;               // lanes of a row
-  long long row;
-  int col;
-  if constexpr (F == DSA_ROW_LATENT_FP8) {
-    const long long blk = u / 9;            // four rows are nine units
-    const int k = (int)(u - blk * 9);
-    row = blk * 4 + (k < 8 ? k >> 1 : lane >> 3);
-    col = k < 8 ? (k & 1) * 256 + lane * 8 : 512 + (lane & 7) * 8;
-  } else if constexpr (F == DSA_ROW_BF16) {  // any multiple of eight columns
-    const long long c = u * 32 + lane;
-    row = c / per;
-    col = (int)(c - row * per) * 8;
-  } else {                                  // 4, 8, 16 or 32 lanes a row
-    row = u * (32 / per) + lane / per;
-    col = (lane & (per - 1)) * 8;
+DSA_DEV Place place(const Params& p, Unit<F> u, int lane) {
+  if constexpr (F == DSA_ROW_BF16) {
+    const int per = p.dim >> 3;             // lanes of a row
+    const unsigned long long c = u * 32 + lane, row = c / per;
+    return {row < (unsigned)p.n_rows ? (int)row : -1, (int)(c - row * per) * 8, 0};
+  } else {
+    uint32_t row;
+    int col, step;
+    if constexpr (F == DSA_ROW_LATENT_FP8) {
+      const uint32_t blk = u / 9, k = u - blk * 9;   // eight rows are nine units
+      row = blk * 8 + (k < 8 ? k : lane >> 2);
+      col = k < 8 ? (lane >> 3) * 128 + (lane & 7) * 8 : 512 + (lane & 3) * 8;
+      step = k < 8 ? 64 : 32;
+    } else {                                // 2, 4, 8 or 16 lanes a row
+      const int per = p.dim >> 4, l = lane & (per - 1), shift = 31 - __clz(per);
+      row = (u << (5 - shift)) + (lane >> shift);
+      col = F == DSA_ROW_MXFP8 ? (l >> 1) * 32 + (l & 1) * 8 : l * 8;
+      step = F == DSA_ROW_MXFP8 ? 16 : p.dim >> 1;
+    }
+    return {row < (uint32_t)p.n_rows ? (int)row : -1, col, step};
   }
-  return {row < p.n_rows ? (int)row : -1, col, 0};
 }
 
 // Physical cache rows of N rows (-1: none, or out of range, which is reported), the loads of all of
@@ -288,14 +278,14 @@ DSA_DEV void write16(const Params& p, const Place& w, int row, const float* x) {
 
 template <int F, int E, int N>
 __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ Params p) {
-  const long long u = ((long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * N;
+  const Unit<F> u = ((Unit<F>)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * N;
   const int lane = threadIdx.x & 31;
   Place w[N];
   Eight<E> x[N][2];
   int dst[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    w[n] = place_write<F>(p, u + n, lane);
+    w[n] = place<F>(p, u + n, lane);
     x[n][0].zero();
     x[n][1].zero();
     if (w[n].row < 0) continue;
@@ -313,7 +303,7 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
   }
 }
 
-// Eight columns of a cache row as they lie there, and their scale.
+// A lane's columns of a cache row as they lie there, and their scale: eight bf16, or twice eight codes.
 struct Packed {
   uint4 bits;
   float scale;
@@ -321,13 +311,13 @@ struct Packed {
 
 template <int F, int E, int N>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ Params p) {
-  const long long u = ((long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * N;
+  const Unit<F> u = ((Unit<F>)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * N;
   const int lane = threadIdx.x & 31;
   Place w[N];
   int src[N];
   Packed v[N];
 #pragma unroll
-  for (int n = 0; n < N; ++n) w[n] = place_read<F>(p, u + n, lane);
+  for (int n = 0; n < N; ++n) w[n] = place<F>(p, u + n, lane);
   cache_rows<N>(p, w, src);
 #pragma unroll
   for (int n = 0; n < N; ++n) {
@@ -338,9 +328,9 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
       v[n].bits = __ldcs(reinterpret_cast<const uint4*>(p.pool + ((long long)src[n] * p.dim + w[n].col) * 2));
     } else {
       const uint8_t* row = p.pool + (long long)src[n] * (F == DSA_ROW_LATENT_FP8 ? kLatentRow : p.dim);
-      const uint2 c = __ldcs(reinterpret_cast<const uint2*>(row + w[n].col));
-      v[n].bits.x = c.x;
-      v[n].bits.y = c.y;
+      const uint2 a = __ldcs(reinterpret_cast<const uint2*>(row + w[n].col));
+      const uint2 b = __ldcs(reinterpret_cast<const uint2*>(row + w[n].col + w[n].step));
+      v[n].bits = make_uint4(a.x, a.y, b.x, b.y);
       if constexpr (F == DSA_ROW_LATENT_FP8) {
         v[n].scale = *reinterpret_cast<const float*>(row + kLatent + (w[n].col >> 7) * 4);
       } else if constexpr (F == DSA_ROW_FP8) {
@@ -355,22 +345,31 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     if (w[n].row < 0) continue;
+    const uint32_t bits[4] = {v[n].bits.x, v[n].bits.y, v[n].bits.z, v[n].bits.w};
+    const long long at = (long long)w[n].row * p.row_stride + w[n].col;
     float y[8];
+    if constexpr (F == DSA_ROW_BF16) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (F == DSA_ROW_BF16) {
-        const uint32_t e = i == 0 ? v[n].bits.x : i == 1 ? v[n].bits.y : i == 2 ? v[n].bits.z : v[n].bits.w;
-        y[2 * i] = __uint_as_float(e << 16);
-        y[2 * i + 1] = __uint_as_float(e & 0xffff0000u);
-      } else {
-        const uint32_t two = ((i < 2 ? v[n].bits.x : v[n].bits.y) >> ((i & 1) * 16)) & 0xffffu;
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        y[2 * i] = f.x * v[n].scale;
-        y[2 * i + 1] = f.y * v[n].scale;
+      for (int i = 0; i < 4; ++i) {
+        y[2 * i] = __uint_as_float(bits[i] << 16);
+        y[2 * i + 1] = __uint_as_float(bits[i] & 0xffff0000u);
+      }
+      store8<E>(p.rows, at, y);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t two = (bits[2 * k + (i >> 1)] >> ((i & 1) * 16)) & 0xffffu;
+          const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          const float2 m = mul2(f.x, f.y, v[n].scale);
+          y[2 * i] = m.x;
+          y[2 * i + 1] = m.y;
+        }
+        store8<E>(p.rows, at + k * w[n].step, y);
       }
     }
-    store8<E>(p.rows, (long long)w[n].row * p.row_stride + w[n].col, y);
   }
 }
 
@@ -386,10 +385,10 @@ Kernel write_variant(int format, int elem) {
   return k[format - 1][elem];
 }
 
-template <int N>
 Kernel read_variant(int format, int elem) {
+  constexpr int N = kUnits, M = kUnitsBf16;
   static const Kernel k[4][3] = {
-      {read_kernel<DSA_ROW_BF16, 0, N>, read_kernel<DSA_ROW_BF16, 1, N>, read_kernel<DSA_ROW_BF16, 2, N>},
+      {read_kernel<DSA_ROW_BF16, 0, M>, read_kernel<DSA_ROW_BF16, 1, M>, read_kernel<DSA_ROW_BF16, 2, M>},
       {read_kernel<DSA_ROW_FP8, 0, N>, read_kernel<DSA_ROW_FP8, 1, N>, read_kernel<DSA_ROW_FP8, 2, N>},
       {read_kernel<DSA_ROW_MXFP8, 0, N>, read_kernel<DSA_ROW_MXFP8, 1, N>, read_kernel<DSA_ROW_MXFP8, 2, N>},
       {read_kernel<DSA_ROW_LATENT_FP8, 0, N>, read_kernel<DSA_ROW_LATENT_FP8, 1, N>,
@@ -422,22 +421,21 @@ dsa_status launch_cache_rows(const dsa_cache_rows_args& a, bool write, cudaStrea
   p.seq = a.seq;
   p.pos = a.pos;
   p.status = a.status;
-  // (a unit of a write is 512 columns, of a read 256)
-  const int latent_rows = write ? 8 : 4, cols = write ? 512 : 256;
-  p.units = a.format == DSA_ROW_LATENT_FP8 ? ((long long)a.n_rows + latent_rows - 1) / latent_rows * 9
+  const int cols = a.format == DSA_ROW_BF16 ? 256 : 512;   // of a unit
+  p.units = a.format == DSA_ROW_LATENT_FP8 ? ((long long)a.n_rows + 7) / 8 * 9
                                            : ((long long)a.n_rows * a.dim + cols - 1) / cols;
   DeviceInfo dev;
   if (!device_info(dev, err)) return DSA_ERR_CUDA;
   const bool few = write && p.units <= (long long)dev.sm_count * 64;   // less than a wave of warps
-  const int each = few ? 1 : write ? kWriteUnits : kReadUnits;
+  const int each = few ? 1 : a.format == DSA_ROW_BF16 ? kUnitsBf16 : kUnits;
   const long long warps = (p.units + each - 1) / each;
   const long long blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7fffffffLL) {
     err = "cache rows: too many rows for one launch";
     return DSA_ERR_UNSUPPORTED;
   }
-  const Kernel k = !write ? read_variant<kReadUnits>(a.format, a.elem)
-                   : few ? write_variant<1>(a.format, a.elem) : write_variant<kWriteUnits>(a.format, a.elem);
+  const Kernel k = !write ? read_variant(a.format, a.elem)
+                   : few ? write_variant<1>(a.format, a.elem) : write_variant<kUnits>(a.format, a.elem);
   k<<<(unsigned)blocks, kThreads, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, write ? "cache_write_quant: launch" : "cache_read: launch", err);
