@@ -177,14 +177,11 @@ struct RowPart {
     s1 = s[1];
   }
   // Into the row's line of N 64-column blocks: chunk q4 + 4 u is pieces 2 q4 and 2 q4 + 1 of block u.
-  template <class Clean>
-  DSA_DEV void store(uint8_t* line, uint32_t piece0, uint32_t piece1, int split, Clean clean) const {
+  DSA_DEV void store(uint8_t* line, uint32_t piece0, uint32_t piece1, int split) const {
 #pragma unroll
     for (int u = 0; u < N; ++u) {
       uint4 lo, hi;
       dequant16(code[u], u >= split ? s1 : s0, lo, hi);
-      clean(lo);
-      clean(hi);
       *reinterpret_cast<uint4*>(line + u * kBlockBytes + piece0) = lo;
       *reinterpret_cast<uint4*>(line + u * kBlockBytes + piece1) = hi;
     }
@@ -534,7 +531,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
         const uint8_t* at = row(id(2 * w.tile0 + mine));
         a.fetch(at, 0, q4);
         b.fetch(at + 8 * kKv8Row, 0, q4);
-        auto as_is = [](uint4&) {};
         int far = -1;
         for (int i = w.tile0; i < w.tile1; ++i, ++it) {
           const uint8_t* next = row(id(2 * i + 2 + mine));
@@ -550,9 +546,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
             uint8_t* line = smem + Layout::k + part * kKGroupBytes + r * 128;
             const int split = part == 1 ? 1 : 2, first = part == 2 ? 0 : part * 12 + 12;
             if (part == 2) at = next;
-            a.store(line, piece0, piece1, split, as_is);
+            a.store(line, piece0, piece1, split);
             a.fetch(at, first, q4);
-            b.store(line + 8 * 128, piece0, piece1, split, as_is);
+            b.store(line + 8 * 128, piece0, piece1, split);
             b.fetch(at + 8 * kKv8Row, first, q4);
             filled(part);
           }
@@ -572,21 +568,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
             // see, what is not finite does (see the softmax warps)
             const bool edge = (i + 1) * kTile > w.seen_first || pg < 0;
             const int pos = i * kTile + part * 64 + r;
-            auto clean = [&](int x) {
-              return [=](uint4& v) {
-                if (!edge) return;
-                if (pg < 0 || pos + x >= w.seen_last)
-                  v = make_uint4(0u, 0u, 0u, 0u);
-                else if (pos + x >= w.seen_first)
-                  v = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w));
-              };
-            };
             if (it > 0) warp_wait(&ctl->v_empty[part], (it - 1) & 1u, abort, p.status);
             uint8_t* line = smem + Layout::v + part * kVPageBytes + r * 128;
-            a.store(line, piece0, piece1, 2, clean(0));
+            a.store(line, piece0, piece1, 2);
             a.fetch(row(next), first, q4);
-            b.store(line + 8 * 128, piece0, piece1, 2, clean(8));
+            b.store(line + 8 * 128, piece0, piece1, 2);
             b.fetch(row(next) + 8 * kKv8Row, first, q4);
+            if (edge) {
+#pragma unroll 1
+              for (int n = 0; n < 16; ++n) {   // row group, block, piece of what this lane has stored
+                const int x = pos + (n >> 3) * 8;
+                uint4* at = reinterpret_cast<uint4*>(line + (n >> 3) * 8 * 128 + ((n >> 1) & 3) * kBlockBytes +
+                                                     (n & 1 ? piece1 : piece0));
+                if (pg < 0 || x >= w.seen_last) {
+                  *at = make_uint4(0u, 0u, 0u, 0u);
+                } else if (x >= w.seen_first) {
+                  const uint4 v = *at;
+                  *at = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w));
+                }
+              }
+            }
             filled(part);
             pg = next;
           }
