@@ -162,24 +162,25 @@ DSA_DEV void dequant16(const uint4& c, float s, uint4& lo, uint4& hi) {
   hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// A lane's N chunks of 16 codes of one FP8 row in one part of a tile, and the row's two scales there;
-// chunks from `split` on have the second.
-template <int N>
+// A lane's chunks of 16 codes of one FP8 row in one part of a tile, three of K or four of V, and the row's
+// two scales there; chunks from `split` on have the second.
 struct RowPart {
-  uint4 code[N];
+  uint4 code[4];
   float s0, s1;
 
-  DSA_DEV void fetch(const uint8_t* row, int first, int q4) {
+  DSA_DEV void fetch(const uint8_t* row, int first, int q4, bool four) {
 #pragma unroll
-    for (int u = 0; u < N; ++u) code[u] = *reinterpret_cast<const uint4*>(row + (first + q4 + 4 * u) * 16);
+    for (int u = 0; u < 4; ++u)
+      if (u < 3 || four) code[u] = *reinterpret_cast<const uint4*>(row + (first + q4 + 4 * u) * 16);
     const float* s = reinterpret_cast<const float*>(row + kDqk) + (first >> 3);
     s0 = s[0];
     s1 = s[1];
   }
-  // Into the row's line of N 64-column blocks: chunk q4 + 4 u is pieces 2 q4 and 2 q4 + 1 of block u.
-  DSA_DEV void store(uint8_t* line, uint32_t piece0, uint32_t piece1, int split) const {
+  // Into the row's line of 64-column blocks: chunk q4 + 4 u is pieces 2 q4 and 2 q4 + 1 of block u.
+  DSA_DEV void store(uint8_t* line, uint32_t piece0, uint32_t piece1, int split, bool four) const {
 #pragma unroll
-    for (int u = 0; u < N; ++u) {
+    for (int u = 0; u < 4; ++u) {
+      if (u == 3 && !four) break;
       uint4 lo, hi;
       dequant16(code[u], u >= split ? s1 : s0, lo, hi);
       *reinterpret_cast<uint4*>(line + u * kBlockBytes + piece0) = lo;
@@ -503,11 +504,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
     // Warps 6 and 7 pass the news on: they order the part toward the tensor core's (async) proxy
     // and tell the issuing CTA.  That fence waits for the thread's outstanding loads too, which would
     // cost these warps an L2 latency a part.
-    uint64_t* written = &ctl->written[warp < 12 ? 0 : kKGroups];
-    auto filled = [&](int part) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&written[part]);
-    };
+    const bool is_v = warp >= 12;
+    const int parts = is_v ? kVPages : kKGroups, part_bytes = is_v ? kVPageBytes : kKGroupBytes;
+    uint64_t* const written = &ctl->written[is_v ? kKGroups : 0];
+    uint64_t* const empty = is_v ? ctl->v_empty : ctl->k_empty;
+    uint8_t* const slot = smem + (is_v ? Layout::v : Layout::k) + r * 128;
+    const int first_v = is_v ? (int)rank * 16 : 0;
     const uint32_t piece0 = (uint32_t)(((q4 * 2) ^ (r & 7)) << 4), piece1 = (uint32_t)(((q4 * 2 + 1) ^ (r & 7)) << 4);
     uint32_t it = 0;
     for (; have; have = w.next(p, lane)) {
@@ -525,74 +527,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
         return __shfl_sync(0xffffffffu, ids, page & 31);
       };
       auto row = [&](int pg) { return p.kv + ((size_t)max(pg, 0) * 64 + r) * kKv8Row; };
-      if (warp < 12) {
-        const int mine = (int)rank;
-        RowPart<3> a, b;
-        const uint8_t* at = row(id(2 * w.tile0 + mine));
-        a.fetch(at, 0, q4);
-        b.fetch(at + 8 * kKv8Row, 0, q4);
-        int far = -1;
-        for (int i = w.tile0; i < w.tile1; ++i, ++it) {
-          const uint8_t* next = row(id(2 * i + 2 + mine));
-          if (warp == 8) {  // a later tile's page into L2, its id loaded a tile ahead
-            if (far >= 0 && far < p.num_pages && lane == 0)
-              prefetch_l2_bulk(p.kv + (size_t)far * 64 * kKv8Row, 64 * kKv8Row);
-            const int page = 2 * (i + kPrefetch + 1) + mine;
-            far = page < pages ? pt[page] : -1;
-          }
-#pragma unroll 1
-          for (int part = 0; part < kKGroups; ++part) {
-            if (it > 0) warp_wait(&ctl->k_empty[part], (it - 1) & 1u, abort, p.status);
-            uint8_t* line = smem + Layout::k + part * kKGroupBytes + r * 128;
-            const int split = part == 1 ? 1 : 2, first = part == 2 ? 0 : part * 12 + 12;
-            if (part == 2) at = next;
-            a.store(line, piece0, piece1, split);
-            a.fetch(at, first, q4);
-            b.store(line + 8 * 128, piece0, piece1, split);
-            b.fetch(at + 8 * kKv8Row, first, q4);
-            filled(part);
-          }
-          if (__any_sync(0xffffffffu, *abort)) break;
+      RowPart a, b;
+      int pg = id(2 * w.tile0 + (is_v ? 0 : (int)rank)), far = -1;
+      a.fetch(row(pg), first_v, q4, is_v);
+      b.fetch(row(pg) + 8 * kKv8Row, first_v, q4, is_v);
+      for (int i = w.tile0; i < w.tile1; ++i, ++it) {
+        if (warp == 8) {  // a later tile's page into L2, its id loaded a tile ahead
+          if (far >= 0 && far < p.num_pages && lane == 0)
+            prefetch_l2_bulk(p.kv + (size_t)far * 64 * kKv8Row, 64 * kKv8Row);
+          const int page = 2 * (i + kPrefetch + 1) + (int)rank;
+          far = page < pages ? pt[page] : -1;
         }
-      } else {
-        const int first = (int)rank * 16;
-        int pg = id(2 * w.tile0);
-        RowPart<4> a, b;
-        a.fetch(row(pg), first, q4);
-        b.fetch(row(pg) + 8 * kKv8Row, first, q4);
-        for (int i = w.tile0; i < w.tile1; ++i, ++it) {
 #pragma unroll 1
-          for (int part = 0; part < kVPages; ++part) {
-            const int next = id(2 * i + part + 1);
-            // rows that no token sees, or that are not there, become zeros; of those that only some
-            // see, what is not finite does (see the softmax warps)
-            const bool edge = (i + 1) * kTile > w.seen_first || pg < 0;
-            const int pos = i * kTile + part * 64 + r;
-            if (it > 0) warp_wait(&ctl->v_empty[part], (it - 1) & 1u, abort, p.status);
-            uint8_t* line = smem + Layout::v + part * kVPageBytes + r * 128;
-            a.store(line, piece0, piece1, 2);
-            a.fetch(row(next), first, q4);
-            b.store(line + 8 * 128, piece0, piece1, 2);
-            b.fetch(row(next) + 8 * kKv8Row, first, q4);
-            if (edge) {
+        for (int part = 0; part < parts; ++part) {
+          const bool turn = is_v || part == kKGroups - 1;   // the next part is of another page
+          const int next = !turn ? pg : id(is_v ? 2 * i + part + 1 : 2 * i + 2 + (int)rank);
+          const int first = is_v ? first_v : turn ? 0 : part * 12 + 12, split = !is_v && part == 1 ? 1 : 2;
+          if (it > 0) warp_wait(empty + part, (it - 1) & 1u, abort, p.status);
+          uint8_t* line = slot + part * part_bytes;
+          a.store(line, piece0, piece1, split, is_v);
+          a.fetch(row(next), first, q4, is_v);
+          b.store(line + 8 * 128, piece0, piece1, split, is_v);
+          b.fetch(row(next) + 8 * kKv8Row, first, q4, is_v);
+          // value rows that no token sees, or that are not there, become zeros; of those that only some
+          // see, what is not finite does (see the softmax warps)
+          if (is_v && ((i + 1) * kTile > w.seen_first || pg < 0)) {
 #pragma unroll 1
-              for (int n = 0; n < 16; ++n) {   // row group, block, piece of what this lane has stored
-                const int x = pos + (n >> 3) * 8;
-                uint4* at = reinterpret_cast<uint4*>(line + (n >> 3) * 8 * 128 + ((n >> 1) & 3) * kBlockBytes +
-                                                     (n & 1 ? piece1 : piece0));
-                if (pg < 0 || x >= w.seen_last) {
-                  *at = make_uint4(0u, 0u, 0u, 0u);
-                } else if (x >= w.seen_first) {
-                  const uint4 v = *at;
-                  *at = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w));
-                }
+            for (int n = 0; n < 16; ++n) {   // row group, block, piece of what this lane has stored
+              const int pos = i * kTile + part * 64 + r + (n >> 3) * 8;
+              uint4* at = reinterpret_cast<uint4*>(line + (n >> 3) * 8 * 128 + ((n >> 1) & 3) * kBlockBytes +
+                                                   (n & 1 ? piece1 : piece0));
+              if (pg < 0 || pos >= w.seen_last) {
+                *at = make_uint4(0u, 0u, 0u, 0u);
+              } else if (pos >= w.seen_first) {
+                const uint4 v = *at;
+                *at = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w));
               }
             }
-            filled(part);
-            pg = next;
           }
-          if (__any_sync(0xffffffffu, *abort)) break;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(written + part);
+          pg = next;
         }
+        if (__any_sync(0xffffffffu, *abort)) break;
       }
       if (__any_sync(0xffffffffu, *abort)) break;
     }
