@@ -24,8 +24,17 @@
 // group cut by a range border leaves normalised fp32 rows and their log-sum-exp in the workspace (at
 // most two such pieces a pair), and a second kernel joins the pieces in order.
 //
+// An FP8 cache is read with plain loads and converted by eight warps into the same operands (at the MMAs'
+// rate a code would need its scale, one a row and 128 columns, which no e4m3 MMA applies).
+//
 // Bound: HBM for one token a sequence (1152 B and 278,528 FLOP a position at H = 128: 242 FLOP/B),
-// the tensor pipe for more.  A tile's 36 + 16 MMAs take 36 * 49 + 16 * 64 = 2,800 cycles.
+// the tensor pipe for more.  A tile's 36 + 16 MMAs take 36 * 49 + 16 * 64 = 2,800 cycles.  With an FP8
+// cache the conversion: K's slots are free only between two Q.K^T, and its three parts, one after the
+// other, are 1,700 cycles each of loads, conversion and stores.
+//
+// Measured (join included): 32 sequences of 32,768, one token: 128 heads 234 us (5.2 TB/s, 78% of a copy's
+// rate; 1,250 TFLOP/s), 16 heads 214 us; one of 131,072: 56 us; one of 4,096, 16 heads: 18 us.  FP8: 32 of
+// 32,768, 128 heads 337 us, 16 ragged ones of up to 131,072 with two tokens and 64 heads 197 us.
 #include <algorithm>
 
 #include "dsa_internal.h"
@@ -499,7 +508,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
     // parts a tile), warps 12-15 both pages' value columns of this CTA into V (two parts).  A warp has
     // 16 rows of a page; four lanes share a row, a lane takes every fourth 16-code chunk of it (two
     // passes of eight rows), so the 16-byte stores into the 128-byte-swizzled blocks meet no bank
-    // conflict.  A part's registers are loaded for the next tile as soon as they are stored.
+    // conflict.  A part's registers are loaded for the next part as soon as they are stored.
+    // One body for both kinds, and the rare cleaning in a pass of its own: the warps' instructions
+    // share one cache (with a body each 32 sequences of 32k tokens took 400 us instead of 337; all
+    // eight warps on each part, eight rows each, 421; row groups in a loop, whose register moves
+    // wait for the loads, 430).
     const int r = (warp & 3) * 16 + (lane >> 2), q4 = lane & 3;
     // Warps 6 and 7 pass the news on: they order the part toward the tensor core's (async) proxy
     // and tell the issuing CTA.  That fence waits for the thread's outstanding loads too, which would
@@ -593,10 +606,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
     constexpr uint32_t idesc_pv = idesc_bf16(128, 256, /*b_mn_major=*/true);
     const uint32_t q_at = smem_u32(smem + Layout::q), k_at = smem_u32(smem + Layout::k),
                    v_at = smem_u32(smem + Layout::v), p_at = smem_u32(smem + Layout::p);
-    // The whole warp walks the tiles and one lane issues, in the order Q.K^T of tile i + 1, P.V of tile i: the softmax of a tile runs under
-    // the next tile's Q.K^T.  Fully unrolled, with operand offsets that are constants: an issue loop
-    // with integer work around each instruction ran at a third of the tensor pipe's rate.  The K
-    // loads say how many tiles each piece has (0: the end) when they arm its Q barrier.
+    // The whole warp walks the tiles and one lane issues, in the order Q.K^T of tile i + 1, P.V of tile
+    // i: the softmax of a tile runs under the next tile's Q.K^T.  Fully unrolled, with operand offsets
+    // that are constants: an issue loop with integer work around each instruction ran at a third of
+    // the tensor pipe's rate.  The K loads say how many tiles each piece has (0: the end) when they
+    // arm its Q barrier.
     {
       const uint32_t me = elect_one();
       auto qk = [&](uint32_t n) {
