@@ -256,6 +256,57 @@ def test_write_then_read_on_another_stream_and_in_a_graph(cuda_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("form,dim", FORMS)
+def test_many_rows_are_written_and_read_as_few_are(cuda_lib, form, dim, dtype):
+    """More than a wave of warps of 512 columns each, in one call and a few rows at a time."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n = sms * 64 * 512 // dim + 1003
+    g = torch.Generator().manual_seed(dim)
+    max_pages = n // 64 + 1
+    pt = torch.randperm(max_pages, generator=g).to(torch.int32)[None].cuda()
+    pos = torch.randperm(n, generator=g).to(torch.int32).cuda()
+    seq = torch.zeros_like(pos)
+    rows = hard_rows(1000, dim, dtype, g).cuda()[torch.arange(n, device="cuda") * 7 % 1000]
+    pool, kw = make_cache(form, dim, max_pages, 64, g)
+    one, one_kw, few, few_kw = cuda(pool), cuda(kw), cuda(pool), cuda(kw)
+    dsa.cache_write_quant(one, pt, seq, pos, rows, **one_kw)
+    step = n // 9
+    for at in range(0, n, step):
+        part = slice(at, at + step)
+        dsa.cache_write_quant(few, pt, seq[part], pos[part], rows[part], **few_kw)
+    assert torch.equal(one.view(torch.uint8), few.view(torch.uint8))
+    assert all(torch.equal(one_kw[k], few_kw[k]) for k in one_kw)
+    got = dsa.cache_read(one, pt, seq, pos, dtype=dtype, **one_kw)
+    again = torch.cat([dsa.cache_read(one, pt, seq[k:k + step], pos[k:k + step], dtype=dtype, **one_kw)
+                       for k in range(0, n, step)])
+    assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(again))
+    assert torch.equal(torch.isnan(got), torch.isnan(again))
+
+
+@pytest.mark.gpu
+def test_offsets_beyond_32_bits(cuda_lib):
+    """A cache of 4.7 GB and rows that lie 2 GB apart."""
+    g = torch.Generator().manual_seed(8)
+    pages = 120001
+    pool = torch.zeros((pages, 64, 608), dtype=torch.uint8, device="cuda")
+    pt = torch.tensor([[pages - 1, 0, pages - 2]], dtype=torch.int32, device="cuda")
+    pos = torch.tensor([63, 64, 191, 0, 130], dtype=torch.int32, device="cuda")
+    seq = torch.zeros_like(pos)
+    values = torch.randn((5, 576), generator=g).bfloat16().cuda()
+    far = torch.zeros(4 * 2 ** 30 + 576, dtype=torch.bfloat16, device="cuda").as_strided((5, 576), (2 ** 30, 1))
+    far.copy_(values)
+    dsa.cache_write_quant(pool, pt, seq, pos, far)
+    small = torch.zeros((3, 64, 608), dtype=torch.uint8, device="cuda")
+    dsa.cache_write_quant(small, torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda"), seq, pos, values)
+    assert torch.equal(pool[0], small[0]) and torch.equal(pool[-2:], small[1:])
+    far.zero_()
+    dsa.cache_read(pool, pt, seq, pos, out=far)
+    want = dsa.cache_read(small, torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda"), seq, pos)
+    assert torch.equal(far, want) and bool(want.any())
+
+
+@pytest.mark.gpu
 def test_the_written_latent_rows_are_the_generators(cuda_lib):
     """The format is the one that dsa_sfa_* are tested on: the generator's rows, from the same fp32
     values, up to codes whose quotient its fp32 division rounds onto a border (about one in 2^20)."""
