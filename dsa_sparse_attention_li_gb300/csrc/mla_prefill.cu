@@ -611,8 +611,8 @@ dsa_status launch_mla_prefill(const dsa_mla_prefill_args& a, cudaStream_t stream
   p.status = a.status;
   // every sequence has at most one block that is not full
   const long long blocks = (long long)a.n_q / kTokens + a.B, grid = blocks * a.H;
-  if (grid > 0x7fff0000LL) {
-    err = "mla_prefill: token blocks * heads must number below 2^31";
+  if (blocks * std::max(a.H, kHeadGroup) > 0x7fff0000LL) {
+    err = "mla_prefill: token blocks * heads (at least 16) must number below 2^31";
     return DSA_ERR_UNSUPPORTED;
   }
   p.blocks = (int)blocks;

@@ -297,8 +297,8 @@ dsa_status dsa_mla_decode(const dsa_mla_decode_args* args, dsa_stream_t stream);
  * array sets DSA_ERR_DEVICE_CHECK, and the sequence is skipped; so do more tokens in a sequence
  * than max_q_per_seq, which are computed all the same.
  *
- * Supported: d_nope 128, d_rope 64, d_v 128; 1 <= H <= 1024; bf16; q, kv and k_rope 16-byte aligned,
- * out 32-byte aligned, k_rope_stride a multiple of 8.
+ * Supported: d_nope 128, d_rope 64, d_v 128; 1 <= H <= 1024; bf16; (n_q / 256 + B) * max(H, 16) below
+ * 2^31; q, kv and k_rope 16-byte aligned, out 32-byte aligned, k_rope_stride a multiple of 8.
  */
 typedef struct {
   int B, n_q, n_kv;

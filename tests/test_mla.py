@@ -648,6 +648,12 @@ def test_mla_prefill_host_validation(over, code):
     assert lib.dsa_mla_prefill(ctypes.byref(_prefill_args(n_q=0)), None) == dsa.DSA_OK
 
 
+@pytest.mark.parametrize("over", [{"B": 1 << 28, "H": 1}, {"n_q": 0x7fffffff, "H": 512}, {"B": 1 << 21, "H": 1024}])
+def test_mla_prefill_refuses_more_blocks_than_it_can_number(over):
+    assert dsa.load().dsa_mla_prefill(ctypes.byref(_prefill_args(**over)), None) == dsa.DSA_ERR_UNSUPPORTED
+    assert "2^31" in dsa.last_error()
+
+
 def test_struct_layouts():
     assert ctypes.sizeof(dsa.MlaDecodeArgs) == 11 * 4 + 4 + 9 * 8 + 8
     assert ctypes.sizeof(dsa.MlaPrefillArgs) == 9 * 4 + 4 + 8 + 8 * 8
