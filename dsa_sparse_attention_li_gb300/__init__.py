@@ -12,6 +12,7 @@ Functions (same names as the C entry points, without the ``dsa_`` prefix):
     sfa_prefill(...)         -> same
     sfa_workspace_bytes(...) -> int
     mla_decode(...)          -> (out [n_q, H, 512] bf16, lse [n_q, H] fp32)   dense, absorbed form
+    mla_decode_workspace_bytes(n_q, H, max_q_per_seq) -> int
     mla_prefill(...)         -> (out [n_q, H, 128] bf16, lse [n_q, H] fp32)   dense, expanded form
     page_bytes(dtype, rows, dim), page_table_validate(...), cache_write(...)
     cache_write_quant(...), cache_read(...): rows into, and out of, the quantised caches
