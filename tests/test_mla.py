@@ -448,11 +448,12 @@ def test_prefill_reports_what_is_out_of_range(cuda_lib):
         assert status == dsa.DSA_ERR_DEVICE_CHECK
         rows = slice(0, 100) if fine == [0] else slice(100, 150)
         assert torch.isfinite(out[rows].float()).all() and not torch.any((out[rows] == 5.0).all(-1))
-    # more tokens than the host's bound: the further ones are skipped and reported
+    # more tokens than the host's bound: reported, and computed all the same
     c = make_prefill([600, 50], [600, 50], 2)
     out, lse, status = run_prefill(c, max_q_per_seq=50)
     assert status == dsa.DSA_ERR_DEVICE_CHECK
     assert torch.all(lse[:50] != 6.0) and torch.all(lse[600:650] != 6.0)
+    verify_prefill(c, out, lse)
 
 
 @pytest.mark.gpu
@@ -528,6 +529,43 @@ def test_prefill_offsets_beyond_32_bits(cuda_lib):
 # ------------------------------------------------------------------------------------------
 # the operators together
 # ------------------------------------------------------------------------------------------
+
+@pytest.mark.gpu
+def test_all_kernels_at_once_and_a_capture_that_allocates(cuda_lib):
+    """Calls on four streams at the same time give what they give alone; a captured call that makes its
+    own workspace and outputs, replayed between other work, too."""
+    cases = [make_decode([5000, 64, 900], [1, 2, 1], 32, fp8, seed=3) for fp8 in (False, True)]
+    fills = [make_prefill([300, 1, 700], [900, 1, 700], 6, seed=s) for s in (1, 2)]
+    decode = lambda c: dsa.mla_decode(c["q"], c["pool"], c["pt"], c["seq_lens"], c["q_start"], softmax_scale=SCALE,
+                                      max_q_per_seq=2)
+    fill = lambda c: dsa.mla_prefill(c["q"], c["kv"], c["rope"], c["q_start"], c["kv_start"], softmax_scale=SCALE,
+                                     max_q_per_seq=700)
+    calls = [(decode, c, sum(c["new"])) for c in cases] + [(fill, c, sum(c["new"])) for c in fills]
+    alone = [f(c) for f, c, _ in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = []
+    for _ in range(6):
+        for (f, c, n), s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                got.append(f(c))
+    torch.cuda.synchronize()
+    for k, (out, lse) in enumerate(got):
+        n = calls[k % 4][2]
+        assert torch.equal(out[:n], alone[k % 4][0][:n]) and torch.equal(lse[:n], alone[k % 4][1][:n])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = [f(c) for f, c, _ in calls]
+    for _ in range(2):
+        for out, lse in kept:
+            out.zero_()
+            lse.zero_()
+        graph.replay()
+        got = [f(c) for f, c, _ in calls]
+        torch.cuda.synchronize()
+        for a, b, (_, _, n) in zip(kept, got, calls):
+            assert torch.equal(a[0][:n], b[0][:n]) and torch.equal(a[1][:n], b[1][:n])
+
 
 @pytest.mark.gpu
 def test_cache_round_trip_absorbed_and_expanded_agree(cuda_lib):
