@@ -414,32 +414,37 @@ def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _fits(*specs):
-    """Each (name, tensor, type, shape) has the type, and where a shape is given the shape, that the C
-    struct takes for granted, and is contiguous; a tensor of None is left out.  (One loop for all of
-    a call's tensors: a helper for each check costs a small call 3 us.)"""
+def _fits(device, *specs):
+    """Each (name, tensor, type, shape) is contiguous, on `device`, the current CUDA device, and has the
+    type, and where a shape is given the shape, that the C struct takes for granted; a tensor of None is
+    left out.  The library's launches go to the current device, so a tensor of another one would be read
+    across, or not at all.  (One loop for all of a call's tensors: a helper for each check costs a small
+    call 3 us.)"""
+    index = device.index
     for name, t, dtype, shape in specs:
-        if t is None or (t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous()):
+        if t is None or (t.dtype is dtype and (shape is None or t.shape == shape) and t.get_device() == index
+                         and t.is_contiguous()):
             continue
         if t.dtype is not dtype:
             raise ValueError("%s must be %s (got %s)" % (name, dtype, t.dtype))
         if shape is not None and t.shape != shape:
             raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+        if device.type != "cuda":
+            raise ValueError("tensors must be on a CUDA device (got %s)" % device)
+        if t.device != device:
+            raise ValueError("%s is on %s, the others are on %s" % (name, t.device, device))
         raise ValueError("%s must be contiguous" % name)
+    if index != torch._C._cuda_getDevice():
+        raise ValueError("tensors are on %s, the current device is cuda:%d" % (device, torch.cuda.current_device()))
 
 
-def _on(device, *tensors):
-    """Every tensor given lives on `device`, the current CUDA device.  The library's launches go to
-    the current device, so a tensor of another one would be read across, or not at all."""
-    if device.type != "cuda":
-        raise ValueError("tensors must be on a CUDA device (got %s)" % device)
-    index = device.index
-    if index != torch.cuda.current_device():
-        raise ValueError("tensors are on %s, the current device is cuda:%d"
-                         % (device, torch.cuda.current_device()))
-    for t in tensors:
-        if t is not None and t.get_device() != index:
-            raise ValueError("a tensor is on %s, the others are on %s" % (t.device, device))
+def _launch_stream(stream, device):
+    """The stream of a launch on `device`, the current one."""
+    if stream is None:
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
+    if getattr(stream, "device", device) != device:
+        raise ValueError("the stream is one of %s, the tensors are on %s" % (stream.device, device))
+    return _stream(stream)
 
 
 def cache_rows_args(pool, page_table, seq, pos, rows, *, scale_pool=None, sf_pool=None, status=None):
@@ -450,7 +455,8 @@ def cache_rows_args(pool, page_table, seq, pos, rows, *, scale_pool=None, sf_poo
         raise ValueError("pool is [num_pages, page_size, width], rows is [n, dim]")
     num_pages, page_size, width = pool.shape
     n, dim = rows.shape
-    if rows.dtype not in _ELEM:
+    elem = _ELEM.get(rows.dtype)
+    if elem is None:
         raise ValueError("rows must be bf16, fp16 or fp32 (got %s)" % rows.dtype)
     if pool.dtype == torch.uint8:
         if width != 608:
@@ -468,20 +474,26 @@ def cache_rows_args(pool, page_table, seq, pos, rows, *, scale_pool=None, sf_poo
         raise ValueError("only an e4m3 cache has scale_pool or sf_pool")
     if dim != want:
         raise ValueError("rows have %d columns, the cache's have %d" % (dim, want))
-    if n > 1 and rows.stride(0) < dim or dim > 1 and rows.stride(1) != 1:
+    stride, step = rows.stride()
+    if n > 1 and stride < dim or dim > 1 and step != 1:
         raise ValueError("the columns of rows must be adjacent, and its rows apart")
     if page_table.dim() != 2:
         raise ValueError("page_table must have one row per sequence")
-    _fits(("pool", pool, pool.dtype, None), ("page_table", page_table, torch.int32, None),
+    device = pool.device
+    _fits(device, ("pool", pool, pool.dtype, None), ("page_table", page_table, torch.int32, None),
           ("seq", seq, torch.int32, (n,)), ("pos", pos, torch.int32, (n,)),
           ("scale_pool", scale_pool, torch.float32, (num_pages, page_size)),
           ("sf_pool", sf_pool, torch.uint8, (num_pages, page_size, dim // 32)), ("status", status, torch.int32, None))
+    if rows.get_device() != device.index:
+        raise ValueError("rows is on %s, the cache on %s" % (rows.device, device))
+    B, max_pages = page_table.shape
     a = CacheRowsArgs()
-    a.n_rows, a.dim, a.B, a.page_size = n, dim, page_table.shape[0], page_size
-    a.max_pages, a.num_pages, a.format, a.elem = page_table.shape[1], num_pages, fmt, _ELEM[rows.dtype]
-    a.row_stride = rows.stride(0) if n > 1 else dim
-    a.rows, a.pool, a.scale_pool, a.sf_pool = rows.data_ptr(), _addr(pool), _addr(scale_pool), _addr(sf_pool)
-    a.page_table, a.seq, a.pos, a.status = _addr(page_table), _addr(seq), _addr(pos), _addr(status)
+    a.n_rows, a.dim, a.B, a.page_size = n, dim, B, page_size
+    a.max_pages, a.num_pages, a.format, a.elem = max_pages, num_pages, fmt, elem
+    a.row_stride = stride if n > 1 else dim
+    a.rows, a.pool, a.page_table = rows.data_ptr(), pool.data_ptr(), page_table.data_ptr()
+    a.seq, a.pos, a.scale_pool, a.sf_pool, a.status = (seq.data_ptr(), pos.data_ptr(), _addr(scale_pool),
+                                                       _addr(sf_pool), _addr(status))
     return a
 
 
@@ -493,8 +505,7 @@ def cache_write_quant(pool, page_table, seq, pos, rows, *, scale_pool=None, sf_p
     lib = load()
     a = cache_rows_args(pool, page_table, seq, pos, rows, scale_pool=scale_pool, sf_pool=sf_pool,
                         status=status)
-    _on(pool.device, page_table, seq, pos, rows, scale_pool, sf_pool, status)
-    _check(lib.dsa_cache_write_quant(ctypes.byref(a), _stream(stream)), "dsa_cache_write_quant")
+    _check(lib.dsa_cache_write_quant(ctypes.byref(a), _launch_stream(stream, pool.device)), "dsa_cache_write_quant")
 
 
 def cache_read(pool, page_table, seq, pos, *, out=None, dtype=torch.bfloat16, scale_pool=None,
@@ -508,8 +519,7 @@ def cache_read(pool, page_table, seq, pos, *, out=None, dtype=torch.bfloat16, sc
                      pool.device)
     a = cache_rows_args(pool, page_table, seq, pos, out, scale_pool=scale_pool, sf_pool=sf_pool,
                         status=status)
-    _on(pool.device, page_table, seq, pos, out, scale_pool, sf_pool, status)
-    _check(lib.dsa_cache_read(ctypes.byref(a), _stream(stream)), "dsa_cache_read")
+    _check(lib.dsa_cache_read(ctypes.byref(a), _launch_stream(stream, pool.device)), "dsa_cache_read")
     return out
 
 
@@ -541,39 +551,38 @@ def mla_decode(q, kv_pool, page_table, seq_lens, q_start, *, softmax_scale, max_
         raise ValueError("q must have shape [n_q, H, 576] (got %s)" % (tuple(q.shape),))
     n_q, H, _ = q.shape
     B = seq_lens.shape[0]
-    fp8 = kv_pool.dtype == torch.uint8
+    fp8 = kv_pool.dtype is torch.uint8
     if kv_pool.dim() != 3 or kv_pool.shape[2] != (608 if fp8 else 576):
         raise ValueError("kv_pool must have shape [num_pages, page_size, 576] (bf16) or [.., 608] (uint8)")
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must have one row per sequence")
-    _fits(("q", q, torch.bfloat16, None), ("kv_pool", kv_pool, torch.uint8 if fp8 else torch.bfloat16, None),
-          ("page_table", page_table, torch.int32, None), ("seq_lens", seq_lens, torch.int32, (B,)),
-          ("q_start", q_start, torch.int32, (B + 1,)), ("out", out, torch.bfloat16, (n_q, H, 512)),
-          ("lse", lse, torch.float32, (n_q, H)), ("status", status, torch.int32, None))
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
     max_q_per_seq = _host_max_q(q_start, max_q_per_seq, n_q)
     device = q.device
-    _on(device, kv_pool, page_table, seq_lens, q_start, out, lse, status, workspace)
+    _fits(device, ("q", q, torch.bfloat16, None), ("kv_pool", kv_pool, torch.uint8 if fp8 else torch.bfloat16, None),
+          ("page_table", page_table, torch.int32, None), ("seq_lens", seq_lens, torch.int32, (B,)),
+          ("q_start", q_start, torch.int32, (B + 1,)), ("out", out, torch.bfloat16, (n_q, H, 512)),
+          ("lse", lse, torch.float32, (n_q, H)), ("status", status, torch.int32, None),
+          ("workspace", workspace, None if workspace is None else workspace.dtype, None))
     if out is None:
         out = _empty(stream, (n_q, H, 512), torch.bfloat16, device)
     if lse is None:
         lse = _empty(stream, (n_q, H), torch.float32, device)
     a = MlaDecodeArgs()
     a.B, a.n_q, a.H, a.d_qk, a.d_v = B, n_q, H, 576, 512
-    a.page_size, a.max_pages, a.num_pages = kv_pool.shape[1], page_table.shape[1], kv_pool.shape[0]
+    a.num_pages, a.page_size, _ = kv_pool.shape
+    a.max_pages = page_table.shape[1]
     a.max_q_per_seq, a.softmax_scale = max_q_per_seq, float(softmax_scale)
     a.kv_dtype = DSA_FP8_E4M3 if fp8 else DSA_BF16
     if workspace is None and n_q:
         nbytes = lib.dsa_mla_decode_workspace_bytes(ctypes.byref(a))
         if nbytes:
             workspace = _empty(stream, (nbytes,), torch.uint8, device)
-    a.q, a.kv_pool, a.page_table = _addr(q), _addr(kv_pool), _addr(page_table)
-    a.seq_lens, a.q_start, a.out, a.lse, a.status = (_addr(seq_lens), _addr(q_start), _addr(out), _addr(lse),
-                                                     _addr(status))
+    a.q, a.kv_pool, a.page_table = q.data_ptr(), kv_pool.data_ptr(), page_table.data_ptr()
+    a.seq_lens = seq_lens.data_ptr()
+    a.q_start, a.out, a.lse, a.status = q_start.data_ptr(), out.data_ptr(), lse.data_ptr(), _addr(status)
     if workspace is not None:
-        a.workspace, a.workspace_bytes = _addr(workspace), workspace.numel() * workspace.element_size()
-    _check(lib.dsa_mla_decode(ctypes.byref(a), _stream(stream)), "dsa_mla_decode")
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(lib.dsa_mla_decode(ctypes.byref(a), _launch_stream(stream, device)), "dsa_mla_decode")
     return out, lse
 
 
@@ -589,17 +598,20 @@ def mla_prefill(q, kv, k_rope, q_start, kv_start, *, softmax_scale, max_q_per_se
     n_q, H, _ = q.shape
     n_kv = kv.shape[0]
     B = q_start.shape[0] - 1
-    _fits(("q", q, torch.bfloat16, None), ("kv", kv, torch.bfloat16, (n_kv, H, 256)),
-          ("q_start", q_start, torch.int32, None), ("kv_start", kv_start, torch.int32, (B + 1,)),
-          ("out", out, torch.bfloat16, (n_q, H, 128)), ("lse", lse, torch.float32, (n_q, H)),
-          ("status", status, torch.int32, None))
     if k_rope.dtype is not torch.bfloat16 or k_rope.shape != (n_kv, 64):
-        raise ValueError("k_rope must be bf16 of shape %s (got %s %s)" % ((n_kv, 64), k_rope.dtype, tuple(k_rope.shape)))
-    if n_kv > 1 and k_rope.stride(0) < 64 or n_kv > 0 and k_rope.stride(1) != 1:
+        raise ValueError("k_rope must be bf16 of shape %s (got %s %s)"
+                         % ((n_kv, 64), k_rope.dtype, tuple(k_rope.shape)))
+    stride, step = k_rope.stride()
+    if n_kv > 1 and stride < 64 or n_kv > 0 and step != 1:
         raise ValueError("the columns of k_rope must be adjacent, and its rows apart")
     max_q_per_seq = _host_max_q(q_start, max_q_per_seq, n_q)
     device = q.device
-    _on(device, kv, k_rope, q_start, kv_start, out, lse, status)
+    _fits(device, ("q", q, torch.bfloat16, None), ("kv", kv, torch.bfloat16, (n_kv, H, 256)),
+          ("q_start", q_start, torch.int32, None), ("kv_start", kv_start, torch.int32, (B + 1,)),
+          ("out", out, torch.bfloat16, (n_q, H, 128)), ("lse", lse, torch.float32, (n_q, H)),
+          ("status", status, torch.int32, None))
+    if k_rope.get_device() != device.index:
+        raise ValueError("k_rope is on %s, the others are on %s" % (k_rope.device, device))
     if out is None:
         out = _empty(stream, (n_q, H, 128), torch.bfloat16, device)
     if lse is None:
@@ -607,11 +619,11 @@ def mla_prefill(q, kv, k_rope, q_start, kv_start, *, softmax_scale, max_q_per_se
     a = MlaPrefillArgs()
     a.B, a.n_q, a.n_kv, a.H, a.d_nope, a.d_rope, a.d_v = B, n_q, n_kv, H, 128, 64, 128
     a.max_q_per_seq, a.softmax_scale = max_q_per_seq, float(softmax_scale)
-    a.k_rope_stride = k_rope.stride(0) if n_kv > 1 else 64
-    a.q, a.kv, a.k_rope = _addr(q), _addr(kv), k_rope.data_ptr()
-    a.q_start, a.kv_start, a.out, a.lse, a.status = (_addr(q_start), _addr(kv_start), _addr(out), _addr(lse),
-                                                     _addr(status))
-    _check(lib.dsa_mla_prefill(ctypes.byref(a), _stream(stream)), "dsa_mla_prefill")
+    a.k_rope_stride = stride if n_kv > 1 else 64
+    a.q, a.kv, a.k_rope = q.data_ptr(), kv.data_ptr(), k_rope.data_ptr()
+    a.q_start, a.kv_start, a.out, a.lse, a.status = (q_start.data_ptr(), kv_start.data_ptr(), out.data_ptr(),
+                                                     lse.data_ptr(), _addr(status))
+    _check(lib.dsa_mla_prefill(ctypes.byref(a), _launch_stream(stream, device)), "dsa_mla_prefill")
     return out, lse
 
 

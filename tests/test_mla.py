@@ -703,6 +703,8 @@ def test_bindings_refuse_a_stream_of_another_device():
 
     with pytest.raises(ValueError, match="stream"):
         dsa._empty(Stream(), (1,), torch.uint8, torch.device("cuda", 0))
+    with pytest.raises(ValueError, match="stream"):
+        dsa._launch_stream(Stream(), torch.device("cuda", 0))
 
 
 def test_bindings_refuse_what_does_not_fit():
