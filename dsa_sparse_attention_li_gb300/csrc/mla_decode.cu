@@ -32,9 +32,9 @@
 // cache the conversion: K's slots are free only between two Q.K^T, and its three parts, one after the
 // other, are 1,700 cycles each of loads, conversion and stores.
 //
-// Measured (join included): 32 sequences of 32,768, one token: 128 heads 234 us (5.2 TB/s, 78% of a copy's
-// rate; 1,250 TFLOP/s), 16 heads 214 us; one of 131,072: 56 us; one of 4,096, 16 heads: 18 us.  FP8: 32 of
-// 32,768, 128 heads 337 us, 16 ragged ones of up to 131,072 with two tokens and 64 heads 197 us.
+// Measured (join included): 32 sequences of 32,768, one token: 128 heads 230 us (5.3 TB/s, 79% of a copy's
+// rate; 1,270 TFLOP/s), 16 heads 214 us; one of 131,072: 56 us; one of 4,096, 16 heads: 18 us.  FP8: 32 of
+// 32,768, 128 heads 335 us, 16 ragged ones of up to 131,072 with two tokens and 64 heads 195 us.
 #include <algorithm>
 
 #include "dsa_internal.h"
@@ -722,17 +722,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
           const int pg = p.page_table[(size_t)w.b * p.max_pages + (pos0 >> 6)];
           if (pg < 0 || pg >= p.num_pages) keep = 0;
         }
-        float mx = -INFINITY;
-        if (__all_sync(0xffffffffu, keep == 64)) {
+        if (!__all_sync(0xffffffffu, keep == 64)) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c) mx = fmaxf(mx, __uint_as_float(sr[c]));
-        } else {
-#pragma unroll
-          for (int c = 0; c < 64; ++c) {
+          for (int c = 0; c < 64; ++c)
             if (c >= keep) sr[c] = 0xff800000u;
-            mx = fmaxf(mx, __uint_as_float(sr[c]));
-          }
         }
+        float m2[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 64; c += 2)
+          m2[(c >> 1) & 1] = max3(m2[(c >> 1) & 1], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+        float mx = fmaxf(m2[0], m2[1]);
         mx *= p.scale_log2;
         // one vote a tile; a warp whose wait gave up brings all to the second one, where they leave
         if (!named_barrier_and(2, 128, !*abort && !(active && mx > m_ref + kRescaleLog2))) {
@@ -764,16 +763,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
         }
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
         if (busy) {
-          float sum0 = 0.f, sum1 = 0.f;
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
-            const float a = fast_exp2(fmaf(__uint_as_float(sr[c]), p.scale_log2, -m_use));
-            const float b = fast_exp2(fmaf(__uint_as_float(sr[c + 1]), p.scale_log2, -m_use));
-            sum0 += a;
-            sum1 += b;
-            sr[c >> 1] = pack_bf16(a, b);  // P.V takes bf16 weights: 2^-8 relative each, unbiased
+            float2 e = fma2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), p.scale_log2, -m_use);
+            e.x = fast_exp2(e.x);
+            e.y = fast_exp2(e.y);
+            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], e);
+            sr[c >> 1] = pack_bf16(e.x, e.y);  // P.V takes bf16 weights: 2^-8 relative each, unbiased
           }
-          l += sum0 + sum1;
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
         // P is free once the previous tile's P.V has read it
         if (it > 0) warp_wait(&ctl->pv_done, (it - 1) & 1u, abort, p.status);
