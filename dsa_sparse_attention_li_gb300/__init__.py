@@ -126,8 +126,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
 
 
 def load_testhooks(build_if_missing: bool = True) -> ctypes.CDLL:
-    """The test build libdsa_testhooks.so (short device-side wait limits and
-    dsa_test_inject_stall; include/dsa_testhooks.h).  For the failure-handling tests only."""
+    """The test build libdsa_testhooks.so (short device-side wait limits and the entry points of
+    include/dsa_testhooks.h).  For the failure-handling tests only."""
     global _hooks
     if _hooks is not None:
         return _hooks
@@ -138,6 +138,9 @@ def load_testhooks(build_if_missing: bool = True) -> ctypes.CDLL:
     lib = _configure(ctypes.CDLL(HOOKS_LIB_PATH))
     lib.dsa_test_inject_stall.argtypes = [ctypes.c_int]
     lib.dsa_test_inject_stall.restype = None
+    I = ctypes.c_int
+    lib.dsa_test_mla_visible_columns.argtypes = [I, I, I, I, ctypes.c_void_p, I]
+    lib.dsa_test_mla_visible_columns.restype = I
     _hooks = lib
     return lib
 

@@ -5,7 +5,7 @@ library statically links the CUDA runtime, so it only needs the NVIDIA driver at
 
 The same sources compiled with -DDSA_TEST_HOOKS give libdsa_testhooks.so (objects in
 _build_hooks/): a test build whose device-side waits give up after 20 ms instead of 1 s and that
-exports dsa_test_inject_stall() (include/dsa_testhooks.h).  Only the failure-handling tests load
+exports the entry points of include/dsa_testhooks.h.  Only the failure-handling tests load
 it; the product path never does.
 """
 import concurrent.futures as cf

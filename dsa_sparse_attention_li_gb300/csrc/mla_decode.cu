@@ -204,6 +204,19 @@ DSA_DEV void warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int*
   __syncwarp();
 }
 
+// How many of the 64 positions from pos0 on, a page of the sequence, a query row may use: those up to `seen`,
+// none of a page that does not exist.  A row that is no one's (`owned` false: it counts as seeing everything)
+// goes on past the sequence's last page, whose table may end there, so its pages are not looked up.
+__host__ __device__ inline int visible_columns(bool owned, int seen, int pos0, bool check_pages, const int* pages,
+                                               int num_pages) {
+  const int keep = seen - pos0 < 64 ? seen - pos0 : 64;
+  if (check_pages && owned && keep > 0) {
+    const int pg = pages[pos0 >> 6];
+    if (pg < 0 || pg >= num_pages) return 0;
+  }
+  return keep;
+}
+
 // A sequence's tokens and length, checked: n = 0 where q_start is out of order.
 struct Seq {
   int s0, n, len;
@@ -717,11 +730,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_remote_relaxed(s_free + buf * 8);
         const int pos0 = i * kTile + half * 64;
-        int keep = min(64, seen - pos0);  // visible columns of ours
-        if (check_pages && keep > 0) {
-          const int pg = p.page_table[(size_t)w.b * p.max_pages + (pos0 >> 6)];
-          if (pg < 0 || pg >= p.num_pages) keep = 0;
-        }
+        const int keep = visible_columns(active, seen, pos0, check_pages, p.page_table + (size_t)w.b * p.max_pages,
+                                         p.num_pages);  // of ours
         if (!__all_sync(0xffffffffu, keep == 64)) {
 #pragma unroll
           for (int c = 0; c < 64; ++c)
@@ -1139,3 +1149,10 @@ dsa_status launch_mla_decode(const dsa_mla_decode_args& a, cudaStream_t stream, 
 }
 
 }  // namespace dsa
+
+#ifdef DSA_TEST_HOOKS
+extern "C" int dsa_test_mla_visible_columns(int owned, int seen, int pos0, int check_pages, const int32_t* pages,
+                                            int num_pages) {
+  return dsa::mlad::visible_columns(owned != 0, seen, pos0, check_pages != 0, pages, num_pages);
+}
+#endif

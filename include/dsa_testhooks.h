@@ -1,7 +1,7 @@
 /*
- * dsa_testhooks.h -- the one extra entry point of the TEST build of the library,
+ * dsa_testhooks.h -- the extra entry points of the TEST build of the library,
  * libdsa_testhooks.so (the same sources compiled with -DDSA_TEST_HOOKS).  The product library
- * libdsa.so does not export it.  The pages have no counterpart: this exists so that the
+ * libdsa.so does not export them.  The pages have no counterpart: they exist so that the
  * failure handling of the kernels can be exercised without faulting or hanging a GPU.
  *
  * In the test build every bounded device-side wait gives up after 20 ms (1 s in the product).
@@ -14,15 +14,23 @@
  * loops through their own bounded waits, every issued copy is drained, tensor memory is
  * freed, and the launch completes: the next call on the same context works.  The output of the
  * stalled launch is unspecified.  Host-side state, not thread-safe; a test setting.
+ *
+ * dsa_test_mla_visible_columns(): on the host, with host pointers, the rule by which dsa_mla_decode's
+ * softmax decides how many of a page's 64 positions a query row may use, lookup of the page id
+ * included.  `pages` is the sequence's row of the page table, pos0 the page's first position.
  */
 #ifndef DSA_TESTHOOKS_H
 #define DSA_TESTHOOKS_H
+
+#include <stdint.h>
 
 #ifdef __cplusplus
 extern "C" {
 #endif
 
 void dsa_test_inject_stall(int kernel);
+int dsa_test_mla_visible_columns(int owned, int seen, int pos0, int check_pages, const int32_t* pages,
+                                 int num_pages);
 
 #ifdef __cplusplus
 }
