@@ -295,6 +295,24 @@ struct Walk {
   DSA_DEV bool whole() const { return tile0 == 0 && tile1 == tiles; }
 };
 
+// Does the value part of a cache row, which a whole warp asks for, hold something that is not finite?
+template <bool KV8>
+DSA_DEV bool value_row_is_odd(const Params& p, int b, int pos, int lane) {
+  const size_t row = (size_t)p.page_table[(size_t)b * p.max_pages + (pos >> 6)] * 64 + (pos & 63);
+  uint4 v, w;
+  if constexpr (KV8) {
+    const uint8_t* r = p.kv + row * kKv8Row;
+    dequant16(reinterpret_cast<const uint4*>(r)[lane], reinterpret_cast<const float*>(r + kDqk)[lane >> 3], v, w);
+  } else {
+    const uint4* r = reinterpret_cast<const uint4*>(p.kv + row * (kDqk * 2));
+    v = r[lane];
+    w = r[lane + 32];
+  }
+  auto odd = [](uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; };   // carries out of an exponent of all ones
+  const uint32_t o = odd(v.x) | odd(v.y) | odd(v.z) | odd(v.w) | odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w);
+  return __any_sync(0xffffffffu, (o & 0x80008000u) != 0u);
+}
+
 template <bool KV8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
     mla_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
@@ -732,6 +750,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
         const int pos0 = i * kTile + half * 64;
         const int keep = visible_columns(active, seen, pos0, check_pages, p.page_table + (size_t)w.b * p.max_pages,
                                          p.num_pages);  // of ours
+        if (w.seen_last > w.seen_first && (i + 1) * kTile > w.seen_first) {
+          // rows that only some of the group's tokens see, whose values lose what is not finite (below).  An
+          // infinite value whose key scores -inf is lost with it: its weight is 0, and 0 times it is NaN, as
+          // it comes out in any other tile.  So such a score becomes NaN.
+          bool low = false;
+#pragma unroll
+          for (int c = 0; c < 64; ++c) low |= sr[c] == 0xff800000u;
+          if (__any_sync(0xffffffffu, active && low)) {
+            const int from = max(0, w.seen_first - pos0);
+            uint32_t lows[2] = {0u, 0u};
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (active && c >= from && c < keep && sr[c] == 0xff800000u) lows[c >> 5] |= 1u << (c & 31);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t odd = 0u;
+              for (uint32_t rest = __reduce_or_sync(0xffffffffu, lows[h]); rest != 0u; rest &= rest - 1u) {
+                const int c = __ffs((int)rest) - 1;
+                if (value_row_is_odd<KV8>(p, w.b, pos0 + h * 32 + c, lane)) odd |= 1u << c;
+              }
+              lows[h] &= odd;
+            }
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (lows[c >> 5] >> (c & 31) & 1u) sr[c] = 0x7fffffffu;
+          }
+        }
         if (!__all_sync(0xffffffffu, keep == 64)) {
 #pragma unroll
           for (int c = 0; c < 64; ++c)
@@ -796,7 +841,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
           // value rows that some row of the group does not see: a weight of 0 times what they hold
           // must be 0.  Past every token's end they become 0; among the tokens' own rows only what
           // is not finite does (the rows that see it get their NaN from the scores, whose keys are
-          // the same columns).
+          // the same columns: NaN as it is, +inf by the exponential, -inf see above).
           warp_wait(&ctl->edge, edges & 1u, abort, p.status);
           ++edges;
           const int r0 = max(0, w.seen_first - i * kTile);

@@ -241,7 +241,8 @@ dsa_status dsa_sfa_decode_static(const dsa_sfa_args* args, dsa_stream_t stream);
  *
  * A value that a token does not see never reaches its output, whatever it holds: cache rows past
  * a sequence's length may hold NaN or infinities, and so may the rows of a sequence's later tokens.
- * A NaN that a token does see makes its whole output row NaN or leaves NaN in the columns it is in.
+ * A NaN or an infinity that a token does see makes its whole output row (and lse) NaN, or leaves NaN in the
+ * columns it is in; an infinity among the d_qk - d_v last columns whose score is -inf has a weight of 0.
  * Rows of out and lse of tokens that no sequence owns (before q_start[0], from q_start[B] on) are
  * left as they were.  A length below 0 or above max_pages * page_size, a page id outside
  * [0, num_pages), and a q_start that decreases or leaves [0, n_q] set DSA_ERR_DEVICE_CHECK; the

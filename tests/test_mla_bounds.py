@@ -8,8 +8,7 @@ import pytest
 import torch
 
 import dsa_sparse_attention_li_gb300 as dsa
-from test_mla import (SCALE, check, definition, make_decode, make_prefill, run_decode, run_prefill, verify_decode,
-                      verify_prefill)
+from test_mla import SCALE, check, make_decode, run_decode, verify_decode
 
 
 @pytest.mark.parametrize("owned", [False, True], ids=["padding", "token"])
@@ -47,3 +46,69 @@ def test_decode_page_that_does_not_exist_in_a_table_that_ends_inside_a_tile(cuda
     c["rows"][1] = c["rows"][1][keep.cuda()]
     c["lens"][1] = int(keep.sum())
     verify_decode(c, out, lse)
+
+
+# ------------------------------------------------------------------------------------------
+# infinities among what a token sees
+# ------------------------------------------------------------------------------------------
+
+def put_inf(c, b, j, col, fp8):
+    """Column `col` of cache row j of sequence b becomes -inf, in the cache and in the reference's rows."""
+    row = c["pool"][int(c["pt"][b, j // 64]), j % 64]
+    if fp8:   # the only code of its 128 columns that is not zero, times a scale that overflows
+        tile = slice(col // 128 * 128, min(576, col // 128 * 128 + 128))
+        row[tile] = 0
+        row[col] = 0xFE   # -448
+        row[576 + col // 128 * 4:580 + col // 128 * 4] = torch.tensor([3.0e38], device="cuda").view(torch.uint8)
+        c["rows"][b][j, tile] = 0
+    else:
+        row[col] = -math.inf
+    c["rows"][b][j, col] = -math.inf
+
+
+def ieee(q, k, v):
+    """Attention of every row of q [n, d] over all of k [L, d], v [L, dv], in 64 bits as the formula stands: a
+    weight of 0 times an infinite value is NaN, and so is the difference of two infinities."""
+    z = (q @ k.T) * SCALE
+    m = z.amax(1, keepdim=True)
+    e = torch.exp(z - m)
+    s = e.sum(1, keepdim=True)
+    mag = (q.abs() @ k.abs().nan_to_num(0, 0, 0).T * SCALE).amax(1)
+    return (e / s) @ v, (m + torch.log(s))[:, 0], torch.nan_to_num(e / s) @ v.abs().nan_to_num(0, 0, 0), mag
+
+
+def check_seen(got, lse, want, want_lse, A, mag, n_products, length):
+    """Where the definition gives NaN, so does the kernel; what it gives else is right, unless the row holds a
+    NaN or an infinity, which may make all of it NaN."""
+    odd = ~torch.isfinite(want).all(1)
+    assert torch.isnan(got[~torch.isfinite(want)]).all()
+    check(got[~odd], lse[~odd], want[~odd], want_lse[~odd], A[~odd], mag[~odd], n_products, length)
+    tol = A * (3 * 2.0 ** -8 + 2 * n_products * 2.0 ** -24 * mag + 2.0 ** -21 + length * 2.0 ** -24)[:, None] + 1e-30
+    fine = torch.isfinite(want) & ~torch.isnan(got)
+    assert torch.all((got.double() - want).abs()[fine] <= tol[fine])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("col", [7, 300, 520], ids=["value0", "value1", "rope"])
+@pytest.mark.parametrize("j", [100, 400, 450, 497])
+def test_decode_infinity_that_a_token_sees(cuda_lib, fp8, col, j):
+    """Row j holds -inf: a score of -inf for the even heads, of +inf for the odd ones.  j lies in a tile that
+    all tokens see to its end (100), or in the last one, seen by all (400, 450) or by the last three
+    tokens only: what a token gets does not depend on that."""
+    c = make_decode([500], [4], 16, fp8)
+    c["q"][..., col] = torch.tensor([1.0, -1.0], device="cuda").repeat(8)
+    clean = run_decode(c)
+    put_inf(c, 0, j, col, fp8)
+    out, lse, status = run_decode(c)
+    assert status == 0
+    for t in range(4):
+        seen = 497 + t
+        if j >= seen:
+            assert torch.equal(out[t], clean[0][t]) and torch.equal(lse[t], clean[1][t])
+            continue
+        kv = c["rows"][0][:seen]
+        want = ieee(c["q"][t].double(), kv, kv[:, :512])
+        assert torch.isnan(want[0][1::2]).all()
+        assert torch.isnan(want[0][::2]).any(1).all() == (col < 512)
+        check_seen(out[t], lse[t], *want, 576, seen)
