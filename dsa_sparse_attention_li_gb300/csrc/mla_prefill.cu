@@ -241,21 +241,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) {
     // ---------------- items and loads
     uint32_t edges = 0, loads_a = 0, loads_b = 0;   // edge tiles, and loads of A's and B's queries, so far
+    // After a wait that gave up nothing is armed any more, and nobody else arrives on what is armed: an
+    // arrival on a barrier whose bytes are still on their way, its only expected one, faulted.
     auto load = [&](const Item& w) {
       // (A's last product with its queries is half a step or more before B's, whose new queries are
       // waited for after the first keys and values)
       auto load_q = [&](int x, uint32_t& loads) {
-        if (loads > 0) mbar_wait_fast(&ctl->q_empty[x], (loads - 1) & 1u, abort, p.status);
+        if (loads > 0 && !mbar_wait_fast(&ctl->q_empty[x], (loads - 1) & 1u, abort, p.status)) return;
         ++loads;
         mbar_arrive_expect_tx(&ctl->q_full[x], 3 * kBlock);
         for (int c = 0; c < 3; ++c)
           tma_load_3d(smem + Layout::q + (x * 3 + c) * kBlock, &tm_q, &ctl->q_full[x], c * 64, w.h, w.tok + x * kRows);
       };
       load_q(0, loads_a);
-      // block i may take its slot once block i - 8 is used up
-      auto arm = [&](uint32_t i, uint64_t* bar) {
+      // block i may take its slot once block i - 8 is used up; null: that wait gave up
+      auto arm = [&](uint32_t i, uint64_t* bar) -> uint8_t* {
         const uint32_t c = i % kBlocks;
-        if (i >= kBlocks) mbar_wait_fast(&ctl->empty[c], (i / kBlocks - 1) & 1u, abort, p.status);
+        if (i >= kBlocks && !mbar_wait_fast(&ctl->empty[c], (i / kBlocks - 1) & 1u, abort, p.status)) return nullptr;
         mbar_arrive_expect_tx(bar, kBlock);
         return smem + Layout::ring + c * kBlock;
       };
@@ -265,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t i = k_block(at, j) + c;
           uint64_t* bar = &ctl->full[i % kBlocks];
           uint8_t* dst = arm(i, bar);
+          if (dst == nullptr) return;
           if (c < 2)
             tma_load_3d(dst, &tm_k, bar, c * 64, w.h, key);
           else
@@ -274,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t i = v_block(at, j) + c;
           uint64_t* bar = j < w.edge0 ? &ctl->full[i % kBlocks] : &ctl->edge[edges & 1u][c];
           uint8_t* dst = arm(i, bar);
+          if (dst == nullptr) return;
           for (int u = 0; u < 2; ++u)
             tma_load_3d(dst + u * (kBlock / 2), &tm_v, bar, 128 + u * 64, w.h, key + c * 64);
         }
@@ -288,10 +292,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         end = line.chunk(p, b0, end, lane, true);
     if (!tell) line.chunk(p, 0, 0, lane, false);
     uint32_t item = 0;
-    // room for item number `item` in its slot, two items back
+    // room for item number `item` in its slot, two items back; false: a wait of the CTA gave up, and the slot
+    // may still be read
     auto room = [&] {
       if (item > 1) mbar_wait_fast(&ctl->item_empty[item & 1u], ((item >> 1) - 1) & 1u, abort, p.status);
-      __syncwarp();
+      return !__any_sync(0xffffffffu, *abort);
     };
     int index = (int)blockIdx.x;
     for (uint32_t asked = 0; index >= 0; ++asked) {
@@ -301,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       Item w;
       if (line.find(p, index, lane, w)) {
-        room();
+        if (!room()) break;
         if (lane == 0) {
           ctl->item[item & 1u] = w;
           mbar_arrive(&ctl->item_full[item & 1u]);
@@ -317,8 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
     }
-    room();
-    if (lane == 0) {
+    if (room() && lane == 0) {   // (else the others leave by the abort flag)
       ctl->item[item & 1u].tiles = 0;
       mbar_arrive(&ctl->item_full[item & 1u]);
     }
@@ -339,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&ctl->item_empty[item & 1u]);
       for (int j = edge0; j < tiles; ++j, ++edges) {
         warp_wait(&ctl->edge[edges & 1u][c], (edges >> 1) & 1u, abort, p.status);
+        if (__any_sync(0xffffffffu, *abort)) break;   // (the tile may never come; see the loads)
         const uint32_t t = at / 5u + j, slot = (v_block(at, j) + c) % kBlocks;
         const int rows = min(max(n_key - j * kKeys - c * 64, 0), 64);   // of the sequence
         uint8_t* half = smem + Layout::ring + slot * kBlock;

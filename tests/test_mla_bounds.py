@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import dsa_sparse_attention_li_gb300 as dsa
-from test_mla import SCALE, check, make_decode, run_decode, verify_decode
+from test_mla import SCALE, check, make_decode, make_prefill, run_decode, run_prefill, verify_decode, verify_prefill
 
 
 @pytest.mark.parametrize("owned", [False, True], ids=["padding", "token"])
@@ -112,3 +112,29 @@ def test_decode_infinity_that_a_token_sees(cuda_lib, fp8, col, j):
         assert torch.isnan(want[0][1::2]).all()
         assert torch.isnan(want[0][::2]).any(1).all() == (col < 512)
         check_seen(out[t], lse[t], *want, 576, seen)
+
+
+# ------------------------------------------------------------------------------------------
+# waits that run out
+# ------------------------------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,keys,H", [([700, 300], [900, 300], 4), ([900], [900], 4), ([300, 20], [3000, 20], 128),
+                                        ([257, 129, 2], [257, 400, 90], 128)], ids=str)
+def test_prefill_waits_that_run_out_at_any_moment(cuda_lib, monkeypatch, new, keys, H):
+    """The first CTA's products never start, so that all its other waits give up, each at its own moment: the
+    loads with part of the ring on its way, the edge tiles' warps ahead of them.  Each launch ends and reports
+    it, whatever the order, and the next call is right."""
+    c = make_prefill(new, keys, H)
+    hooks = dsa.load_testhooks()
+    with monkeypatch.context() as m:
+        m.setattr(dsa, "_lib", hooks)
+        for _ in range(12):
+            hooks.dsa_test_inject_stall(4)
+            try:
+                assert run_prefill(c)[2] == dsa.DSA_ERR_TIMEOUT
+            finally:
+                hooks.dsa_test_inject_stall(0)
+        out, lse, status = run_prefill(c)
+    assert status == 0
+    verify_prefill(c, out, lse)
