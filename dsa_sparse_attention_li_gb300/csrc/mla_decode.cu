@@ -60,6 +60,7 @@ constexpr int kVHalfBytes = 2 * kBlockBytes;   // 128 columns of a page
 constexpr int kVPageBytes = 2 * kVHalfBytes;
 constexpr int kPrefetch = 3;    // tiles
 constexpr float kRescaleLog2 = 8.0f;
+constexpr float kNoScore = -3.402823466e38f;   // log-sum-exp of a piece with positions, but no score above -inf
 constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 
 struct Params {
@@ -294,6 +295,17 @@ struct Walk {
   }
   DSA_DEV bool whole() const { return tile0 == 0 && tile1 == tiles; }
 };
+
+// Does a query row, which sees the sequence up to `seen`, see any position of the piece?
+DSA_DEV bool sees_any(const Params& p, const Walk& w, int seen, bool check_pages) {
+  const int from = w.tile0 * kTile, to = min(seen, w.tile1 * kTile);
+  if (!check_pages) return from < to;
+  for (int i = from >> 6; i * 64 < to; ++i) {
+    const int pg = p.page_table[(size_t)w.b * p.max_pages + i];
+    if (pg >= 0 && pg < p.num_pages) return true;
+  }
+  return false;
+}
 
 // Does the value part of a cache row, which a whole warp asks for, hold something that is not finite?
 template <bool KV8>
@@ -873,9 +885,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
       if (!ok) break;
       tc_fence_after();
       const float l_all = ctl->x[row] + ctl->x[row + 64];
-      const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
-      const float lse2 = l_all == 0.f ? -INFINITY : m_ref + log2f(l_all);
+      float inv = l_all == 0.f ? 0.f : 1.f / l_all;
+      float lse2 = l_all == 0.f ? -INFINITY : m_ref + log2f(l_all);
       const bool whole = w.whole();
+      // a row that sees something and has no weight: its scores are all -inf, or +inf by the scale
+      if (active && l_all == 0.f && sees_any(p, w, seen, check_pages)) {
+        lse2 = whole || m_ref > 0.f ? __uint_as_float(0x7fffffffu) : kNoScore;
+        if (whole) inv = lse2;
+      }
       const size_t slot = (size_t)pair * 2 + (w.first ? 0 : 1);
       if (busy) {
         const size_t grow = (size_t)w.t0 * p.H + mrow;
@@ -962,7 +979,8 @@ DSA_DEV void add_to(float4& o, float e, const float4& x) {
 }
 
 // Weights of the pieces whose log-sum-exps (log2) start in slot z, relative to the largest: into wgt,
-// by a whole warp; returns the reference (NaN if a piece is, 0 if nothing was seen) and their sum.
+// by a whole warp; returns the reference (NaN if a piece is, 0 if nothing was seen, kNoScore if no
+// score is above -inf) and their sum.
 // (Out of line: inlined twice it cost the join half of its registers.)
 __device__ __noinline__ float2 join_weights(const float* lse, int z, int parts, int rows, float* wgt, int lane) {
   float top = -INFINITY;
@@ -998,7 +1016,7 @@ struct Pieces {
   int4 j;
   int r, col4, lane;
   float* wgt;
-  float m, sum;      // reference of the weights (NaN if a piece has one), their sum
+  float m, sum;      // reference of the weights (see join_weights), their sum
   float4 o[C];
 
   // piece 0 lies in slot j.z, the following ones each at the start of the next pair's range
@@ -1035,13 +1053,15 @@ struct Pieces {
     }
   }
   DSA_DEV void finish() const {
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const bool none = m == kNoScore;   // a softmax of -inf only: NaN
+    const float inv = none ? __uint_as_float(0x7fffffffu) : sum == 0.f ? 0.f : 1.f / sum;
     const size_t grow = (size_t)j.x * p.H + r;
 #pragma unroll
     for (int c = 0; c < C; ++c)
       reinterpret_cast<uint2*>(p.out + grow * kDv)[col4 + c * 32] =
           make_uint2(pack_bf16(o[c].x * inv, o[c].y * inv), pack_bf16(o[c].z * inv, o[c].w * inv));
-    if (col4 == 0 && p.lse) p.lse[grow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+    if (col4 == 0 && p.lse)
+      p.lse[grow] = none ? inv : sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
   }
 };
 

@@ -237,7 +237,8 @@ dsa_status dsa_sfa_decode_static(const dsa_sfa_args* args, dsa_stream_t stream);
  *   out[t][h][:] = sum_j exp(z_j - m) kv[j][0:d_v] / sum_j exp(z_j - m),   m = max_j z_j
  *   lse[t][h]    = m + ln(sum_j exp(z_j - m))
  * q is the query with the keys' up-projection absorbed; the value is the leading d_v columns of
- * the latent row.  A token that sees nothing (p < 0) gets out = 0 and lse = -inf.
+ * the latent row.  A token that sees nothing (p < 0, or only pages that do not exist) gets out = 0 and
+ * lse = -inf; one whose logits, which are held in fp32, are all -inf, or one of them +inf, gets NaN in both.
  *
  * A value that a token does not see never reaches its output, whatever it holds: cache rows past
  * a sequence's length may hold NaN or infinities, and so may the rows of a sequence's later tokens.

@@ -8,7 +8,8 @@ import pytest
 import torch
 
 import dsa_sparse_attention_li_gb300 as dsa
-from test_mla import SCALE, check, make_decode, make_prefill, run_decode, run_prefill, verify_decode, verify_prefill
+from test_mla import (SCALE, check, definition, make_decode, make_prefill, run_decode, run_prefill,
+                      verify_decode, verify_prefill)
 
 
 @pytest.mark.parametrize("owned", [False, True], ids=["padding", "token"])
@@ -112,6 +113,59 @@ def test_decode_infinity_that_a_token_sees(cuda_lib, fp8, col, j):
         assert torch.isnan(want[0][1::2]).all()
         assert torch.isnan(want[0][::2]).any(1).all() == (col < 512)
         check_seen(out[t], lse[t], *want, 576, seen)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_decode_scores_that_are_all_minus_infinity(cuda_lib, fp8):
+    """A token that sees positions but no finite score has no softmax: NaN, and not the zeros of a token
+    that sees nothing.  Positions that score -inf beside others have a weight of 0."""
+    lens, new = [1, 70, 9000, 3, 4000, 9000], [1, 2, 1, 5, 1, 1]
+    c = make_decode(lens, new, 16, fp8, tail=0)
+    c["q"][..., 520] = 1.0
+    for b, part in ((0, (0, 1)), (1, (0, 70)), (2, (0, 9000)), (3, (0, 3)), (4, (0, 2500)), (5, (4444, 9000))):
+        c["rows"][b][part[0]:part[1], 512:] = 0     # as put_inf, for many rows at once
+        c["rows"][b][part[0]:part[1], 520] = -math.inf
+        j = torch.arange(*part, device="cuda")
+        pool, at = c["pool"].view(-1, c["pool"].shape[-1]), c["pt"][b].long()[j // 64] * 64 + j % 64
+        if fp8:
+            row = pool[at]
+            row[:, 512:576] = 0
+            row[:, 520] = 0xFE
+            row[:, 592:596] = torch.tensor([3.0e38], device="cuda").view(torch.uint8)
+            pool[at] = row
+        else:
+            pool[at, 512:] = 0
+            pool[at, 520] = -math.inf
+    out, lse, status = run_decode(c)
+    assert status == 0
+    for t in (0, 1, 2, 3, 6, 7, 8):
+        assert torch.isnan(out[t]).all() and torch.isnan(lse[t]).all(), t
+    assert torch.all(out[4:6] == 0) and torch.isneginf(lse[4:6]).all()
+    for t, b, part in ((9, 4, slice(2500, 4000)), (10, 5, slice(0, 4444))):
+        kv = c["rows"][b][part]
+        want = definition(c["q"][t].double(), kv, kv[:, :512], torch.ones((16, len(kv)), dtype=torch.bool, device="cuda"),
+                          SCALE)
+        check(out[t], lse[t], *want, 576, lens[b])
+    # none of whose pages exist: nothing is seen, whatever the scores
+    c["pt"][2], c["pt"][0] = -1, 2 ** 30
+    out, lse, status = run_decode(c)
+    assert status == dsa.DSA_ERR_DEVICE_CHECK
+    for t in (0, 3):
+        assert torch.all(out[t] == 0) and torch.isneginf(lse[t]).all()
+    # some of them do, with scores of -inf only
+    c["pt"][2, 3] = c["pt"][5, 100]
+    out, lse, status = run_decode(c)
+    assert torch.isnan(out[3]).all() and torch.isnan(lse[3]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_decode_scores_beyond_fp32_give_nan(cuda_lib, fp8):
+    """Logits of 1e39 and more are infinite in fp32: the output says so."""
+    out, lse, status = run_decode(make_decode([5000, 90], [1, 2], 16, fp8, tail=0), softmax_scale=1.9e38)
+    assert status == 0
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
 
 
 # ------------------------------------------------------------------------------------------
