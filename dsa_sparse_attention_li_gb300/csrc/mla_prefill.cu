@@ -565,7 +565,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n > 0) {
         warp_wait(&ctl->pv_done[x], (done - 1) & 1u, abort, p.status);
         tc_fence_after();
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        // (no weight, but something seen: the scores are all -inf, or +inf by the scale)
+        const float none = seen > 0 ? __uint_as_float(0x7fffffffu) : 0.f;
+        const float inv = l == 0.f ? none : 1.f / l;
         const size_t to = (size_t)(w.tok + x * kRows + row) * p.H + w.h;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -580,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             st_global_v8(p.out + to * kDv + c * 32 + 16, o + 8);
           }
         }
-        if (row < rows && p.lse) p.lse[to] = l == 0.f ? -INFINITY : m_ref * 0.69314718055994531f + logf(l);
+        if (row < rows && p.lse) p.lse[to] = l == 0.f ? (seen > 0 ? none : -INFINITY) : m_ref * 0.69314718055994531f + logf(l);
       }
       at += 5u * w.tiles;
       __syncwarp();

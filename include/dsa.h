@@ -292,8 +292,8 @@ dsa_status dsa_mla_decode(const dsa_mla_decode_args* args, dsa_stream_t stream);
  *   z_j = softmax_scale * (q[t][h][0:128] . kv[j][h][0:128] + q[t][h][128:192] . k_rope[j])
  *   out[t][h][:] = softmax(z) . kv[:][h][128:256],   lse[t][h] = ln sum_j exp(z_j)
  * With q_absorbed = [W_uk[h]^T q_nope | q_rope], dsa_mla_decode followed by W_uv gives the same
- * output up to rounding.  A token that sees nothing gets out = 0 and lse = -inf; tokens that no
- * sequence owns keep their rows.  Keys and values of other sequences, and of later tokens, never
+ * output up to rounding.  A token that sees nothing gets out = 0 and lse = -inf, one whose logits (fp32)
+ * are all -inf, or one of them +inf, NaN in both; tokens that no sequence owns keep their rows.  Keys and values of other sequences, and of later tokens, never
  * reach a token's output, whatever they hold; a NaN or infinity among the values that a token
  * does see may make its whole output row NaN.  A q_start or kv_start that decreases or leaves its
  * array sets DSA_ERR_DEVICE_CHECK, and the sequence is skipped; so do more tokens in a sequence

@@ -168,6 +168,36 @@ def test_decode_scores_beyond_fp32_give_nan(cuda_lib, fp8):
     assert torch.isnan(out).all() and torch.isnan(lse).all()
 
 
+@pytest.mark.gpu
+def test_prefill_scores_beyond_fp32_give_nan(cuda_lib):
+    out, lse, status = run_prefill(make_prefill([130], [400], 2, tail=0), softmax_scale=1.9e38)
+    assert status == 0
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.gpu
+def test_prefill_scores_that_are_all_minus_infinity(cuda_lib):
+    """As for decode: sequence 1 has no finite score, 2 has some, two tokens of 3 see nothing and the others
+    no finite score."""
+    new, keys = [40, 300, 200, 5], [40, 400, 200, 3]
+    c = make_prefill(new, keys, 3, tail=0)
+    c["q"][..., 130] = 1.0
+    for rows in (slice(40, 440), slice(440, 500), slice(640, 643)):
+        c["rope"][rows, 2] = -math.inf
+    out, lse, status = run_prefill(c)
+    assert status == 0
+    nan = torch.cat([torch.arange(40, 340), torch.arange(340, 400), torch.arange(542, 545)]).cuda()
+    assert torch.isnan(out[nan]).all() and torch.isnan(lse[nan]).all()
+    assert torch.all(out[540:542] == 0) and torch.isneginf(lse[540:542]).all()
+    ok = torch.cat([torch.arange(0, 40), torch.arange(400, 540)]).cuda()
+    assert torch.isfinite(out[ok].float()).all() and torch.isfinite(lse[ok]).all()
+    for h in range(3):
+        kv, rope = c["kv"][500:640, h].double(), c["rope"][500:640].double()
+        seen = torch.arange(140, device="cuda")[None] <= torch.arange(140, device="cuda")[:, None]
+        want = definition(c["q"][400:540, h].double(), torch.cat([kv[:, :128], rope], 1), kv[:, 128:], seen, SCALE)
+        check(out[400:540, h], lse[400:540, h], *want, 192, 200)
+
+
 # ------------------------------------------------------------------------------------------
 # waits that run out
 # ------------------------------------------------------------------------------------------
