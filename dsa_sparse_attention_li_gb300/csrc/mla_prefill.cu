@@ -121,11 +121,20 @@ DSA_DEV uint32_t v_block(uint32_t at, int j) { return at + 5u * j + 3u; }
 
 // The line of all sequences' token blocks, one sequence after the other, of which p.blocks is the
 // host's bound; the loading warp looks items up in it.  Lane i holds sequence b0 + i.
+// The bound holds for sequences that share no token.  Where q_start falls, two could claim the same ones:
+// the first has them, and one that starts before the end of an earlier one is skipped.
 struct Line {
   int s0, s1, k0, k1, first, count;   // its ranges, and its blocks in the line
+  int ends;      // where the sequences so far end, at most
+  bool rising;   // no q_start so far was out of order
 
-  // Sequences b0 .. b0 + 31, which the line reaches at `before`; returns where they end.
+  // Sequences b0 .. b0 + 31, which the line reaches at `before` (the chunks in their order, the first
+  // one at 0); returns where they end.
   DSA_DEV int chunk(const Params& p, int b0, int before, int lane, bool tell) {
+    if (b0 == 0) {
+      ends = 0;
+      rising = true;
+    }
     const int b = b0 + lane;
     s0 = s1 = k0 = k1 = 0;
     if (b < p.B) {
@@ -134,7 +143,18 @@ struct Line {
       k0 = p.kv_start[b];
       k1 = p.kv_start[b + 1];
     }
-    const bool fine = s0 >= 0 && s1 >= s0 && s1 <= p.n_q && k0 >= 0 && k1 >= k0 && k1 <= p.n_kv;
+    bool fine = s0 >= 0 && s1 >= s0 && s1 <= p.n_q;
+    const int end = fine && s1 > s0 ? s1 : 0;
+    rising = rising && __all_sync(0xffffffffu, fine);   // (each starts where the one before it ends)
+    if (!rising) {
+      int upto = max(ends, __shfl_up_sync(0xffffffffu, end, 1));   // the earlier ones' ends
+      if (lane == 0) upto = ends;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) upto = max(upto, __shfl_up_sync(0xffffffffu, upto, o));
+      fine = fine && s0 >= upto;
+    }
+    ends = max(ends, __reduce_max_sync(0xffffffffu, end));
+    fine = fine && k0 >= 0 && k1 >= k0 && k1 <= p.n_kv;
     if (tell && (!fine || s1 - s0 > p.max_q)) report(p.status, kStatusDeviceCheck);
     count = fine ? (s1 - s0 + kTokens - 1) / kTokens : 0;
     int upto = count;

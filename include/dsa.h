@@ -247,7 +247,8 @@ dsa_status dsa_sfa_decode_static(const dsa_sfa_args* args, dsa_stream_t stream);
  * Rows of out and lse of tokens that no sequence owns (before q_start[0], from q_start[B] on) are
  * left as they were.  A length below 0 or above max_pages * page_size, a page id outside
  * [0, num_pages), and a q_start that decreases or leaves [0, n_q] set DSA_ERR_DEVICE_CHECK; the
- * length is clamped, the page's positions are skipped, the sequence is skipped.
+ * length is clamped, the page's positions are skipped, the sequence is skipped.  (Tokens that two of the
+ * remaining sequences then claim get rows of either.)
  *
  * Workspace: dsa_mla_decode_workspace_bytes() bytes, no initial value; a call leaves nothing in it
  * that a later call needs.  Calls that may overlap on the GPU need one each.
@@ -296,8 +297,9 @@ dsa_status dsa_mla_decode(const dsa_mla_decode_args* args, dsa_stream_t stream);
  * are all -inf, or one of them +inf, NaN in both; tokens that no sequence owns keep their rows.  Keys and values of other sequences, and of later tokens, never
  * reach a token's output, whatever they hold; a NaN or infinity among the values that a token
  * does see may make its whole output row NaN.  A q_start or kv_start that decreases or leaves its
- * array sets DSA_ERR_DEVICE_CHECK, and the sequence is skipped; so do more tokens in a sequence
- * than max_q_per_seq, which are computed all the same.
+ * array sets DSA_ERR_DEVICE_CHECK, and the sequence is skipped; so is, after a q_start that decreases, a
+ * sequence whose tokens start before an earlier one's end (a token belongs to the first that claims it).
+ * More tokens in a sequence than max_q_per_seq set it too, and are computed all the same.
  *
  * Supported: d_nope 128, d_rope 64, d_v 128; 1 <= H <= 1024; bf16; (n_q / 256 + B) * max(H, 16) below
  * 2^31; q, kv and k_rope 16-byte aligned, out 32-byte aligned, k_rope_stride a multiple of 8.

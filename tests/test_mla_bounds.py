@@ -199,6 +199,70 @@ def test_prefill_scores_that_are_all_minus_infinity(cuda_lib):
 
 
 # ------------------------------------------------------------------------------------------
+# bounds out of order
+# ------------------------------------------------------------------------------------------
+
+def starts(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def check_prefill_rows(c, out, lse, t, n, k, L):
+    """Tokens t .. t + n - 1 as the last ones of the keys k .. k + L - 1."""
+    seen = torch.arange(L, device="cuda")[None] <= (L - n + torch.arange(n, device="cuda"))[:, None]
+    for h in range(c["H"]):
+        kv = c["kv"][k:k + L, h].double()
+        keys = torch.cat([kv[:, :128], c["rope"][k:k + L].double()], 1)
+        want = definition(c["q"][t:t + n, h].double(), keys, kv[:, 128:], seen, SCALE)
+        check(out[t:t + n, h], lse[t:t + n, h], *want, 192, L)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("more", [0, 40], ids=["few", "many"])
+def test_prefill_falling_q_start(cuda_lib, more):
+    """A token belongs to the first sequence that claims it; sequences that fall, and those that start
+    before another's end, are skipped, and the others are whole.  `more` empty sequences in front take
+    the batch beyond the lanes of a warp."""
+    c = make_prefill([1000, 600], [1000, 600], 2)
+
+    def run(q_start, kv_start, owned):
+        c["q_start"], c["kv_start"] = (starts(*x[:1] * more, *x) for x in (q_start, kv_start))
+        out, lse, status = run_prefill(c, max_q_per_seq=1600)
+        assert status == dsa.DSA_ERR_DEVICE_CHECK
+        free = torch.ones(1602, dtype=torch.bool, device="cuda")
+        for t, n, k, L in owned:
+            check_prefill_rows(c, out, lse, t, n, k, L)
+            free[t:t + n] = False
+        assert torch.all(out[free] == 5.0) and torch.all(lse[free] == 6.0)
+
+    run([0, 1000, 0, 1000], [0, 1000, 1000, 1600], [(0, 1000, 0, 1000)])
+    run([0, 1000, 0, 1000, 0, 1000, 0, 1000], [0, 1000, 1000, 1000, 1000, 1000, 1000, 1000], [(0, 1000, 0, 1000)])
+    run([0, 300, 200, 1600], [0, 300, 300, 1600], [(0, 300, 0, 300)])
+    run([0, 300, 250, 300, 900], [0, 300, 300, 300, 900], [(0, 300, 0, 300), (300, 600, 300, 600)])
+    run([500, 0, 1000], [0, 0, 1000], [(0, 1000, 0, 1000)])
+    run([0, 300, 10 ** 6, 300, 900], [0, 300, 300, 300, 900], [(0, 300, 0, 300), (300, 600, 300, 600)])
+    run([-7, 300, 900], [0, 300, 900], [(300, 600, 300, 600)])
+    run([0, 1000, 1600], [0, 1000, 900], [(0, 1000, 0, 1000)])
+
+
+@pytest.mark.gpu
+def test_prefill_falling_q_start_in_front_of_many_sequences(cuda_lib):
+    """An error in the first 32 sequences is remembered in the following ones."""
+    new = [40] * 100
+    c = make_prefill(new, new, 1)
+    q_start = [40 * i for i in range(101)]
+    q_start[5] = 3900      # sequence 4 claims 160 .. 3899, sequence 5 falls, the ones up to 3899 come too late
+    c["q_start"] = starts(*q_start)
+    out, lse, status = run_prefill(c, max_q_per_seq=4000)
+    assert status == dsa.DSA_ERR_DEVICE_CHECK
+    for b in (0, 3, 98, 99):
+        check_prefill_rows(c, out, lse, 40 * b, 40, 40 * b, 40)
+    # of sequence 4's 3,740 tokens the last 40 see its 40 keys, the others nothing
+    assert torch.all(out[160:3860] == 0) and torch.isneginf(lse[160:3860]).all()
+    check_prefill_rows(c, out, lse, 3860, 40, 160, 40)
+    assert torch.all(out[3900:3920] == 5.0) and torch.all(lse[3900:3920] == 6.0)
+
+
+# ------------------------------------------------------------------------------------------
 # waits that run out
 # ------------------------------------------------------------------------------------------
 
