@@ -533,13 +533,10 @@ def mla_decode_workspace_bytes(n_q: int, H: int, max_q_per_seq: int) -> int:
     return int(load().dsa_mla_decode_workspace_bytes(ctypes.byref(a)))
 
 
-def _host_max_q(q_start, max_q_per_seq, n_q):
-    """The host's bound of a sequence's tokens (reading device tensors would synchronise)."""
+def _token_bound(max_q_per_seq, n_q):
+    """The host's bound of a sequence's tokens, at least 1."""
     if max_q_per_seq is None:
-        if q_start.is_cuda:
-            raise ValueError("max_q_per_seq is required with device tensors (reading it back "
-                             "would synchronise the stream)")
-        max_q_per_seq = int((q_start[1:] - q_start[:-1]).max())
+        raise ValueError("max_q_per_seq is required (reading it from q_start would synchronise the stream)")
     return max(1, min(int(max_q_per_seq), n_q))
 
 
@@ -547,8 +544,8 @@ def mla_decode(q, kv_pool, page_table, seq_lens, q_start, *, softmax_scale, max_
                lse=None, status=None, workspace=None, stream=None):
     """Dense latent attention, absorbed form: every query token attends to all positions it sees of
     the paged latent cache (bf16 [num_pages, 64, 576], or FP8 rows uint8 [num_pages, 64, 608]).
-    Returns (out [n_q, H, 512] bf16, lse [n_q, H] fp32).  ``max_q_per_seq`` bounds the tokens of a
-    sequence; ``workspace`` (mla_decode_workspace_bytes) is allocated here unless given."""
+    Returns (out [n_q, H, 512] bf16, lse [n_q, H] fp32).  ``max_q_per_seq`` (required) bounds the tokens of
+    a sequence; ``workspace`` (mla_decode_workspace_bytes) is allocated here unless given."""
     lib = load()
     if q.dim() != 3 or q.shape[2] != 576:
         raise ValueError("q must have shape [n_q, H, 576] (got %s)" % (tuple(q.shape),))
@@ -559,13 +556,13 @@ def mla_decode(q, kv_pool, page_table, seq_lens, q_start, *, softmax_scale, max_
         raise ValueError("kv_pool must have shape [num_pages, page_size, 576] (bf16) or [.., 608] (uint8)")
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must have one row per sequence")
-    max_q_per_seq = _host_max_q(q_start, max_q_per_seq, n_q)
     device = q.device
     _fits(device, ("q", q, torch.bfloat16, None), ("kv_pool", kv_pool, torch.uint8 if fp8 else torch.bfloat16, None),
           ("page_table", page_table, torch.int32, None), ("seq_lens", seq_lens, torch.int32, (B,)),
           ("q_start", q_start, torch.int32, (B + 1,)), ("out", out, torch.bfloat16, (n_q, H, 512)),
           ("lse", lse, torch.float32, (n_q, H)), ("status", status, torch.int32, None),
           ("workspace", workspace, None if workspace is None else workspace.dtype, None))
+    bound = _token_bound(max_q_per_seq, n_q)
     if out is None:
         out = _empty(stream, (n_q, H, 512), torch.bfloat16, device)
     if lse is None:
@@ -574,7 +571,7 @@ def mla_decode(q, kv_pool, page_table, seq_lens, q_start, *, softmax_scale, max_
     a.B, a.n_q, a.H, a.d_qk, a.d_v = B, n_q, H, 576, 512
     a.num_pages, a.page_size, _ = kv_pool.shape
     a.max_pages = page_table.shape[1]
-    a.max_q_per_seq, a.softmax_scale = max_q_per_seq, float(softmax_scale)
+    a.max_q_per_seq, a.softmax_scale = bound, float(softmax_scale)
     a.kv_dtype = DSA_FP8_E4M3 if fp8 else DSA_BF16
     if workspace is None and n_q:
         nbytes = lib.dsa_mla_decode_workspace_bytes(ctypes.byref(a))
@@ -594,7 +591,8 @@ def mla_prefill(q, kv, k_rope, q_start, kv_start, *, softmax_scale, max_q_per_se
     """Dense latent attention, expanded form: q [n_q, H, 192] against every head's keys and values
     kv [n_kv, H, 256] (128 key columns, 128 value columns: the up-projection's output) and the
     shared rope keys k_rope [n_kv, 64], which may be a strided view of the latent rows.  The
-    tokens of a sequence are its last positions.  Returns (out [n_q, H, 128] bf16, lse [n_q, H])."""
+    tokens of a sequence are its last positions, ``max_q_per_seq`` (required) of them at most.  Returns
+    (out [n_q, H, 128] bf16, lse [n_q, H])."""
     lib = load()
     if q.dim() != 3 or q.shape[2] != 192:
         raise ValueError("q must have shape [n_q, H, 192] (got %s)" % (tuple(q.shape),))
@@ -607,7 +605,6 @@ def mla_prefill(q, kv, k_rope, q_start, kv_start, *, softmax_scale, max_q_per_se
     stride, step = k_rope.stride()
     if n_kv > 1 and stride < 64 or n_kv > 0 and step != 1:
         raise ValueError("the columns of k_rope must be adjacent, and its rows apart")
-    max_q_per_seq = _host_max_q(q_start, max_q_per_seq, n_q)
     device = q.device
     _fits(device, ("q", q, torch.bfloat16, None), ("kv", kv, torch.bfloat16, (n_kv, H, 256)),
           ("q_start", q_start, torch.int32, None), ("kv_start", kv_start, torch.int32, (B + 1,)),
@@ -615,13 +612,14 @@ def mla_prefill(q, kv, k_rope, q_start, kv_start, *, softmax_scale, max_q_per_se
           ("status", status, torch.int32, None))
     if k_rope.get_device() != device.index:
         raise ValueError("k_rope is on %s, the others are on %s" % (k_rope.device, device))
+    bound = _token_bound(max_q_per_seq, n_q)
     if out is None:
         out = _empty(stream, (n_q, H, 128), torch.bfloat16, device)
     if lse is None:
         lse = _empty(stream, (n_q, H), torch.float32, device)
     a = MlaPrefillArgs()
     a.B, a.n_q, a.n_kv, a.H, a.d_nope, a.d_rope, a.d_v = B, n_q, n_kv, H, 128, 64, 128
-    a.max_q_per_seq, a.softmax_scale = max_q_per_seq, float(softmax_scale)
+    a.max_q_per_seq, a.softmax_scale = bound, float(softmax_scale)
     a.k_rope_stride = stride if n_kv > 1 else 64
     a.q, a.kv, a.k_rope = q.data_ptr(), kv.data_ptr(), k_rope.data_ptr()
     a.q_start, a.kv_start, a.out, a.lse, a.status = (q_start.data_ptr(), kv_start.data_ptr(), out.data_ptr(),

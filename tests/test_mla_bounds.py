@@ -286,3 +286,21 @@ def test_prefill_waits_that_run_out_at_any_moment(cuda_lib, monkeypatch, new, ke
         out, lse, status = run_prefill(c)
     assert status == 0
     verify_prefill(c, out, lse)
+
+
+# ------------------------------------------------------------------------------------------
+# the host's bound of the tokens
+# ------------------------------------------------------------------------------------------
+
+@pytest.mark.gpu
+def test_the_bound_of_the_tokens_is_asked_for(cuda_lib):
+    """It cannot come from q_start: on the device that would be a synchronisation, on the host the kernels
+    could not read it."""
+    c, f = make_decode([100], [1], 16, False), make_prefill([5], [9], 2)
+    for at in ("cuda", "cpu"):
+        for op, kw in ((dsa.mla_decode, dict(q=c["q"], kv_pool=c["pool"], page_table=c["pt"], seq_lens=c["seq_lens"],
+                                             q_start=c["q_start"].to(at))),
+                       (dsa.mla_prefill, dict(q=f["q"], kv=f["kv"], k_rope=f["rope"], q_start=f["q_start"].to(at),
+                                              kv_start=f["kv_start"]))):
+            with pytest.raises(ValueError, match="max_q_per_seq" if at == "cuda" else "q_start is on cpu"):
+                op(**kw, softmax_scale=SCALE)
