@@ -262,6 +262,138 @@ def test_prefill_falling_q_start_in_front_of_many_sequences(cuda_lib):
     assert torch.all(out[3900:3920] == 5.0) and torch.all(lse[3900:3920] == 6.0)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("q_start,owned", [([0, 1, 99], 0), ([0, 1, 0], 0), ([-1, 1, 2], 1), ([5, 1, 2], 1)])
+def test_decode_skips_a_sequence_whose_q_start_is_out_of_order(cuda_lib, fp8, q_start, owned):
+    """Its rows stay as they were, and the other sequence is whole."""
+    c = make_decode([100, 1200], [1, 1], 16, fp8, tail=0)
+    c["q_start"] = starts(*q_start)
+    out, lse, status = run_decode(c)
+    assert status == dsa.DSA_ERR_DEVICE_CHECK
+    assert torch.all(out[1 - owned] == 5.0) and torch.all(lse[1 - owned] == 6.0)
+    kv = c["rows"][owned]
+    want = definition(c["q"][owned].double(), kv, kv[:, :512],
+                      torch.ones((16, len(kv)), dtype=torch.bool, device="cuda"), SCALE)
+    check(out[owned], lse[owned], *want, 576, len(kv))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [4, 5, 30], ids=["first", "second", "last"])
+def test_decode_fp8_page_that_does_not_exist(cuda_lib, page):
+    """The first or the second page of a tile, or the last page of the sequence: page 0, which stands in for it,
+    belongs to the other sequence and must not count."""
+    c = make_decode([1980, 640], [1, 2], 16, True, tail=0)
+    assert int((c["pt"][1, :10] == 0).sum()) + int((c["pt"][0, :31] == 0).sum()) <= 1
+    c["pt"][0, page] = -3
+    out, lse, status = run_decode(c)
+    assert status == dsa.DSA_ERR_DEVICE_CHECK
+    keep = torch.ones(1980, dtype=torch.bool, device="cuda")
+    keep[64 * page:64 * page + 64] = False
+    c["rows"][0] = c["rows"][0][keep]
+    c["lens"][0] = int(keep.sum())
+    verify_decode(c, out, lse)
+
+
+@pytest.mark.gpu
+def test_decode_fp8_length_beyond_the_page_table_and_below_zero(cuda_lib):
+    c = make_decode([448, 200], [1, 1], 16, True, extra=0, tail=0)
+    c["seq_lens"][0] = 10 ** 6
+    c["seq_lens"][1] = -5
+    out, lse, status = run_decode(c)
+    assert status == dsa.DSA_ERR_DEVICE_CHECK
+    c["lens"], c["rows"][1] = [448, 0], c["rows"][1][:0]
+    verify_decode(c, out, lse)
+
+
+@pytest.mark.gpu
+def test_decode_fp8_offsets_beyond_32_bits(cuda_lib):
+    """The sequence's pages lie at the end of a cache of 4.7 GB."""
+    pages = 120001
+    c = make_decode([1000], [2], 16, True, tail=0)
+    pool = torch.full((pages, 64, 608), 0x7F, dtype=torch.uint8, device="cuda")
+    own = c["pt"][0, :16].long()
+    pool[pages - 1 - own] = c["pool"][own]
+    c["pt"][0, :16] = (pages - 1 - own).int()
+    c["pool"] = pool
+    out, lse, status = run_decode(c)
+    assert status == 0
+    verify_decode(c, out, lse)
+
+
+# ------------------------------------------------------------------------------------------
+# every tile counts once
+# ------------------------------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("H,lens,new", [(1, [60001], [3]), (24, [65536, 20011, 777], [4, 1, 2]),
+                                        (128, [40000, 129, 30000], [1, 1, 1])], ids=str)
+def test_decode_weight_of_every_tile(cuda_lib, fp8, H, lens, new):
+    """Value column c is 1 in tile c of 128 positions and 0 elsewhere, so that an output element is the weight
+    of one tile: nothing cancels in it, and a tile lost or counted twice is an error of all of it.  The
+    scores are the rope columns'."""
+    c = make_decode(lens, new, H, fp8)
+    c["q"][..., :512] = 0
+    pool = c["pool"].view(-1, c["pool"].shape[-1])
+    for b, L in enumerate(lens):
+        j = torch.arange(L, device="cuda")
+        at = c["pt"][b].long()[j // 64] * 64 + j % 64
+        one = torch.zeros((L, 512), device="cuda")
+        one[j, j // 128] = 1.0
+        c["rows"][b][:, :512] = one.double()
+        if fp8:
+            pool[at, :512] = one.to(torch.float8_e4m3fn).view(torch.uint8)
+            row = pool[at]
+            row[:, 576:592] = torch.ones((L, 4), device="cuda").view(torch.uint8)
+            pool[at] = row
+        else:
+            pool[at, :512] = one.bfloat16()
+    out, lse, status = run_decode(c)
+    assert status == 0
+    verify_decode(c, out, lse)
+
+
+@pytest.mark.gpu
+def test_prefill_weight_of_every_tile(cuda_lib):
+    """The same in the expanded form: 128 tiles of 128 keys, and a prompt of its own."""
+    new, keys = [300, 700], [16384, 700]
+    c = make_prefill(new, keys, 2)
+    tile = torch.cat([torch.arange(n, device="cuda") // 128 for n in keys])
+    c["kv"][:sum(keys), :, 128:] = torch.nn.functional.one_hot(tile, 128)[:, None].bfloat16()
+    out, lse, status = run_prefill(c)
+    assert status == 0
+    verify_prefill(c, out, lse)
+
+
+@pytest.mark.gpu
+def test_prefill_value_that_is_nan_reaches_the_tokens_that_see_it(cuda_lib):
+    """A few NaN values per head, in tiles that all tokens of a block see and in those that only some do, with
+    several items a CTA, so that the marks of one tile follow on another's: NaN in that column for every
+    token that sees it, and every other token as without it."""
+    new, keys = [500, 130, 300], [500, 400, 300]
+    c = make_prefill(new, keys, 128)
+    good = run_prefill(c)
+    g = torch.Generator().manual_seed(6)
+    t = k = 0
+    nan = torch.zeros((932, 128, 128), dtype=torch.bool)
+    hit = torch.zeros((932, 128), dtype=torch.bool)
+    for n, L in zip(new, keys):
+        for h in range(128):
+            for _ in range(h % 4):    # every fourth head has none
+                j, col = int(torch.randint(L, (1,), generator=g)), int(torch.randint(128, (1,), generator=g))
+                c["kv"][k + j, h, 128 + col] = math.nan
+                first = t + max(0, j - (L - n))    # the first token that sees key j
+                nan[first:t + n, h, col] = True
+                hit[first:t + n, h] = True
+        t, k = t + n, k + L
+    out, lse, status = run_prefill(c)
+    assert status == 0
+    out, lse = out.cpu(), lse.cpu()
+    assert torch.isnan(out[nan]).all()
+    assert torch.equal(out[~hit], good[0].cpu()[~hit]) and torch.equal(lse[~hit], good[1].cpu()[~hit])
+
+
 # ------------------------------------------------------------------------------------------
 # waits that run out
 # ------------------------------------------------------------------------------------------
