@@ -296,33 +296,39 @@ struct Walk {
   DSA_DEV bool whole() const { return tile0 == 0 && tile1 == tiles; }
 };
 
-// Does a query row, which sees the sequence up to `seen`, see any position of the piece?
-DSA_DEV bool sees_any(const Params& p, const Walk& w, int seen, bool check_pages) {
-  const int from = w.tile0 * kTile, to = min(seen, w.tile1 * kTile);
-  if (!check_pages) return from < to;
-  for (int i = from >> 6; i * 64 < to; ++i) {
-    const int pg = p.page_table[(size_t)w.b * p.max_pages + i];
-    if (pg >= 0 && pg < p.num_pages) return true;
-  }
+// Two rare questions, out of line: inlined, the code that is skipped cost a call on one page 4 us of 19
+// (instructions come from memory then).
+
+// Does a query row, which sees the sequence up to `seen`, see any position of the tiles [tile0, tile1)?
+__device__ __noinline__ bool sees_any(const int* pages, int num_pages, int tile0, int tile1, int seen) {
+  const int to = min(seen, tile1 * kTile);
+  for (int i = tile0 * 2; i * 64 < to; ++i)
+    if (pages[i] >= 0 && pages[i] < num_pages) return true;
   return false;
 }
 
-// Does the value part of a cache row, which a whole warp asks for, hold something that is not finite?
+// First of the positions [first, last), which lie in one page, whose value columns hold something that is not
+// finite; a large number if none does.  For a whole warp.
 template <bool KV8>
-DSA_DEV bool value_row_is_odd(const Params& p, int b, int pos, int lane) {
-  const size_t row = (size_t)p.page_table[(size_t)b * p.max_pages + (pos >> 6)] * 64 + (pos & 63);
-  uint4 v, w;
-  if constexpr (KV8) {
-    const uint8_t* r = p.kv + row * kKv8Row;
-    dequant16(reinterpret_cast<const uint4*>(r)[lane], reinterpret_cast<const float*>(r + kDqk)[lane >> 3], v, w);
-  } else {
-    const uint4* r = reinterpret_cast<const uint4*>(p.kv + row * (kDqk * 2));
-    v = r[lane];
-    w = r[lane + 32];
+__device__ __noinline__ int first_odd_row(const uint8_t* kv, const int* pages, int num_pages, int first, int last) {
+  const int pg = first < last ? pages[first >> 6] : -1, lane = threadIdx.x & 31;
+  if (pg < 0 || pg >= num_pages) return 0x7fffffff;
+  for (int j = first; j < last; ++j) {
+    const size_t row = (size_t)pg * 64 + (j & 63);
+    uint4 v, w;
+    if constexpr (KV8) {
+      const uint8_t* r = kv + row * kKv8Row;
+      dequant16(reinterpret_cast<const uint4*>(r)[lane], reinterpret_cast<const float*>(r + kDqk)[lane >> 3], v, w);
+    } else {
+      const uint4* r = reinterpret_cast<const uint4*>(kv + row * (kDqk * 2));
+      v = r[lane];
+      w = r[lane + 32];
+    }
+    auto odd = [](uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; };   // carries out of an exponent of all ones
+    const uint32_t o = odd(v.x) | odd(v.y) | odd(v.z) | odd(v.w) | odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w);
+    if (__any_sync(0xffffffffu, (o & 0x80008000u) != 0u)) return j;
   }
-  auto odd = [](uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; };   // carries out of an exponent of all ones
-  const uint32_t o = odd(v.x) | odd(v.y) | odd(v.z) | odd(v.w) | odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w);
-  return __any_sync(0xffffffffu, (o & 0x80008000u) != 0u);
+  return 0x7fffffff;
 }
 
 template <bool KV8>
@@ -763,31 +769,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
         const int keep = visible_columns(active, seen, pos0, check_pages, p.page_table + (size_t)w.b * p.max_pages,
                                          p.num_pages);  // of ours
         if (w.seen_last > w.seen_first && (i + 1) * kTile > w.seen_first) {
-          // rows that only some of the group's tokens see, whose values lose what is not finite (below).  An
-          // infinite value whose key scores -inf is lost with it: its weight is 0, and 0 times it is NaN, as
-          // it comes out in any other tile.  So such a score becomes NaN.
-          bool low = false;
+          // cache rows that only some of the group's tokens see lose what is not finite in their values
+          // (below).  An infinite value makes a score that is not finite: NaN or +inf makes the row NaN as
+          // it is; -inf has a weight of 0, and 0 times infinity is NaN where the tile is not cleaned.  So
+          // a row that sees an infinite value here becomes NaN by its sum.
+          float low = INFINITY;
 #pragma unroll
-          for (int c = 0; c < 64; ++c) low |= sr[c] == 0xff800000u;
-          if (__any_sync(0xffffffffu, active && low)) {
-            const int from = max(0, w.seen_first - pos0);
-            uint32_t lows[2] = {0u, 0u};
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (active && c >= from && c < keep && sr[c] == 0xff800000u) lows[c >> 5] |= 1u << (c & 31);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t odd = 0u;
-              for (uint32_t rest = __reduce_or_sync(0xffffffffu, lows[h]); rest != 0u; rest &= rest - 1u) {
-                const int c = __ffs((int)rest) - 1;
-                if (value_row_is_odd<KV8>(p, w.b, pos0 + h * 32 + c, lane)) odd |= 1u << c;
-              }
-              lows[h] &= odd;
-            }
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (lows[c >> 5] >> (c & 31) & 1u) sr[c] = 0x7fffffffu;
-          }
+          for (int c = 0; c < 64; c += 2) low = min3(low, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+          if (__any_sync(0xffffffffu, low == -INFINITY) &&
+              seen > first_odd_row<KV8>(p.kv, p.page_table + (size_t)w.b * p.max_pages, p.num_pages,
+                                        max(w.seen_first, pos0), min(w.seen_last, pos0 + 64)))
+            l = __uint_as_float(0x7fffffffu);
         }
         if (!__all_sync(0xffffffffu, keep == 64)) {
 #pragma unroll
@@ -853,7 +845,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
           // value rows that some row of the group does not see: a weight of 0 times what they hold
           // must be 0.  Past every token's end they become 0; among the tokens' own rows only what
           // is not finite does (the rows that see it get their NaN from the scores, whose keys are
-          // the same columns: NaN as it is, +inf by the exponential, -inf see above).
+          // the same columns, or, see above, from their sums).
           warp_wait(&ctl->edge, edges & 1u, abort, p.status);
           ++edges;
           const int r0 = max(0, w.seen_first - i * kTile);
@@ -889,7 +881,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
       float lse2 = l_all == 0.f ? -INFINITY : m_ref + log2f(l_all);
       const bool whole = w.whole();
       // a row that sees something and has no weight: its scores are all -inf, or +inf by the scale
-      if (active && l_all == 0.f && sees_any(p, w, seen, check_pages)) {
+      if (active && l_all == 0.f && sees_any(p.page_table + (size_t)w.b * p.max_pages, p.num_pages,
+                                                w.tile0, w.tile1, seen)) {
         lse2 = whole || m_ref > 0.f ? __uint_as_float(0x7fffffffu) : kNoScore;
         if (whole) inv = lse2;
       }

@@ -119,6 +119,15 @@ DSA_DEV void warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int*
 DSA_DEV uint32_t k_block(uint32_t at, int j) { return at + 5u * j; }
 DSA_DEV uint32_t v_block(uint32_t at, int j) { return at + 5u * j + 3u; }
 
+// Where the sequences before the lane's end, at most: `ends` for those of earlier chunks.
+__device__ __noinline__ int earlier_end(int end, int ends) {
+  const int lane = threadIdx.x & 31;
+  int upto = max(ends, __shfl_up_sync(0xffffffffu, end, 1));
+  if (lane == 0) upto = ends;
+  for (int o = 1; o < 32; o <<= 1) upto = max(upto, __shfl_up_sync(0xffffffffu, upto, o));
+  return upto;
+}
+
 // The line of all sequences' token blocks, one sequence after the other, of which p.blocks is the
 // host's bound; the loading warp looks items up in it.  Lane i holds sequence b0 + i.
 // The bound holds for sequences that share no token.  Where q_start falls, two could claim the same ones:
@@ -147,11 +156,8 @@ struct Line {
     const int end = fine && s1 > s0 ? s1 : 0;
     rising = rising && __all_sync(0xffffffffu, fine);   // (each starts where the one before it ends)
     if (!rising) {
-      int upto = max(ends, __shfl_up_sync(0xffffffffu, end, 1));   // the earlier ones' ends
-      if (lane == 0) upto = ends;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) upto = max(upto, __shfl_up_sync(0xffffffffu, upto, o));
-      fine = fine && s0 >= upto;
+      const int from = earlier_end(end, ends);   // (of the whole warp)
+      fine = fine && s0 >= from;
     }
     ends = max(ends, __reduce_max_sync(0xffffffffu, end));
     fine = fine && k0 >= 0 && k1 >= k0 && k1 <= p.n_kv;
@@ -261,8 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) {
     // ---------------- items and loads
     uint32_t edges = 0, loads_a = 0, loads_b = 0;   // edge tiles, and loads of A's and B's queries, so far
-    // After a wait that gave up nothing is armed any more, and nobody else arrives on what is armed: an
-    // arrival on a barrier whose bytes are still on their way, its only expected one, faulted.
+    // After a wait that gave up nothing is armed any more, and the warps of the edge tiles arrive on nothing
+    // that is: an arrival on a barrier whose bytes are still on their way, its only expected one, faulted.
     auto load = [&](const Item& w) {
       // (A's last product with its queries is half a step or more before B's, whose new queries are
       // waited for after the first keys and values)
@@ -274,20 +280,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(smem + Layout::q + (x * 3 + c) * kBlock, &tm_q, &ctl->q_full[x], c * 64, w.h, w.tok + x * kRows);
       };
       load_q(0, loads_a);
-      // block i may take its slot once block i - 8 is used up; null: that wait gave up
-      auto arm = [&](uint32_t i, uint64_t* bar) -> uint8_t* {
-        const uint32_t c = i % kBlocks;
-        if (i >= kBlocks && !mbar_wait_fast(&ctl->empty[c], (i / kBlocks - 1) & 1u, abort, p.status)) return nullptr;
+      // block i may take its slot once block i - 8 is used up
+      auto free = [&](uint32_t i) {
+        if (i >= kBlocks) mbar_wait_fast(&ctl->empty[i % kBlocks], (i / kBlocks - 1) & 1u, abort, p.status);
+        return !*abort;
+      };
+      auto arm = [&](uint32_t i, uint64_t* bar) {
         mbar_arrive_expect_tx(bar, kBlock);
-        return smem + Layout::ring + c * kBlock;
+        return smem + Layout::ring + (i % kBlocks) * kBlock;
       };
       for (int j = 0; j < w.tiles && !*abort; ++j) {
         const int key = w.key + j * kKeys;
         for (int c = 0; c < 3; ++c) {
           const uint32_t i = k_block(at, j) + c;
           uint64_t* bar = &ctl->full[i % kBlocks];
+          if (!free(i)) return;
           uint8_t* dst = arm(i, bar);
-          if (dst == nullptr) return;
           if (c < 2)
             tma_load_3d(dst, &tm_k, bar, c * 64, w.h, key);
           else
@@ -296,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 2; ++c) {
           const uint32_t i = v_block(at, j) + c;
           uint64_t* bar = j < w.edge0 ? &ctl->full[i % kBlocks] : &ctl->edge[edges & 1u][c];
+          if (!free(i)) return;
           uint8_t* dst = arm(i, bar);
-          if (dst == nullptr) return;
           for (int u = 0; u < 2; ++u)
             tma_load_3d(dst + u * (kBlock / 2), &tm_v, bar, 128 + u * 64, w.h, key + c * 64);
         }
@@ -307,16 +315,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     Line line;
     const bool tell = blockIdx.x == 0;   // this CTA looks at every sequence
-    if (tell)
-      for (int b0 = 32, end = line.chunk(p, 0, 0, lane, true); b0 < p.B; b0 += 32)
-        end = line.chunk(p, b0, end, lane, true);
-    if (!tell) line.chunk(p, 0, 0, lane, false);
+    for (int b0 = 0, end = 0; b0 < (tell ? p.B : min(p.B, 32)); b0 += 32) end = line.chunk(p, b0, end, lane, tell);
     uint32_t item = 0;
-    // room for item number `item` in its slot, two items back; false: a wait of the CTA gave up, and the slot
-    // may still be read
+    // room for item number `item` in its slot, two items back (after a wait that gave up the slot may still be
+    // read: it stays as it is, and the others leave by the abort flag)
     auto room = [&] {
       if (item > 1) mbar_wait_fast(&ctl->item_empty[item & 1u], ((item >> 1) - 1) & 1u, abort, p.status);
-      return !__any_sync(0xffffffffu, *abort);
+      __syncwarp();
     };
     int index = (int)blockIdx.x;
     for (uint32_t asked = 0; index >= 0; ++asked) {
@@ -326,8 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       Item w;
       if (line.find(p, index, lane, w)) {
-        if (!room()) break;
-        if (lane == 0) {
+        room();
+        if (lane == 0 && !*abort) {
           ctl->item[item & 1u] = w;
           mbar_arrive(&ctl->item_full[item & 1u]);
           load(w);
@@ -342,7 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
     }
-    if (room() && lane == 0) {   // (else the others leave by the abort flag)
+    room();
+    if (lane == 0 && !*abort) {
       ctl->item[item & 1u].tiles = 0;
       mbar_arrive(&ctl->item_full[item & 1u]);
     }
@@ -363,7 +369,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&ctl->item_empty[item & 1u]);
       for (int j = edge0; j < tiles; ++j, ++edges) {
         warp_wait(&ctl->edge[edges & 1u][c], (edges >> 1) & 1u, abort, p.status);
-        if (__any_sync(0xffffffffu, *abort)) break;   // (the tile may never come; see the loads)
         const uint32_t t = at / 5u + j, slot = (v_block(at, j) + c) % kBlocks;
         const int rows = min(max(n_key - j * kKeys - c * 64, 0), 64);   // of the sequence
         uint8_t* half = smem + Layout::ring + slot * kBlock;
@@ -397,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (any && lane == 0) ctl->any_bad[t & 1u][c] = t + 1u;
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->full[slot]);
+        if (lane == 0 && !*abort) mbar_arrive(&ctl->full[slot]);   // (see the loads)
       }
       at += 5u * tiles;
     }
@@ -585,9 +590,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n > 0) {
         warp_wait(&ctl->pv_done[x], (done - 1) & 1u, abort, p.status);
         tc_fence_after();
-        // (no weight, but something seen: the scores are all -inf, or +inf by the scale)
-        const float none = seen > 0 ? __uint_as_float(0x7fffffffu) : 0.f;
-        const float inv = l == 0.f ? none : 1.f / l;
+        if (l == 0.f && seen > 0) l = __uint_as_float(0x7fffffffu);   // all scores -inf, or +inf by the scale
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t to = (size_t)(w.tok + x * kRows + row) * p.H + w.h;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -602,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             st_global_v8(p.out + to * kDv + c * 32 + 16, o + 8);
           }
         }
-        if (row < rows && p.lse) p.lse[to] = l == 0.f ? (seen > 0 ? none : -INFINITY) : m_ref * 0.69314718055994531f + logf(l);
+        if (row < rows && p.lse) p.lse[to] = l == 0.f ? -INFINITY : m_ref * 0.69314718055994531f + logf(l);
       }
       at += 5u * w.tiles;
       __syncwarp();

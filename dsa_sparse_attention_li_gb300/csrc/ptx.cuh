@@ -649,10 +649,15 @@ DSA_DEV void st_global_v8(void* p, const uint32_t* r) {
                : "memory");
 }
 
-// Largest of three (a NaN loses), one instruction.
+// Largest, and smallest, of three (a NaN loses), one instruction.
 DSA_DEV float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+DSA_DEV float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 // a * s + t on two values, and the sum of two pairs: one packed instruction each.
