@@ -80,7 +80,8 @@ struct Params {
                    // pair's first unit continues; pieces 0: none, or another pair joins it
   int ws_rows;
 #ifdef DSA_TEST_HOOKS
-  int stall;       // test build: the first pair's MMA warp waits on a barrier nothing arrives on
+  int stall;       // test build: the first pair's MMA warp waits on a barrier nothing arrives on (3), or
+                   // the first CTA's first load of keys (5) or values (6) is left out
 #endif
 };
 
@@ -198,6 +199,15 @@ struct RowPart {
     }
   }
 };
+
+// Test build: whether the first CTA leaves a load out, so that its bytes never come.
+DSA_DEV bool lost(const Params& p, int which) {
+#ifdef DSA_TEST_HOOKS
+  return p.stall == which && blockIdx.x == 0;
+#else
+  return false;
+#endif
+}
 
 // Bounded wait of a whole warp, which is converged again after it.
 DSA_DEV void warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
@@ -492,7 +502,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
             if (rank == 0) mbar_arrive_expect_tx(&ctl->k_full[c], 2 * kKGroupBytes);
 #pragma unroll
             for (int u = 0; u < 3; ++u)
-              tma_load_2d_pair(smem + Layout::k + (3 * c + u) * kBlockBytes, &tm_kv, k_full + c * 8, (3 * c + u) * 64, y);
+              if (!(it == 0 && c == 0 && u == 0 && lost(p, 5)))
+                tma_load_2d_pair(smem + Layout::k + (3 * c + u) * kBlockBytes, &tm_kv, k_full + c * 8, (3 * c + u) * 64, y);
           }
         }
         if (i == w.tile0)  // (after the first tile's loads, which are waited for)
@@ -540,12 +551,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
               if (rank == 0) mbar_arrive(&ctl->v_full[s]);
 #pragma unroll
               for (int u = 0; u < 4; ++u)
-                tma_load_2d(dst + u * kBlockBytes, &tm_kv, &ctl->edge, (int)rank * 256 + u * 64, y);
+                if (!(it == 0 && u == 0 && lost(p, 6)))
+                  tma_load_2d(dst + u * kBlockBytes, &tm_kv, &ctl->edge, (int)rank * 256 + u * 64, y);
             } else {
               if (rank == 0) mbar_arrive_expect_tx(&ctl->v_full[s], 2 * kVPageBytes);
 #pragma unroll
               for (int u = 0; u < 4; ++u)
-                tma_load_2d_pair(dst + u * kBlockBytes, &tm_kv, v_full + s * 8, (int)rank * 256 + u * 64, y);
+                if (!(it == 0 && u == 0 && lost(p, 6)))
+                  tma_load_2d_pair(dst + u * kBlockBytes, &tm_kv, v_full + s * 8, (int)rank * 256 + u * 64, y);
             }
           }
         }
@@ -662,13 +675,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
     // arm its Q barrier.
     {
       const uint32_t me = elect_one();
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        mbar_wait_issue<true>(bar, parity, abort, p.status);
+        __syncwarp();
+      };
       auto qk = [&](uint32_t n) {
-        if (n >= 2) warp_wait(&ctl->s_free[n & 1u], ((n >> 1) - 1) & 1u, abort, p.status);
+        if (n >= 2) wait(&ctl->s_free[n & 1u], ((n >> 1) - 1) & 1u);
         const uint32_t d = tmem + kColS + (n & 1u) * 64u;
         const uint64_t qd = sdesc_sw128(fresh(q_at), 16, 1024), kd = sdesc_sw128(fresh(k_at), 16, 1024);
 #pragma unroll
         for (int c = 0; c < kKGroups; ++c) {
-          warp_wait(&ctl->k_full[c], n & 1u, abort, p.status);
+          wait(&ctl->k_full[c], n & 1u);
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 12; ++kk) {
@@ -680,11 +697,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
         mma2_commit_both(&ctl->s_full[n & 1u], me);
       };
       auto pv = [&](uint32_t n, bool first) {
-        warp_wait(&ctl->p_full, n & 1u, abort, p.status);
+        wait(&ctl->p_full, n & 1u);
         const uint64_t pd = sdesc_sw128(fresh(p_at), 16, 1024), vd = sdesc_sw128(fresh(v_at), kBlockBytes, 1024);
 #pragma unroll
         for (int v = 0; v < kVPages; ++v) {
-          warp_wait(&ctl->v_full[v], n & 1u, abort, p.status);
+          wait(&ctl->v_full[v], n & 1u);
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
@@ -704,7 +721,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
       uint32_t n = 0;       // tiles whose Q.K^T is issued; their P.V runs one behind
       bool behind_first = false;
       for (uint32_t seg = 0;; ++seg) {
-        warp_wait(&ctl->q_full, seg & 1u, abort, p.status);
+        wait(&ctl->q_full, seg & 1u);
         const int tiles = __shfl_sync(0xffffffffu, ctl->piece[seg & 1u], 0);
         if (tiles == 0 || __any_sync(0xffffffffu, *abort)) break;
 #pragma unroll 1
@@ -714,7 +731,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
           if (i + 1 == tiles) mma2_commit_both(&ctl->q_empty, me);
           if (n > 0) pv(n - 1, behind_first);
           // O is the previous piece's until its rows have been read
-          if (i == 0 && seg > 0) warp_wait(&ctl->o_free, (seg - 1) & 1u, abort, p.status);
+          if (i == 0 && seg > 0) wait(&ctl->o_free, (seg - 1) & 1u);
           behind_first = i == 0;
         }
       }
@@ -841,12 +858,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
             *reinterpret_cast<uint4*>(p_row + ((c ^ (row & 7)) << 4)) =
                 make_uint4(sr[4 * c], sr[4 * c + 1], sr[4 * c + 2], sr[4 * c + 3]);
         }
+        bool come = true;   // the tile's values (else its weights are not handed over, and its slots not released)
         if (!KV8 && (i + 1) * kTile > w.seen_first) {
           // value rows that some row of the group does not see: a weight of 0 times what they hold
           // must be 0.  Past every token's end they become 0; among the tokens' own rows only what
           // is not finite does (the rows that see it get their NaN from the scores, whose keys are
           // the same columns, or, see above, from their sums).
-          warp_wait(&ctl->edge, edges & 1u, abort, p.status);
+          come = mbar_wait_fast(&ctl->edge, edges & 1u, abort, p.status);
+          __syncwarp();
           ++edges;
           const int r0 = max(0, w.seen_first - i * kTile);
           for (int c = r0 * 32 + tid; c < kTile * 32; c += 128) {
@@ -867,7 +886,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KV8>, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_pair(p_full);
+        if (lane == 0 && come) mbar_arrive_pair(p_full);
       }
       // ---------------- the piece's rows: O is complete once its last P.V is
       if (!ok) break;

@@ -51,7 +51,8 @@ struct Params {
   float* lse;
   int* status;
 #ifdef DSA_TEST_HOOKS
-  int stall;       // test build: the first CTA's MMA warp waits on a barrier nothing arrives on
+  int stall;       // test build: the first CTA's MMA warp waits on a barrier nothing arrives on (4), or
+                   // its first load of keys (7), of values (8) or of queries (9) is left out
 #endif
 };
 
@@ -267,6 +268,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) {
     // ---------------- items and loads
     uint32_t edges = 0, loads_a = 0, loads_b = 0;   // edge tiles, and loads of A's and B's queries, so far
+    // (test build: whether the first CTA leaves a load out, so that its bytes never come)
+    auto lost = [&](int which) {
+#ifdef DSA_TEST_HOOKS
+      return p.stall == which && blockIdx.x == 0;
+#else
+      return false;
+#endif
+    };
     // After a wait that gave up nothing is armed any more, and the warps of the edge tiles arrive on nothing
     // that is: an arrival on a barrier whose bytes are still on their way, its only expected one, faulted.
     auto load = [&](const Item& w) {
@@ -276,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (loads > 0 && !mbar_wait_fast(&ctl->q_empty[x], (loads - 1) & 1u, abort, p.status)) return;
         ++loads;
         mbar_arrive_expect_tx(&ctl->q_full[x], 3 * kBlock);
-        for (int c = 0; c < 3; ++c)
+        for (int c = lost(9) ? 1 : 0; c < 3; ++c)
           tma_load_3d(smem + Layout::q + (x * 3 + c) * kBlock, &tm_q, &ctl->q_full[x], c * 64, w.h, w.tok + x * kRows);
       };
       load_q(0, loads_a);
@@ -296,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint64_t* bar = &ctl->full[i % kBlocks];
           if (!free(i)) return;
           uint8_t* dst = arm(i, bar);
+          if (i == 0 && lost(7)) continue;
           if (c < 2)
             tma_load_3d(dst, &tm_k, bar, c * 64, w.h, key);
           else
@@ -306,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint64_t* bar = j < w.edge0 ? &ctl->full[i % kBlocks] : &ctl->edge[edges & 1u][c];
           if (!free(i)) return;
           uint8_t* dst = arm(i, bar);
-          for (int u = 0; u < 2; ++u)
+          for (int u = i == 3 && lost(8) ? 1 : 0; u < 2; ++u)
             tma_load_3d(dst + u * (kBlock / 2), &tm_v, bar, 128 + u * 64, w.h, key + c * 64);
         }
         if (j >= w.edge0) ++edges;
@@ -414,8 +424,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t kd = sdesc_sw128(smem_u32(smem + Layout::ring), 16, 1024);
     const uint64_t vd = sdesc_sw128(smem_u32(smem + Layout::ring), kBlock / 2, 1024);
     const uint32_t me = elect_one();
+    auto issue_wait = [&](uint64_t* bar, uint32_t parity) {
+      mbar_wait_issue<false>(bar, parity, abort, p.status);
+      __syncwarp();
+    };
     auto wait_block = [&](uint32_t i) {
-      warp_wait(&ctl->full[i % kBlocks], (i / kBlocks) & 1u, abort, p.status);
+      issue_wait(&ctl->full[i % kBlocks], (i / kBlocks) & 1u);
       tc_fence_after();
     };
     // Q_x . K(j)^T; the first row tile to use a key tile waits for it, the last one releases it
@@ -445,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           if (kk % (8 / kParts) == 0) {
-            warp_wait(&ctl->p_full[x][(c * 4 + kk) * kParts / 8], (done[x] + j) & 1u, abort, p.status);
+            issue_wait(&ctl->p_full[x][(c * 4 + kk) * kParts / 8], (done[x] + j) & 1u);
             tc_fence_after();
           }
           mma_f16_ts_by(tmem + kColO + x * 128, tmem + kColS + x * 128 + c * 32 + kk * 8, desc_at(v, kk * 2048),
@@ -468,10 +482,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tiles == 0 || __any_sync(0xffffffffu, *abort)) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->item_empty[item & 1u]);
-      warp_wait(&ctl->q_full[0], item & 1u, abort, p.status);
+      issue_wait(&ctl->q_full[0], item & 1u);
       qk(0, 0, true, nb == 0, na == 1);
       if (nb > 0) {
-        warp_wait(&ctl->q_full[1], with_b & 1u, abort, p.status);
+        issue_wait(&ctl->q_full[1], with_b & 1u);
         ++with_b;
         qk(1, 0, false, true, nb == 1);
       }

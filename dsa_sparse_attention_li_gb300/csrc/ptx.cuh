@@ -193,6 +193,31 @@ DSA_DEV bool mbar_wait_fast(uint64_t* bar, uint32_t parity, volatile int* abort,
   return mbar_test(bar, parity) || mbar_wait_slow(bar, parity, abort, status);
 }
 
+// The same for the warp that issues a CTA's (or a CTA pair's, kPair) MMAs.  After a wait that gave up it goes on
+// through its program, and commits on the release of parts that never came; a loader that took such a release
+// would arm a barrier whose bytes are outstanding, one arrival too many.  So it tells the pair's other CTA
+// (rank 1) too and stays here until every loader has noticed (a waiting thread looks at the abort flag every
+// four suspensions, 80 us) and left.  (An issue that can be called off instead, by a predicate that changes, took
+// a third longer for a whole call.)
+template <bool kPair>
+static __device__ __noinline__ bool mbar_wait_issue_slow(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                                         int* status) {
+  if (!*abort && mbar_wait(bar, parity, abort, status)) return true;
+  if (kPair)
+    asm volatile(
+        "{\n .reg .u32 a;\n mapa.shared::cluster.u32 a, %0, 1;\n st.volatile.shared::cluster.u32 [a], 1;\n}\n" ::"r"(
+            smem_u32(const_cast<const int*>(abort)))
+        : "memory");
+  const uint64_t t0 = globaltimer();
+  while (globaltimer() - t0 < 1000000u) {
+  }
+  return false;
+}
+template <bool kPair>
+DSA_DEV bool mbar_wait_issue(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  return mbar_test(bar, parity) || mbar_wait_issue_slow<kPair>(bar, parity, abort, status);
+}
+
 // Bounded wait that does not give up when the CTA has aborted: for draining asynchronous copies
 // that were issued and will complete (their bytes exist) before their destination is reused or
 // the CTA exits.

@@ -14,6 +14,9 @@
  * loops through their own bounded waits, every issued copy is drained, tensor memory is
  * freed, and the launch completes: the next call on the same context works.  The output of the
  * stalled launch is unspecified.  Host-side state, not thread-safe; a test setting.
+ * With 5 to 9 that CTA leaves a load out instead, so that what waits for its bytes gives up: 5 and 6 the
+ * first keys and the first values of dsa_mla_decode over a bf16 cache, 7, 8 and 9 the first keys, the first
+ * values and the queries of dsa_mla_prefill.
  *
  * dsa_test_mla_visible_columns(): on the host, with host pointers, the rule by which dsa_mla_decode's
  * softmax decides how many of a page's 64 positions a query row may use, lookup of the page id

@@ -420,6 +420,31 @@ def test_prefill_waits_that_run_out_at_any_moment(cuda_lib, monkeypatch, new, ke
     verify_prefill(c, out, lse)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("what,case", [
+    (5, ([9000, 700], [1, 2], 64)), (5, ([100], [1], 16)), (6, ([9000, 700], [1, 2], 64)), (6, ([100], [1], 16)),
+    (7, ([700, 300], [900, 300], 128)), (8, ([700, 300], [900, 300], 128)), (8, ([100], [100], 4)),
+    (9, ([700, 300], [900, 300], 128))], ids=str)
+def test_a_load_that_never_comes(cuda_lib, monkeypatch, what, case):
+    """The first CTA leaves a load out: keys, values (of a tile that all tokens see to its end, and of an edge
+    tile) or queries.  Whoever waits for its bytes gives up, nothing is loaded into what still waits for
+    them, and the launch ends with the error; the next call is right."""
+    c, run, verify = ((make_decode(*case, False), run_decode, verify_decode) if what < 7 else
+                      (make_prefill(*case), run_prefill, verify_prefill))
+    hooks = dsa.load_testhooks()
+    with monkeypatch.context() as m:
+        m.setattr(dsa, "_lib", hooks)
+        for _ in range(3):
+            hooks.dsa_test_inject_stall(what)
+            try:
+                assert run(c)[2] == dsa.DSA_ERR_TIMEOUT
+            finally:
+                hooks.dsa_test_inject_stall(0)
+            out, lse, status = run(c)
+            assert status == 0
+            verify(c, out, lse)
+
+
 # ------------------------------------------------------------------------------------------
 # the host's bound of the tokens
 # ------------------------------------------------------------------------------------------
