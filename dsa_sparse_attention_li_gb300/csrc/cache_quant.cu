@@ -177,13 +177,6 @@ DSA_DEV void store8(uint8_t* base, long long at, const float* y) {
   }
 }
 
-DSA_DEV float2 mul2(float a, float b, float s) {
-  float2 d;
-  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mul.rn.f32x2 x, x, y;\n"
-      " mov.b64 {%0, %1}, x;\n}\n" : "=f"(d.x), "=f"(d.y) : "f"(a), "f"(b), "f"(s));
-  return d;
-}
-
 DSA_DEV uint32_t e4m3x2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
@@ -210,7 +203,7 @@ DSA_DEV uint2 quantise8(const float* x, float s, float inv) {
   uint32_t lo[4], hi[4], differ = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 l = mul2(x[2 * i], x[2 * i + 1], down), h = mul2(x[2 * i], x[2 * i + 1], up);
+    const float2 l = mul2(make_float2(x[2 * i], x[2 * i + 1]), down), h = mul2(make_float2(x[2 * i], x[2 * i + 1]), up);
     lo[i] = e4m3x2(l.x, l.y);
     hi[i] = e4m3x2(h.x, h.y);
     differ |= lo[i] ^ hi[i];
@@ -363,7 +356,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
           const uint32_t two = (bits[2 * k + (i >> 1)] >> ((i & 1) * 16)) & 0xffffu;
           const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
           const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-          const float2 m = mul2(f.x, f.y, v[n].scale);
+          const float2 m = mul2(f, v[n].scale);
           y[2 * i] = m.x;
           y[2 * i + 1] = m.y;
         }

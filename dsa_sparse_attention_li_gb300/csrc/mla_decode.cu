@@ -114,47 +114,11 @@ struct Ctl {
 };
 static_assert(sizeof(Ctl) <= 2048, "control block");
 
-DSA_DEV float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// A shared-memory matrix descriptor moved by a constant (the address field cannot carry: every operand
-// lies below 256 KiB).
-DSA_DEV uint64_t desc_at(uint64_t d, int bytes) {
-  uint32_t lo = (uint32_t)d, hi = (uint32_t)(d >> 32);
-  lo += (uint32_t)(bytes >> 4);
-  return ((uint64_t)hi << 32) | lo;
-}
-
 // The same value, newly made: what is computed from it is not kept in registers over a loop (the MMA
 // warp's 104 descriptor words cost the other warps their registers).
 DSA_DEV uint32_t fresh(uint32_t x) {
   asm volatile("" : "+r"(x));
   return x;
-}
-
-DSA_DEV uint32_t pack_bf16(float a, float b) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
-// Two bf16 with what is not finite set to zero.
-DSA_DEV uint32_t finite_bf16x2(uint32_t e) {
-  if ((e & 0x7f80u) == 0x7f80u) e &= 0xffff0000u;
-  if ((e & 0x7f800000u) == 0x7f800000u) e &= 0xffffu;
-  return e;
-}
-
-// Two fp32 products with one factor (a packed multiplication: one instruction for both).
-DSA_DEV float2 mul2(float2 a, float s) {
-  float2 d;
-  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mul.rn.f32x2 z, x, y;\n"
-      " mov.b64 {%0, %1}, z;\n}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(s));
-  return d;
 }
 
 // 16 e4m3 codes times their scale as bf16 (fp32 product, both roundings to nearest even): the operand
@@ -207,12 +171,6 @@ DSA_DEV bool lost(const Params& p, int which) {
 #else
   return false;
 #endif
-}
-
-// Bounded wait of a whole warp, which is converged again after it.
-DSA_DEV void warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
-  mbar_wait_fast(bar, parity, abort, status);
-  __syncwarp();
 }
 
 // How many of the 64 positions from pos0 on, a page of the sequence, a query row may use: those up to `seen`,

@@ -90,31 +90,6 @@ struct Ctl {
 };
 static_assert(sizeof(Ctl) <= 2048, "control block");
 
-DSA_DEV float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-DSA_DEV uint32_t pack_bf16(float a, float b) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-// Two bf16 with what is not finite set to zero.
-DSA_DEV uint32_t finite_bf16x2(uint32_t e) {
-  if ((e & 0x7f80u) == 0x7f80u) e &= 0xffff0000u;
-  if ((e & 0x7f800000u) == 0x7f800000u) e &= 0xffffu;
-  return e;
-}
-DSA_DEV uint64_t desc_at(uint64_t d, int bytes) {
-  uint32_t lo = (uint32_t)d, hi = (uint32_t)(d >> 32);
-  lo += (uint32_t)(bytes >> 4);
-  return ((uint64_t)hi << 32) | lo;
-}
-DSA_DEV void warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
-  mbar_wait_fast(bar, parity, abort, status);
-  __syncwarp();
-}
-
 // Position of a key tile's first block, and of a value tile's, in the line of blocks that the ring
 // carries (`at`: the item's first); block i lies in slot i % 8, in its (i / 8)th use.
 DSA_DEV uint32_t k_block(uint32_t at, int j) { return at + 5u * j; }

@@ -193,7 +193,13 @@ DSA_DEV bool mbar_wait_fast(uint64_t* bar, uint32_t parity, volatile int* abort,
   return mbar_test(bar, parity) || mbar_wait_slow(bar, parity, abort, status);
 }
 
-// The same for the warp that issues a CTA's (or a CTA pair's, kPair) MMAs.  After a wait that gave up it goes on
+// Bounded wait of a whole warp, which is converged again after it.
+DSA_DEV void warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  mbar_wait_fast(bar, parity, abort, status);
+  __syncwarp();
+}
+
+// mbar_wait_fast for the warp that issues a CTA's (or a CTA pair's, kPair) MMAs.  After a wait that gave up it goes on
 // through its program, and commits on the release of parts that never came; a loader that took such a release
 // would arm a barrier whose bytes are outstanding, one arrival too many.  So it tells the pair's other CTA
 // (rank 1) too and stays here until every loader has noticed (a waiting thread looks at the abort flag every
@@ -667,6 +673,14 @@ DSA_DEV int clc_block(const void* response) {
 
 // ---------------------------------------------------------------- misc
 
+// A shared-memory matrix descriptor moved by a constant (the address field cannot carry: every operand
+// lies below 256 KiB).
+DSA_DEV uint64_t desc_at(uint64_t d, int bytes) {
+  uint32_t lo = (uint32_t)d, hi = (uint32_t)(d >> 32);
+  lo += (uint32_t)(bytes >> 4);
+  return ((uint64_t)hi << 32) | lo;
+}
+
 // 32 bytes to global memory, a full sector (32-byte aligned).
 DSA_DEV void st_global_v8(void* p, const uint32_t* r) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
@@ -683,6 +697,32 @@ DSA_DEV float max3(float a, float b, float c) {
 DSA_DEV float min3(float a, float b, float c) {
   float d;
   asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// 2^x with the hardware approximation (flush-to-zero; 2^-inf = 0).  The weights are rounded to
+// bf16 right after, so its ~2-ulp fp32 error is far below what the output keeps.
+DSA_DEV float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+DSA_DEV uint32_t pack_bf16(float a, float b) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+// Two bf16 with what is not finite set to zero.
+DSA_DEV uint32_t finite_bf16x2(uint32_t e) {
+  if ((e & 0x7f80u) == 0x7f80u) e &= 0xffff0000u;
+  if ((e & 0x7f800000u) == 0x7f800000u) e &= 0xffffu;
+  return e;
+}
+// Two fp32 products with one factor (a packed multiplication: one instruction for both).
+DSA_DEV float2 mul2(float2 a, float s) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mul.rn.f32x2 z, x, y;\n"
+      " mov.b64 {%0, %1}, z;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(s));
   return d;
 }
 // a * s + t on two values, and the sum of two pairs: one packed instruction each.

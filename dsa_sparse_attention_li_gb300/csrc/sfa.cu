@@ -180,19 +180,6 @@ DSA_DEV int find_seq(const int* q_start, int B, int t) {
   return lo;
 }
 
-DSA_DEV uint32_t pack_bf16(float a, float b) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
-// 2^x with the hardware approximation (flush-to-zero; 2^-inf = 0).  The weights are rounded to
-// bf16 right after, so its ~2-ulp fp32 error is far below what the output keeps.
-DSA_DEV float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // 16-byte asynchronous copy global -> shared; src_bytes = 0 writes zeros.
 DSA_DEV void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
