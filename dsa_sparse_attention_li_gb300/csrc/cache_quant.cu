@@ -10,8 +10,8 @@
 // e4m3() rounds to nearest even and saturates at 448.  x_i / s is not rounded before e4m3(): a
 // quotient rounded to fp32 first can land exactly on the border between two codes.  The fast
 // path multiplies by 1/s (1 - 2^-21) and 1/s (1 + 2^-21), between which the quotient lies, and keeps a
-// code on which both agree; the few others, about one element in 2^16, compare |x| with border * s in
-// 64 bits, where that product is exact.
+// code on which both agree; the few others, about one element in 2^16, take the sign of |x| - border * s,
+// which one fused multiply-add keeps (see settle()).
 //
 // Both kernels move each byte once and are bound by HBM, with short rows by instruction issue (key rows: 70%
 // of the issue slots).  The unit of work of a warp is 512 columns, two pieces of eight a lane (16- or
