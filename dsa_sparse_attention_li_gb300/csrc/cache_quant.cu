@@ -28,8 +28,9 @@
 // us against 8, launch included; a read of 50 rows is 7 us either way).  Blocks of four warps: of eight,
 // whose last warps hold the SM longer, 65,536 latent rows took 35 us.
 //
-// Measured, launch included: 65,536 fp32 latent rows written in 31 us (6.1 TB/s), 262,144 fp16 key rows of
-// 128 in 25 us (4.1 TB/s), 61,440 latent rows read as bf16 in 18 us (5.9 TB/s).
+// Measured, launch included, alone: 65,536 fp32 latent rows written in 31 us (6.1 TB/s; 34 to 35 us, 5.5 TB/s, in a
+// run of calls), 262,144 fp16 key rows of 128 in 25 us (4.2 TB/s; the same), 61,440 latent rows read as
+// bf16 in 18 us (5.9 TB/s; 20.5 us, 5.3 TB/s).
 #include <type_traits>
 
 #include "dsa_internal.h"

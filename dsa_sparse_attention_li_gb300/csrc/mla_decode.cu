@@ -32,9 +32,10 @@
 // cache the conversion: K's slots are free only between two Q.K^T, and its three parts, one after the
 // other, are 1,700 cycles each of loads, conversion and stores.
 //
-// Measured (join included): 32 sequences of 32,768, one token: 128 heads 230 us (5.3 TB/s, 79% of a copy's
-// rate; 1,270 TFLOP/s), 16 heads 214 us; one of 131,072: 56 us; one of 4,096, 16 heads: 18 us.  FP8: 32 of
-// 32,768, 128 heads 335 us, 16 ragged ones of up to 131,072 with two tokens and 64 heads 195 us.
+// Measured (join included, alone): 32 sequences of 32,768, one token: 128 heads 230 to 238 us by the GPU (5.2 TB/s,
+// 78% of a copy's rate; 1,250 TFLOP/s; 250 us in a run of calls, at a lower clock), 16 heads 216 us; one of
+// 131,072: 55 us; one of 4,096, 16 heads: 19 us.  FP8: 32 of 32,768, 128 heads 335 us, 16 ragged ones of
+// up to 131,072 with two tokens and 64 heads 196 us.
 #include <algorithm>
 
 #include "dsa_internal.h"

@@ -41,6 +41,8 @@
 extern "C" {
 #endif
 
+/* Raised when a struct or a call changes so that an older caller would go wrong; an entry point that is only
+ * added is found by its symbol. */
 #define DSA_ABI_VERSION 7
 
 /* Same type as cudaStream_t. */
