@@ -16,6 +16,9 @@ Functions (same names as the C entry points, without the ``dsa_`` prefix):
     mla_prefill(...)         -> (out [n_q, H, 128] bf16, lse [n_q, H] fp32)   dense, expanded form
     page_bytes(dtype, rows, dim), page_table_validate(...), cache_write(...)
     cache_write_quant(...), cache_read(...): rows into, and out of, the quantised caches
+    rms_norm_quant(...)      -> (codes [n, dim] e4m3, scale [n, ceil(dim / 128)] fp32[, sum])
+    quant_rows(...)          -> (codes, scale)
+    matmul_fp8(...)          -> out [M, N]: 8-bit rows times block-scaled e4m3 weights
 """
 from __future__ import annotations
 
@@ -40,7 +43,8 @@ SYMBOLS = ["dsa_status_string", "dsa_last_error", "dsa_abi_version", "dsa_li_wor
            "dsa_sfa_workspace_bytes", "dsa_sfa_decode", "dsa_sfa_prefill",
            "dsa_sfa_decode_static", "dsa_mla_decode_workspace_bytes", "dsa_mla_decode", "dsa_mla_prefill",
            "dsa_page_bytes", "dsa_page_table_validate",
-           "dsa_cache_write", "dsa_cache_write_quant", "dsa_cache_read", "dsa_prolog_workspace_bytes", "dsa_indexer_prolog", "dsa_topk_merge"]
+           "dsa_cache_write", "dsa_cache_write_quant", "dsa_cache_read", "dsa_prolog_workspace_bytes", "dsa_indexer_prolog", "dsa_topk_merge",
+           "dsa_rms_norm_quant", "dsa_quant_rows", "dsa_matmul_fp8"]
 
 # Capacity of the library's fixed scratch array used by dsa_sfa_decode_static.
 SFA_STATIC_SCRATCH_BYTES = 20 * 1024 * 1024
@@ -106,6 +110,25 @@ class CacheRowsArgs(ctypes.Structure):
         "n_rows", "dim", "B", "page_size", "max_pages", "num_pages", "format", "elem")] + [
         ("row_stride", ctypes.c_longlong)] + [(n, ctypes.c_void_p) for n in (
             "rows", "pool", "scale_pool", "sf_pool", "page_table", "seq", "pos", "status")]
+
+
+class RmsNormQuantArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("n_rows", "dim", "elem", "weight_elem")] + [("eps", ctypes.c_float)] + [
+        (n, ctypes.c_longlong) for n in ("x_stride", "residual_stride", "sum_stride", "y_stride", "codes_stride",
+                                         "scale_stride")] + [
+        (n, ctypes.c_void_p) for n in ("x", "weight", "residual", "sum", "y", "codes", "scale")]
+
+
+class QuantRowsArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("n_rows", "dim", "elem")] + [
+        (n, ctypes.c_longlong) for n in ("x_stride", "codes_stride", "scale_stride")] + [
+        (n, ctypes.c_void_p) for n in ("x", "codes", "scale")]
+
+
+class MatmulFp8Args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("M", "N", "K", "elem")] + [
+        (n, ctypes.c_longlong) for n in ("a_stride", "a_scale_stride", "b_stride", "b_scale_stride", "out_stride")] + [
+        (n, ctypes.c_void_p) for n in ("a", "a_scale", "b", "b_scale", "out", "status")]
 
 
 _lib = None
@@ -182,6 +205,10 @@ def _configure(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.dsa_mla_prefill.restype = ctypes.c_int
     for f in (lib.dsa_cache_write_quant, lib.dsa_cache_read):
         f.argtypes = [ctypes.POINTER(CacheRowsArgs), P]
+        f.restype = ctypes.c_int
+    for f, t in ((lib.dsa_rms_norm_quant, RmsNormQuantArgs), (lib.dsa_quant_rows, QuantRowsArgs),
+                 (lib.dsa_matmul_fp8, MatmulFp8Args)):
+        f.argtypes = [ctypes.POINTER(t), P]
         f.restype = ctypes.c_int
     return lib
 
@@ -626,6 +653,126 @@ def mla_prefill(q, kv, k_rope, q_start, kv_start, *, softmax_scale, max_q_per_se
                                                      lse.data_ptr(), _addr(status))
     _check(lib.dsa_mla_prefill(ctypes.byref(a), _launch_stream(stream, device)), "dsa_mla_prefill")
     return out, lse
+
+
+def _row_stride(name, t, dtype, rows, cols, device):
+    """Elements from one row to the next of a tensor [rows, cols] of `dtype` on `device` whose columns are adjacent
+    and whose rows lie apart (the current CUDA device is checked by the caller)."""
+    if t.dtype is not dtype:
+        raise ValueError("%s must be %s (got %s)" % (name, dtype, t.dtype))
+    if t.shape != (rows, cols):
+        raise ValueError("%s must have shape %s (got %s)" % (name, (rows, cols), tuple(t.shape)))
+    if t.get_device() != device.index:
+        raise ValueError("%s is on %s, the others are on %s" % (name, t.device, device))
+    stride, step = t.stride()
+    if rows > 1 and stride < cols or cols > 1 and rows > 0 and step != 1:
+        raise ValueError("the columns of %s must be adjacent, and its rows apart" % name)
+    return stride if rows > 1 else cols
+
+
+def _rows_in(x):
+    """(rows, columns, element type) of rows that are quantised, on the current device."""
+    if x.dim() != 2:
+        raise ValueError("x must have shape [n, dim] (got %s)" % (tuple(x.shape),))
+    elem = _ELEM.get(x.dtype)
+    if elem is None:
+        raise ValueError("x must be bf16, fp16 or fp32 (got %s)" % x.dtype)
+    _on_current(x.device)
+    return x.shape[0], x.shape[1], elem
+
+
+def _on_current(device):
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device (got %s)" % device)
+    if device.index != torch._C._cuda_getDevice():
+        raise ValueError("tensors are on %s, the current device is cuda:%d" % (device, torch.cuda.current_device()))
+
+
+def rms_norm_quant(x, weight, *, eps=1e-6, residual=None, residual_out=None, codes=None, scale=None, y=None,
+                   stream=None):
+    """Root-mean-square norm of the rows x [n, dim] (bf16, fp16 or fp32), after the addition of ``residual``, into
+    8-bit rows: returns (codes [n, dim] e4m3, scale [n, ceil(dim / 128)] fp32), and with a residual the sum,
+    rounded to x's type, as a third (in ``residual_out``, which may be ``residual`` itself, or a new tensor).
+    ``weight`` [dim] has x's type or is fp32; ``y`` [n, dim] takes the normed rows in x's type too.  All rows may be
+    strided, their columns adjacent.  ``codes`` and ``scale`` are what matmul_fp8 takes."""
+    lib = load()
+    n, dim, elem = _rows_in(x)
+    device, dtype, groups = x.device, x.dtype, (dim + 127) // 128
+    if weight.dtype is not dtype and weight.dtype is not torch.float32:
+        raise ValueError("weight must be %s or fp32 (got %s)" % (dtype, weight.dtype))
+    if weight.shape != (dim,) or weight.get_device() != device.index or not weight.is_contiguous():
+        raise ValueError("weight must be contiguous, on %s and have shape (%d,)" % (device, dim))
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out goes with residual")
+    a = RmsNormQuantArgs()
+    a.n_rows, a.dim, a.elem, a.weight_elem, a.eps = n, dim, elem, _ELEM[weight.dtype], float(eps)
+    a.x_stride, a.x, a.weight = _row_stride("x", x, dtype, n, dim, device), x.data_ptr(), weight.data_ptr()
+    if codes is None:
+        codes = _empty(stream, (n, dim), torch.float8_e4m3fn, device)
+    if scale is None:
+        scale = _empty(stream, (n, groups), torch.float32, device)
+    a.codes_stride, a.codes = _row_stride("codes", codes, torch.float8_e4m3fn, n, dim, device), codes.data_ptr()
+    a.scale_stride, a.scale = _row_stride("scale", scale, torch.float32, n, groups, device), scale.data_ptr()
+    if residual is not None:
+        a.residual_stride, a.residual = _row_stride("residual", residual, dtype, n, dim, device), residual.data_ptr()
+        if residual_out is None:
+            residual_out = _empty(stream, (n, dim), dtype, device)
+        a.sum_stride, a.sum = _row_stride("residual_out", residual_out, dtype, n, dim, device), residual_out.data_ptr()
+    if y is not None:
+        a.y_stride, a.y = _row_stride("y", y, dtype, n, dim, device), y.data_ptr()
+    _check(lib.dsa_rms_norm_quant(ctypes.byref(a), _launch_stream(stream, device)), "dsa_rms_norm_quant")
+    return (codes, scale) if residual is None else (codes, scale, residual_out)
+
+
+def quant_rows(x, *, codes=None, scale=None, stream=None):
+    """Rows x [n, dim] (bf16, fp16 or fp32; they may be strided, their columns adjacent) into 8-bit rows: (codes
+    [n, dim] e4m3, scale [n, ceil(dim / 128)] fp32), what matmul_fp8 takes."""
+    lib = load()
+    n, dim, elem = _rows_in(x)
+    device, groups = x.device, (dim + 127) // 128
+    if codes is None:
+        codes = _empty(stream, (n, dim), torch.float8_e4m3fn, device)
+    if scale is None:
+        scale = _empty(stream, (n, groups), torch.float32, device)
+    a = QuantRowsArgs()
+    a.n_rows, a.dim, a.elem = n, dim, elem
+    a.x_stride, a.x = _row_stride("x", x, x.dtype, n, dim, device), x.data_ptr()
+    a.codes_stride, a.codes = _row_stride("codes", codes, torch.float8_e4m3fn, n, dim, device), codes.data_ptr()
+    a.scale_stride, a.scale = _row_stride("scale", scale, torch.float32, n, groups, device), scale.data_ptr()
+    _check(lib.dsa_quant_rows(ctypes.byref(a), _launch_stream(stream, device)), "dsa_quant_rows")
+    return codes, scale
+
+
+def matmul_fp8(a, a_scale, b, b_scale, *, out=None, dtype=torch.bfloat16, status=None, stream=None):
+    """8-bit rows a [M, K] e4m3 with a_scale [M, ceil(K / 128)] fp32 times weights b [N, K] e4m3 with b_scale
+    [ceil(N / 128), ceil(K / 128)] fp32: out [M, N] = a b^T, into ``out`` (bf16, fp16 or fp32) or a new tensor of
+    ``dtype``.  K is a multiple of 16.  All rows may be strided, their columns adjacent: ``a`` and ``a_scale`` can be
+    views of the rows of an FP8 latent cache."""
+    lib = load()
+    if a.dim() != 2 or b.dim() != 2:
+        raise ValueError("a is [M, K], b is [N, K]")
+    M, K = a.shape
+    N, blocks = b.shape[0], (K + 127) // 128
+    device = a.device
+    _on_current(device)
+    if out is None:
+        out = _empty(stream, (M, N), dtype, device)
+    elem = _ELEM.get(out.dtype)
+    if elem is None:
+        raise ValueError("out must be bf16, fp16 or fp32 (got %s)" % out.dtype)
+    if status is not None:
+        _fits(device, ("status", status, torch.int32, None))
+    g = MatmulFp8Args()
+    g.M, g.N, g.K, g.elem = M, N, K, elem
+    g.a_stride, g.a = _row_stride("a", a, torch.float8_e4m3fn, M, K, device), a.data_ptr()
+    g.a_scale_stride, g.a_scale = _row_stride("a_scale", a_scale, torch.float32, M, blocks, device), a_scale.data_ptr()
+    g.b_stride, g.b = _row_stride("b", b, torch.float8_e4m3fn, N, K, device), b.data_ptr()
+    g.b_scale_stride = _row_stride("b_scale", b_scale, torch.float32, (N + 127) // 128, blocks, device)
+    g.b_scale = b_scale.data_ptr()
+    g.out_stride, g.out = _row_stride("out", out, out.dtype, M, N, device), out.data_ptr()
+    g.status = _addr(status)
+    _check(lib.dsa_matmul_fp8(ctypes.byref(g), _launch_stream(stream, device)), "dsa_matmul_fp8")
+    return out
 
 
 def topk_merge(cand_idx, cand_score, shard_offset, K, *, out_idx=None, out_cnt=None, stream=None):

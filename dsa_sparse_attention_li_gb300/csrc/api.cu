@@ -310,6 +310,106 @@ dsa_status dsa_mla_prefill(const dsa_mla_prefill_args* a, dsa_stream_t stream) {
   return s;
 }
 
+static bool elem_ok(dsa_elem e) { return e == DSA_ELEM_BF16 || e == DSA_ELEM_FP16 || e == DSA_ELEM_FP32; }
+
+// Rows of `dim` elements (of 2 or 4 bytes) that lie `stride` elements apart start on 16 bytes; one row has no stride.
+static const char* rows_wrong(const void* p, long long stride, int rows, int dim, dsa_elem e) {
+  if (!aligned16(p)) return "must be 16-byte aligned";
+  if (rows <= 1) return nullptr;
+  if (stride < dim || stride > (1LL << 40)) return "has a row stride below dim, or beyond 2^40";
+  return stride % (e == DSA_ELEM_FP32 ? 4 : 8) ? "has rows that do not start 16-byte aligned" : nullptr;
+}
+
+// The 8-bit rows that a call writes.
+static const char* rows8_wrong(const void* codes, long long codes_stride, const float* scale, long long scale_stride,
+                               int rows, int dim) {
+  if ((reinterpret_cast<uintptr_t>(codes) & 7u) || (rows > 1 && codes_stride % 8)) return "codes must have rows that start 8-byte aligned";
+  if (reinterpret_cast<uintptr_t>(scale) & 3u) return "scale must be 4-byte aligned";
+  if (rows > 1 && (codes_stride < dim || codes_stride > (1LL << 40))) return "codes has a row stride below dim, or beyond 2^40";
+  if (rows > 1 && (scale_stride < (dim + 127) / 128 || scale_stride > (1LL << 40))) return "scale has a row stride below its columns, or beyond 2^40";
+  return nullptr;
+}
+
+dsa_status dsa_rms_norm_quant(const dsa_rms_norm_quant_args* a, dsa_stream_t stream) {
+  g_last_error.clear();
+  const std::string name = "rms_norm_quant: ";
+  if (!a) return fail(DSA_ERR_INVALID_ARG, name + "args is NULL");
+  if (a->n_rows < 0 || a->dim <= 0) return fail(DSA_ERR_INVALID_ARG, name + "non-positive size");
+  if (!elem_ok(a->elem) || !elem_ok(a->weight_elem)) return fail(DSA_ERR_INVALID_ARG, name + "unknown element type");
+  if (a->weight_elem != a->elem && a->weight_elem != DSA_ELEM_FP32)
+    return fail(DSA_ERR_UNSUPPORTED, name + "weight must have the type of x, or fp32");
+  if (a->dim % 8 || a->dim > 32768) return fail(DSA_ERR_UNSUPPORTED, name + "dim must be a multiple of 8, up to 32768");
+  if (!(a->eps >= 0.f && a->eps <= 3.0e38f)) return fail(DSA_ERR_INVALID_ARG, name + "eps must be finite and not negative");
+  if (a->n_rows == 0) return DSA_OK;
+  if (!a->x || !a->weight || !a->codes || !a->scale) return fail(DSA_ERR_INVALID_ARG, name + "null device pointer");
+  if ((a->residual == nullptr) != (a->sum == nullptr))
+    return fail(DSA_ERR_INVALID_ARG, name + "residual and sum go together");
+  if (!aligned16(a->weight)) return fail(DSA_ERR_INVALID_ARG, name + "weight must be 16-byte aligned");
+  const struct { const char* what; const void* p; long long stride; } rows[] = {
+      {"x ", a->x, a->x_stride}, {"residual ", a->residual, a->residual_stride}, {"sum ", a->sum, a->sum_stride},
+      {"y ", a->y, a->y_stride}};
+  for (const auto& r : rows) {
+    const char* why = r.p ? rows_wrong(r.p, r.stride, a->n_rows, a->dim, a->elem) : nullptr;
+    if (why) return fail(DSA_ERR_INVALID_ARG, name + r.what + why);
+  }
+  if (const char* why = rows8_wrong(a->codes, a->codes_stride, a->scale, a->scale_stride, a->n_rows, a->dim))
+    return fail(DSA_ERR_INVALID_ARG, name + why);
+  std::string err;
+  const dsa_status s = dsa::launch_rms_norm_quant(*a, reinterpret_cast<cudaStream_t>(stream), err);
+  if (s != DSA_OK) g_last_error = err;
+  return s;
+}
+
+dsa_status dsa_quant_rows(const dsa_quant_rows_args* a, dsa_stream_t stream) {
+  g_last_error.clear();
+  const std::string name = "quant_rows: ";
+  if (!a) return fail(DSA_ERR_INVALID_ARG, name + "args is NULL");
+  if (a->n_rows < 0 || a->dim <= 0) return fail(DSA_ERR_INVALID_ARG, name + "non-positive size");
+  if (!elem_ok(a->elem)) return fail(DSA_ERR_INVALID_ARG, name + "unknown element type");
+  if (a->dim % 8 || a->dim > 0x40000000) return fail(DSA_ERR_UNSUPPORTED, name + "dim must be a multiple of 8, up to 2^30");
+  if (a->n_rows == 0) return DSA_OK;
+  if (!a->x || !a->codes || !a->scale) return fail(DSA_ERR_INVALID_ARG, name + "null device pointer");
+  if (const char* why = rows_wrong(a->x, a->x_stride, a->n_rows, a->dim, a->elem))
+    return fail(DSA_ERR_INVALID_ARG, name + "x " + why);
+  if (const char* why = rows8_wrong(a->codes, a->codes_stride, a->scale, a->scale_stride, a->n_rows, a->dim))
+    return fail(DSA_ERR_INVALID_ARG, name + why);
+  std::string err;
+  const dsa_status s = dsa::launch_quant_rows(*a, reinterpret_cast<cudaStream_t>(stream), err);
+  if (s != DSA_OK) g_last_error = err;
+  return s;
+}
+
+dsa_status dsa_matmul_fp8(const dsa_matmul_fp8_args* a, dsa_stream_t stream) {
+  g_last_error.clear();
+  const std::string name = "matmul_fp8: ";
+  if (!a) return fail(DSA_ERR_INVALID_ARG, name + "args is NULL");
+  if (a->M < 0 || a->N <= 0 || a->K <= 0) return fail(DSA_ERR_INVALID_ARG, name + "non-positive size");
+  if (!elem_ok(a->elem)) return fail(DSA_ERR_INVALID_ARG, name + "unknown element type");
+  if (a->K % 16) return fail(DSA_ERR_UNSUPPORTED, name + "K must be a multiple of 16");
+  if (a->M > 0x7fffff00 || a->N > 0x7fffff00 || a->K > 0x7fffff00)
+    return fail(DSA_ERR_UNSUPPORTED, name + "M, N and K must be at most 2^31 - 256");
+  if (a->M == 0) return DSA_OK;
+  if (!a->a || !a->a_scale || !a->b || !a->b_scale || !a->out)
+    return fail(DSA_ERR_INVALID_ARG, name + "null device pointer");
+  const long long blocks = ((long long)a->K + 127) / 128, n_blocks = ((long long)a->N + 127) / 128;
+  const struct { const char* what; const void* p; long long stride, rows, least, align; } parts[] = {
+      {"a ", a->a, a->a_stride, a->M, a->K, 16}, {"b ", a->b, a->b_stride, a->N, a->K, 16},
+      {"a_scale ", a->a_scale, a->a_scale_stride * 4, a->M, blocks * 4, 4},
+      {"b_scale ", a->b_scale, a->b_scale_stride * 4, n_blocks, blocks * 4, 4},
+      {"out ", a->out, a->out_stride * (a->elem == DSA_ELEM_FP32 ? 4 : 2), a->M,
+       (long long)a->N * (a->elem == DSA_ELEM_FP32 ? 4 : 2), a->elem == DSA_ELEM_FP32 ? 4 : 2}};
+  for (const auto& r : parts) {
+    if (reinterpret_cast<uintptr_t>(r.p) % r.align || (r.rows > 1 && r.stride % r.align))
+      return fail(DSA_ERR_INVALID_ARG, name + r.what + "must have rows that start " + std::to_string(r.align) + "-byte aligned");
+    if (r.rows > 1 && (r.stride < r.least || r.stride >= (1LL << 40)))
+      return fail(DSA_ERR_INVALID_ARG, name + r.what + "has a row stride below its columns, or of 2^40 bytes");
+  }
+  std::string err;
+  const dsa_status s = dsa::launch_matmul_fp8(*a, reinterpret_cast<cudaStream_t>(stream), err);
+  if (s != DSA_OK) g_last_error = err;
+  return s;
+}
+
 dsa_status dsa_topk_merge(const dsa_topk_merge_args* a, dsa_stream_t stream) {
   g_last_error.clear();
   if (!a) return fail(DSA_ERR_INVALID_ARG, "topk_merge: null args");

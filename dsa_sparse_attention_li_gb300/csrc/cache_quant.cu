@@ -7,11 +7,7 @@
 // Quantisation of a group of columns with largest finite magnitude a:
 //   FP8:    s = fp32(a / 448), 1 for a = 0, at least 2^-126;   c_i = e4m3(x_i / s)
 //   MXFP8:  e = max(floor(log2 a) - 8, -127), 0 for a = 0;     c_i = e4m3(x_i 2^-e)
-// e4m3() rounds to nearest even and saturates at 448.  x_i / s is not rounded before e4m3(): a
-// quotient rounded to fp32 first can land exactly on the border between two codes.  The fast
-// path multiplies by 1/s (1 - 2^-21) and 1/s (1 + 2^-21), between which the quotient lies, and keeps a
-// code on which both agree; the few others, about one element in 2^16, take the sign of |x| - border * s,
-// which one fused multiply-add keeps (see settle()).
+// e4m3() rounds to nearest even and saturates at 448; x_i / s is not rounded before it (see quant.cuh).
 //
 // Both kernels move each byte once and are bound by HBM, with short rows by instruction issue (key rows: 70%
 // of the issue slots).  The unit of work of a warp is 512 columns, two pieces of eight a lane (16- or
@@ -34,7 +30,7 @@
 #include <type_traits>
 
 #include "dsa_internal.h"
-#include "ptx.cuh"
+#include "quant.cuh"
 
 namespace dsa {
 namespace cq {
@@ -119,121 +115,11 @@ DSA_DEV void cache_rows(const Params& p, const Place* w, int* at) {
   }
 }
 
-// Eight columns of a row as they lie there: half the registers of their fp32 values while 16-bit rows are on
-// their way.
-template <int E>
-struct Eight {
-  static constexpr int kWords = E == DSA_ELEM_FP32 ? 2 : 1;
-  uint4 v[kWords];
-
-  DSA_DEV void load(const uint8_t* base, long long at) {
-    const uint4* s = reinterpret_cast<const uint4*>(base + at * (E == DSA_ELEM_FP32 ? 4 : 2));
-#pragma unroll
-    for (int k = 0; k < kWords; ++k) v[k] = __ldcs(s + k);
-  }
-  DSA_DEV void zero() {
-#pragma unroll
-    for (int k = 0; k < kWords; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
-  }
-  DSA_DEV void values(float* x) const {
-#pragma unroll
-    for (int k = 0; k < kWords; ++k) {
-      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (E == DSA_ELEM_FP32) {
-          x[4 * k + i] = __uint_as_float(w[i]);
-        } else if constexpr (E == DSA_ELEM_BF16) {
-          x[2 * i] = __uint_as_float(w[i] << 16);
-          x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        } else {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-          x[2 * i] = f.x;
-          x[2 * i + 1] = f.y;
-        }
-      }
-    }
-  }
-};
-
-template <int E>
-DSA_DEV void store8(uint8_t* base, long long at, const float* y) {
-  if constexpr (E == DSA_ELEM_FP32) {
-    float4* d = reinterpret_cast<float4*>(base + at * 4);
-    d[0] = make_float4(y[0], y[1], y[2], y[3]);
-    d[1] = make_float4(y[4], y[5], y[6], y[7]);
-  } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (E == DSA_ELEM_BF16) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&v);
-      } else {
-        const __half2 v = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&v);
-      }
-    }
-    *reinterpret_cast<uint4*>(base + at * 2) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
-
-DSA_DEV uint32_t e4m3x2(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
-
-DSA_DEV float e4m3_value(uint32_t code) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3);
-  return __half2float(*reinterpret_cast<const __half*>(&h));
-}
-
-// The code of x / s between its neighbours `lo` (toward zero) and `hi`, which differ by one: by the sign
-// of |x| - border s, which one fused rounding keeps unless the scale is so small that it underflows.
-// (16-bit rows meet exact borders often, about one element in 2^10.)
-DSA_DEV uint32_t settle(float x, float s, uint32_t lo, uint32_t hi) {
-  const float border = 0.5f * (e4m3_value(lo & 0x7f) + e4m3_value(hi & 0x7f));
-  float d = fmaf(-border, s, fabsf(x));
-  if (s < 0x1p-100f) d = fmaf(-border, s * 0x1p60f, fabsf(x) * 0x1p60f);  // both products exact
-  const uint32_t even = (hi & 1u) ? lo : hi;
-  return d > 0.f ? hi : d < 0.f ? lo : even;
-}
-
-// Eight columns with scale s, and inv about 1 / s -> eight codes.
-DSA_DEV uint2 quantise8(const float* x, float s, float inv) {
-  const float down = inv * (1.f - 0x1p-21f), up = inv * (1.f + 0x1p-21f);
-  uint32_t lo[4], hi[4], differ = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 l = mul2(make_float2(x[2 * i], x[2 * i + 1]), down), h = mul2(make_float2(x[2 * i], x[2 * i + 1]), up);
-    lo[i] = e4m3x2(l.x, l.y);
-    hi[i] = e4m3x2(h.x, h.y);
-    differ |= lo[i] ^ hi[i];
-  }
-  if (differ) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (lo[i] == hi[i]) continue;
-      const uint32_t l0 = lo[i] & 0xff, h0 = hi[i] & 0xff, l1 = lo[i] >> 8, h1 = hi[i] >> 8;
-      lo[i] = (l0 == h0 ? l0 : settle(x[2 * i], s, l0, h0)) | ((l1 == h1 ? l1 : settle(x[2 * i + 1], s, l1, h1)) << 8);
-    }
-  }
-  return make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-}
-
 // A lane's sixteen columns x of a row to cache row dst (< 0: nowhere).  The whole warp takes part.
 template <int F>
 DSA_DEV void write16(const Params& p, const Place& w, int row, const float* x) {
   const long long dst = row;
-  // the group's largest finite magnitude: a NaN (which every maximum loses) or an infinity does not
-  // cost its neighbours
-  float a = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; i += 2) a = max3(a, fabsf(x[i]), fabsf(x[i + 1]));
-  if (a == INFINITY) {
-    a = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
-  }
+  float a = finite_max16(x);   // of the group, after the shuffles
   constexpr int kMost = F == DSA_ROW_MXFP8 ? 2 : F == DSA_ROW_FP8 ? 16 : 8;   // lanes of a group
   const int lanes = F == DSA_ROW_MXFP8 ? 2 : w.step >> 3;
 #pragma unroll
@@ -256,8 +142,7 @@ DSA_DEV void write16(const Params& p, const Place& w, int row, const float* x) {
     if ((w.col & 31) == 0) p.sf_pool[dst * (p.dim >> 5) + (w.col >> 5)] = (uint8_t)(e + 127);
   } else {
     const float s = a > 0.f ? fmaxf(__fdiv_rn(a, 448.f), 0x1p-126f) : 1.f;
-    float inv;   // within 2^-23; with the two roundings that follow, well inside 2^-21
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    const float inv = fast_inverse(s);   // with the two roundings that follow, well inside 2^-21
     uint8_t* d = p.pool + dst * (F == DSA_ROW_FP8 ? p.dim : kLatentRow);
     *reinterpret_cast<uint2*>(d + w.col) = quantise8(x, s, inv);
     *reinterpret_cast<uint2*>(d + w.col + w.step) = quantise8(x + 8, s, inv);

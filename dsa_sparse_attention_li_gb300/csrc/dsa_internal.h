@@ -47,6 +47,9 @@ dsa_status launch_cache_rows(const dsa_cache_rows_args& a, bool write, cudaStrea
 dsa_status launch_mla_decode(const dsa_mla_decode_args& a, cudaStream_t stream, std::string& err);
 size_t mla_decode_workspace_bytes(const dsa_mla_decode_args& a);
 dsa_status launch_mla_prefill(const dsa_mla_prefill_args& a, cudaStream_t stream, std::string& err);
+dsa_status launch_rms_norm_quant(const dsa_rms_norm_quant_args& a, cudaStream_t stream, std::string& err);
+dsa_status launch_quant_rows(const dsa_quant_rows_args& a, cudaStream_t stream, std::string& err);
+dsa_status launch_matmul_fp8(const dsa_matmul_fp8_args& a, cudaStream_t stream, std::string& err);
 
 // 2-D tiled TMA descriptor over a row-major [outer][inner] array (inner contiguous).
 bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,

@@ -509,6 +509,14 @@ DSA_DEV void mma_f16_ts_by(uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(issuer)
       : "memory");
 }
+DSA_DEV void mma_f8_ss_by(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate,
+                          uint32_t issuer) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(issuer)
+      : "memory");
+}
 DSA_DEV void mma_commit_by(uint64_t* bar, uint32_t issuer) {
   asm volatile(
       "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
@@ -548,6 +556,14 @@ DSA_DEV void mma2_f16_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t id
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
       " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(issuer)
+      : "memory");
+}
+DSA_DEV void mma2_f8_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate,
+                        uint32_t issuer) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(issuer)
       : "memory");
 }
@@ -732,6 +748,15 @@ DSA_DEV float2 fma2(float2 a, float s, float t) {
       " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(s), "f"(t));
+  return d;
+}
+// a * s + c, pair by pair.
+DSA_DEV float2 fma2(float2 a, float s, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mov.b64 z, {%5, %6};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(s), "f"(c.x), "f"(c.y));
   return d;
 }
 DSA_DEV float2 add2(float2 a, float2 b) {

@@ -327,6 +327,98 @@ typedef struct {
 dsa_status dsa_mla_prefill(const dsa_mla_prefill_args* args, dsa_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------ */
+/* 8-bit rows and their product                                                                */
+/* ------------------------------------------------------------------------------------------ */
+
+/*
+ * What stands between the residual stream and the calls above in a model that is served in FP8 ("Inference
+ * Optimization for Kimi K3.1 Pro", section 4: one scale per token and 128 columns, as in the latent cache): the
+ * norm before a projection, the projection, and what the attention leaves on its way into the next one.  The
+ * pages define no interface for these.
+ *
+ * An 8-bit row is dim e4m3 codes and ceil(dim / 128) fp32 scales, each of 128 columns (the last of what is left):
+ * with a the largest finite magnitude of a group's values, s = fp32(a / 448), 1 when a = 0 and at least 2^-126,
+ * code = e4m3(value / s), to nearest even, saturated at 448 (infinities too); a NaN is kept.
+ */
+typedef enum { DSA_ELEM_BF16 = 0, DSA_ELEM_FP16 = 1, DSA_ELEM_FP32 = 2 } dsa_elem;
+
+/*
+ * Root-mean-square norm with the residual's addition, into 8-bit rows; T is the type of x:
+ *   h = T(x + residual)  (h = x without a residual),   stored to sum
+ *   r = 1 / sqrt(mean(h^2) + eps),   v[d] = h[d] * weight[d] * r   -> codes, scale, and T(v) -> y
+ * mean(h^2) and r are held in fp32: a row whose sum of squares is beyond fp32 has r = 0, one with a NaN is all
+ * NaN.  h * weight is rounded to fp32 (exact for 16-bit types); v itself is not rounded before it is quantised.
+ *
+ * sum and y may be x or residual themselves (same address and stride); outputs overlap nothing else.  Supported:
+ * dim a multiple of 8, up to 32768; weight of T or fp32; rows of x, residual, sum, y and weight 16-byte aligned,
+ * those of codes 8-byte aligned.
+ */
+typedef struct {
+  int n_rows;
+  int dim;
+  dsa_elem elem;           /* T: type of x, residual, sum and y                              */
+  dsa_elem weight_elem;    /* T or DSA_ELEM_FP32                                             */
+  float eps;               /* >= 0                                                           */
+  long long x_stride, residual_stride, sum_stride, y_stride; /* elements from row to row     */
+  long long codes_stride;  /* bytes                                                          */
+  long long scale_stride;  /* elements                                                       */
+  const void* x;           /* [n_rows][dim]                                                  */
+  const void* weight;      /* [dim]                                                          */
+  const void* residual;    /* [n_rows][dim], or NULL                                         */
+  void* sum;               /* [n_rows][dim]: with a residual only                            */
+  void* y;                 /* [n_rows][dim], or NULL                                         */
+  void* codes;             /* [n_rows][dim] e4m3                                             */
+  float* scale;            /* [n_rows][ceil(dim / 128)]                                      */
+} dsa_rms_norm_quant_args;
+
+dsa_status dsa_rms_norm_quant(const dsa_rms_norm_quant_args* args, dsa_stream_t stream);
+
+/* Rows as they are into 8-bit rows.  Supported: dim a multiple of 8; rows of x 16-byte, of codes 8-byte aligned. */
+typedef struct {
+  int n_rows;
+  int dim;
+  dsa_elem elem;           /* type of x                                                      */
+  long long x_stride;      /* elements                                                       */
+  long long codes_stride;  /* bytes                                                          */
+  long long scale_stride;  /* elements                                                       */
+  const void* x;           /* [n_rows][dim]                                                  */
+  void* codes;             /* [n_rows][dim] e4m3                                             */
+  float* scale;            /* [n_rows][ceil(dim / 128)]                                      */
+} dsa_quant_rows_args;
+
+dsa_status dsa_quant_rows(const dsa_quant_rows_args* args, dsa_stream_t stream);
+
+/*
+ * Product of 8-bit rows with e4m3 weights that have one fp32 scale per block of 128 rows and 128 columns:
+ *   out[m][n] = sum_i fp32(a_scale[m][i] * b_scale[n / 128][i]) * sum_{k in columns of block i} a[m][k] * b[n][k]
+ * for i < ceil(K / 128).  A block's products are added by the tensor cores with fp32 accumulators, the blocks'
+ * sums with fp32 multiply-adds, and the result is rounded once to the type of out.  A NaN or an infinity in a row
+ * of either operand (or in its scales) reaches the outputs of that row alone.
+ *
+ * a may be the rows of an FP8 latent cache as they lie there (a_stride 608, a_scale 576 bytes on, a_scale_stride
+ * 152): the up-projection of dsa_mla_prefill's keys and values reads no converted copy.
+ *
+ * Supported: K a multiple of 16; any M and N; rows of a and b 16-byte aligned.
+ */
+typedef struct {
+  int M, N, K;
+  dsa_elem elem;             /* type of out                                                  */
+  long long a_stride;        /* bytes from row to row                                        */
+  long long a_scale_stride;  /* elements                                                     */
+  long long b_stride;        /* bytes                                                        */
+  long long b_scale_stride;  /* elements                                                     */
+  long long out_stride;      /* elements                                                     */
+  const void* a;             /* [M][K] e4m3                                                  */
+  const float* a_scale;      /* [M][ceil(K / 128)]                                           */
+  const void* b;             /* [N][K] e4m3                                                  */
+  const float* b_scale;      /* [ceil(N / 128)][ceil(K / 128)]                               */
+  void* out;                 /* [M][N]                                                       */
+  int32_t* status;           /* device int32 error word, or NULL                             */
+} dsa_matmul_fp8_args;
+
+dsa_status dsa_matmul_fp8(const dsa_matmul_fp8_args* args, dsa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
 /* Context-parallel top-K merge                                                                */
 /* ------------------------------------------------------------------------------------------ */
 
@@ -490,7 +582,6 @@ dsa_status dsa_cache_write(void* pool, float* scale_pool, int num_pages, int pag
  * and pool 16-byte aligned, row_stride * element size a multiple of 16, row_stride >= dim.
  */
 typedef enum { DSA_ROW_BF16 = 0, DSA_ROW_FP8 = 1, DSA_ROW_MXFP8 = 2, DSA_ROW_LATENT_FP8 = 3 } dsa_row_format;
-typedef enum { DSA_ELEM_BF16 = 0, DSA_ELEM_FP16 = 1, DSA_ELEM_FP32 = 2 } dsa_elem;
 
 typedef struct {
   int n_rows;

@@ -1,0 +1,338 @@
+"""Product of 8-bit rows with block-scaled e4m3 weights, and the calls around the attention in a run.
+
+Small whole codes with scales that are powers of two make every product and every sum exact in fp32, so those
+outputs match the definition bit for bit after its one rounding to the output's type.  With any codes and scales, a
+block's 128 products are added by the tensor cores: at most 4 instructions, each of which aligns 33 terms to the largest
+and may cut each at 2^-24 of it: 132 * 2^-24 of the block's sum of magnitudes, below 2^-16.  Per block the scales'
+product and the multiply-add round by 2^-24 of what they give, up to 128 blocks of them here: below 2^-16 again.  So an
+output is off by less than 2^-15 of its sum of magnitudes, and half a step of its type.
+"""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import dsa_sparse_attention_li_gb300 as dsa
+
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+OFF = 2.0 ** -15
+
+
+def definition(a, a_scale, b, b_scale):
+    """The product, and the sum of its terms' magnitudes, in 64 bits."""
+    n, k = b.shape
+    x = a.double() * a_scale.double().repeat_interleave(128, 1)[:, :k]
+    w = b.double() * b_scale.double().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+    return x @ w.T, x.abs() @ w.abs().T
+
+
+def whole(m, n, k, g):
+    """Operands whose every sum is exact in fp32: codes in -3 .. 3 (a 7168-column sum is below 2^16), scales 2^-1, 1, 2."""
+    blocks = -(-k // 128)
+    a = torch.randint(-3, 4, (m, k), generator=g, device="cuda").float().to(torch.float8_e4m3fn)
+    b = torch.randint(-3, 4, (n, k), generator=g, device="cuda").float().to(torch.float8_e4m3fn)
+    a_scale = torch.exp2(torch.randint(-1, 2, (m, blocks), generator=g, device="cuda").float())
+    b_scale = torch.exp2(torch.randint(-1, 2, (-(-n // 128), blocks), generator=g, device="cuda").float())
+    return a, a_scale, b, b_scale
+
+
+def any_values(m, n, k, g):
+    blocks = -(-k // 128)
+    a, b = ((110 * torch.randn((r, k), generator=g, device="cuda")).clamp_(-448, 448).to(torch.float8_e4m3fn) for r in (m, n))
+    a_scale, b_scale = (torch.exp(torch.randn((r, blocks), generator=g, device="cuda")) / 110 for r in (m, -(-n // 128)))
+    return a, a_scale, b, b_scale / math.sqrt(k)
+
+
+def gen(*seed):
+    return torch.Generator(device="cuda").manual_seed(sum(s * 31 ** i for i, s in enumerate(seed)))
+
+
+SIZES = [(1, 1, 16), (1, 128, 128), (1, 2112, 7168), (2, 130, 144), (3, 576, 112), (7, 100, 256), (8, 1000, 1536), (16, 64, 7168),
+         (17, 129, 272), (31, 2112, 512), (32, 7168, 2048), (33, 257, 400), (64, 200, 576), (65, 640, 16384), (100, 5000, 640),
+         (127, 1111, 1024), (128, 128, 128), (129, 4096, 528), (200, 8192, 1536), (255, 576, 7168), (256, 256, 256),
+         (257, 2050, 384), (500, 3000, 1008), (777, 1536, 1536), (1000, 130, 96), (1025, 7168, 512), (2048, 576, 1024),
+         (4097, 320, 640), (3001, 2500, 272)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", SIZES)
+def test_whole_products_are_exact(cuda_lib, m, n, k):
+    a, a_scale, b, b_scale = whole(m, n, k, gen(m, n, k))
+    want, _ = definition(a, a_scale, b, b_scale)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for dtype in TYPES:
+        out = dsa.matmul_fp8(a, a_scale, b, b_scale, dtype=dtype, status=status)
+        assert out.dtype == dtype and torch.equal(out, want.float().to(dtype)), dtype
+    assert int(status) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("m,n,k", SIZES)
+def test_any_values(cuda_lib, m, n, k, dtype):
+    a, a_scale, b, b_scale = any_values(m, n, k, gen(n, m, k))
+    want, size = definition(a, a_scale, b, b_scale)
+    out = dsa.matmul_fp8(a, a_scale, b, b_scale, dtype=dtype)
+    tiny = torch.finfo(dtype).smallest_normal
+    off = size * OFF + (want.abs() + tiny) * torch.finfo(dtype).eps / 2
+    assert torch.all((out.double() - want).abs() <= off)
+    # the same call gives the same bits
+    assert torch.equal(out, dsa.matmul_fp8(a, a_scale, b, b_scale, dtype=dtype))
+
+
+def spread(t, rows_apart, fill):
+    """The same rows, `rows_apart` elements from one to the next, in memory filled with `fill`."""
+    wide = torch.full((t.shape[0], rows_apart), fill, device=t.device).to(t.dtype)
+    wide[:, :t.shape[1]] = t
+    return wide[:, :t.shape[1]]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("m,n,k", [(5, 100, 144), (130, 384, 208), (300, 515, 640), (700, 2000, 512)])
+def test_strided_rows(cuda_lib, m, n, k, dtype):
+    """Operands inside NaN, scales inside NaN, outputs inside memory that has to stay as it is."""
+    a, a_scale, b, b_scale = whole(m, n, k, gen(m, k))
+    want = definition(a, a_scale, b, b_scale)[0].float().to(dtype)
+    blocks = a_scale.shape[1]
+    out = torch.full((m + 1, n + 3), 5.0, dtype=dtype, device="cuda")
+    dsa.matmul_fp8(spread(a, k + 48, math.nan), spread(a_scale, blocks + 3, math.nan), spread(b, k + 32, math.nan),
+                   spread(b_scale, blocks + 1, math.nan), out=out[:m, :n])
+    assert torch.equal(out[:m, :n], want)
+    assert torch.all(out[m:] == 5.0) and torch.all(out[:, n:] == 5.0)
+    # an output that starts on an odd element
+    odd = torch.full((m, n + 1), 5.0, dtype=dtype, device="cuda")
+    dsa.matmul_fp8(a, a_scale, b, b_scale, out=odd[:, 1:])
+    assert torch.equal(odd[:, 1:], want) and torch.all(odd[:, 0] == 5.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [1, 20, 130, 600])
+def test_what_is_not_finite_stays_in_its_row(cuda_lib, m):
+    n, k = 300, 400
+    a, a_scale, b, b_scale = whole(m, n, k, gen(m))
+    clean = dsa.matmul_fp8(a, a_scale, b, b_scale, dtype=torch.float32)
+    row, col = m // 2, 133
+    a2, b2, a_scale2 = a.clone(), b.clone(), a_scale.clone()
+    a2.view(torch.uint8)[row, k - 1] = 0x7f
+    got = dsa.matmul_fp8(a2, a_scale, b, b_scale, dtype=torch.float32)
+    keep = torch.arange(m, device="cuda") != row
+    assert torch.all(got[row].isnan()) and torch.equal(got[keep], clean[keep])
+    b2.view(torch.uint8)[col, 0] = 0xff
+    got = dsa.matmul_fp8(a, a_scale, b2, b_scale, dtype=torch.float32)
+    cols = torch.arange(n, device="cuda") != col
+    assert torch.all(got[:, col].isnan()) and torch.equal(got[:, cols], clean[:, cols])
+    a_scale2[row, 1] = math.nan
+    got = dsa.matmul_fp8(a, a_scale2, b, b_scale, dtype=torch.float32)
+    assert torch.all(got[row].isnan()) and torch.equal(got[keep], clean[keep])
+    a_scale2[row, 1] = math.inf
+    got = dsa.matmul_fp8(a, a_scale2, b, b_scale, dtype=torch.float32)
+    assert not torch.isfinite(got[row]).any() and torch.equal(got[keep], clean[keep])
+
+
+@pytest.mark.gpu
+def test_largest_codes_and_small_scales(cuda_lib):
+    """Sums of 448 * 448 at their largest, beside scales that make fp16 overflow or vanish."""
+    m, n, k = 40, 256, 2048
+    a = torch.full((m, k), 448.0, device="cuda").to(torch.float8_e4m3fn)
+    b = torch.full((n, k), 448.0, device="cuda").to(torch.float8_e4m3fn)
+    a_scale, b_scale = torch.ones((m, 16), device="cuda"), torch.ones((2, 16), device="cuda")
+    out = dsa.matmul_fp8(a, a_scale, b, b_scale, dtype=torch.float32)
+    assert torch.all(out == 448.0 * 448.0 * k)
+    assert torch.all(dsa.matmul_fp8(a, a_scale, b, b_scale, dtype=torch.float16).isinf())
+    a_scale.fill_(2.0 ** -126)
+    out = dsa.matmul_fp8(a, a_scale, b, b_scale, dtype=torch.float32)
+    assert torch.all(out == 448.0 * 448.0 * k * 2.0 ** -126)
+
+
+@pytest.mark.gpu
+def test_rows_of_an_fp8_latent_cache(cuda_lib):
+    """The rows' first 512 codes and their scales, as they lie in the pages that cache_write_quant wrote."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    L, n = 500, 768
+    pool = torch.full((9, 64, 608), 0xff, dtype=torch.uint8, device="cuda")
+    pt = torch.arange(9, dtype=torch.int32, device="cuda")[None]
+    pos = torch.arange(L, dtype=torch.int32, device="cuda")
+    dsa.cache_write_quant(pool, pt, torch.zeros_like(pos), pos, torch.randn((L, 576), generator=g, device="cuda"))
+    a = pool.view(torch.float8_e4m3fn).view(-1, 608)[:L, :512]
+    a_scale = pool.view(torch.float32).view(-1, 152)[:L, 144:148]
+    _, _, b, b_scale = any_values(1, n, 512, g)
+    want, size = definition(a, a_scale, b, b_scale)
+    out = dsa.matmul_fp8(a, a_scale, b, b_scale)
+    assert torch.all((out.double() - want).abs() <= size * OFF + want.abs() * 2.0 ** -8)
+
+
+@pytest.mark.gpu
+def test_offsets_beyond_32_bits(cuda_lib):
+    """Rows that lie 1 GB apart in every tensor."""
+    m, n, k = 5, 9, 256
+    a, a_scale, b, b_scale = whole(m, n, k, gen(3))
+    want = dsa.matmul_fp8(a, a_scale, b, b_scale)
+    raw = torch.zeros(9 * 2 ** 30, dtype=torch.uint8, device="cuda")
+    far = lambda t, size, at: raw.view(t.dtype)[at:].as_strided(t.shape, (2 ** 30 // size, 1))
+    fa, fb, fs, fo = far(a, 1, 0), far(b, 1, 4096), far(a_scale, 4, 4096), far(want, 2, 16384)
+    fa.copy_(a), fb.copy_(b), fs.copy_(a_scale)
+    dsa.matmul_fp8(fa, fs, fb, b_scale, out=fo)
+    assert torch.equal(fo, want)
+
+
+@pytest.mark.gpu
+def test_an_output_beyond_32_bits(cuda_lib):
+    """2.2e9 outputs: the last rows are those of a call of their own."""
+    m, n, k = 33000, 66000, 16
+    a, a_scale, b, b_scale = whole(m, n, k, gen(4))
+    out = dsa.matmul_fp8(a, a_scale, b, b_scale)
+    assert torch.equal(out[-300:], dsa.matmul_fp8(a[-300:], a_scale[-300:], b, b_scale))
+    assert torch.equal(out[:50], dsa.matmul_fp8(a[:50], a_scale[:50], b, b_scale))
+
+
+@pytest.mark.gpu
+def test_no_rows(cuda_lib):
+    a, a_scale, b, b_scale = whole(4, 64, 128, gen(5))
+    assert dsa.matmul_fp8(a[:0], a_scale[:0], b, b_scale).shape == (0, 64)
+
+
+@pytest.mark.gpu
+def test_streams_and_graphs(cuda_lib):
+    """Calls on four streams at once, and a captured run of the three operators, replayed on new inputs."""
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    cases = [whole(m, n, k, gen(m)) for m, n, k in ((1, 2112, 7168), (32, 1024, 2048), (200, 640, 512), (900, 1536, 768))]
+    want = [definition(*c)[0].float().bfloat16() for c in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for s, c in zip(streams, cases):
+            with torch.cuda.stream(s):
+                got.append(dsa.matmul_fp8(*c))
+    outs = [dsa.matmul_fp8(*c, stream=s) for s, c in zip(streams, cases)]
+    torch.cuda.synchronize()
+    for i, o in enumerate(got + outs):
+        assert torch.equal(o, want[i % 4])
+
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x, r = (torch.randn((40, 1536), generator=g, device="cuda").bfloat16() for _ in range(2))
+    w = torch.rand(1536, generator=g, device="cuda").bfloat16()
+    _, _, b, b_scale = any_values(1, 1536, 1536, g)
+
+    def step():
+        codes, scale, total = dsa.rms_norm_quant(x, w, residual=r)
+        y = dsa.matmul_fp8(codes, scale, b, b_scale)
+        return dsa.matmul_fp8(*dsa.quant_rows(y), b, b_scale, dtype=torch.float32), total
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, total = step()
+    for _ in range(3):
+        x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+        graph.replay()
+        again = step()
+        assert torch.equal(out, again[0]) and torch.equal(total, again[1])
+
+
+@pytest.mark.gpu
+def test_a_layer_around_the_attention(cuda_lib):
+    """One decode step of a layer: norm, down-projection, the cache rows' write, the up-projections, dense latent attention
+    in the expanded form on rows that the product reads from the cache, and the output projection; against the same
+    steps in 64 bits on the values that each step got.  (Each step's own tolerance is derived where it is tested
+    alone: here a wrong row, scale or stride would be off by the size of the values.)"""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    L, T, H, D, DQ = 200, 5, 4, 1024, 512
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")
+    weights = lambda n, k: any_values(1, n, k, g)[2:]
+    wd, wq, wkv, wo = weights(DQ + 576, D), weights(H * 192, DQ), weights(H * 256, 512), weights(D, H * 128)
+    value = lambda b, s: b.double() * s.double().repeat_interleave(128, 0)[:b.shape[0]].repeat_interleave(128, 1)[:, :b.shape[1]]
+    near = lambda got, want, tol: bool((got.double() - want).norm() <= tol * want.norm())
+    x, res, gamma, gamma_q = rnd(L, D).bfloat16(), rnd(L, D).bfloat16(), rnd(D).abs() + 0.5, rnd(DQ).abs() + 0.5
+    codes, scale, h = dsa.rms_norm_quant(x, gamma, residual=res)
+    down = dsa.matmul_fp8(codes, scale, *wd, dtype=torch.float32)
+    hd = h.double()
+    v = hd / torch.sqrt((hd * hd).mean(1, keepdim=True) + 1e-6) * gamma.double()
+    assert near(down, v @ value(*wd).T, 0.06)     # e4m3 rows: half a step is 2^-4 at most, 2^-5.4 in the mean square
+    qc, qs = dsa.rms_norm_quant(down[-T:, :DQ], gamma_q)
+    q = dsa.matmul_fp8(qc, qs, *wq).view(T, H, 192)
+    pool = torch.zeros((4, 64, 608), dtype=torch.uint8, device="cuda")
+    pt, pos = torch.arange(4, dtype=torch.int32, device="cuda")[None], torch.arange(L, dtype=torch.int32, device="cuda")
+    dsa.cache_write_quant(pool, pt, torch.zeros_like(pos), pos, down[:, DQ:])
+    rows = pool.view(-1, 608)
+    kv = dsa.matmul_fp8(rows.view(torch.float8_e4m3fn)[:L, :512], pool.view(torch.float32).view(-1, 152)[:L, 144:148], *wkv)
+    back = dsa.cache_read(pool, pt, torch.zeros_like(pos), pos)
+    # bf16 copies of the rows, then bf16 outputs: 2^-8 each at most
+    assert near(kv, back[:, :512].double() @ value(*wkv).T, 2.0 ** -7)
+    at = lambda *n: torch.tensor(n, dtype=torch.int32, device="cuda")
+    o, _ = dsa.mla_prefill(q, kv.view(L, H, 256), back[:, 512:], at(0, T), at(0, L), softmax_scale=0.07, max_q_per_seq=T)
+    y = dsa.matmul_fp8(*dsa.quant_rows(o.view(T, H * 128)), *wo)
+    z = 0.07 * (torch.einsum("thd,jhd->htj", q[..., :128].double(), kv.view(L, H, 256)[..., :128].double())
+                + torch.einsum("thd,jd->htj", q[..., 128:].double(), back[:, 512:].double()))
+    z.masked_fill_(pos[None] > pos[-T:, None], -math.inf)
+    want = torch.einsum("htj,jhd->thd", z.softmax(-1), kv.view(L, H, 256)[..., 128:].double())
+    assert near(y, want.reshape(T, -1) @ value(*wo).T, 0.06)
+
+
+def _args(**over):
+    a = dsa.MatmulFp8Args()
+    a.M, a.N, a.K, a.elem = 4, 256, 512, 0
+    a.a_stride, a.a_scale_stride, a.b_stride, a.b_scale_stride, a.out_stride = 512, 4, 512, 4, 256
+    for n in ("a", "a_scale", "b", "b_scale", "out"):
+        setattr(a, n, 4096)  # fake, aligned, never dereferenced on these error paths
+    for k, v in over.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("over,code", [
+    ({"M": -1}, dsa.DSA_ERR_INVALID_ARG),
+    ({"N": 0}, dsa.DSA_ERR_INVALID_ARG),
+    ({"K": 0}, dsa.DSA_ERR_INVALID_ARG),
+    ({"K": 520}, dsa.DSA_ERR_UNSUPPORTED),
+    ({"M": 0x7fffff80}, dsa.DSA_ERR_UNSUPPORTED),
+    ({"elem": 3}, dsa.DSA_ERR_INVALID_ARG),
+    ({"a": None}, dsa.DSA_ERR_INVALID_ARG),
+    ({"b_scale": None}, dsa.DSA_ERR_INVALID_ARG),
+    ({"out": None}, dsa.DSA_ERR_INVALID_ARG),
+    ({"a": 4104}, dsa.DSA_ERR_INVALID_ARG),
+    ({"b": 4097}, dsa.DSA_ERR_INVALID_ARG),
+    ({"out": 4097}, dsa.DSA_ERR_INVALID_ARG),
+    ({"a_scale": 4098}, dsa.DSA_ERR_INVALID_ARG),
+    ({"a_stride": 496}, dsa.DSA_ERR_INVALID_ARG),
+    ({"b_stride": 520}, dsa.DSA_ERR_INVALID_ARG),
+    ({"b_stride": 1 << 40}, dsa.DSA_ERR_INVALID_ARG),
+    ({"a_scale_stride": 3}, dsa.DSA_ERR_INVALID_ARG),
+    ({"out_stride": 255}, dsa.DSA_ERR_INVALID_ARG),
+])
+def test_host_validation(over, code):
+    lib = dsa.load()
+    assert lib.dsa_matmul_fp8(ctypes.byref(_args(**over)), None) == code, dsa.last_error()
+    assert dsa.last_error()
+    assert lib.dsa_matmul_fp8(None, None) == dsa.DSA_ERR_INVALID_ARG
+    assert lib.dsa_matmul_fp8(ctypes.byref(_args(M=0)), None) == dsa.DSA_OK
+
+
+def test_struct_layout():
+    assert ctypes.sizeof(dsa.MatmulFp8Args) == 4 * 4 + 5 * 8 + 6 * 8
+
+
+def test_binding_refuses_cpu_tensors():
+    a, s = torch.zeros((4, 256)).to(torch.float8_e4m3fn), torch.ones((4, 2))
+    with pytest.raises(ValueError):
+        dsa.matmul_fp8(a, s, a, s[:1])
+
+
+@pytest.mark.gpu
+def test_binding_refuses_what_does_not_fit(cuda_lib):
+    a, a_scale, b, b_scale = whole(4, 256, 512, gen(6))
+    out = torch.empty((4, 256), device="cuda")
+    for bad in (dict(a=a.view(torch.uint8)), dict(a=a[0]), dict(a=a[:, :256]), dict(a=a[:1].expand(4, 512)),
+                dict(a=a.T.contiguous().T), dict(a_scale=a_scale[:, :3]), dict(a_scale=a_scale.double()),
+                dict(a_scale=a_scale.cpu()), dict(b=b[:, :256]), dict(b=b.float()), dict(b_scale=b_scale[:1]),
+                dict(b_scale=b_scale.T.contiguous().T), dict(out=out.double()), dict(out=out[:, :255]),
+                dict(out=out.T.contiguous().T), dict(dtype=torch.float64), dict(dtype=torch.int32),
+                dict(status=torch.zeros(1, device="cuda"))):
+        kw = dict(a=a, a_scale=a_scale, b=b, b_scale=b_scale)
+        kw.update(bad)
+        with pytest.raises(ValueError):
+            dsa.matmul_fp8(**kw)
+    with pytest.raises(dsa.DsaError):
+        dsa.matmul_fp8(a[:, 8:264], a_scale[:, :2], b[:, :256], b_scale[:, :2])   # rows that start on 8 bytes

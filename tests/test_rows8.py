@@ -1,0 +1,300 @@
+"""8-bit rows: the root-mean-square norm with the residual's addition, and rows as they are.
+
+Both are compared with their definition in 64 bits.  Rows without a norm match bit for bit, as the
+quantised cache write does.  With a norm, the sum of squares is held in fp32: a thread adds up to 16
+squares in each of two sums, the two, and five times its warp's (the warps' sums are added without loss), 22 roundings of
+at most 2^-24 each, half of which reach 1 / sqrt; with the rounding of h * weight, and of r and s, v / s is off by less
+than 14 * 2^-24 < 2^-20.  So a code lies between those of v / s (1 - 2^-20) and v / s (1 + 2^-20).
+"""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import dsa_sparse_attention_li_gb300 as dsa
+from test_cache_quant import hard_rows, nearest_code
+
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+OFF = 2.0 ** -20
+
+
+def group_scales(v):
+    """fp32(a / 448) of every group of 128 columns of v (64 bits), a its largest finite magnitude."""
+    n, d = v.shape
+    v = torch.nn.functional.pad(v, (0, -d % 128)).view(n, -1, 128)
+    a = torch.where(torch.isfinite(v), v.abs(), 0.0).amax(2)
+    return torch.where(a > 0, (a / 448).clamp(min=2.0 ** -126), 1.0).float()
+
+
+def columns(s, d):
+    return s.double().repeat_interleave(128, 1)[:, :d]
+
+
+def same_codes(got, q):
+    """Whether e4m3 codes are those nearest to the quotients q (64 bits), bit for bit but for a NaN's sign."""
+    code, sign = nearest_code(q)
+    raw = got.view(torch.uint8).long()
+    want = code + 128 * sign.long()
+    return torch.where(code == 127, (raw & 127) == 127, raw == want)
+
+
+def check_norm(x, w, residual, eps, codes, scale, total, y):
+    """All outputs (on the CPU) of one call against the definition."""
+    kind, d = x.dtype, x.shape[1]
+    h = x
+    if residual is not None:
+        h = (x.float() + residual.float()).to(kind)
+        assert torch.equal(torch.nan_to_num(total), torch.nan_to_num(h)) and torch.equal(total.isnan(), h.isnan())
+    h = h.double()
+    r = 1 / torch.sqrt((h * h).mean(1, keepdim=True) + eps)
+    v = h * w.double() * r
+    under = r * 2.0 ** -149    # h * w below fp32's normal range is off by half its smallest step, twice that here
+    want = group_scales(v).double()
+    assert torch.all((scale.double() - want).abs() <= want * OFF + under + 2.0 ** -149)
+    q = v / columns(scale, d)
+    off = q.abs() * OFF + under / columns(scale, d)
+    low, _ = nearest_code((q.abs() - off).clamp(min=0))
+    high, _ = nearest_code(q.abs() + off)
+    got = codes.view(torch.uint8).long() & 127
+    assert torch.all((got >= low) & (got <= high))
+    assert torch.all((torch.signbit(codes.float()) == torch.signbit(v)) | (got == 127))
+    if y is not None:
+        # (below the type's normal range a rounding is off by half its smallest step)
+        step = torch.finfo(kind).eps / 2
+        off = v.abs() * (step + OFF) + torch.finfo(kind).smallest_normal * step + under
+        good = torch.isfinite(v) & (v.abs() < torch.finfo(kind).max)
+        assert torch.all(((y.double() - v).abs() <= off)[good])
+        assert torch.equal(y.isnan(), v.isnan())
+
+
+def strided(t, pad):
+    wide = torch.full((t.shape[0], t.shape[1] + pad), 3.0, device=t.device).to(t.dtype)
+    wide[:, :t.shape[1]] = t
+    return wide[:, :t.shape[1]]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("n,d", [(1, 8), (3, 64), (5, 120), (37, 128), (6, 136), (9, 256), (4, 264), (7, 512), (3, 520),
+                                 (5, 576), (11, 1536), (2, 4104), (33, 7168), (3, 16384), (2, 16392), (2, 32768)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_matches_the_definition(cuda_lib, n, d, dtype, residual):
+    g = torch.Generator().manual_seed(n * 7 + d)
+    x = (torch.randn((n, d), generator=g) * torch.exp(torch.randn((n, 1), generator=g))).to(dtype)
+    r = (3 * torch.randn((n, d), generator=g)).to(dtype) if residual else None
+    w = (1 + 0.3 * torch.randn(d, generator=g)).to(torch.float32 if n % 2 else dtype)
+    pad = 8 * (n % 3)
+    y = strided(torch.zeros((n, d), dtype=dtype, device="cuda"), pad)
+    got = dsa.rms_norm_quant(strided(x.cuda(), pad), w.cuda(), eps=1e-6, y=y,
+                             residual=None if r is None else strided(r.cuda(), 8))
+    codes, scale = got[:2]
+    assert codes.dtype == torch.float8_e4m3fn and codes.shape == (n, d) and scale.shape == (n, -(-d // 128))
+    check_norm(x, w, r, 1e-6, codes.cpu(), scale.cpu(), got[2].cpu() if residual else None, y.cpu())
+    if pad:  # nothing beyond a row's columns is written
+        assert torch.all(y.as_strided((n, pad), (y.stride(0), 1), d)[:, :].float() == 3.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("d", [72, 576, 2048])
+def test_norm_of_hard_rows(cuda_lib, d, dtype):
+    """Rows of zeros, of the type's smallest and largest values, with infinities and NaN."""
+    g = torch.Generator().manual_seed(d)
+    x = hard_rows(24, d, dtype, g)
+    w = (1 + 0.3 * torch.randn(d, generator=g)).to(dtype)
+    y = torch.empty((24, d), dtype=dtype, device="cuda")
+    codes, scale = dsa.rms_norm_quant(x.cuda(), w.cuda(), eps=1e-5, y=y)
+    codes, scale, y = codes.cpu().view(torch.uint8), scale.cpu(), y.cpu()
+    # rows whose sum of squares fits fp32; the others have r = 0, or are all NaN
+    squares = (x.double() ** 2).sum(1)
+    fits = squares < 2.0 ** 127
+    check_norm(x[fits], w, None, 1e-5, codes[fits].view(torch.float8_e4m3fn), scale[fits], None, y[fits])
+    nan = torch.isnan(x).any(1)
+    assert torch.all((codes[nan] & 127) == 127) and torch.all(y[nan].isnan())
+    assert torch.all(scale[nan] == 1.0)
+    over = ~nan & ~(squares < 2.0 ** 130)
+    finite = torch.isfinite(x[over])
+    assert torch.all((codes[over] & 127)[finite] == 0) and torch.all(scale[over] == 1.0)
+    assert torch.all((codes[over] & 127)[~finite] == 127)
+
+
+@pytest.mark.gpu
+def test_norm_of_zero_rows_without_epsilon(cuda_lib):
+    """0 / 0: NaN, as the formula has it, in that row alone."""
+    x = torch.randn((3, 200), generator=torch.Generator().manual_seed(0)).bfloat16()
+    x[1] = 0
+    w = torch.ones(200, dtype=torch.bfloat16)
+    codes, scale = dsa.rms_norm_quant(x.cuda(), w.cuda(), eps=0.0)
+    codes = codes.cpu().view(torch.uint8)
+    assert torch.all((codes[1] & 127) == 127) and torch.all(scale[1] == 1.0)
+    check_norm(x[[0, 2]], w, None, 0.0, codes[[0, 2]].view(torch.float8_e4m3fn), scale.cpu()[[0, 2]], None, None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [128, 7168])
+def test_norm_in_place(cuda_lib, d):
+    """The sum in the residual's place, and the normed rows in x's."""
+    g = torch.Generator().manual_seed(d)
+    x, r = (torch.randn((19, d), generator=g).bfloat16().cuda() for _ in range(2))
+    w = torch.rand(d, generator=g).bfloat16().cuda()
+    y = torch.empty_like(x)
+    want = dsa.rms_norm_quant(x, w, residual=r, y=y)
+    x2, r2 = x.clone(), r.clone()
+    got = dsa.rms_norm_quant(x2, w, residual=r2, residual_out=r2, y=x2)
+    assert got[2] is r2 and torch.equal(r2, want[2]) and torch.equal(x2, y)
+    assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("n,d", [(1, 8), (16, 64), (9, 200), (203, 128), (24, 576), (8, 16384), (1, 40000)])
+def test_rows_match_the_definition(cuda_lib, n, d, dtype):
+    g = torch.Generator().manual_seed(n + d)
+    x = hard_rows(n, d, dtype, g)
+    codes = strided(torch.zeros((n, d), device="cuda").to(torch.float8_e4m3fn), 8)
+    scale = strided(torch.zeros((n, -(-d // 128)), device="cuda"), 3)
+    dsa.quant_rows(strided(x.cuda(), 16), codes=codes, scale=scale)
+    s = group_scales(x.double())
+    assert torch.equal(scale.cpu(), s)
+    assert torch.all(same_codes(codes.cpu().contiguous(), x.double() / columns(s, d)))
+    assert torch.all(codes.as_strided((n, 8), (d + 8, 1), d).float() == 3.0)
+
+
+@pytest.mark.gpu
+def test_many_rows_and_far_rows(cuda_lib):
+    """Rows that lie 2 GB apart, and more rows than a wave of blocks, one by one as all at once."""
+    g = torch.Generator().manual_seed(4)
+    values = torch.randn((5, 1024), generator=g).bfloat16().cuda()
+    far = torch.zeros(4 * 2 ** 30 + 1024, dtype=torch.bfloat16, device="cuda").as_strided((5, 1024), (2 ** 30, 1))
+    far.copy_(values)
+    w = torch.ones(1024, device="cuda")
+    for call in (dsa.quant_rows, lambda x: dsa.rms_norm_quant(x, w)):
+        a, b = call(far), call(values)
+        assert torch.equal(a[0].view(torch.uint8), b[0].view(torch.uint8)) and torch.equal(a[1], b[1])
+    codes = torch.zeros(4 * 2 ** 30 + 1024, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    codes = codes.as_strided((5, 1024), (2 ** 30, 1))
+    dsa.quant_rows(values, codes=codes)
+    assert torch.equal(codes.contiguous().view(torch.uint8), dsa.quant_rows(values)[0].view(torch.uint8))
+    del far, codes
+    x = torch.randn((30011, 136), generator=g).cuda()
+    w = torch.rand(136, generator=g).cuda()
+    for call in (dsa.quant_rows, lambda x: dsa.rms_norm_quant(x, w)):
+        a = call(x)
+        b = [call(x[i:i + 977]) for i in range(0, len(x), 977)]
+        assert torch.equal(a[0].view(torch.uint8), torch.cat([p[0].view(torch.uint8) for p in b]))
+        assert torch.equal(a[1], torch.cat([p[1] for p in b]))
+
+
+@pytest.mark.gpu
+def test_no_rows(cuda_lib):
+    x = torch.zeros((0, 256), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    assert dsa.quant_rows(x)[0].shape == (0, 256)
+    assert [tuple(t.shape) for t in dsa.rms_norm_quant(x, w, residual=x)] == [(0, 256), (0, 2), (0, 256)]
+
+
+def _norm(**over):
+    a = dsa.RmsNormQuantArgs()
+    a.n_rows, a.dim, a.elem, a.weight_elem, a.eps = 4, 576, 0, 0, 1e-6
+    a.x_stride = a.residual_stride = a.sum_stride = a.y_stride = a.codes_stride = 576
+    a.scale_stride = 5
+    for n in ("x", "weight", "residual", "sum", "codes", "scale"):
+        setattr(a, n, 4096)  # fake, aligned, never dereferenced on these error paths
+    for k, v in over.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("over,code", [
+    ({"n_rows": -1}, dsa.DSA_ERR_INVALID_ARG),
+    ({"dim": 0}, dsa.DSA_ERR_INVALID_ARG),
+    ({"dim": 580}, dsa.DSA_ERR_UNSUPPORTED),
+    ({"dim": 32776}, dsa.DSA_ERR_UNSUPPORTED),
+    ({"elem": 3}, dsa.DSA_ERR_INVALID_ARG),
+    ({"weight_elem": 1}, dsa.DSA_ERR_UNSUPPORTED),
+    ({"elem": 2, "weight_elem": 0}, dsa.DSA_ERR_UNSUPPORTED),
+    ({"eps": -1e-6}, dsa.DSA_ERR_INVALID_ARG),
+    ({"eps": math.inf}, dsa.DSA_ERR_INVALID_ARG),
+    ({"eps": math.nan}, dsa.DSA_ERR_INVALID_ARG),
+    ({"x": None}, dsa.DSA_ERR_INVALID_ARG),
+    ({"codes": None}, dsa.DSA_ERR_INVALID_ARG),
+    ({"sum": None}, dsa.DSA_ERR_INVALID_ARG),
+    ({"residual": None}, dsa.DSA_ERR_INVALID_ARG),
+    ({"x": 4104}, dsa.DSA_ERR_INVALID_ARG),
+    ({"y": 4104}, dsa.DSA_ERR_INVALID_ARG),
+    ({"weight": 4104}, dsa.DSA_ERR_INVALID_ARG),
+    ({"codes": 4100}, dsa.DSA_ERR_INVALID_ARG),
+    ({"x_stride": 568}, dsa.DSA_ERR_INVALID_ARG),
+    ({"residual_stride": 580}, dsa.DSA_ERR_INVALID_ARG),
+    ({"codes_stride": 580}, dsa.DSA_ERR_INVALID_ARG),
+    ({"scale_stride": 4}, dsa.DSA_ERR_INVALID_ARG),
+])
+def test_norm_host_validation(over, code):
+    lib = dsa.load()
+    assert lib.dsa_rms_norm_quant(ctypes.byref(_norm(**over)), None) == code, dsa.last_error()
+    assert dsa.last_error()
+    assert lib.dsa_rms_norm_quant(None, None) == dsa.DSA_ERR_INVALID_ARG
+    assert lib.dsa_rms_norm_quant(ctypes.byref(_norm(n_rows=0)), None) == dsa.DSA_OK
+
+
+def _rows(**over):
+    a = dsa.QuantRowsArgs()
+    a.n_rows, a.dim, a.elem, a.x_stride, a.codes_stride, a.scale_stride = 4, 576, 0, 576, 576, 5
+    a.x = a.codes = a.scale = 4096
+    for k, v in over.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("over,code", [
+    ({"n_rows": -1}, dsa.DSA_ERR_INVALID_ARG),
+    ({"dim": -8}, dsa.DSA_ERR_INVALID_ARG),
+    ({"dim": 12}, dsa.DSA_ERR_UNSUPPORTED),
+    ({"elem": -1}, dsa.DSA_ERR_INVALID_ARG),
+    ({"scale": None}, dsa.DSA_ERR_INVALID_ARG),
+    ({"x": 4104}, dsa.DSA_ERR_INVALID_ARG),
+    ({"x_stride": 572}, dsa.DSA_ERR_INVALID_ARG),
+    ({"codes_stride": 568}, dsa.DSA_ERR_INVALID_ARG),
+    ({"scale": 4098}, dsa.DSA_ERR_INVALID_ARG),
+])
+def test_rows_host_validation(over, code):
+    lib = dsa.load()
+    assert lib.dsa_quant_rows(ctypes.byref(_rows(**over)), None) == code, dsa.last_error()
+    assert dsa.last_error()
+    assert lib.dsa_quant_rows(None, None) == dsa.DSA_ERR_INVALID_ARG
+    assert lib.dsa_quant_rows(ctypes.byref(_rows(n_rows=0)), None) == dsa.DSA_OK
+
+
+def test_struct_layouts():
+    assert ctypes.sizeof(dsa.RmsNormQuantArgs) == 5 * 4 + 4 + 6 * 8 + 7 * 8
+    assert ctypes.sizeof(dsa.QuantRowsArgs) == 3 * 4 + 4 + 3 * 8 + 3 * 8
+
+
+def test_binding_refuses_cpu_tensors_and_shapes():
+    x, w = torch.zeros((4, 576), dtype=torch.bfloat16), torch.ones(576, dtype=torch.bfloat16)
+    for bad in (dict(x=x), dict(x=x.double()), dict(x=x[0])):
+        with pytest.raises(ValueError):
+            dsa.quant_rows(**bad)
+        with pytest.raises(ValueError):
+            dsa.rms_norm_quant(weight=w, **bad)
+
+
+@pytest.mark.gpu
+def test_binding_refuses_what_does_not_fit(cuda_lib):
+    x, w = torch.zeros((4, 576), dtype=torch.bfloat16, device="cuda"), torch.ones(576, dtype=torch.bfloat16, device="cuda")
+    codes, scale = torch.zeros((4, 576), device="cuda").to(torch.float8_e4m3fn), torch.zeros((4, 5), device="cuda")
+    for bad in (dict(weight=w[:512]), dict(weight=w.half()), dict(weight=w.cpu()), dict(residual=x.float()),
+                dict(residual=x[:3]), dict(residual_out=x), dict(residual=x, residual_out=x[:, :512]),
+                dict(y=x.float()), dict(codes=codes[:, :512]), dict(codes=x), dict(scale=scale[:, :4]),
+                dict(scale=scale.T.contiguous().T), dict(residual=x[:1].expand(4, 576)), dict(residual=x.cpu())):
+        kw = dict(x=x, weight=w)
+        kw.update(bad)
+        with pytest.raises(ValueError):
+            dsa.rms_norm_quant(**kw)
+    for bad in (dict(codes=codes[:3]), dict(codes=codes.view(torch.uint8)), dict(scale=scale.double()),
+                dict(x=x.T), dict(x=x[:, ::2])):
+        kw = dict(x=x)
+        kw.update(bad)
+        with pytest.raises(ValueError):
+            dsa.quant_rows(**kw)
