@@ -1,107 +1,592 @@
 // matmul_fp8.cu -- product of e4m3 rows with one fp32 scale per 128 columns and e4m3 weights with one per block of
 // 128 x 128:
-//   out[m][n] = sum_b a_scale[m][b] b_scale[n / 128][b] sum_{k in block b} a[m][k] b[n][k]
+//   out[m][n] = sum_i f_i(m, n) P_i(m, n),   f_i = a_scale[m][i] b_scale[n / 128][i],
+//   P_i = the product over the 128 columns of block i, four tcgen05 MMAs of 32 columns
 //
-// Simple form: a block of 256 threads has 64 x 64 outputs, a thread 4 x 4, over blocks of 128 columns whose codes it
-// turns into fp32 in shared memory.
+// No e4m3 MMA applies an fp32 scale, so every P_i passes through registers: the MMAs write it to one of two buffers in
+// tensor memory, and eight warps add f_i P_i to fp32 sums that they hold in registers, a row of the tile a thread (f_i
+// is then one number, or two, a thread), while the MMAs fill the other buffer.
+//
+// Wide tiles (prompts): 256 rows x 256 columns by a CTA pair (cta_group::2; each CTA has 128 rows of a, 128 of b
+// and 128 x 256 sums), a ring of six 32-KB stages, one persistent pair per two SMs.  Bound: the tensor pipe, 512 cycles
+// a block and pair.
+//
+// Narrow tiles (few rows): 128 rows x 32 to 128 columns a CTA.  A cluster of up to eight CTAs shares a tile's blocks, and
+// its parts are added in rank order through distributed shared memory: many CTAs stream the weights, the result does not
+// depend on their timing, and there is no workspace.  Two CTAs an SM, so that one's start and end run under the
+// other's stream.  Bound: HBM.
+#include <algorithm>
+
 #include "dsa_internal.h"
-#include "quant.cuh"
+#include "ptx.cuh"
 
 namespace dsa {
 namespace mm {
 
-constexpr int kTile = 64, kBlock = 128, kPitch = kBlock + 1;
+constexpr int kThreads = 320;     // of a narrow CTA: warps 0-7 add up, 8 MMA, 9 loads
+constexpr int kWideThreads = 384; // of a wide one: two idle warps fill a warpgroup, whose registers go to the sums
+constexpr int kRows = 128;        // of a CTA's tile
+constexpr int kBlock = 128;       // columns of a scale block: a row of a stage
+constexpr int kMostStages = 16;
+constexpr int kRing = 96 * 1024;  // of a narrow CTA
+constexpr int kGroupRows = 8;     // wide tiles of a column of tiles that run one after the other
 
 struct Params {
-  int M, N, K;
-  long long a_stride, a_scale_stride, b_stride, b_scale_stride, out_stride;
-  const uint8_t* a;
+  int M, N, blocks;
+  int elem;
+  int vec;                 // rows of out start 32-byte aligned
+  int tiles_m, tiles_n;
+  int a_box, stages;       // narrow: rows of a that are loaded, stages of the ring
+  long long a_scale_stride, b_scale_stride, out_stride;
   const float* a_scale;
-  const uint8_t* b;
   const float* b_scale;
   uint8_t* out;
+  int* status;
+#ifdef DSA_TEST_HOOKS
+  int stall;               // test build: the first CTA's MMA warp waits on a barrier nothing arrives on (10), or its
+                           // first load of a (11) is left out
+#endif
 };
 
-template <int E>
-__global__ void __launch_bounds__(256) simple_kernel(const __grid_constant__ Params p) {
-  extern __shared__ float smem[];
-  float* as = smem;
-  float* bs = smem + kTile * kPitch;
-  const int tid = threadIdx.x, m0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile;
-  const int tm = (tid >> 4) * 4, tn = (tid & 15) * 4;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < p.K; k0 += kBlock) {
-    for (int i = tid; i < kTile * kBlock; i += 256) {
-      const int r = i >> 7, k = i & 127;
-      const bool in = k0 + k < p.K;
-      as[r * kPitch + k] = in && m0 + r < p.M ? e4m3_value(p.a[(long long)(m0 + r) * p.a_stride + k0 + k]) : 0.f;
-      bs[r * kPitch + k] = in && n0 + r < p.N ? e4m3_value(p.b[(long long)(n0 + r) * p.b_stride + k0 + k]) : 0.f;
+struct Ctl {
+  uint64_t full[kMostStages], empty[kMostStages];
+  uint64_t sum_full[2], sum_free[2];
+#ifdef DSA_TEST_HOOKS
+  uint64_t never;          // test build: no thread ever arrives here
+#endif
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Ctl) <= 1024, "control block");
+
+// N values to element `at` of out on, `left` columns from the end of its row.
+template <int N>
+DSA_DEV void store(const Params& p, long long at, int left, const float* v) {
+  if (left <= 0) return;
+  if (p.elem == DSA_ELEM_FP32) {
+    float* o = reinterpret_cast<float*>(p.out) + at;
+    if (p.vec && left >= N) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < left) o[i] = v[i];
     }
-    __syncthreads();
-    float part[4][4] = {};
-    for (int k = 0; k < kBlock; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) part[i][j] = fmaf(as[(tm + i) * kPitch + k], bs[(tn + j) * kPitch + k], part[i][j]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int m = m0 + tm + i, n = n0 + tn + j;
-        if (m >= p.M || n >= p.N) continue;
-        const float s = p.a_scale[m * p.a_scale_stride + (k0 >> 7)] * p.b_scale[(n >> 7) * p.b_scale_stride + (k0 >> 7)];
-        acc[i][j] = fmaf(s, part[i][j], acc[i][j]);
-      }
-    __syncthreads();
+    return;
   }
+  uint32_t w[N / 2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + tm + i, n = n0 + tn + j;
-      if (m >= p.M || n >= p.N) continue;
-      const long long at = m * p.out_stride + n;
-      if constexpr (E == DSA_ELEM_FP32)
-        reinterpret_cast<float*>(p.out)[at] = acc[i][j];
-      else if constexpr (E == DSA_ELEM_BF16)
-        reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(acc[i][j]);
-      else
-        reinterpret_cast<__half*>(p.out)[at] = __float2half_rn(acc[i][j]);
+  for (int i = 0; i < N / 2; ++i) {
+    if (p.elem == DSA_ELEM_BF16) {
+      w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    } else {
+      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
+  }
+  uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + at;
+  if (p.vec && left >= N) {
+    if constexpr (N == 16)
+      st_global_v8(o, w);
+    else
+      *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < left) o[i] = (uint16_t)(w[i >> 1] >> ((i & 1) * 16));
+  }
+}
+
+// A thread's sums of one row over kCols columns, and the scales that go with them; kStep columns at a time come from
+// tensor memory.
+template <int kCols, int kStep>
+struct Sums {
+  float2 v[kCols / 2];
+  const float* a_scale;     // of the row
+  const float* b_scale[2];  // of the columns' two blocks
+  int split;                // columns of the first
+
+  DSA_DEV void start(const Params& p, int row, int col) {
+#pragma unroll
+    for (int i = 0; i < kCols / 2; ++i) v[i] = make_float2(0.f, 0.f);
+    a_scale = p.a_scale + (long long)min(row, p.M - 1) * p.a_scale_stride;
+    const int first = min(col, p.N - 1) >> 7, last = min(col + kCols - 1, p.N - 1) >> 7;
+    b_scale[0] = p.b_scale + first * p.b_scale_stride;
+    b_scale[1] = p.b_scale + last * p.b_scale_stride;
+    split = first == last ? kCols : (first + 1) * kBlock - col;
+  }
+  DSA_DEV float2 factors(int block) const {
+    const float a = __ldg(a_scale + block);
+    return make_float2(a * __ldg(b_scale[0] + block), a * __ldg(b_scale[1] + block));
+  }
+  // Adds f times the block's products at `tmem`.
+  DSA_DEV void add(uint32_t tmem, float2 f) {
+    constexpr int kLoads = kCols / kStep;
+    static_assert(kCols % kStep == 0, "whole steps");
+#pragma unroll
+    for (int c = 0; c < kLoads; ++c) {
+      uint32_t r[kStep];
+      if constexpr (kStep == 32)
+        tmem_ld_x32(tmem + c * kStep, r);
+      else
+        tmem_ld_x16(tmem + c * kStep, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < kStep; i += 2) {
+        const float s = c * kStep + (i & 16) < split ? f.x : f.y;
+        float2& x = v[(c * kStep + i) / 2];
+        x = fma2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), s, x);
+      }
+    }
+  }
+};
+
+// The copies of a call that gave up may still be in flight: gives them time to land.
+DSA_DEV void drain(const Ctl* ctl) {
+  if (!*(volatile const int*)&ctl->abort) return;
+  const uint64_t t0 = globaltimer();
+  while (globaltimer() - t0 < 2000000u) {
+  }
+}
+
+// ---------------------------------------------------------------- narrow tiles
+
+// CH: 32-column steps of a tile.
+template <int CH>
+__global__ void __launch_bounds__(kThreads, 2)
+    narrow_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Params p) {
+  constexpr int BN = 32 * CH, HC = BN / 2, kBuf = CH == 1 ? 32 : CH == 2 ? 64 : 128, kPitch = BN + 4;
+  static_assert(kRows * kPitch * 4 <= kRing, "parts of a tile");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + kRing);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  volatile int* abort = &ctl->abort;
+  const int splits = (int)cluster_nrank(), rank = (int)cluster_rank();
+  const int m0 = (int)blockIdx.y * kRows, n0 = (int)blockIdx.x / splits * BN;
+  const int first = (int)((long long)p.blocks * rank / splits), n = (int)((long long)p.blocks * (rank + 1) / splits) - first;
+  const int a_bytes = p.a_box * kBlock, b_at = p.stages * a_bytes;   // (the MMAs read 128 rows of a: of later slots, and b)
+
+  if (tid == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->sum_full[i], 1);
+      mbar_init(&ctl->sum_free[i], 8);
+    }
+#ifdef DSA_TEST_HOOKS
+    mbar_init(&ctl->never, 1);
+#endif
+    ctl->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&ctl->tmem_base, 2 * kBuf);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
+  griddep_wait();  // nothing above reads global memory
+
+  float* part = reinterpret_cast<float*>(smem);   // [128][kPitch], once the ring is done with
+  if (warp == 9) {
+    // ---------------- loads
+    if (lane == 0) {
+      int slot = 0;
+      uint32_t turn = 0;
+      for (int i = 0; i < n; ++i) {
+        if (turn > 0 && !mbar_wait_fast(&ctl->empty[slot], (turn - 1) & 1u, abort, p.status)) break;
+        mbar_arrive_expect_tx(&ctl->full[slot], a_bytes + BN * kBlock);
+        bool load_a = true;
+#ifdef DSA_TEST_HOOKS
+        load_a = !(p.stall == 11 && blockIdx.x == 0 && i == 0);
+#endif
+        if (load_a) tma_load_2d(smem + slot * a_bytes, &tm_a, &ctl->full[slot], (first + i) * kBlock, m0);
+        tma_load_2d(smem + b_at + slot * BN * kBlock, &tm_b, &ctl->full[slot], (first + i) * kBlock, n0);
+        if (++slot == p.stages) {
+          slot = 0;
+          ++turn;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // ---------------- MMA issue: the whole warp walks, one lane issues
+    constexpr uint32_t idesc = idesc_e4m3(kRows, BN);
+    const uint64_t ad = sdesc_sw128(smem_u32(smem), 16, 1024), bd = sdesc_sw128(smem_u32(smem + b_at), 16, 1024);
+    const uint32_t me = elect_one();
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      mbar_wait_issue<false>(bar, parity, abort, p.status);
+      __syncwarp();
+    };
+#ifdef DSA_TEST_HOOKS
+    if (p.stall == 10 && blockIdx.x == 0) warp_wait(&ctl->never, 0, abort, p.status);
+#endif
+    int slot = 0;
+    uint32_t turn = 0;
+    for (int i = 0; i < n; ++i) {
+      wait(&ctl->full[slot], turn & 1u);
+      if (i >= 2) wait(&ctl->sum_free[i & 1], ((i >> 1) - 1) & 1u);
+      if (__any_sync(0xffffffffu, *abort)) break;
+      tc_fence_after();
+      const uint64_t a = desc_at(ad, slot * a_bytes), b = desc_at(bd, slot * BN * kBlock);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        mma_f8_ss_by(tmem + (i & 1) * kBuf, desc_at(a, k * 32), desc_at(b, k * 32), idesc, k > 0 ? 1u : 0u, me);
+      mma_commit_by(&ctl->empty[slot], me);
+      mma_commit_by(&ctl->sum_full[i & 1], me);
+      if (++slot == p.stages) {
+        slot = 0;
+        ++turn;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- sums
+    const int local = (warp & 3) * 32 + lane, half = (warp >> 2) * HC;
+    const bool any = m0 + (warp & 3) * 32 < p.M;   // some row of the warp's
+    Sums<HC, 16> sums;
+    sums.start(p, m0 + local, n0 + half);
+    const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half;
+    float2 f = sums.factors(first);
+    for (int i = 0; i < n; ++i) {
+      const float2 next = i + 1 < n ? sums.factors(first + i + 1) : f;
+      warp_wait(&ctl->sum_full[i & 1], (i >> 1) & 1u, abort, p.status);
+      if (__any_sync(0xffffffffu, *abort)) break;
+      if (any) {
+        tc_fence_after();
+        sums.add(at + (i & 1) * kBuf, f);
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->sum_free[i & 1]);
+      f = next;
+    }
+    if (splits == 1) {
+      if (m0 + local < p.M && !*abort) {
+        const long long out = (long long)(m0 + local) * p.out_stride + n0 + half;
+#pragma unroll
+        for (int c = 0; c < HC; c += 16) store<16>(p, out + c, p.N - n0 - half - c, &sums.v[c / 2].x);
+      }
+    } else if (any && !*abort) {
+      // (every MMA of this CTA is done: the last block's sums have been read)
+      float* to = part + local * kPitch + half;
+#pragma unroll
+      for (int c = 0; c < HC; c += 4)
+        *reinterpret_cast<float4*>(to + c) = make_float4(sums.v[c / 2].x, sums.v[c / 2].y, sums.v[c / 2 + 1].x, sums.v[c / 2 + 1].y);
+    }
+  }
+  __syncwarp();
+  if (splits > 1) {
+    // ---------------- the parts of a tile: each CTA adds up those of its share of the columns, in rank order
+    cluster_sync();
+    const int quads = BN / 4 / splits, items = min(kRows, p.M - m0) * quads;
+    for (int it = tid; it < items; it += kThreads) {
+      const int row = it / quads, col = (rank * quads + it - row * quads) * 4;
+      const float* from = part + row * kPitch + col;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s = 0; s < splits; ++s) {
+        const uint4 u = ld_cluster_v4(map_cluster(from, (uint32_t)s));
+        v.x += __uint_as_float(u.x);
+        v.y += __uint_as_float(u.y);
+        v.z += __uint_as_float(u.z);
+        v.w += __uint_as_float(u.w);
+      }
+      store<4>(p, (long long)(m0 + row) * p.out_stride + n0 + col, p.N - n0 - col, &v.x);
+    }
+  }
+  drain(ctl);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (splits > 1) cluster_sync();   // no CTA's parts go before all have read them
+  if (warp == 8) tmem_dealloc(tmem, 2 * kBuf);
+}
+
+// ---------------------------------------------------------------- wide tiles
+
+template <int BN>
+struct Wide {
+  static constexpr int kCols = BN / 2;                       // of a thread
+  static constexpr int kA = kRows * kBlock, kB = BN / 2 * kBlock, kStage = kA + kB;
+  static constexpr int kStages = 6;
+  static constexpr int ctl = kStages * kStage, total = ctl + 1024;
+};
+
+template <int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
+    wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Params p) {
+  using W = Wide<BN>;
+  constexpr int kCols = W::kCols;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + W::ctl);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  volatile int* abort = &ctl->abort;
+  const int rank = (int)cluster_rank(), pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1;
+  const long long tiles = (long long)p.tiles_m * p.tiles_n;
+
+  if (tid == 0) {
+    for (int i = 0; i < W::kStages; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->sum_full[i], 1);
+      mbar_init(&ctl->sum_free[i], 16);   // eight warps of either CTA
+    }
+#ifdef DSA_TEST_HOOKS
+    mbar_init(&ctl->never, 1);
+#endif
+    ctl->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc2(&ctl->tmem_base, 512);
+    tmem_relinquish2();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // barriers and tensor memory of both CTAs are ready
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
+  griddep_wait();  // nothing above reads global memory
+
+  // Tiles in groups of kGroupRows rows of tiles, column by column: what runs at one time shares rows of a and of b.
+  auto place = [&](long long t, int& m0, int& n0) {
+    const long long group = (long long)kGroupRows * p.tiles_n;
+    const int g = (int)(t / group), in = (int)(t - g * group);
+    const int rows = min(kGroupRows, p.tiles_m - g * kGroupRows);
+    m0 = (g * kGroupRows + in % rows) * 2 * kRows;
+    n0 = in / rows * BN;
+  };
+
+  // (2 * 216 + 72: the 3 * 168 registers a lane that the three warpgroups were launched with)
+  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  if (warp == 9) {
+    // ---------------- loads: this CTA's half of a's rows and of b's, counted on the even CTA's barrier
+    if (lane == 0) {
+      const uint32_t full = map_cluster(&ctl->full[0], 0);
+      int slot = 0;
+      uint32_t turn = 0;
+      bool ok = true;
+      for (long long t = pair; t < tiles && ok; t += pairs) {
+        int m0, n0;
+        place(t, m0, n0);
+        for (int i = 0; i < p.blocks; ++i) {
+          ok = turn == 0 || mbar_wait_fast(&ctl->empty[slot], (turn - 1) & 1u, abort, p.status);
+          if (!ok) break;
+          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[slot], 2 * W::kStage);
+          uint8_t* to = smem + slot * W::kStage;
+          bool load_a = true;
+#ifdef DSA_TEST_HOOKS
+          load_a = !(p.stall == 11 && blockIdx.x == 0 && t == pair && i == 0);
+#endif
+          if (load_a) tma_load_2d_pair(to, &tm_a, full + slot * 8, i * kBlock, m0 + rank * kRows);
+          tma_load_2d_pair(to + W::kA, &tm_b, full + slot * 8, i * kBlock, n0 + rank * (BN / 2));
+          if (++slot == W::kStages) {
+            slot = 0;
+            ++turn;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 8 && rank == 0) {
+    // ---------------- MMA issue, for both CTAs: the whole warp walks, one lane issues
+    constexpr uint32_t idesc = idesc_e4m3(2 * kRows, BN);
+    const uint64_t ad = sdesc_sw128(smem_u32(smem), 16, 1024), bd = sdesc_sw128(smem_u32(smem + W::kA), 16, 1024);
+    const uint32_t me = elect_one();
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      mbar_wait_issue<true>(bar, parity, abort, p.status);
+      __syncwarp();
+    };
+#ifdef DSA_TEST_HOOKS
+    if (p.stall == 10 && blockIdx.x == 0) warp_wait(&ctl->never, 0, abort, p.status);
+#endif
+    int slot = 0;
+    uint32_t turn = 0, it = 0;
+    bool go = true;
+    for (long long t = pair; t < tiles && go; t += pairs) {
+#pragma unroll 1
+      for (int i = 0; i < p.blocks; ++i, ++it) {
+        wait(&ctl->full[slot], turn & 1u);
+        if (it >= 2) wait(&ctl->sum_free[it & 1u], ((it >> 1) - 1) & 1u);
+        go = !__any_sync(0xffffffffu, *abort);
+        if (!go) break;
+        tc_fence_after();
+        const uint64_t a = desc_at(ad, slot * W::kStage), b = desc_at(bd, slot * W::kStage);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma2_f8_ss(tmem + (it & 1u) * 256u, desc_at(a, k * 32), desc_at(b, k * 32), idesc, k > 0 ? 1u : 0u, me);
+        mma2_commit_both(&ctl->empty[slot], me);
+        mma2_commit_both(&ctl->sum_full[it & 1u], me);
+        if (++slot == W::kStages) {
+          slot = 0;
+          ++turn;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ---------------- sums
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int local = (warp & 3) * 32 + lane, half = (warp >> 2) * kCols;
+    const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half;
+    const uint32_t sum_free = map_cluster(&ctl->sum_free[0], 0);
+    uint32_t it = 0;
+    bool go = true;
+    for (long long t = pair; t < tiles && go; t += pairs) {
+      int m0, n0;
+      place(t, m0, n0);
+      const int row = m0 + rank * kRows + local;
+      Sums<kCols, 32> sums;
+      sums.start(p, row, n0 + half);
+      float2 f = sums.factors(0);
+#pragma unroll 1
+      for (int i = 0; i < p.blocks; ++i, ++it) {
+        const float2 next = i + 1 < p.blocks ? sums.factors(i + 1) : f;
+        mbar_wait(&ctl->sum_full[it & 1u], (it >> 1) & 1u, abort, p.status);   // (a call would cost registers)
+        __syncwarp();
+        go = !__any_sync(0xffffffffu, *abort);
+        if (!go) break;
+        tc_fence_after();
+        sums.add(at + (it & 1u) * 256u, f);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_pair(sum_free + (it & 1u) * 8);
+        f = next;
+      }
+      if (go && row < p.M) {
+        const long long out = (long long)row * p.out_stride + n0 + half;
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16) store<16>(p, out + c, p.N - n0 - half - c, &sums.v[c / 2].x);
+      }
+    }
+    __syncwarp();
+  }
+  __syncwarp();
+  drain(ctl);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 8) tmem_dealloc2(tmem, 512);
+}
+
+using Kernel = void (*)(CUtensorMap, CUtensorMap, Params);
+
+struct Plan {
+  bool wide;
+  int bn, splits;
+};
+
+// The plan with the least estimated time.  Both kinds stream blocks of 128 columns; a wide tile's block takes the tensor
+// pipe 512 cycles, a narrow one's what its bytes take of an SM's share of the HBM rate (23 bytes a cycle), or the sums.
+Plan plan(int M, int N, int blocks, int sms) {
+  const double pairs = std::max(1, sms / 2);
+  const double wide_tiles = std::ceil(M / 256.0) * std::ceil(N / 256.0);
+  Plan best = {true, 256, 1};
+  double least = std::ceil(wide_tiles / pairs) * (blocks * 540.0 + 1500.0) + 3000.0;
+  const double tiles_m = std::ceil(M / 128.0);
+  if (tiles_m > 65535) return best;
+  for (int bn = 32; bn <= 128; bn += 32)
+    for (int s = 1; s <= 8 && s <= blocks; s *= 2) {
+      const double ctas = tiles_m * std::ceil((double)N / bn) * s, rounds = std::max(1.0, ctas / (2.0 * sms));
+      const double rows = std::min(M, 128);
+      // two CTAs share an SM
+      const double block = std::max({bn * 128.0 / 23.0 * (ctas > sms ? 2 : 1), (bn + rows) * 128.0 / 60.0, 300.0});
+      const double t = std::ceil(rounds) * (std::ceil((double)blocks / s) * block + 2500.0) + (s > 1 ? 2000.0 : 0.0);
+      if (t < least) {
+        least = t;
+        best = {false, bn, s};
+      }
+    }
+  return best;
 }
 
 }  // namespace mm
 
 dsa_status launch_matmul_fp8(const dsa_matmul_fp8_args& a, cudaStream_t stream, std::string& err) {
   using namespace mm;
+  DeviceInfo dev;
+  if (!device_info(dev, err)) return DSA_ERR_CUDA;
   Params p;
   p.M = a.M;
   p.N = a.N;
-  p.K = a.K;
-  p.a_stride = a.a_stride;
+  p.blocks = (a.K + kBlock - 1) / kBlock;
+  p.elem = a.elem;
+  const int size = a.elem == DSA_ELEM_FP32 ? 4 : 2;
+  p.vec = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 && (a.M == 1 || a.out_stride * size % 32 == 0);
   p.a_scale_stride = a.a_scale_stride;
-  p.b_stride = a.b_stride;
   p.b_scale_stride = a.b_scale_stride;
   p.out_stride = a.out_stride;
-  p.a = reinterpret_cast<const uint8_t*>(a.a);
   p.a_scale = a.a_scale;
-  p.b = reinterpret_cast<const uint8_t*>(a.b);
   p.b_scale = a.b_scale;
   p.out = reinterpret_cast<uint8_t*>(a.out);
-  const dim3 grid((a.N + kTile - 1) / kTile, (a.M + kTile - 1) / kTile);
-  if (grid.y > 65535) {
-    err = "matmul_fp8: too many rows for one launch";
-    return DSA_ERR_UNSUPPORTED;
+  p.status = a.status;
+#ifdef DSA_TEST_HOOKS
+  p.stall = g_test_stall;
+#endif
+  const Plan w = plan(a.M, a.N, p.blocks, dev.sm_count);
+  const int rows = w.wide ? 2 * kRows : kRows;
+  p.tiles_m = (int)(((long long)a.M + rows - 1) / rows);
+  p.tiles_n = (int)(((long long)a.N + w.bn - 1) / w.bn);
+  p.a_box = w.wide ? kRows : std::min(kRows, (a.M + 7) / 8 * 8);
+  p.stages = w.wide ? Wide<256>::kStages : std::min(kMostStages, kRing / ((p.a_box + w.bn) * kBlock));
+  CUtensorMap tm_a, tm_b;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  const uint64_t K = (uint64_t)a.K;
+  if (!encode_tmap_2d(&tm_a, u8, a.a, K, (uint64_t)a.M, a.M == 1 ? K : (uint64_t)a.a_stride, kBlock, (uint32_t)p.a_box, sw, err) ||
+      !encode_tmap_2d(&tm_b, u8, a.b, K, (uint64_t)a.N, a.N == 1 ? K : (uint64_t)a.b_stride, kBlock,
+                      (uint32_t)(w.wide ? w.bn / 2 : w.bn), sw, err))
+    return DSA_ERR_CUDA;
+  Kernel k;
+  int smem;
+  static std::atomic<uint64_t> done[5];
+  int which = 0;
+  if (w.wide) {
+    k = wide_kernel<256>;
+    smem = Wide<256>::total + 1024;
+  } else {
+    which = w.bn / 32;
+    k = which == 1 ? narrow_kernel<1> : which == 2 ? narrow_kernel<2> : which == 3 ? narrow_kernel<3> : narrow_kernel<4>;
+    smem = kRing + 1024 + 1024;
   }
-  const int smem = 2 * kTile * kPitch * 4;
-  const auto k = a.elem == DSA_ELEM_BF16   ? simple_kernel<DSA_ELEM_BF16>
-                 : a.elem == DSA_ELEM_FP16 ? simple_kernel<DSA_ELEM_FP16>
-                                           : simple_kernel<DSA_ELEM_FP32>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem, dev.device, done[which]);
   if (e != cudaSuccess) return cuda_fail(e, "matmul_fp8: set shared memory size", err);
-  k<<<grid, 256, smem, stream>>>(p);
-  e = cudaGetLastError();
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  if (w.wide) {
+    const long long tiles = (long long)p.tiles_m * p.tiles_n;
+    cfg.gridDim = dim3((unsigned)std::min<long long>(tiles, std::max(1, dev.sm_count / 2)) * 2);
+    cfg.numAttrs = 1;
+  } else {
+    const long long grid = (long long)p.tiles_n * w.splits;
+    if (grid > 0x7fffffffLL) {
+      err = "matmul_fp8: too many columns for one launch";
+      return DSA_ERR_UNSUPPORTED;
+    }
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)p.tiles_m);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)w.splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  cfg.blockDim = dim3(w.wide ? kWideThreads : kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  e = cudaLaunchKernelEx(&cfg, k, tm_a, tm_b, p);
   if (e != cudaSuccess) return cuda_fail(e, "matmul_fp8: launch", err);
   return DSA_OK;
 }
