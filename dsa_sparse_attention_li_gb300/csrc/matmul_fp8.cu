@@ -23,9 +23,11 @@
 namespace dsa {
 namespace mm {
 
-constexpr int kThreads = 320;     // of a narrow CTA: warps 0-7 add up, 8 MMA, 9 loads
-constexpr int kWideThreads = 384; // of a wide one: two idle warps fill a warpgroup, whose registers go to the sums
 constexpr int kRows = 128;        // of a CTA's tile
+constexpr int kThreads = 320;     // of a narrow CTA: warps 0-7 add up, 8 MMA, 9 loads
+constexpr int kWideThreads = 384; // of a wide one: 10 and 11 multiply the scales
+constexpr int kScaleBlocks = 8;   // blocks whose scales are multiplied at a time
+constexpr int kScalePitch = kRows + 4;   // floats from one block's to the next
 constexpr int kBlock = 128;       // columns of a scale block: a row of a stage
 constexpr int kMostStages = 16;
 constexpr int kRing = 96 * 1024;  // of a narrow CTA
@@ -34,7 +36,7 @@ constexpr int kGroupRows = 8;     // wide tiles of a column of tiles that run on
 struct Params {
   int M, N, blocks;
   int elem;
-  int vec;                 // rows of out start 32-byte aligned
+  int vec;                 // rows of out start 32-byte aligned (wide: 16-byte aligned)
   int tiles_m, tiles_n;
   int a_box, stages;       // narrow: rows of a that are loaded, stages of the ring
   long long a_scale_stride, b_scale_stride, out_stride;
@@ -50,7 +52,8 @@ struct Params {
 
 struct Ctl {
   uint64_t full[kMostStages], empty[kMostStages];
-  uint64_t sum_full[2], sum_free[2];
+  uint64_t sum_full[2][2], sum_free[2][2];   // by buffer and half of the columns (narrow: the first half's)
+  uint64_t scale_full[2], scale_free[2];
 #ifdef DSA_TEST_HOOKS
   uint64_t never;          // test build: no thread ever arrives here
 #endif
@@ -58,6 +61,27 @@ struct Ctl {
   int abort;
 };
 static_assert(sizeof(Ctl) <= 1024, "control block");
+
+DSA_DEV uint32_t pack16(int elem, float a, float b) {
+  if (elem == DSA_ELEM_BF16) return pack_bf16(a, b);
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A box of 32 rows and 32 columns in shared memory (in the layout that a store by TMA takes) to outputs whose rows a TMA
+// store cannot reach: a row at a time, a column a lane.
+__device__ __noinline__ void store_box(const Params& p, const uint8_t* box, int m0, int n0) {
+  const int lane = threadIdx.x & 31, rows = min(32, p.M - m0);
+  if (n0 + lane >= p.N) return;
+  for (int r = 0; r < rows; ++r) {
+    const long long at = (long long)(m0 + r) * p.out_stride + n0 + lane;
+    if (p.elem == DSA_ELEM_FP32)
+      reinterpret_cast<float*>(p.out)[at] = *reinterpret_cast<const float*>(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+    else
+      reinterpret_cast<uint16_t*>(p.out)[at] =
+          *reinterpret_cast<const uint16_t*>(box + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
+  }
+}
 
 // N values to element `at` of out on, `left` columns from the end of its row.
 template <int N>
@@ -77,14 +101,7 @@ DSA_DEV void store(const Params& p, long long at, int left, const float* v) {
   }
   uint32_t w[N / 2];
 #pragma unroll
-  for (int i = 0; i < N / 2; ++i) {
-    if (p.elem == DSA_ELEM_BF16) {
-      w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-    } else {
-      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  }
+  for (int i = 0; i < N / 2; ++i) w[i] = pack16(p.elem, v[2 * i], v[2 * i + 1]);
   uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + at;
   if (p.vec && left >= N) {
     if constexpr (N == 16)
@@ -98,46 +115,59 @@ DSA_DEV void store(const Params& p, long long at, int left, const float* v) {
   }
 }
 
-// A thread's sums of one row over kCols columns, and the scales that go with them; kStep columns at a time come from
-// tensor memory.
+// A thread's sums of one row over kCols columns; a step of kStep columns at a time comes from tensor memory, two steps in
+// flight.
 template <int kCols, int kStep>
 struct Sums {
-  float2 v[kCols / 2];
-  const float* a_scale;     // of the row
-  const float* b_scale[2];  // of the columns' two blocks
-  int split;                // columns of the first
+  static constexpr int kSteps = kCols / kStep;
+  static_assert(kCols % kStep == 0 && (kStep == 16 || kStep == 32), "whole steps");
+  uint64_t v[kCols / 2];    // two columns each
 
-  DSA_DEV void start(const Params& p, int row, int col) {
+  DSA_DEV void clear() {
 #pragma unroll
-    for (int i = 0; i < kCols / 2; ++i) v[i] = make_float2(0.f, 0.f);
-    a_scale = p.a_scale + (long long)min(row, p.M - 1) * p.a_scale_stride;
-    const int first = min(col, p.N - 1) >> 7, last = min(col + kCols - 1, p.N - 1) >> 7;
-    b_scale[0] = p.b_scale + first * p.b_scale_stride;
-    b_scale[1] = p.b_scale + last * p.b_scale_stride;
-    split = first == last ? kCols : (first + 1) * kBlock - col;
+    for (int i = 0; i < kCols / 2; ++i) v[i] = 0u;
   }
-  DSA_DEV float2 factors(int block) const {
-    const float a = __ldg(a_scale + block);
-    return make_float2(a * __ldg(b_scale[0] + block), a * __ldg(b_scale[1] + block));
+  static DSA_DEV void load(uint32_t tmem, uint32_t* r) {
+    if constexpr (kStep == 32)
+      tmem_ld_x32(tmem, r);
+    else
+      tmem_ld_x16(tmem, r);
   }
-  // Adds f times the block's products at `tmem`.
-  DSA_DEV void add(uint32_t tmem, float2 f) {
-    constexpr int kLoads = kCols / kStep;
-    static_assert(kCols % kStep == 0, "whole steps");
+  DSA_DEV void multiply_add(int step, const uint32_t* r, uint64_t f0, uint64_t f1, int split) {
 #pragma unroll
-    for (int c = 0; c < kLoads; ++c) {
-      uint32_t r[kStep];
-      if constexpr (kStep == 32)
-        tmem_ld_x32(tmem + c * kStep, r);
-      else
-        tmem_ld_x16(tmem + c * kStep, r);
-      tmem_ld_wait();
+    for (int i = 0; i < kStep; i += 2) {
+      uint64_t& x = v[(step * kStep + i) / 2];
+      x = fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), step * kStep + (i & 16) < split ? f0 : f1, x);
+    }
+  }
+  // Sixteen columns from the c-th on.
+  DSA_DEV void values(int c, float* x) const {
 #pragma unroll
-      for (int i = 0; i < kStep; i += 2) {
-        const float s = c * kStep + (i & 16) < split ? f.x : f.y;
-        float2& x = v[(c * kStep + i) / 2];
-        x = fma2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), s, x);
-      }
+    for (int i = 0; i < 16; i += 2) {
+      const float2 two = unpack2(v[(c + i) / 2]);
+      x[i] = two.x;
+      x[i + 1] = two.y;
+    }
+  }
+  // Adds the block's products at `tmem`, times the first of the factors for columns below `split`, a multiple of 16,
+  // and times the second for the others; factors() is asked while the first products are on their way, done() called
+  // once all have been read.
+  template <class Factors, class Done>
+  DSA_DEV void add(uint32_t tmem, int split, Factors&& factors, Done&& done) {
+    uint32_t r[2][kStep];
+    load(tmem, r[0]);
+    if (kSteps > 1) load(tmem + kStep, r[1]);
+    const float2 f = factors();
+    const uint64_t f0 = pack2(f.x, f.x), f1 = pack2(f.y, f.y);
+#pragma unroll
+    for (int c = 0; c < kSteps; c += 2) {
+      tmem_ld_wait_for<kStep>(r[0]);
+      if (c + 1 < kSteps) tmem_ld_wait_for<kStep>(r[1]);
+      if (c + 2 >= kSteps) done();
+      multiply_add(c, r[0], f0, f1, split);
+      if (c + 2 < kSteps) load(tmem + (c + 2) * kStep, r[0]);
+      if (c + 1 < kSteps) multiply_add(c + 1, r[1], f0, f1, split);
+      if (c + 3 < kSteps) load(tmem + (c + 3) * kStep, r[1]);
     }
   }
 };
@@ -155,7 +185,8 @@ DSA_DEV void drain(const Ctl* ctl) {
 // CH: 32-column steps of a tile.
 template <int CH>
 __global__ void __launch_bounds__(kThreads, 2)
-    narrow_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Params p) {
+    narrow_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                  const __grid_constant__ Params p) {
   constexpr int BN = 32 * CH, HC = BN / 2, kBuf = CH == 1 ? 32 : CH == 2 ? 64 : 128, kPitch = BN + 4;
   static_assert(kRows * kPitch * 4 <= kRing, "parts of a tile");
   extern __shared__ uint8_t smem_raw[];
@@ -174,8 +205,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(&ctl->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl->sum_full[i], 1);
-      mbar_init(&ctl->sum_free[i], 8);
+      mbar_init(&ctl->sum_full[i][0], 1);
+      mbar_init(&ctl->sum_free[i][0], 8);
     }
 #ifdef DSA_TEST_HOOKS
     mbar_init(&ctl->never, 1);
@@ -231,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t turn = 0;
     for (int i = 0; i < n; ++i) {
       wait(&ctl->full[slot], turn & 1u);
-      if (i >= 2) wait(&ctl->sum_free[i & 1], ((i >> 1) - 1) & 1u);
+      if (i >= 2) wait(&ctl->sum_free[i & 1][0], ((i >> 1) - 1) & 1u);
       if (__any_sync(0xffffffffu, *abort)) break;
       tc_fence_after();
       const uint64_t a = desc_at(ad, slot * a_bytes), b = desc_at(bd, slot * BN * kBlock);
@@ -239,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int k = 0; k < 4; ++k)
         mma_f8_ss_by(tmem + (i & 1) * kBuf, desc_at(a, k * 32), desc_at(b, k * 32), idesc, k > 0 ? 1u : 0u, me);
       mma_commit_by(&ctl->empty[slot], me);
-      mma_commit_by(&ctl->sum_full[i & 1], me);
+      mma_commit_by(&ctl->sum_full[i & 1][0], me);
       if (++slot == p.stages) {
         slot = 0;
         ++turn;
@@ -251,34 +282,55 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int local = (warp & 3) * 32 + lane, half = (warp >> 2) * HC;
     const bool any = m0 + (warp & 3) * 32 < p.M;   // some row of the warp's
     Sums<HC, 16> sums;
-    sums.start(p, m0 + local, n0 + half);
+    sums.clear();
+    // the scales of the row, and of the columns' one or two blocks
+    const float* a_scale = p.a_scale + (long long)min(m0 + local, p.M - 1) * p.a_scale_stride + first;
+    const int block0 = min(n0 + half, p.N - 1) >> 7, block1 = min(n0 + half + HC - 1, p.N - 1) >> 7;
+    const float* b_scale0 = p.b_scale + block0 * p.b_scale_stride + first;
+    const float* b_scale1 = p.b_scale + block1 * p.b_scale_stride + first;
+    const int split = block0 == block1 ? HC : (block0 + 1) * kBlock - n0 - half;
     const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half;
-    float2 f = sums.factors(first);
+    // a block ahead, and multiplied when they are used: what needs a load holds up the warp until it is there
+    float a = __ldg(a_scale), b0 = __ldg(b_scale0), b1 = __ldg(b_scale1);
     for (int i = 0; i < n; ++i) {
-      const float2 next = i + 1 < n ? sums.factors(first + i + 1) : f;
-      warp_wait(&ctl->sum_full[i & 1], (i >> 1) & 1u, abort, p.status);
+      const int next = min(i + 1, n - 1);
+      const float next_a = __ldg(a_scale + next), next_b0 = __ldg(b_scale0 + next), next_b1 = __ldg(b_scale1 + next);
+      warp_wait(&ctl->sum_full[i & 1][0], (i >> 1) & 1u, abort, p.status);
       if (__any_sync(0xffffffffu, *abort)) break;
-      if (any) {
-        tc_fence_after();
-        sums.add(at + (i & 1) * kBuf, f);
+      auto done = [&] {
         tc_fence_before();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->sum_free[i & 1]);
-      f = next;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->sum_free[i & 1][0]);
+      };
+      tc_fence_after();
+      if (any)
+        sums.add(at + (i & 1) * kBuf, split, [&] { return make_float2(a * b0, a * b1); }, done);
+      else
+        done();
+      a = next_a;
+      b0 = next_b0;
+      b1 = next_b1;
     }
     if (splits == 1) {
       if (m0 + local < p.M && !*abort) {
         const long long out = (long long)(m0 + local) * p.out_stride + n0 + half;
 #pragma unroll
-        for (int c = 0; c < HC; c += 16) store<16>(p, out + c, p.N - n0 - half - c, &sums.v[c / 2].x);
+        for (int c = 0; c < HC; c += 16) {
+          float x[16];
+          sums.values(c, x);
+          store<16>(p, out + c, p.N - n0 - half - c, x);
+        }
       }
     } else if (any && !*abort) {
       // (every MMA of this CTA is done: the last block's sums have been read)
       float* to = part + local * kPitch + half;
 #pragma unroll
-      for (int c = 0; c < HC; c += 4)
-        *reinterpret_cast<float4*>(to + c) = make_float4(sums.v[c / 2].x, sums.v[c / 2].y, sums.v[c / 2 + 1].x, sums.v[c / 2 + 1].y);
+      for (int c = 0; c < HC; c += 16) {
+        float x[16];
+        sums.values(c, x);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(to + c + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+      }
     }
   }
   __syncwarp();
@@ -314,31 +366,38 @@ template <int BN>
 struct Wide {
   static constexpr int kCols = BN / 2;                       // of a thread
   static constexpr int kA = kRows * kBlock, kB = BN / 2 * kBlock, kStage = kA + kB;
-  static constexpr int kStages = 6;
-  static constexpr int ctl = kStages * kStage, total = ctl + 1024;
+  static constexpr int kStages = 5;
+  static constexpr int kOut = 4096;                          // of a warp: 32 rows x 32 columns, twice for 16-bit types
+  static constexpr int kScales = kScaleBlocks * kScalePitch * 4;   // of a half's columns
+  static constexpr int out = kStages * kStage, scales = out + 8 * kOut, ctl = scales + 4 * kScales, total = ctl + 1024;
 };
 
 template <int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
-    wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Params p) {
+    wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ Params p) {
   using W = Wide<BN>;
-  constexpr int kCols = W::kCols;
+  constexpr int kCols = W::kCols, kSteps = kCols / 32;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + W::ctl);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   volatile int* abort = &ctl->abort;
   const int rank = (int)cluster_rank(), pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1;
-  const long long tiles = (long long)p.tiles_m * p.tiles_n;
+  const int tiles = p.tiles_m * p.tiles_n;
 
   if (tid == 0) {
     for (int i = 0; i < W::kStages; ++i) {
       mbar_init(&ctl->full[i], 1);
       mbar_init(&ctl->empty[i], 1);
     }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&ctl->sum_full[i >> 1][i & 1], 1);
+      mbar_init(&ctl->sum_free[i >> 1][i & 1], 8);   // four warps of either CTA
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl->sum_full[i], 1);
-      mbar_init(&ctl->sum_free[i], 16);   // eight warps of either CTA
+      mbar_init(&ctl->scale_full[i], 2);
+      mbar_init(&ctl->scale_free[i], 8);
     }
 #ifdef DSA_TEST_HOOKS
     mbar_init(&ctl->never, 1);
@@ -358,16 +417,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
   griddep_wait();  // nothing above reads global memory
 
   // Tiles in groups of kGroupRows rows of tiles, column by column: what runs at one time shares rows of a and of b.
-  auto place = [&](long long t, int& m0, int& n0) {
-    const long long group = (long long)kGroupRows * p.tiles_n;
-    const int g = (int)(t / group), in = (int)(t - g * group);
+  auto place = [&](int t, int& m0, int& n0) {
+    const int group = kGroupRows * p.tiles_n;
+    const int g = t / group, in = t - g * group;
     const int rows = min(kGroupRows, p.tiles_m - g * kGroupRows);
     m0 = (g * kGroupRows + in % rows) * 2 * kRows;
     n0 = in / rows * BN;
   };
 
-  // (2 * 216 + 72: the 3 * 168 registers a lane that the three warpgroups were launched with)
-  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  // (2 * 232 + 40: the 3 * 168 registers a lane that the three warpgroups were launched with)
+  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
   if (warp == 9) {
     // ---------------- loads: this CTA's half of a's rows and of b's, counted on the even CTA's barrier
     if (lane == 0) {
@@ -375,7 +434,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       int slot = 0;
       uint32_t turn = 0;
       bool ok = true;
-      for (long long t = pair; t < tiles && ok; t += pairs) {
+      for (int t = pair; t < tiles && ok; t += pairs) {
         int m0, n0;
         place(t, m0, n0);
         for (int i = 0; i < p.blocks; ++i) {
@@ -388,7 +447,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
           load_a = !(p.stall == 11 && blockIdx.x == 0 && t == pair && i == 0);
 #endif
           if (load_a) tma_load_2d_pair(to, &tm_a, full + slot * 8, i * kBlock, m0 + rank * kRows);
-          tma_load_2d_pair(to + W::kA, &tm_b, full + slot * 8, i * kBlock, n0 + rank * (BN / 2));
+          for (int h = 0; h < 2; ++h)
+            tma_load_2d_pair(to + W::kA + h * (W::kB / 2), &tm_b, full + slot * 8, i * kBlock, n0 + h * kCols + rank * (kCols / 2));
           if (++slot == W::kStages) {
             slot = 0;
             ++turn;
@@ -399,12 +459,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     __syncwarp();
   } else if (warp == 8 && rank == 0) {
     // ---------------- MMA issue, for both CTAs: the whole warp walks, one lane issues
-    constexpr uint32_t idesc = idesc_e4m3(2 * kRows, BN);
+    constexpr uint32_t idesc = idesc_e4m3(2 * kRows, kCols);
     const uint64_t ad = sdesc_sw128(smem_u32(smem), 16, 1024), bd = sdesc_sw128(smem_u32(smem + W::kA), 16, 1024);
     const uint32_t me = elect_one();
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      mbar_wait_issue<true>(bar, parity, abort, p.status);
-      __syncwarp();
+    auto wait = [&](uint64_t* bar, uint32_t parity) {   // false: it gave up
+      const bool ok = mbar_test(bar, parity) || mbar_try_wait(bar, parity) || mbar_wait_issue<true>(bar, parity, abort, p.status);
+      return (bool)__all_sync(0xffffffffu, ok);
     };
 #ifdef DSA_TEST_HOOKS
     if (p.stall == 10 && blockIdx.x == 0) warp_wait(&ctl->never, 0, abort, p.status);
@@ -412,20 +472,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     int slot = 0;
     uint32_t turn = 0, it = 0;
     bool go = true;
-    for (long long t = pair; t < tiles && go; t += pairs) {
+    for (int t = pair; t < tiles && go; t += pairs) {
 #pragma unroll 1
       for (int i = 0; i < p.blocks; ++i, ++it) {
-        wait(&ctl->full[slot], turn & 1u);
-        if (it >= 2) wait(&ctl->sum_free[it & 1u], ((it >> 1) - 1) & 1u);
-        go = !__any_sync(0xffffffffu, *abort);
-        if (!go) break;
-        tc_fence_after();
+        go = wait(&ctl->full[slot], turn & 1u);
         const uint64_t a = desc_at(ad, slot * W::kStage), b = desc_at(bd, slot * W::kStage);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma2_f8_ss(tmem + (it & 1u) * 256u, desc_at(a, k * 32), desc_at(b, k * 32), idesc, k > 0 ? 1u : 0u, me);
-        mma2_commit_both(&ctl->empty[slot], me);
-        mma2_commit_both(&ctl->sum_full[it & 1u], me);
+        for (int h = 0; h < 2; ++h) {
+          if (it >= 2) go = go && wait(&ctl->sum_free[it & 1u][h], ((it >> 1) - 1) & 1u);
+          if (!go) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma2_f8_ss(tmem + (it & 1u) * 256u + h * kCols, desc_at(a, k * 32), desc_at(b, h * (W::kB / 2) + k * 32), idesc,
+                       k > 0 ? 1u : 0u, me);
+          if (h == 1) mma2_commit_both(&ctl->empty[slot], me);
+          mma2_commit_both(&ctl->sum_full[it & 1u][h], me);
+        }
+        if (!go) break;
         if (++slot == W::kStages) {
           slot = 0;
           ++turn;
@@ -433,41 +497,151 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp < 8) {
-    // ---------------- sums
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    const int local = (warp & 3) * 32 + lane, half = (warp >> 2) * kCols;
-    const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half;
-    const uint32_t sum_free = map_cluster(&ctl->sum_free[0], 0);
-    uint32_t it = 0;
+  } else if (warp >= 10) {
+    // ---------------- scales: products a_scale b_scale of the tile's rows with a half of the columns, eight blocks at a
+    // time, a lane a block and every fourth row.  (Loaded by the sums, a row a lane, they took 32 lines of L1 a load,
+    // beside the MMAs' operands.)
+    const int h = warp - 10, in = lane & (kScaleBlocks - 1), first = lane / kScaleBlocks;
+    uint32_t set = 0;
     bool go = true;
-    for (long long t = pair; t < tiles && go; t += pairs) {
+    for (int t = pair; t < tiles && go; t += pairs) {
       int m0, n0;
       place(t, m0, n0);
-      const int row = m0 + rank * kRows + local;
-      Sums<kCols, 32> sums;
-      sums.start(p, row, n0 + half);
-      float2 f = sums.factors(0);
-#pragma unroll 1
-      for (int i = 0; i < p.blocks; ++i, ++it) {
-        const float2 next = i + 1 < p.blocks ? sums.factors(i + 1) : f;
-        mbar_wait(&ctl->sum_full[it & 1u], (it >> 1) & 1u, abort, p.status);   // (a call would cost registers)
-        __syncwarp();
-        go = !__any_sync(0xffffffffu, *abort);
+      m0 += rank * kRows;
+      const float* b = p.b_scale + (min(n0 + h * kCols, p.N - 1) >> 7) * p.b_scale_stride;
+      for (int i = 0; i < p.blocks; i += kScaleBlocks, ++set) {
+        const int block = min(i + in, p.blocks - 1);
+        const float* a = p.a_scale + block;
+        const float bs = __ldg(b + block);
+        go = set < 2 || mbar_wait_fast(&ctl->scale_free[set & 1u], ((set >> 1) - 1) & 1u, abort, p.status);
+        go = __all_sync(0xffffffffu, go);
         if (!go) break;
-        tc_fence_after();
-        sums.add(at + (it & 1u) * 256u, f);
-        tc_fence_before();
+        float* to = reinterpret_cast<float*>(smem + W::scales + ((set & 1u) * 2 + h) * W::kScales) + in * kScalePitch;
+#pragma unroll 8
+        for (int r = first; r < kRows; r += 32 / kScaleBlocks)
+          to[r] = __ldg(a + (long long)min(m0 + r, p.M - 1) * p.a_scale_stride) * bs;
         __syncwarp();
-        if (lane == 0) mbar_arrive_pair(sum_free + (it & 1u) * 8);
-        f = next;
-      }
-      if (go && row < p.M) {
-        const long long out = (long long)row * p.out_stride + n0 + half;
-#pragma unroll
-        for (int c = 0; c < kCols; c += 16) store<16>(p, out + c, p.N - n0 - half - c, &sums.v[c / 2].x);
+        if (lane == 0) mbar_arrive(&ctl->scale_full[set & 1u]);
       }
     }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ---------------- sums
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    const int local = (warp & 3) * 32 + lane, h = warp >> 2, half = h * kCols;
+    const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half;
+    const uint32_t sum_free = map_cluster(&ctl->sum_free[0][h], 0);
+    const float* scales = reinterpret_cast<const float*>(smem + W::scales + h * W::kScales) + local;
+    uint32_t it = 0, set = 0;
+    bool go = true;
+    for (int t = pair; t < tiles && go; t += pairs) {
+      Sums<kCols, 32> sums;
+      sums.clear();
+      // Two steps of 32 columns in turn: one is on its way while the other's products are added, a block's first while
+      // the last one's are.
+      uint32_t r0[32], r1[32];
+      auto full = [&](uint32_t block) { return &ctl->sum_full[block & 1u][h]; };
+      auto products = [&](uint32_t block) { return at + (block & 1u) * 256u; };
+      // (waits stand inline: a call would cost registers)
+      go = mbar_wait(full(it), (it >> 1) & 1u, abort, p.status);
+      go = __all_sync(0xffffffffu, go);
+      if (!go) break;
+      tc_fence_after();
+      tmem_ld_x32(products(it), r0);
+#pragma unroll 1
+      for (int i = 0;; ++i) {
+        const int in = i & (kScaleBlocks - 1);
+        if (in == 0) go = mbar_wait(&ctl->scale_full[set & 1u], (set >> 1) & 1u, abort, p.status);
+        const float f = scales[(set & 1u) * (2 * W::kScales / 4) + in * kScalePitch];
+        const uint64_t ff = pack2(f, f);
+#pragma unroll
+        for (int c = 0; c < kSteps - 1; ++c) {
+          uint32_t* r = c & 1 ? r1 : r0;
+          tmem_ld_wait_for<32>(r);
+          tmem_ld_x32(products(it) + (c + 1) * 32, c & 1 ? r0 : r1);
+          sums.multiply_add(c, r, ff, ff, kCols);
+        }
+        uint32_t* last = kSteps & 1 ? r0 : r1;
+        tmem_ld_wait_for<32>(last);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_pair(sum_free + (it & 1u) * 16);
+        if (in == kScaleBlocks - 1 || i + 1 == p.blocks) {
+          if (lane == 0) mbar_arrive(&ctl->scale_free[set & 1u]);
+          ++set;
+        }
+        ++it;
+        if (i + 1 == p.blocks) {
+          sums.multiply_add(kSteps - 1, last, ff, ff, kCols);
+          break;
+        }
+        static_assert((kSteps & 1) == 0, "a block's first step is r0");
+        const bool ready = __all_sync(0xffffffffu, mbar_test(full(it), (it >> 1) & 1u));
+        if (ready) {
+          tc_fence_after();
+          tmem_ld_x32(products(it), r0);
+        }
+        sums.multiply_add(kSteps - 1, last, ff, ff, kCols);
+        if (!ready) {
+          go = mbar_wait(full(it), (it >> 1) & 1u, abort, p.status) && go;
+          __syncwarp();
+          tc_fence_after();
+          tmem_ld_x32(products(it), r0);
+        }
+        go = __all_sync(0xffffffffu, go);
+        if (!go) {
+          tmem_ld_wait();
+          break;
+        }
+      }
+      if (!go) break;
+      // The warp's 32 rows go out in boxes of 32 columns, by way of shared memory (a row a lane, stores to memory took a
+      // line of it each: 8,192 x 32,768 outputs of 512 columns 213 us).
+      int m0, n0;
+      place(t, m0, n0);
+      m0 += rank * kRows + (warp & 3) * 32;
+      n0 += half;
+      if (m0 >= p.M) continue;
+      uint8_t* buffer = smem + W::out + warp * W::kOut;
+#pragma unroll
+      for (int c = 0; c < kCols; c += 32) {
+        if (n0 + c >= p.N) break;
+        float x[32];
+        sums.values(c, x);
+        sums.values(c + 16, x + 16);
+        uint8_t* box = buffer;
+        if (p.elem == DSA_ELEM_FP32) {
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(box + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        } else {
+          box += (c & 32) * (W::kOut / 64);
+          if (lane == 0) bulk_wait_read_but_one();
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(box + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(pack16(p.elem, x[8 * i], x[8 * i + 1]), pack16(p.elem, x[8 * i + 2], x[8 * i + 3]),
+                           pack16(p.elem, x[8 * i + 4], x[8 * i + 5]), pack16(p.elem, x[8 * i + 6], x[8 * i + 7]));
+        }
+        if (p.vec) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tm_out, box, n0 + c, m0);
+            bulk_commit();
+          }
+        } else {
+          __syncwarp();
+          store_box(p, box, m0, n0 + c);
+          __syncwarp();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
   __syncwarp();
@@ -479,7 +653,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
   if (warp == 8) tmem_dealloc2(tmem, 512);
 }
 
-using Kernel = void (*)(CUtensorMap, CUtensorMap, Params);
+using NarrowKernel = void (*)(CUtensorMap, CUtensorMap, Params);
 
 struct Plan {
   bool wide;
@@ -545,28 +719,33 @@ dsa_status launch_matmul_fp8(const dsa_matmul_fp8_args& a, cudaStream_t stream, 
   const uint64_t K = (uint64_t)a.K;
   if (!encode_tmap_2d(&tm_a, u8, a.a, K, (uint64_t)a.M, a.M == 1 ? K : (uint64_t)a.a_stride, kBlock, (uint32_t)p.a_box, sw, err) ||
       !encode_tmap_2d(&tm_b, u8, a.b, K, (uint64_t)a.N, a.N == 1 ? K : (uint64_t)a.b_stride, kBlock,
-                      (uint32_t)(w.wide ? w.bn / 2 : w.bn), sw, err))
+                      (uint32_t)(w.wide ? w.bn / 4 : w.bn), sw, err))
     return DSA_ERR_CUDA;
-  Kernel k;
-  int smem;
+  const NarrowKernel narrow = w.bn == 32   ? narrow_kernel<1>
+                              : w.bn == 64 ? narrow_kernel<2>
+                              : w.bn == 96 ? narrow_kernel<3>
+                                           : narrow_kernel<4>;
+  const void* k = w.wide ? reinterpret_cast<const void*>(wide_kernel<256>) : reinterpret_cast<const void*>(narrow);
+  const int smem = w.wide ? Wide<256>::total + 1024 : kRing + 1024 + 1024;
   static std::atomic<uint64_t> done[5];
-  int which = 0;
-  if (w.wide) {
-    k = wide_kernel<256>;
-    smem = Wide<256>::total + 1024;
-  } else {
-    which = w.bn / 32;
-    k = which == 1 ? narrow_kernel<1> : which == 2 ? narrow_kernel<2> : which == 3 ? narrow_kernel<3> : narrow_kernel<4>;
-    smem = kRing + 1024 + 1024;
-  }
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem, dev.device, done[which]);
+  cudaError_t e = allow_smem(k, smem, dev.device, done[w.wide ? 0 : w.bn / 32]);
   if (e != cudaSuccess) return cuda_fail(e, "matmul_fp8: set shared memory size", err);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
+  CUtensorMap tm_out;
   if (w.wide) {
+    p.vec = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && (a.M == 1 || a.out_stride * size % 16 == 0);
+    if (p.vec && !encode_tmap_2d(&tm_out, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, a.out,
+                                 (uint64_t)a.N, (uint64_t)a.M, a.M == 1 ? ((uint64_t)a.N * size + 15) / 16 * 16 : (uint64_t)a.out_stride * size, 32, 32,
+                                 size == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, err))
+      return DSA_ERR_CUDA;
     const long long tiles = (long long)p.tiles_m * p.tiles_n;
+    if (tiles > 0x70000000LL) {
+      err = "matmul_fp8: too many outputs for one launch";
+      return DSA_ERR_UNSUPPORTED;
+    }
     cfg.gridDim = dim3((unsigned)std::min<long long>(tiles, std::max(1, dev.sm_count / 2)) * 2);
     cfg.numAttrs = 1;
   } else {
@@ -586,7 +765,7 @@ dsa_status launch_matmul_fp8(const dsa_matmul_fp8_args& a, cudaStream_t stream, 
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  e = cudaLaunchKernelEx(&cfg, k, tm_a, tm_b, p);
+  e = w.wide ? cudaLaunchKernelEx(&cfg, wide_kernel<256>, tm_a, tm_b, tm_out, p) : cudaLaunchKernelEx(&cfg, narrow, tm_a, tm_b, p);
   if (e != cudaSuccess) return cuda_fail(e, "matmul_fp8: launch", err);
   return DSA_OK;
 }

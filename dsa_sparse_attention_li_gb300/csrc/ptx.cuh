@@ -193,6 +193,15 @@ DSA_DEV bool mbar_wait_fast(uint64_t* bar, uint32_t parity, volatile int* abort,
   return mbar_test(bar, parity) || mbar_wait_slow(bar, parity, abort, status);
 }
 
+// As mbar_wait_fast, with up to 32 tests before the call: for hand-overs of some hundred cycles that the wake-up
+// of a suspended thread would lengthen.
+DSA_DEV bool mbar_spin(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (mbar_test(bar, parity)) return true;
+  return false;
+}
+
 // Bounded wait of a whole warp, which is converged again after it.
 DSA_DEV void warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
   mbar_wait_fast(bar, parity, abort, status);
@@ -468,6 +477,19 @@ DSA_DEV void tmem_ld_x32(uint32_t taddr, uint32_t* r) {
 
 DSA_DEV void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// The same, with registers that earlier loads wrote: what reads them cannot move before the wait.
+template <int N>
+DSA_DEV void tmem_ld_wait_for(uint32_t* r) {
+  static_assert(N % 16 == 0, "groups of sixteen");
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < N; i += 16)
+    asm volatile(""
+                 : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                   "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
+                   "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15]));
+}
+
 DSA_DEV void tmem_st_x1(uint32_t taddr, uint32_t v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
 }
@@ -649,9 +671,20 @@ DSA_DEV void bulk_copy_to_cluster(uint32_t dst_cluster, const void* src, uint32_
           "r"(dst_cluster), "r"(smem_u32(src)), "r"(bytes), "r"(remote_bar)
       : "memory");
 }
+// One box from shared memory to a 2-D map (what lies outside is left out), in the thread's bulk group.
+DSA_DEV void tma_store_2d(const CUtensorMap* m, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(smem_u32(src)), "r"(x), "r"(y)
+               : "memory");
+}
 DSA_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Wait until every committed bulk copy of this thread has finished reading its source.
 DSA_DEV void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// ... all but the last one.
+DSA_DEV void bulk_wait_read_but_one() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+// Wait until every committed bulk copy of this thread is complete.
+DSA_DEV void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 DSA_DEV uint4 ld_cluster_v4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -750,13 +783,21 @@ DSA_DEV float2 fma2(float2 a, float s, float t) {
       : "f"(a.x), "f"(a.y), "f"(s), "f"(t));
   return d;
 }
-// a * s + c, pair by pair.
-DSA_DEV float2 fma2(float2 a, float s, float2 c) {
+// Two floats as one operand of the packed instructions (two adjacent registers).
+DSA_DEV uint64_t pack2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+DSA_DEV float2 unpack2(uint64_t a) {
   float2 d;
-  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mov.b64 z, {%5, %6};\n"
-      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(s), "f"(c.x), "f"(c.y));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+  return d;
+}
+// a * b + c, pair by pair.
+DSA_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
 DSA_DEV float2 add2(float2 a, float2 b) {
