@@ -16,6 +16,7 @@
 // depend on their timing, and there is no workspace.  Two CTAs an SM, so that one's start and end run under the
 // other's stream.  Bound: HBM.
 #include <algorithm>
+#include <type_traits>
 
 #include "dsa_internal.h"
 #include "ptx.cuh"
@@ -62,24 +63,32 @@ struct Ctl {
 };
 static_assert(sizeof(Ctl) <= 1024, "control block");
 
-DSA_DEV uint32_t pack16(int elem, float a, float b) {
-  if (elem == DSA_ELEM_BF16) return pack_bf16(a, b);
+template <int E>
+DSA_DEV uint32_t pack16(float a, float b) {
+  if (E == DSA_ELEM_BF16) return pack_bf16(a, b);
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// A box of 32 rows and 32 columns in shared memory (in the layout that a store by TMA takes) to outputs whose rows a TMA
-// store cannot reach: a row at a time, a column a lane.
+// A box of 32 rows and 64 bytes in shared memory (in the layout that a store by TMA takes) to outputs whose rows a TMA
+// store cannot reach: a column a lane, in 32 bits two rows at a time.
 __device__ __noinline__ void store_box(const Params& p, const uint8_t* box, int m0, int n0) {
   const int lane = threadIdx.x & 31, rows = min(32, p.M - m0);
-  if (n0 + lane >= p.N) return;
-  for (int r = 0; r < rows; ++r) {
-    const long long at = (long long)(m0 + r) * p.out_stride + n0 + lane;
-    if (p.elem == DSA_ELEM_FP32)
-      reinterpret_cast<float*>(p.out)[at] = *reinterpret_cast<const float*>(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-    else
-      reinterpret_cast<uint16_t*>(p.out)[at] =
-          *reinterpret_cast<const uint16_t*>(box + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
+  if (p.elem == DSA_ELEM_FP32) {
+    const int col = lane & 15;
+    if (n0 + col >= p.N) return;
+#pragma unroll 8
+    for (int r = lane >> 4; r < 32; r += 2)
+      if (r < rows)
+        reinterpret_cast<float*>(p.out)[(long long)(m0 + r) * p.out_stride + n0 + col] =
+            *reinterpret_cast<const float*>(box + r * 64 + (((col >> 2) ^ ((r >> 1) & 3)) << 4) + (col & 3) * 4);
+  } else {
+    if (n0 + lane >= p.N) return;
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r)
+      if (r < rows)
+        reinterpret_cast<uint16_t*>(p.out)[(long long)(m0 + r) * p.out_stride + n0 + lane] =
+            *reinterpret_cast<const uint16_t*>(box + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
   }
 }
 
@@ -101,7 +110,8 @@ DSA_DEV void store(const Params& p, long long at, int left, const float* v) {
   }
   uint32_t w[N / 2];
 #pragma unroll
-  for (int i = 0; i < N / 2; ++i) w[i] = pack16(p.elem, v[2 * i], v[2 * i + 1]);
+  for (int i = 0; i < N / 2; ++i)
+    w[i] = p.elem == DSA_ELEM_BF16 ? pack16<DSA_ELEM_BF16>(v[2 * i], v[2 * i + 1]) : pack16<DSA_ELEM_FP16>(v[2 * i], v[2 * i + 1]);
   uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + at;
   if (p.vec && left >= N) {
     if constexpr (N == 16)
@@ -133,11 +143,11 @@ struct Sums {
     else
       tmem_ld_x16(tmem, r);
   }
-  DSA_DEV void multiply_add(int step, const uint32_t* r, uint64_t f0, uint64_t f1, int split) {
+  DSA_DEV void multiply_add(int step, const uint32_t* r, uint64_t f) {
 #pragma unroll
     for (int i = 0; i < kStep; i += 2) {
       uint64_t& x = v[(step * kStep + i) / 2];
-      x = fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), step * kStep + (i & 16) < split ? f0 : f1, x);
+      x = fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f, x);
     }
   }
   // Sixteen columns from the c-th on.
@@ -149,7 +159,7 @@ struct Sums {
       x[i + 1] = two.y;
     }
   }
-  // Adds the block's products at `tmem`, times the first of the factors for columns below `split`, a multiple of 16,
+  // Adds the block's products at `tmem`, times the first of the factors for columns below `split`, a multiple of kStep,
   // and times the second for the others; factors() is asked while the first products are on their way, done() called
   // once all have been read.
   template <class Factors, class Done>
@@ -164,9 +174,9 @@ struct Sums {
       tmem_ld_wait_for<kStep>(r[0]);
       if (c + 1 < kSteps) tmem_ld_wait_for<kStep>(r[1]);
       if (c + 2 >= kSteps) done();
-      multiply_add(c, r[0], f0, f1, split);
+      multiply_add(c, r[0], c * kStep < split ? f0 : f1);
       if (c + 2 < kSteps) load(tmem + (c + 2) * kStep, r[0]);
-      if (c + 1 < kSteps) multiply_add(c + 1, r[1], f0, f1, split);
+      if (c + 1 < kSteps) multiply_add(c + 1, r[1], (c + 1) * kStep < split ? f0 : f1);
       if (c + 3 < kSteps) load(tmem + (c + 3) * kStep, r[1]);
     }
   }
@@ -362,22 +372,24 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // ---------------------------------------------------------------- wide tiles
 
-template <int BN>
+constexpr int kWideCols = 256;
 struct Wide {
-  static constexpr int kCols = BN / 2;                       // of a thread
-  static constexpr int kA = kRows * kBlock, kB = BN / 2 * kBlock, kStage = kA + kB;
+  static constexpr int kCols = kWideCols / 2;                // of a thread: a block of b
+  static constexpr int kA = kRows * kBlock, kB = kCols * kBlock, kStage = kA + kB;
   static constexpr int kStages = 5;
-  static constexpr int kOut = 4096;                          // of a warp: 32 rows x 32 columns, twice for 16-bit types
-  static constexpr int kScales = kScaleBlocks * kScalePitch * 4;   // of a half's columns
-  static constexpr int out = kStages * kStage, scales = out + 8 * kOut, ctl = scales + 4 * kScales, total = ctl + 1024;
+  static constexpr int kBox = 32 * 64, kBoxes = 3;           // of a warp's outputs: 32 rows of 64 bytes
+  static constexpr int kScales = kScaleBlocks * kScalePitch; // floats, of a half's columns
+  static constexpr int out = kStages * kStage, scales = out + 8 * kBoxes * kBox, ctl = scales + 4 * kScales * 4,
+                       total = ctl + 1024;
 };
+static_assert(Wide::total + 1024 <= 232448, "shared memory of a CTA");
 
-template <int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ Params p) {
-  using W = Wide<BN>;
+  using W = Wide;
   constexpr int kCols = W::kCols, kSteps = kCols / 32;
+  static_assert(kCols == kBlock && kSteps % 2 == 0, "one block of b, and a block's first step is r0");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + W::ctl);
@@ -422,7 +434,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     const int g = t / group, in = t - g * group;
     const int rows = min(kGroupRows, p.tiles_m - g * kGroupRows);
     m0 = (g * kGroupRows + in % rows) * 2 * kRows;
-    n0 = in / rows * BN;
+    n0 = in / rows * kWideCols;
   };
 
   // (2 * 232 + 40: the 3 * 168 registers a lane that the three warpgroups were launched with)
@@ -516,7 +528,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         go = set < 2 || mbar_wait_fast(&ctl->scale_free[set & 1u], ((set >> 1) - 1) & 1u, abort, p.status);
         go = __all_sync(0xffffffffu, go);
         if (!go) break;
-        float* to = reinterpret_cast<float*>(smem + W::scales + ((set & 1u) * 2 + h) * W::kScales) + in * kScalePitch;
+        float* to = reinterpret_cast<float*>(smem + W::scales) + ((set & 1u) * 2 + h) * W::kScales + in * kScalePitch;
 #pragma unroll 8
         for (int r = first; r < kRows; r += 32 / kScaleBlocks)
           to[r] = __ldg(a + (long long)min(m0 + r, p.M - 1) * p.a_scale_stride) * bs;
@@ -531,8 +543,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     const int local = (warp & 3) * 32 + lane, h = warp >> 2, half = h * kCols;
     const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half;
     const uint32_t sum_free = map_cluster(&ctl->sum_free[0][h], 0);
-    const float* scales = reinterpret_cast<const float*>(smem + W::scales + h * W::kScales) + local;
+    const float* scales = reinterpret_cast<const float*>(smem + W::scales) + h * W::kScales + local;
     uint32_t it = 0, set = 0;
+    int box = 0;
     bool go = true;
     for (int t = pair; t < tiles && go; t += pairs) {
       Sums<kCols, 32> sums;
@@ -552,36 +565,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       for (int i = 0;; ++i) {
         const int in = i & (kScaleBlocks - 1);
         if (in == 0) go = mbar_wait(&ctl->scale_full[set & 1u], (set >> 1) & 1u, abort, p.status);
-        const float f = scales[(set & 1u) * (2 * W::kScales / 4) + in * kScalePitch];
+        const float f = scales[(set & 1u) * (2 * W::kScales) + in * kScalePitch];
         const uint64_t ff = pack2(f, f);
 #pragma unroll
         for (int c = 0; c < kSteps - 1; ++c) {
           uint32_t* r = c & 1 ? r1 : r0;
           tmem_ld_wait_for<32>(r);
           tmem_ld_x32(products(it) + (c + 1) * 32, c & 1 ? r0 : r1);
-          sums.multiply_add(c, r, ff, ff, kCols);
+          sums.multiply_add(c, r, ff);
         }
-        uint32_t* last = kSteps & 1 ? r0 : r1;
-        tmem_ld_wait_for<32>(last);
+        tmem_ld_wait_for<32>(r1);
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_pair(sum_free + (it & 1u) * 16);
+        mbar_arrive_pair_by(sum_free + (it & 1u) * 16, lane == 0);   // (the loads' wait is the whole warp's)
         if (in == kScaleBlocks - 1 || i + 1 == p.blocks) {
           if (lane == 0) mbar_arrive(&ctl->scale_free[set & 1u]);
           ++set;
         }
         ++it;
         if (i + 1 == p.blocks) {
-          sums.multiply_add(kSteps - 1, last, ff, ff, kCols);
+          sums.multiply_add(kSteps - 1, r1, ff);
           break;
         }
-        static_assert((kSteps & 1) == 0, "a block's first step is r0");
         const bool ready = __all_sync(0xffffffffu, mbar_test(full(it), (it >> 1) & 1u));
         if (ready) {
           tc_fence_after();
           tmem_ld_x32(products(it), r0);
         }
-        sums.multiply_add(kSteps - 1, last, ff, ff, kCols);
+        sums.multiply_add(kSteps - 1, r1, ff);
         if (!ready) {
           go = mbar_wait(full(it), (it >> 1) & 1u, abort, p.status) && go;
           __syncwarp();
@@ -602,42 +612,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       m0 += rank * kRows + (warp & 3) * 32;
       n0 += half;
       if (m0 >= p.M) continue;
-      uint8_t* buffer = smem + W::out + warp * W::kOut;
+      uint8_t* boxes = smem + W::out + warp * (W::kBoxes * W::kBox);
+      // a box of 64 bytes a row, from four times 16 bytes that piece() gives
+      auto put = [&](int col, auto&& piece) {
+        if (col >= p.N) return;
+        uint8_t* to = boxes + box * W::kBox;
+        box = box + 1 == W::kBoxes ? 0 : box + 1;
+        if (lane == 0) bulk_wait_read_but_two();   // (a store reads its box some time after it is issued)
+        __syncwarp();
 #pragma unroll
-      for (int c = 0; c < kCols; c += 32) {
-        if (n0 + c >= p.N) break;
-        float x[32];
-        sums.values(c, x);
-        sums.values(c + 16, x + 16);
-        uint8_t* box = buffer;
-        if (p.elem == DSA_ELEM_FP32) {
-          if (lane == 0) bulk_wait_read_all();
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(box + lane * 128 + ((i ^ (lane & 7)) << 4)) =
-                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-        } else {
-          box += (c & 32) * (W::kOut / 64);
-          if (lane == 0) bulk_wait_read_but_one();
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(box + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
-                make_uint4(pack16(p.elem, x[8 * i], x[8 * i + 1]), pack16(p.elem, x[8 * i + 2], x[8 * i + 3]),
-                           pack16(p.elem, x[8 * i + 4], x[8 * i + 5]), pack16(p.elem, x[8 * i + 6], x[8 * i + 7]));
-        }
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(to + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = piece(i);
         if (p.vec) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_2d(&tm_out, box, n0 + c, m0);
+            tma_store_2d(&tm_out, to, col, m0);
             bulk_commit();
           }
         } else {
           __syncwarp();
-          store_box(p, box, m0, n0 + c);
+          store_box(p, to, m0, col);
           __syncwarp();
+        }
+      };
+      auto put16 = [&](auto type) {
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) {
+          float x[32];
+          sums.values(c, x);
+          sums.values(c + 16, x + 16);
+          put(n0 + c, [&](int i) {
+            const float* v = x + 8 * i;
+            constexpr int E = decltype(type)::value;
+            return make_uint4(pack16<E>(v[0], v[1]), pack16<E>(v[2], v[3]), pack16<E>(v[4], v[5]), pack16<E>(v[6], v[7]));
+          });
+        }
+      };
+      if (p.elem == DSA_ELEM_BF16) {
+        put16(std::integral_constant<int, DSA_ELEM_BF16>());
+      } else if (p.elem == DSA_ELEM_FP16) {
+        put16(std::integral_constant<int, DSA_ELEM_FP16>());
+      } else {
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16) {
+          float x[16];
+          sums.values(c, x);
+          put(n0 + c, [&](int i) {
+            const float* v = x + 4 * i;
+            return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+          });
         }
       }
     }
@@ -664,9 +687,8 @@ struct Plan {
 // pipe 512 cycles, a narrow one's what its bytes take of an SM's share of the HBM rate (23 bytes a cycle), or the sums.
 Plan plan(int M, int N, int blocks, int sms) {
   const double pairs = std::max(1, sms / 2);
-  const double wide_tiles = std::ceil(M / 256.0) * std::ceil(N / 256.0);
-  Plan best = {true, 256, 1};
-  double least = std::ceil(wide_tiles / pairs) * (blocks * 540.0 + 1500.0) + 3000.0;
+  Plan best = {true, kWideCols, 1};
+  double least = std::ceil(std::ceil(M / 256.0) * std::ceil((double)N / kWideCols) / pairs) * (blocks * 800.0 + 1500.0) + 3000.0;
   const double tiles_m = std::ceil(M / 128.0);
   if (tiles_m > 65535) return best;
   for (int bn = 32; bn <= 128; bn += 32)
@@ -712,7 +734,7 @@ dsa_status launch_matmul_fp8(const dsa_matmul_fp8_args& a, cudaStream_t stream, 
   p.tiles_m = (int)(((long long)a.M + rows - 1) / rows);
   p.tiles_n = (int)(((long long)a.N + w.bn - 1) / w.bn);
   p.a_box = w.wide ? kRows : std::min(kRows, (a.M + 7) / 8 * 8);
-  p.stages = w.wide ? Wide<256>::kStages : std::min(kMostStages, kRing / ((p.a_box + w.bn) * kBlock));
+  p.stages = w.wide ? 0 : std::min(kMostStages, kRing / ((p.a_box + w.bn) * kBlock));
   CUtensorMap tm_a, tm_b;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
@@ -725,8 +747,8 @@ dsa_status launch_matmul_fp8(const dsa_matmul_fp8_args& a, cudaStream_t stream, 
                               : w.bn == 64 ? narrow_kernel<2>
                               : w.bn == 96 ? narrow_kernel<3>
                                            : narrow_kernel<4>;
-  const void* k = w.wide ? reinterpret_cast<const void*>(wide_kernel<256>) : reinterpret_cast<const void*>(narrow);
-  const int smem = w.wide ? Wide<256>::total + 1024 : kRing + 1024 + 1024;
+  const void* k = w.wide ? reinterpret_cast<const void*>(wide_kernel) : reinterpret_cast<const void*>(narrow);
+  const int smem = w.wide ? Wide::total + 1024 : kRing + 1024 + 1024;
   static std::atomic<uint64_t> done[5];
   cudaError_t e = allow_smem(k, smem, dev.device, done[w.wide ? 0 : w.bn / 32]);
   if (e != cudaSuccess) return cuda_fail(e, "matmul_fp8: set shared memory size", err);
@@ -738,8 +760,8 @@ dsa_status launch_matmul_fp8(const dsa_matmul_fp8_args& a, cudaStream_t stream, 
   if (w.wide) {
     p.vec = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && (a.M == 1 || a.out_stride * size % 16 == 0);
     if (p.vec && !encode_tmap_2d(&tm_out, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, a.out,
-                                 (uint64_t)a.N, (uint64_t)a.M, a.M == 1 ? ((uint64_t)a.N * size + 15) / 16 * 16 : (uint64_t)a.out_stride * size, 32, 32,
-                                 size == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, err))
+                                 (uint64_t)a.N, (uint64_t)a.M, a.M == 1 ? ((uint64_t)a.N * size + 15) / 16 * 16 : (uint64_t)a.out_stride * size, 64 / size, 32,
+                                 CU_TENSOR_MAP_SWIZZLE_64B, err))
       return DSA_ERR_CUDA;
     const long long tiles = (long long)p.tiles_m * p.tiles_n;
     if (tiles > 0x70000000LL) {
@@ -765,7 +787,7 @@ dsa_status launch_matmul_fp8(const dsa_matmul_fp8_args& a, cudaStream_t stream, 
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  e = w.wide ? cudaLaunchKernelEx(&cfg, wide_kernel<256>, tm_a, tm_b, tm_out, p) : cudaLaunchKernelEx(&cfg, narrow, tm_a, tm_b, p);
+  e = w.wide ? cudaLaunchKernelEx(&cfg, wide_kernel, tm_a, tm_b, tm_out, p) : cudaLaunchKernelEx(&cfg, narrow, tm_a, tm_b, p);
   if (e != cudaSuccess) return cuda_fail(e, "matmul_fp8: launch", err);
   return DSA_OK;
 }

@@ -617,6 +617,15 @@ DSA_DEV void mbar_arrive_pair(uint32_t bar_cluster) {
                : "memory");
 }
 
+// The same of the threads whose `me` is not 0, with no branch around it.
+DSA_DEV void mbar_arrive_pair_by(uint32_t bar_cluster, uint32_t me) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];\n}\n" ::"r"(
+          bar_cluster),
+      "r"(me)
+      : "memory");
+}
+
 // ---------------------------------------------------------------- cluster
 
 DSA_DEV uint32_t cluster_rank() {
@@ -681,8 +690,8 @@ DSA_DEV void tma_store_2d(const CUtensorMap* m, const void* src, int x, int y) {
 DSA_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Wait until every committed bulk copy of this thread has finished reading its source.
 DSA_DEV void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-// ... all but the last one.
-DSA_DEV void bulk_wait_read_but_one() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+// ... all but the last two.
+DSA_DEV void bulk_wait_read_but_two() { asm volatile("cp.async.bulk.wait_group.read 2;" ::: "memory"); }
 // Wait until every committed bulk copy of this thread is complete.
 DSA_DEV void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 DSA_DEV uint4 ld_cluster_v4(uint32_t addr) {
