@@ -31,6 +31,7 @@ constexpr int kScaleBlocks = 8;   // blocks whose scales are multiplied at a tim
 constexpr int kScalePitch = kRows + 4;   // floats from one block's to the next
 constexpr int kBlock = 128;       // columns of a scale block: a row of a stage
 constexpr int kMostStages = 16;
+constexpr int kMostSplits = 8;    // CTAs of a portable cluster
 constexpr int kRing = 96 * 1024;  // of a narrow CTA
 constexpr int kGroupRows = 8;     // wide tiles of a column of tiles that run one after the other
 
@@ -207,6 +208,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int splits = (int)cluster_nrank(), rank = (int)cluster_rank();
   const int m0 = (int)blockIdx.y * kRows, n0 = (int)blockIdx.x / splits * BN;
   const int first = (int)((long long)p.blocks * rank / splits), n = (int)((long long)p.blocks * (rank + 1) / splits) - first;
+  const int quarters = min(4, (p.M - m0 + 31) / 32);   // of the tile's rows, a warp each, that have any
   const int a_bytes = p.a_box * kBlock, b_at = p.stages * a_bytes;   // (the MMAs read 128 rows of a: of later slots, and b)
 
   if (tid == 0) {
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->sum_full[i][0], 1);
-      mbar_init(&ctl->sum_free[i][0], 8);
+      mbar_init(&ctl->sum_free[i][0], 2 * quarters);
     }
 #ifdef DSA_TEST_HOOKS
     mbar_init(&ctl->never, 1);
@@ -287,10 +289,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     __syncwarp();
-  } else {
+  } else if ((warp & 3) < quarters) {
     // ---------------- sums
     const int local = (warp & 3) * 32 + lane, half = (warp >> 2) * HC;
-    const bool any = m0 + (warp & 3) * 32 < p.M;   // some row of the warp's
     Sums<HC, 16> sums;
     sums.clear();
     // the scales of the row, and of the columns' one or two blocks
@@ -313,10 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) mbar_arrive(&ctl->sum_free[i & 1][0]);
       };
       tc_fence_after();
-      if (any)
-        sums.add(at + (i & 1) * kBuf, split, [&] { return make_float2(a * b0, a * b1); }, done);
-      else
-        done();
+      sums.add(at + (i & 1) * kBuf, split, [&] { return make_float2(a * b0, a * b1); }, done);
       a = next_a;
       b0 = next_b0;
       b1 = next_b1;
@@ -331,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           store<16>(p, out + c, p.N - n0 - half - c, x);
         }
       }
-    } else if (any && !*abort) {
+    } else if (!*abort) {
       // (every MMA of this CTA is done: the last block's sums have been read)
       float* to = part + local * kPitch + half;
 #pragma unroll
@@ -352,12 +350,17 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int row = it / quads, col = (rank * quads + it - row * quads) * 4;
       const float* from = part + row * kPitch + col;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int s = 0; s < splits; ++s) {
-        const uint4 u = ld_cluster_v4(map_cluster(from, (uint32_t)s));
-        v.x += __uint_as_float(u.x);
-        v.y += __uint_as_float(u.y);
-        v.z += __uint_as_float(u.z);
-        v.w += __uint_as_float(u.w);
+      uint4 u[kMostSplits];   // (all on their way before the first is used)
+#pragma unroll
+      for (int s = 0; s < kMostSplits; ++s)
+        if (s < splits) u[s] = ld_cluster_v4(map_cluster(from, (uint32_t)s));
+#pragma unroll
+      for (int s = 0; s < kMostSplits; ++s) {
+        if (s >= splits) break;
+        v.x += __uint_as_float(u[s].x);
+        v.y += __uint_as_float(u[s].y);
+        v.z += __uint_as_float(u[s].z);
+        v.w += __uint_as_float(u[s].w);
       }
       store<4>(p, (long long)(m0 + row) * p.out_stride + n0 + col, p.N - n0 - col, &v.x);
     }
@@ -683,21 +686,30 @@ struct Plan {
   int bn, splits;
 };
 
-// The plan with the least estimated time.  Both kinds stream blocks of 128 columns; a wide tile's block takes the tensor
-// pipe 512 cycles, a narrow one's what its bytes take of an SM's share of the HBM rate (23 bytes a cycle), or the sums.
+// The plan with the least estimated time (us).  Measured, launch included:
+//   wide     4, and a round of tiles 1 and 0.42 a block of 128 columns
+//   narrow   4, or 5 with splits, a round of CTAs, two an SM (a cluster has to find its CTAs in one group of SMs, which
+//            leaves 5% and 15% of them out with four and eight), and the longest of
+//            - a CTA's blocks, 0.2 + 0.0014 a column each, a sixth more with two CTAs an SM,
+//            - the weights at 6.0 TB/s,
+//            - all that the CTAs load, 12.5 TB/s from L2;
+//            then with splits a CTA's sums, 20 KB a us.
+// For instance (rows x columns x K; best narrow against wide): 1 x 2,112 x 7,168 9 against 25, 32 x 7,168 x 16,384 25
+// against 53, 200 x 8,192 x 1,536 9.7 against 11.4, 300 x 4,096 x 4,096 14.6 against 18.1, 777 x 24,576 x 1,536 48 against 40.
 Plan plan(int M, int N, int blocks, int sms) {
   const double pairs = std::max(1, sms / 2);
+  auto up = [](double a, double b) { return std::ceil(a / b); };
   Plan best = {true, kWideCols, 1};
-  double least = std::ceil(std::ceil(M / 256.0) * std::ceil((double)N / kWideCols) / pairs) * (blocks * 800.0 + 1500.0) + 3000.0;
-  const double tiles_m = std::ceil(M / 128.0);
+  double least = 4.0 + up(up(M, 256) * up(N, kWideCols), pairs) * (1.0 + 0.42 * blocks);
+  const double tiles_m = up(M, kRows), rows = std::min(M, kRows), K = blocks * 128.0;
   if (tiles_m > 65535) return best;
   for (int bn = 32; bn <= 128; bn += 32)
-    for (int s = 1; s <= 8 && s <= blocks; s *= 2) {
-      const double ctas = tiles_m * std::ceil((double)N / bn) * s, rounds = std::max(1.0, ctas / (2.0 * sms));
-      const double rows = std::min(M, 128);
-      // two CTAs share an SM
-      const double block = std::max({bn * 128.0 / 23.0 * (ctas > sms ? 2 : 1), (bn + rows) * 128.0 / 60.0, 300.0});
-      const double t = std::ceil(rounds) * (std::ceil((double)blocks / s) * block + 2500.0) + (s > 1 ? 2000.0 : 0.0);
+    for (int s = 1; s <= kMostSplits && s <= blocks; s *= 2) {
+      const double ctas = tiles_m * up(N, bn) * s, rounds = up(ctas, 2.0 * sms * (s == 8 ? 0.85 : s == 4 ? 0.95 : 1.0));
+      const double block = (0.2 + 0.0014 * bn) * (ctas > sms ? 1.15 : 1.0);
+      const double t = rounds * (s > 1 ? 5.0 : 4.0) +
+                       std::max({rounds * up(blocks, s) * block, N * K / 6.0e6, ctas / s * (bn + rows) * K / 12.5e6}) +
+                       (s > 1 ? up(ctas, sms) * rows * bn * 4 / 20e3 : 0.0);
       if (t < least) {
         least = t;
         best = {false, bn, s};
