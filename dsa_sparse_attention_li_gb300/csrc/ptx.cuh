@@ -803,6 +803,11 @@ DSA_DEV float2 unpack2(uint64_t a) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
   return d;
 }
+DSA_DEV uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 // a * b + c, pair by pair.
 DSA_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;

@@ -59,6 +59,34 @@ struct Eight {
       v[k] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
+  // The same as four packed pairs.
+  DSA_DEV void pairs(uint64_t* x) const {
+    float f[8];
+    values(f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = pack2(f[2 * i], f[2 * i + 1]);
+  }
+  // Adds other columns, each sum rounded once to the type.
+  DSA_DEV void add(const Eight& o) {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+      uint32_t a[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      const uint32_t b[4] = {o.v[k].x, o.v[k].y, o.v[k].z, o.v[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (E == DSA_ELEM_FP32) {
+          a[i] = __float_as_uint(__fadd_rn(__uint_as_float(a[i]), __uint_as_float(b[i])));
+        } else if constexpr (E == DSA_ELEM_BF16) {
+          const __nv_bfloat162 s = __hadd2_rn(*reinterpret_cast<const __nv_bfloat162*>(&a[i]), *reinterpret_cast<const __nv_bfloat162*>(&b[i]));
+          a[i] = *reinterpret_cast<const uint32_t*>(&s);
+        } else {
+          const __half2 s = __hadd2_rn(*reinterpret_cast<const __half2*>(&a[i]), *reinterpret_cast<const __half2*>(&b[i]));
+          a[i] = *reinterpret_cast<const uint32_t*>(&s);
+        }
+      }
+      v[k] = make_uint4(a[0], a[1], a[2], a[3]);
+    }
+  }
   DSA_DEV void values(float* x) const {
 #pragma unroll
     for (int k = 0; k < kWords; ++k) {
@@ -96,6 +124,9 @@ DSA_DEV float e4m3_value(uint32_t code) {
   return __half2float(*reinterpret_cast<const __half*>(&h));
 }
 
+// The quotient lies between x inv kDown and x inv kUp, where inv is off by 2^-23 and x by 2^-24 of itself.
+constexpr float kDown = 1.f - 0x1p-21f, kUp = 1.f + 0x1p-21f;
+
 // The code of x / s between its neighbours `lo` (toward zero) and `hi`, which differ by one: by the sign
 // of |x| - border s, which one fused rounding keeps unless the scale is so small that it underflows.
 // (16-bit rows meet exact borders often, about one element in 2^10.)
@@ -107,11 +138,9 @@ DSA_DEV uint32_t settle(float x, float s, uint32_t lo, uint32_t hi) {
   return d > 0.f ? hi : d < 0.f ? lo : even;
 }
 
-// Eight columns x and inv, about 1 / s -> eight codes; settle(i, lo, hi) takes column i's code between two that
-// differ by one.  (x and inv may be off by 2^-23 of themselves each.)
-template <class Settle>
-DSA_DEV uint2 quantise8_by(const float* x, float inv, Settle&& settle) {
-  const float down = inv * (1.f - 0x1p-21f), up = inv * (1.f + 0x1p-21f);
+// Eight columns with scale s, and inv about 1 / s -> eight codes.
+DSA_DEV uint2 quantise8(const float* x, float s, float inv) {
+  const float down = inv * kDown, up = inv * kUp;
   uint32_t lo[4], hi[4], differ = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -125,15 +154,30 @@ DSA_DEV uint2 quantise8_by(const float* x, float inv, Settle&& settle) {
     for (int i = 0; i < 4; ++i) {
       if (lo[i] == hi[i]) continue;
       const uint32_t l0 = lo[i] & 0xff, h0 = hi[i] & 0xff, l1 = lo[i] >> 8, h1 = hi[i] >> 8;
-      lo[i] = (l0 == h0 ? l0 : settle(2 * i, l0, h0)) | ((l1 == h1 ? l1 : settle(2 * i + 1, l1, h1)) << 8);
+      lo[i] = (l0 == h0 ? l0 : settle(x[2 * i], s, l0, h0)) | ((l1 == h1 ? l1 : settle(x[2 * i + 1], s, l1, h1)) << 8);
     }
   }
   return make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
 }
 
-// Eight columns with scale s, and inv about 1 / s -> eight codes.
-DSA_DEV uint2 quantise8(const float* x, float s, float inv) {
-  return quantise8_by(x, inv, [&](int i, uint32_t lo, uint32_t hi) { return settle(x[i], s, lo, hi); });
+// Eight columns (packed pairs) x and their factors down and up, about 1 / s on either side -> the codes toward zero, and in
+// `open` the columns that have another: two codes that differ by one differ in their last bit, and column i's, the j-th
+// four's (i & 3)-th, gets bit 8 (i & 3) + j.
+DSA_DEV uint2 codes8(const uint64_t* x, uint64_t down, uint64_t up, int j, uint32_t& open) {
+  uint32_t word[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint32_t lo[2], hi[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 l = unpack2(mul2(x[2 * k + i], down)), h = unpack2(mul2(x[2 * k + i], up));
+      lo[i] = e4m3x2(l.x, l.y);
+      hi[i] = e4m3x2(h.x, h.y);
+    }
+    word[k] = __byte_perm(lo[0], lo[1], 0x5410);
+    open |= ((word[k] ^ __byte_perm(hi[0], hi[1], 0x5410)) & 0x01010101u) << (j + k);
+  }
+  return make_uint2(word[0], word[1]);
 }
 
 // Largest finite magnitude of sixteen columns: a NaN (which every maximum loses) or an infinity does not cost
