@@ -164,6 +164,8 @@ def load_testhooks(build_if_missing: bool = True) -> ctypes.CDLL:
     I = ctypes.c_int
     lib.dsa_test_mla_visible_columns.argtypes = [I, I, I, I, ctypes.c_void_p, I]
     lib.dsa_test_mla_visible_columns.restype = I
+    lib.dsa_test_matmul_plan.argtypes = [I, I, I, I]
+    lib.dsa_test_matmul_plan.restype = I
     _hooks = lib
     return lib
 
@@ -688,6 +690,23 @@ def _on_current(device):
         raise ValueError("tensors are on %s, the current device is cuda:%d" % (device, torch.cuda.current_device()))
 
 
+def _rows8_out(a, codes, scale, n, dim, device, stream):
+    """The 8-bit rows that a call writes, new ones where None is given; their addresses and strides go into ``a``.
+    (What is new needs no checks, which take 2 us a tensor.)"""
+    groups = (dim + 127) // 128
+    a.codes_stride, a.scale_stride = dim, groups
+    if codes is None:
+        codes = _empty(stream, (n, dim), torch.float8_e4m3fn, device)
+    else:
+        a.codes_stride = _row_stride("codes", codes, torch.float8_e4m3fn, n, dim, device)
+    if scale is None:
+        scale = _empty(stream, (n, groups), torch.float32, device)
+    else:
+        a.scale_stride = _row_stride("scale", scale, torch.float32, n, groups, device)
+    a.codes, a.scale = codes.data_ptr(), scale.data_ptr()
+    return codes, scale
+
+
 def rms_norm_quant(x, weight, *, eps=1e-6, residual=None, residual_out=None, codes=None, scale=None, y=None,
                    stream=None):
     """Root-mean-square norm of the rows x [n, dim] (bf16, fp16 or fp32), after the addition of ``residual``, into
@@ -697,7 +716,7 @@ def rms_norm_quant(x, weight, *, eps=1e-6, residual=None, residual_out=None, cod
     strided, their columns adjacent.  ``codes`` and ``scale`` are what matmul_fp8 takes."""
     lib = load()
     n, dim, elem = _rows_in(x)
-    device, dtype, groups = x.device, x.dtype, (dim + 127) // 128
+    device, dtype = x.device, x.dtype
     if weight.dtype is not dtype and weight.dtype is not torch.float32:
         raise ValueError("weight must be %s or fp32 (got %s)" % (dtype, weight.dtype))
     if weight.shape != (dim,) or weight.get_device() != device.index or not weight.is_contiguous():
@@ -707,17 +726,15 @@ def rms_norm_quant(x, weight, *, eps=1e-6, residual=None, residual_out=None, cod
     a = RmsNormQuantArgs()
     a.n_rows, a.dim, a.elem, a.weight_elem, a.eps = n, dim, elem, _ELEM[weight.dtype], float(eps)
     a.x_stride, a.x, a.weight = _row_stride("x", x, dtype, n, dim, device), x.data_ptr(), weight.data_ptr()
-    if codes is None:
-        codes = _empty(stream, (n, dim), torch.float8_e4m3fn, device)
-    if scale is None:
-        scale = _empty(stream, (n, groups), torch.float32, device)
-    a.codes_stride, a.codes = _row_stride("codes", codes, torch.float8_e4m3fn, n, dim, device), codes.data_ptr()
-    a.scale_stride, a.scale = _row_stride("scale", scale, torch.float32, n, groups, device), scale.data_ptr()
+    codes, scale = _rows8_out(a, codes, scale, n, dim, device, stream)
     if residual is not None:
         a.residual_stride, a.residual = _row_stride("residual", residual, dtype, n, dim, device), residual.data_ptr()
+        a.sum_stride = dim
         if residual_out is None:
             residual_out = _empty(stream, (n, dim), dtype, device)
-        a.sum_stride, a.sum = _row_stride("residual_out", residual_out, dtype, n, dim, device), residual_out.data_ptr()
+        else:
+            a.sum_stride = _row_stride("residual_out", residual_out, dtype, n, dim, device)
+        a.sum = residual_out.data_ptr()
     if y is not None:
         a.y_stride, a.y = _row_stride("y", y, dtype, n, dim, device), y.data_ptr()
     _check(lib.dsa_rms_norm_quant(ctypes.byref(a), _launch_stream(stream, device)), "dsa_rms_norm_quant")
@@ -729,16 +746,11 @@ def quant_rows(x, *, codes=None, scale=None, stream=None):
     [n, dim] e4m3, scale [n, ceil(dim / 128)] fp32), what matmul_fp8 takes."""
     lib = load()
     n, dim, elem = _rows_in(x)
-    device, groups = x.device, (dim + 127) // 128
-    if codes is None:
-        codes = _empty(stream, (n, dim), torch.float8_e4m3fn, device)
-    if scale is None:
-        scale = _empty(stream, (n, groups), torch.float32, device)
+    device = x.device
     a = QuantRowsArgs()
     a.n_rows, a.dim, a.elem = n, dim, elem
     a.x_stride, a.x = _row_stride("x", x, x.dtype, n, dim, device), x.data_ptr()
-    a.codes_stride, a.codes = _row_stride("codes", codes, torch.float8_e4m3fn, n, dim, device), codes.data_ptr()
-    a.scale_stride, a.scale = _row_stride("scale", scale, torch.float32, n, groups, device), scale.data_ptr()
+    codes, scale = _rows8_out(a, codes, scale, n, dim, device, stream)
     _check(lib.dsa_quant_rows(ctypes.byref(a), _launch_stream(stream, device)), "dsa_quant_rows")
     return codes, scale
 
@@ -755,11 +767,9 @@ def matmul_fp8(a, a_scale, b, b_scale, *, out=None, dtype=torch.bfloat16, status
     N, blocks = b.shape[0], (K + 127) // 128
     device = a.device
     _on_current(device)
-    if out is None:
-        out = _empty(stream, (M, N), dtype, device)
-    elem = _ELEM.get(out.dtype)
+    elem = _ELEM.get(dtype if out is None else out.dtype)
     if elem is None:
-        raise ValueError("out must be bf16, fp16 or fp32 (got %s)" % out.dtype)
+        raise ValueError("out must be bf16, fp16 or fp32 (got %s)" % (dtype if out is None else out.dtype))
     if status is not None:
         _fits(device, ("status", status, torch.int32, None))
     g = MatmulFp8Args()
@@ -769,7 +779,11 @@ def matmul_fp8(a, a_scale, b, b_scale, *, out=None, dtype=torch.bfloat16, status
     g.b_stride, g.b = _row_stride("b", b, torch.float8_e4m3fn, N, K, device), b.data_ptr()
     g.b_scale_stride = _row_stride("b_scale", b_scale, torch.float32, (N + 127) // 128, blocks, device)
     g.b_scale = b_scale.data_ptr()
-    g.out_stride, g.out = _row_stride("out", out, out.dtype, M, N, device), out.data_ptr()
+    if out is None:
+        out, g.out_stride = _empty(stream, (M, N), dtype, device), N
+    else:
+        g.out_stride = _row_stride("out", out, out.dtype, M, N, device)
+    g.out = out.data_ptr()
     g.status = _addr(status)
     _check(lib.dsa_matmul_fp8(ctypes.byref(g), _launch_stream(stream, device)), "dsa_matmul_fp8")
     return out

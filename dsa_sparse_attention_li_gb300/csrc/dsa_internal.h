@@ -63,8 +63,8 @@ bool encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* bas
 #ifdef DSA_TEST_HOOKS
 // Test build only: which kernel's first CTA makes one of its waits wait on a barrier that nothing
 // arrives on (0 none, 1 li_topk, 2 sparse attention,
-// 3 mla_decode, 4 mla_prefill), or leaves a load out (5, 6 mla_decode, 7 to 9 mla_prefill); set by
-// dsa_test_inject_stall().
+// 3 mla_decode, 4 mla_prefill), or leaves a load out (5, 6 mla_decode, 7 to 9 mla_prefill; 10, 11 matmul_fp8,
+// in turn); set by dsa_test_inject_stall().
 extern int g_test_stall;
 #endif
 

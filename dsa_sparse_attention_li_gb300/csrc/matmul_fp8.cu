@@ -720,6 +720,13 @@ Plan plan(int M, int N, int blocks, int sms) {
 
 }  // namespace mm
 
+#ifdef DSA_TEST_HOOKS
+extern "C" int dsa_test_matmul_plan(int M, int N, int K, int sms) {
+  const mm::Plan w = mm::plan(M, N, (K + mm::kBlock - 1) / mm::kBlock, sms);
+  return w.wide ? 0 : w.bn * 16 + w.splits;
+}
+#endif
+
 dsa_status launch_matmul_fp8(const dsa_matmul_fp8_args& a, cudaStream_t stream, std::string& err) {
   using namespace mm;
   DeviceInfo dev;

@@ -16,11 +16,14 @@
  * stalled launch is unspecified.  Host-side state, not thread-safe; a test setting.
  * With 5 to 9 that CTA leaves a load out instead, so that what waits for its bytes gives up: 5 and 6 the
  * first keys and the first values of dsa_mla_decode over a bf16 cache, 7, 8 and 9 the first keys, the first
- * values and the queries of dsa_mla_prefill.
+ * values and the queries of dsa_mla_prefill.  10 is the stall for dsa_matmul_fp8, 11 leaves its first load of a out.
  *
  * dsa_test_mla_visible_columns(): on the host, with host pointers, the rule by which dsa_mla_decode's
  * softmax decides how many of a page's 64 positions a query row may use, lookup of the page id
  * included.  `pages` is the sequence's row of the page table, pos0 the page's first position.
+ *
+ * dsa_test_matmul_plan(): how dsa_matmul_fp8 would divide a product of this size on a GPU of `sms` SMs: 0 in wide
+ * tiles, else the columns of a narrow tile times 16 plus the CTAs that share its blocks.
  */
 #ifndef DSA_TESTHOOKS_H
 #define DSA_TESTHOOKS_H
@@ -34,6 +37,7 @@ extern "C" {
 void dsa_test_inject_stall(int kernel);
 int dsa_test_mla_visible_columns(int owned, int seen, int pos0, int check_pages, const int32_t* pages,
                                  int num_pages);
+int dsa_test_matmul_plan(int M, int N, int K, int sms);
 
 #ifdef __cplusplus
 }

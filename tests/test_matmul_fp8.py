@@ -336,3 +336,89 @@ def test_binding_refuses_what_does_not_fit(cuda_lib):
             dsa.matmul_fp8(**kw)
     with pytest.raises(dsa.DsaError):
         dsa.matmul_fp8(a[:, 8:264], a_scale[:, :2], b[:, :256], b_scale[:, :2])   # rows that start on 8 bytes
+
+
+# Sizes that large calls divide into wide tiles: blocks below, at and above the eight whose scales are multiplied at a time,
+# last blocks of 16 columns, a last tile of one row or column, rows of out that a TMA store cannot reach
+WIDE = [(2500, 2500, 16), (2300, 2560, 896), (2300, 2561, 1024), (2049, 2304, 1152), (5000, 1537, 2192), (20000, 256, 144),
+        (4100, 5121, 400), (700, 7000, 2064), (257, 16000, 1200), (130, 20000, 640), (8193, 2049, 1040)]
+# ... and into narrow ones of every width and number of splits
+NARROW = [(9, 2112, 7168), (40, 7168, 16384), (100, 7168, 7168), (16, 24576, 1536), (5, 1000, 400), (64, 100, 16384),
+          (128, 640, 3600), (90, 2000, 2048), (128, 576, 7168), (1, 7168, 1040), (64, 7168, 1040), (200, 8192, 1024),
+          (160, 2112, 3584), (120, 5000, 3600)]
+
+
+def test_the_sizes_reach_every_variant():
+    plan = dsa.load_testhooks().dsa_test_matmul_plan
+    assert all(plan(*s, 152) == 0 for s in WIDE)
+    got = {plan(*s, 152) for s in NARROW + SIZES}
+    assert {divmod(v, 16)[0] for v in got} >= {32, 64, 96, 128} and {v % 16 for v in got} == {0, 1, 2, 4, 8}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", WIDE + NARROW)
+def test_whole_products_of_every_variant_are_exact(cuda_lib, m, n, k):
+    a, a_scale, b, b_scale = whole(m, n, k, gen(m, n, k))
+    want = definition(a, a_scale, b, b_scale)[0].float()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for dtype in TYPES:
+        out = torch.full((m, n), math.nan, dtype=dtype, device="cuda")
+        dsa.matmul_fp8(a, a_scale, b, b_scale, out=out, status=status)
+        assert torch.equal(out, want.to(dtype)), dtype
+    assert int(status) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [WIDE[1], WIDE[2], WIDE[4], NARROW[0], NARROW[2], NARROW[5]])
+def test_any_values_of_every_variant(cuda_lib, m, n, k):
+    a, a_scale, b, b_scale = any_values(m, n, k, gen(n, k, m))
+    want, size = definition(a, a_scale, b, b_scale)
+    out = dsa.matmul_fp8(a, a_scale, b, b_scale, dtype=torch.float32)
+    assert torch.all((out.double() - want).abs() <= size * OFF + want.abs() * 2.0 ** -24)
+    assert torch.equal(out, dsa.matmul_fp8(a, a_scale, b, b_scale, dtype=torch.float32))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(2300, 2560, 896), (700, 7000, 2064)])
+def test_wide_tiles_with_strided_rows(cuda_lib, m, n, k):
+    """As test_strided_rows: operands and scales inside NaN, and what is not written stays, with a TMA store and without."""
+    a, a_scale, b, b_scale = whole(m, n, k, gen(m, k))
+    want = definition(a, a_scale, b, b_scale)[0].float()
+    args = (spread(a, k + 48, math.nan), spread(a_scale, a_scale.shape[1] + 3, math.nan), spread(b, k + 32, math.nan),
+            spread(b_scale, b_scale.shape[1] + 1, math.nan))
+    for dtype in TYPES:
+        for left, right in ((0, 16), (8, 8), (1, 2)):
+            out = torch.full((m + 1, left + n + right), 5.0, dtype=dtype, device="cuda")
+            dsa.matmul_fp8(*args, out=out[:m, left:left + n])
+            assert torch.equal(out[:m, left:left + n], want.to(dtype))
+            out[:m, left:left + n] = 5.0
+            assert torch.all(out == 5.0)
+
+
+@pytest.mark.gpu
+def test_what_is_not_finite_stays_in_its_row_of_a_wide_tile(cuda_lib):
+    m, n, k = 2300, 2560, 896
+    a, a_scale, b, b_scale = whole(m, n, k, gen(8))
+    clean = dsa.matmul_fp8(a, a_scale, b, b_scale, dtype=torch.float32)
+    a.view(torch.uint8)[777, 500], b.view(torch.uint8)[1300, 3], a_scale[2299, 6] = 0x7f, 0xff, math.nan
+    got = dsa.matmul_fp8(a, a_scale, b, b_scale, dtype=torch.float32)
+    bad = torch.zeros((m, n), dtype=torch.bool, device="cuda")
+    bad[777], bad[2299], bad[:, 1300] = True, True, True
+    assert torch.all(got[bad].isnan()) and torch.equal(got[~bad], clean[~bad])
+
+
+@pytest.mark.gpu
+def test_wide_and_narrow_calls_at_once(cuda_lib):
+    """Both kinds on four streams: each keeps tensor memory that the other waits for."""
+    sizes = [(2300, 2560, 896), (9, 2112, 7168), (2049, 2304, 1152), (100, 7168, 1024)]
+    cases = [whole(m, n, k, gen(m, n)) for m, n, k in sizes]
+    want = [definition(*c)[0].float().bfloat16() for c in cases]
+    streams = [torch.cuda.Stream() for _ in sizes]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for s, c in zip(streams, cases):
+            with torch.cuda.stream(s):
+                got.append(dsa.matmul_fp8(*c))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i % 4]) for i, o in enumerate(got))
