@@ -8,13 +8,22 @@
 // is then one number, or two, a thread), while the MMAs fill the other buffer.
 //
 // Wide tiles (prompts): 256 rows x 256 columns by a CTA pair (cta_group::2; each CTA has 128 rows of a, 128 of b
-// and 128 x 256 sums), a ring of six 32-KB stages, one persistent pair per two SMs.  Bound: the tensor pipe, 512 cycles
-// a block and pair.
+// and 128 x 256 sums), a ring of five 32-KB stages, one persistent pair per two SMs.  A block's MMAs, 512 cycles at
+// the nominal rate, are issued and handed over in halves of 128 columns (one scale of b each), which leaves the sums
+// 768 cycles until a buffer is wanted back; a warp's products come from tensor memory a step of 32 columns ahead of its
+// multiply-adds, across blocks.  Two warps multiply the scales, eight blocks at a time.  Rows go out by TMA.
+// Bound: loads and MMAs alone run 4,096 x 7,168 x 16,384 in 250 us (3,850 TFLOP/s, at the power limit: 1,440 MHz
+// after a second of it); the multiply-adds, 256 of a block's cycles on the fp32 pipe, their hand-over and their power
+// make it 325 us (2,960 TFLOP/s; 370 us, 1,620 MHz, after a second).  With 512 columns in all a tile's end, 2,000 cycles,
+// is as long as its sums: 8,192 x 32,768 in 168 us.
+// Measured on the way: waits by suspension or by spinning alike; loads a row a lane of the scales by the sums
+// themselves 430 (each takes 32 lines of L1); halves of 96 columns (256 x 192) 390; sums that spill one register 510.
 //
 // Narrow tiles (few rows): 128 rows x 32 to 128 columns a CTA.  A cluster of up to eight CTAs shares a tile's blocks, and
 // its parts are added in rank order through distributed shared memory: many CTAs stream the weights, the result does not
 // depend on their timing, and there is no workspace.  Two CTAs an SM, so that one's start and end run under the
-// other's stream.  Bound: HBM.
+// other's stream.  Bound: HBM with long rows (32 x 7,168 x 16,384 in 25 us, 4.8 TB/s of weights), else launch, a
+// tile's chain of blocks (0.25 to 0.38 us each) and the parts' exchange (1 x 2,112 x 7,168 in 9 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -38,7 +47,7 @@ constexpr int kGroupRows = 8;     // wide tiles of a column of tiles that run on
 struct Params {
   int M, N, blocks;
   int elem;
-  int vec;                 // rows of out start 32-byte aligned (wide: 16-byte aligned)
+  int vec;                 // rows of out start 16-byte aligned
   int tiles_m, tiles_n;
   int a_box, stages;       // narrow: rows of a that are loaded, stages of the ring
   long long a_scale_stride, b_scale_stride, out_stride;
@@ -71,26 +80,39 @@ DSA_DEV uint32_t pack16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// A box of 32 rows and 64 bytes in shared memory (in the layout that a store by TMA takes) to outputs whose rows a TMA
-// store cannot reach: a column a lane, in 32 bits two rows at a time.
-__device__ __noinline__ void store_box(const Params& p, const uint8_t* box, int m0, int n0) {
-  const int lane = threadIdx.x & 31, rows = min(32, p.M - m0);
-  if (p.elem == DSA_ELEM_FP32) {
-    const int col = lane & 15;
-    if (n0 + col >= p.N) return;
-#pragma unroll 8
-    for (int r = lane >> 4; r < 32; r += 2)
-      if (r < rows)
-        reinterpret_cast<float*>(p.out)[(long long)(m0 + r) * p.out_stride + n0 + col] =
-            *reinterpret_cast<const float*>(box + r * 64 + (((col >> 2) ^ ((r >> 1) & 3)) << 4) + (col & 3) * 4);
-  } else {
-    if (n0 + lane >= p.N) return;
-#pragma unroll 8
-    for (int r = 0; r < 32; ++r)
-      if (r < rows)
-        reinterpret_cast<uint16_t*>(p.out)[(long long)(m0 + r) * p.out_stride + n0 + lane] =
-            *reinterpret_cast<const uint16_t*>(box + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
-  }
+// `cols` outputs (at most 128) from column n on of rows m, m + step, ..., `some` of them and R at a time, value(r, c) the
+// c-th of the r-th, by a whole warp, a column a lane: for rows of out that start anywhere.  Bound by instructions: 4
+// bytes a lane, with the lines' ends apart, took 340 us for 4,096 x 20,001 bf16 of 512 columns.
+template <int R, class Value>
+DSA_DEV void store_rows(const Params& p, int m, int step, int some, int n, int cols, Value&& value) {
+  const int lane = threadIdx.x & 31;
+  auto each = [&](auto* out, auto&& rounded) {
+    auto* o = out + ((long long)m * p.out_stride + n + lane);
+    const long long apart = (long long)step * p.out_stride;
+#pragma unroll
+    for (int c = 0; c < 128; c += 32) {
+      if (c + lane >= cols) break;
+      float x[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) x[r] = r < some ? value(r, c + lane) : 0.f;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r < some) o[r * apart + c] = rounded(x[r]);
+    }
+  };
+  if (p.elem == DSA_ELEM_FP32)
+    each(reinterpret_cast<float*>(p.out), [](float x) { return x; });
+  else if (p.elem == DSA_ELEM_BF16)
+    each(reinterpret_cast<__nv_bfloat16*>(p.out), [](float x) { return __float2bfloat16_rn(x); });
+  else
+    each(reinterpret_cast<__half*>(p.out), [](float x) { return __float2half_rn(x); });
+}
+
+// Eight rows of 128 sums in shared memory, 16-byte piece i of row r at i ^ r, to rows m .. of out, columns n on.
+__device__ __noinline__ void store_eight(const Params& p, const uint8_t* rows, int m, int n) {
+  store_rows<8>(p, m, 1, p.M - m, n, min(128, p.N - n), [&](int r, int c) {
+    return *reinterpret_cast<const float*>(rows + r * 512 + (((c >> 2) ^ r) << 4) + (c & 3) * 4);
+  });
 }
 
 // N values to element `at` of out on, `left` columns from the end of its row.
@@ -115,10 +137,12 @@ DSA_DEV void store(const Params& p, long long at, int left, const float* v) {
     w[i] = p.elem == DSA_ELEM_BF16 ? pack16<DSA_ELEM_BF16>(v[2 * i], v[2 * i + 1]) : pack16<DSA_ELEM_FP16>(v[2 * i], v[2 * i + 1]);
   uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + at;
   if (p.vec && left >= N) {
-    if constexpr (N == 16)
-      st_global_v8(o, w);
-    else
+    if constexpr (N == 16) {
+      *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(o + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
       *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -209,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int m0 = (int)blockIdx.y * kRows, n0 = (int)blockIdx.x / splits * BN;
   const int first = (int)((long long)p.blocks * rank / splits), n = (int)((long long)p.blocks * (rank + 1) / splits) - first;
   const int quarters = min(4, (p.M - m0 + 31) / 32);   // of the tile's rows, a warp each, that have any
+  const bool direct = splits == 1 && p.vec;             // sums go out as they lie in registers
   const int a_bytes = p.a_box * kBlock, b_at = p.stages * a_bytes;   // (the MMAs read 128 rows of a: of later slots, and b)
 
   if (tid == 0) {
@@ -302,10 +327,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int split = block0 == block1 ? HC : (block0 + 1) * kBlock - n0 - half;
     const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half;
     // a block ahead, and multiplied when they are used: what needs a load holds up the warp until it is there
-    float a = __ldg(a_scale), b0 = __ldg(b_scale0), b1 = __ldg(b_scale1);
+    float a = a_scale[0], b0 = b_scale0[0], b1 = b_scale1[0];
     for (int i = 0; i < n; ++i) {
       const int next = min(i + 1, n - 1);
-      const float next_a = __ldg(a_scale + next), next_b0 = __ldg(b_scale0 + next), next_b1 = __ldg(b_scale1 + next);
+      const float next_a = a_scale[next], next_b0 = b_scale0[next], next_b1 = b_scale1[next];
       warp_wait(&ctl->sum_full[i & 1][0], (i >> 1) & 1u, abort, p.status);
       if (__any_sync(0xffffffffu, *abort)) break;
       auto done = [&] {
@@ -319,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       b0 = next_b0;
       b1 = next_b1;
     }
-    if (splits == 1) {
+    if (direct) {
       if (m0 + local < p.M && !*abort) {
         const long long out = (long long)(m0 + local) * p.out_stride + n0 + half;
 #pragma unroll
@@ -342,27 +367,49 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   __syncwarp();
-  if (splits > 1) {
-    // ---------------- the parts of a tile: each CTA adds up those of its share of the columns, in rank order
-    cluster_sync();
-    const int quads = BN / 4 / splits, items = min(kRows, p.M - m0) * quads;
-    for (int it = tid; it < items; it += kThreads) {
-      const int row = it / quads, col = (rank * quads + it - row * quads) * 4;
-      const float* from = part + row * kPitch + col;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      uint4 u[kMostSplits];   // (all on their way before the first is used)
+  if (!direct) {
+    // ---------------- the parts of a tile: each CTA adds up those of its share, in rank order
+    if (splits > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    const int rows = min(kRows, p.M - m0);
+    if (p.vec) {   // a share of the columns, four at a time
+      const int quads = BN / 4 / splits, items = rows * quads;
+      for (int it = tid; it < items; it += kThreads) {
+        const int row = it / quads, col = (rank * quads + it - row * quads) * 4;
+        const float* from = part + row * kPitch + col;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        uint4 u[kMostSplits];   // (all on their way before the first is used)
 #pragma unroll
-      for (int s = 0; s < kMostSplits; ++s)
-        if (s < splits) u[s] = ld_cluster_v4(map_cluster(from, (uint32_t)s));
+        for (int s = 0; s < kMostSplits; ++s)
+          if (s < splits) u[s] = ld_cluster_v4(map_cluster(from, (uint32_t)s));
 #pragma unroll
-      for (int s = 0; s < kMostSplits; ++s) {
-        if (s >= splits) break;
-        v.x += __uint_as_float(u[s].x);
-        v.y += __uint_as_float(u[s].y);
-        v.z += __uint_as_float(u[s].z);
-        v.w += __uint_as_float(u[s].w);
+        for (int s = 0; s < kMostSplits; ++s) {
+          if (s >= splits) break;
+          v.x += __uint_as_float(u[s].x);
+          v.y += __uint_as_float(u[s].y);
+          v.z += __uint_as_float(u[s].z);
+          v.w += __uint_as_float(u[s].w);
+        }
+        store<4>(p, (long long)(m0 + row) * p.out_stride + n0 + col, p.N - n0 - col, &v.x);
       }
-      store<4>(p, (long long)(m0 + row) * p.out_stride + n0 + col, p.N - n0 - col, &v.x);
+    } else {       // a share of the rows
+      const int cols = min(BN, p.N - n0), step = kThreads / 32 * splits;
+      for (int row = warp * splits + rank; row < rows; row += 4 * step)
+        store_rows<4>(p, m0 + row, step, (rows - row + step - 1) / step, n0, cols, [&](int r, int c) {
+          const float* from = part + (row + r * step) * kPitch + c;
+          if (splits == 1) return *from;
+          uint32_t u[kMostSplits];
+#pragma unroll
+          for (int s = 0; s < kMostSplits; ++s)
+            if (s < splits) u[s] = ld_cluster_u32(map_cluster(from, (uint32_t)s));
+          float v = 0.f;
+#pragma unroll
+          for (int s = 0; s < kMostSplits; ++s)
+            if (s < splits) v += __uint_as_float(u[s]);
+          return v;
+        });
     }
   }
   drain(ctl);
@@ -527,14 +574,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       for (int i = 0; i < p.blocks; i += kScaleBlocks, ++set) {
         const int block = min(i + in, p.blocks - 1);
         const float* a = p.a_scale + block;
-        const float bs = __ldg(b + block);
+        const float bs = b[block];
         go = set < 2 || mbar_wait_fast(&ctl->scale_free[set & 1u], ((set >> 1) - 1) & 1u, abort, p.status);
         go = __all_sync(0xffffffffu, go);
         if (!go) break;
         float* to = reinterpret_cast<float*>(smem + W::scales) + ((set & 1u) * 2 + h) * W::kScales + in * kScalePitch;
 #pragma unroll 8
         for (int r = first; r < kRows; r += 32 / kScaleBlocks)
-          to[r] = __ldg(a + (long long)min(m0 + r, p.M - 1) * p.a_scale_stride) * bs;
+          to[r] = a[(long long)min(m0 + r, p.M - 1) * p.a_scale_stride] * bs;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->scale_full[set & 1u]);
       }
@@ -616,6 +663,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       n0 += half;
       if (m0 >= p.M) continue;
       uint8_t* boxes = smem + W::out + warp * (W::kBoxes * W::kBox);
+      if (!p.vec) {
+        if (n0 >= p.N) continue;
+#pragma unroll 1
+        for (int r = 0; r < 32; r += 8) {   // eight rows at a time
+          if ((lane & ~7) == r) {
+#pragma unroll
+            for (int c = 0; c < kCols; c += 16) {
+              float x[16];
+              sums.values(c, x);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4*>(boxes + (lane & 7) * 512 + ((((c >> 2) + i) ^ (lane & 7)) << 4)) =
+                    make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            }
+          }
+          __syncwarp();
+          store_eight(p, boxes, m0 + r, n0);
+          __syncwarp();
+        }
+        continue;
+      }
       // a box of 64 bytes a row, from four times 16 bytes that piece() gives
       auto put = [&](int col, auto&& piece) {
         if (col >= p.N) return;
@@ -625,17 +693,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(to + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = piece(i);
-        if (p.vec) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&tm_out, to, col, m0);
-            bulk_commit();
-          }
-        } else {
-          __syncwarp();
-          store_box(p, to, m0, col);
-          __syncwarp();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&tm_out, to, col, m0);
+          bulk_commit();
         }
       };
       auto put16 = [&](auto type) {
@@ -737,7 +799,7 @@ dsa_status launch_matmul_fp8(const dsa_matmul_fp8_args& a, cudaStream_t stream, 
   p.blocks = (a.K + kBlock - 1) / kBlock;
   p.elem = a.elem;
   const int size = a.elem == DSA_ELEM_FP32 ? 4 : 2;
-  p.vec = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 && (a.M == 1 || a.out_stride * size % 32 == 0);
+  p.vec = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && (a.M == 1 || a.out_stride * size % 16 == 0);
   p.a_scale_stride = a.a_scale_stride;
   p.b_scale_stride = a.b_scale_stride;
   p.out_stride = a.out_stride;
@@ -777,7 +839,6 @@ dsa_status launch_matmul_fp8(const dsa_matmul_fp8_args& a, cudaStream_t stream, 
   cudaLaunchConfig_t cfg = {};
   CUtensorMap tm_out;
   if (w.wide) {
-    p.vec = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && (a.M == 1 || a.out_stride * size % 16 == 0);
     if (p.vec && !encode_tmap_2d(&tm_out, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, a.out,
                                  (uint64_t)a.N, (uint64_t)a.M, a.M == 1 ? ((uint64_t)a.N * size + 15) / 16 * 16 : (uint64_t)a.out_stride * size, 64 / size, 32,
                                  CU_TENSOR_MAP_SWIZZLE_64B, err))

@@ -398,7 +398,11 @@ dsa_status dsa_quant_rows(const dsa_quant_rows_args* args, dsa_stream_t stream);
  * a may be the rows of an FP8 latent cache as they lie there (a_stride 608, a_scale 576 bytes on, a_scale_stride
  * 152): the up-projection of dsa_mla_prefill's keys and values reads no converted copy.
  *
- * Supported: K a multiple of 16; any M and N; rows of a and b 16-byte aligned.
+ * Few rows stream the weights, many run on tiles of 256 x 256; each output is added up in an order that
+ * depends on the sizes alone, so that a call gives the same bits every time.  Rows of out that start 16-byte
+ * aligned are stored fastest.  Launched as a programmatic dependent, as dsa_sfa_decode is (see above).
+ *
+ * Supported: K a multiple of 16; any M and N; rows of a and b 16-byte aligned; out overlaps no input.
  */
 typedef struct {
   int M, N, K;

@@ -298,3 +298,57 @@ def test_binding_refuses_what_does_not_fit(cuda_lib):
         kw.update(bad)
         with pytest.raises(ValueError):
             dsa.quant_rows(**kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("d", [136, 4096, 16384])
+def test_norm_of_hard_sums(cuda_lib, d, dtype):
+    """The sum with a residual of values across the type's whole range, subnormal ones and infinities among them, in
+    place and out of it."""
+    g = torch.Generator().manual_seed(d + 1)
+    x, r = hard_rows(24, d, dtype, g), hard_rows(24, d, dtype, g)[torch.randperm(24, generator=g)]
+    w = (1 + 0.3 * torch.randn(d, generator=g)).to(dtype)
+    want = (x.float() + r.float()).to(dtype)
+    xd, rd = x.cuda(), r.cuda()
+    codes, scale, total = dsa.rms_norm_quant(xd, w.cuda(), eps=1e-5, residual=rd)
+    same = lambda a, b: torch.equal(a.isnan(), b.isnan()) and torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))
+    assert same(total.cpu(), want)
+    # the same rows without a residual, and with the sum in the residual's or in x's place
+    c2, s2 = dsa.rms_norm_quant(total, w.cuda(), eps=1e-5)
+    assert torch.equal(codes.view(torch.uint8), c2.view(torch.uint8)) and torch.equal(scale, s2)
+    for place in (rd, xd):
+        a, b = xd.clone(), rd.clone()
+        at = a if place is xd else b
+        c3, s3, t3 = dsa.rms_norm_quant(a, w.cuda(), eps=1e-5, residual=b, residual_out=at, y=b if place is xd else a)
+        assert t3 is at and same(t3.cpu(), want)
+        assert torch.equal(codes.view(torch.uint8), c3.view(torch.uint8)) and torch.equal(scale, s3)
+
+
+@pytest.mark.gpu
+def test_rows_on_another_stream_and_in_a_graph(cuda_lib):
+    """New outputs of a given stream, and a captured norm in place, replayed."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((300, 7168), generator=g, device="cuda").bfloat16()
+    w = torch.rand(7168, generator=g, device="cuda").bfloat16()
+    want = dsa.rms_norm_quant(x, w, residual=x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = [dsa.rms_norm_quant(x, w, residual=x, stream=side) for _ in range(3)]
+    rows = [dsa.quant_rows(x, stream=side) for _ in range(3)]
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    for a in got:
+        assert all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in zip(a, want))
+    for a in rows:
+        assert all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in zip(a, dsa.quant_rows(x)))
+    r = x.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        codes, scale, _ = dsa.rms_norm_quant(x, w, residual=r, residual_out=r)
+    total = x.clone()
+    for _ in range(3):
+        graph.replay()
+        c, s, total = dsa.rms_norm_quant(x, w, residual=total)
+        assert torch.equal(r, total) and torch.equal(codes.view(torch.uint8), c.view(torch.uint8)) and torch.equal(scale, s)
