@@ -175,10 +175,11 @@ struct Sums {
       x = fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f, x);
     }
   }
-  // Sixteen columns from the c-th on.
-  DSA_DEV void values(int c, float* x) const {
+  // N columns from the c-th on.
+  template <int N>
+  DSA_DEV void values(int c, float (&x)[N]) const {
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
+    for (int i = 0; i < N; i += 2) {
       const float2 two = unpack2(v[(c + i) / 2]);
       x[i] = two.x;
       x[i + 1] = two.y;
@@ -426,8 +427,8 @@ constexpr int kWideCols = 256;
 struct Wide {
   static constexpr int kCols = kWideCols / 2;                // of a thread: a block of b
   static constexpr int kA = kRows * kBlock, kB = kCols * kBlock, kStage = kA + kB;
-  static constexpr int kStages = 5;
-  static constexpr int kBox = 32 * 64, kBoxes = 3;           // of a warp's outputs: 32 rows of 64 bytes
+  static constexpr int kStages = 4;
+  static constexpr int kBox = 32 * 64, kBoxes = 4;           // of a warp's outputs: 32 rows of 64 bytes
   static constexpr int kScales = kScaleBlocks * kScalePitch; // floats, of a half's columns
   static constexpr int out = kStages * kStage, scales = out + 8 * kBoxes * kBox, ctl = scales + 4 * kScales * 4,
                        total = ctl + 1024;
@@ -595,7 +596,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     const uint32_t sum_free = map_cluster(&ctl->sum_free[0][h], 0);
     const float* scales = reinterpret_cast<const float*>(smem + W::scales) + h * W::kScales + local;
     uint32_t it = 0, set = 0;
-    int box = 0;
     bool go = true;
     for (int t = pair; t < tiles && go; t += pairs) {
       Sums<kCols, 32> sums;
@@ -684,34 +684,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         }
         continue;
       }
-      // a box of 64 bytes a row, from four times 16 bytes that piece() gives
-      auto put = [&](int col, auto&& piece) {
-        if (col >= p.N) return;
-        uint8_t* to = boxes + box * W::kBox;
-        box = box + 1 == W::kBoxes ? 0 : box + 1;
-        if (lane == 0) bulk_wait_read_but_two();   // (a store reads its box some time after it is issued)
+      // Four boxes of 64 bytes a row, `cols` columns each, go out together: piece(i, k) gives the k-th 16 bytes of the
+      // i-th.  (A store reads its box some time after it is issued.)
+      static_assert(W::kBoxes == 4, "boxes that go out together");
+      auto put = [&](int col, int cols, auto&& piece) {
+        if (lane == 0) bulk_wait_read_all();
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(to + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = piece(i);
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(boxes + i * W::kBox + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = piece(i, k);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_2d(&tm_out, to, col, m0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (col + i * cols < p.N) tma_store_2d(&tm_out, boxes + i * W::kBox, col + i * cols, m0);
           bulk_commit();
         }
       };
       auto put16 = [&](auto type) {
-#pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
-          float x[32];
-          sums.values(c, x);
-          sums.values(c + 16, x + 16);
-          put(n0 + c, [&](int i) {
-            const float* v = x + 8 * i;
-            constexpr int E = decltype(type)::value;
-            return make_uint4(pack16<E>(v[0], v[1]), pack16<E>(v[2], v[3]), pack16<E>(v[4], v[5]), pack16<E>(v[6], v[7]));
-          });
-        }
+        put(n0, 32, [&](int i, int k) {
+          constexpr int E = decltype(type)::value;
+          float x[8];
+          sums.values(i * 32 + k * 8, x);
+          return make_uint4(pack16<E>(x[0], x[1]), pack16<E>(x[2], x[3]), pack16<E>(x[4], x[5]), pack16<E>(x[6], x[7]));
+        });
       };
       if (p.elem == DSA_ELEM_BF16) {
         put16(std::integral_constant<int, DSA_ELEM_BF16>());
@@ -719,14 +718,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         put16(std::integral_constant<int, DSA_ELEM_FP16>());
       } else {
 #pragma unroll
-        for (int c = 0; c < kCols; c += 16) {
-          float x[16];
-          sums.values(c, x);
-          put(n0 + c, [&](int i) {
-            const float* v = x + 4 * i;
-            return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        for (int c = 0; c < kCols; c += 64)
+          put(n0 + c, 16, [&](int i, int k) {
+            float x[4];
+            sums.values(c + i * 16 + k * 4, x);
+            return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
           });
-        }
       }
     }
     if (lane == 0) bulk_wait_all();

@@ -690,8 +690,6 @@ DSA_DEV void tma_store_2d(const CUtensorMap* m, const void* src, int x, int y) {
 DSA_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Wait until every committed bulk copy of this thread has finished reading its source.
 DSA_DEV void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-// ... all but the last two.
-DSA_DEV void bulk_wait_read_but_two() { asm volatile("cp.async.bulk.wait_group.read 2;" ::: "memory"); }
 // Wait until every committed bulk copy of this thread is complete.
 DSA_DEV void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 DSA_DEV uint4 ld_cluster_v4(uint32_t addr) {
