@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kMost, kMost == kFew<DSA_ELEM_BF16> ? 2 : 1) n
   const int col = (l / kLanes) * kGroup + (l % kLanes) * 8;   // the unit's columns: eight from here on, and 32, 64 and 96 on
   const int pieces = row < p.n_rows && col < p.dim ? min(kPieces, (p.dim - col + 31) / 32) : 0;
 
+  griddep_wait();   // nothing above reads global memory
   uint64_t h[kUnit / 2];   // two columns each
   {
     Eight<E> x[kPieces];
@@ -268,6 +269,7 @@ __global__ void __launch_bounds__(128) quant_kernel(const __grid_constant__ Quan
   int group[N], pieces[N];
   Eight<E> x[N][kPieces];
   const int in = (int)(threadIdx.x % kLanes) * 8;   // of the group's columns
+  griddep_wait();   // nothing above reads global memory
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     const uint32_t u = blockIdx.x * (N * 128u) + n * 128u + threadIdx.x, g = u / kLanes;   // groups, row after row
@@ -314,6 +316,21 @@ NormKernel norm_variant(int threads) {
   return threads <= kFew<E> ? norm_kernel<E, WE, kFew<E>> : norm_kernel<E, WE, 1024>;
 }
 
+// A launch that may begin while the kernel before it ends (the kernels wait for that before they read anything).
+template <class Params>
+cudaError_t launch_early(void (*k)(Params), unsigned blocks, int threads, cudaStream_t stream, const Params& p) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, p);
+}
+
 }  // namespace nq
 
 dsa_status launch_rms_norm_quant(const dsa_rms_norm_quant_args& a, cudaStream_t stream, std::string& err) {
@@ -351,8 +368,7 @@ dsa_status launch_rms_norm_quant(const dsa_rms_norm_quant_args& a, cudaStream_t 
       a.elem == DSA_ELEM_FP32   ? norm_variant<DSA_ELEM_FP32, DSA_ELEM_FP32>(threads)
       : a.elem == DSA_ELEM_BF16 ? same ? norm_variant<DSA_ELEM_BF16, DSA_ELEM_BF16>(threads) : norm_variant<DSA_ELEM_BF16, DSA_ELEM_FP32>(threads)
       : same                    ? norm_variant<DSA_ELEM_FP16, DSA_ELEM_FP16>(threads) : norm_variant<DSA_ELEM_FP16, DSA_ELEM_FP32>(threads);
-  k<<<(unsigned)blocks, threads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_early(k, (unsigned)blocks, threads, stream, p);
   if (e != cudaSuccess) return cuda_fail(e, "rms_norm_quant: launch", err);
   return DSA_OK;
 }
@@ -383,8 +399,7 @@ dsa_status launch_quant_rows(const dsa_quant_rows_args& a, cudaStream_t stream, 
   const auto k = a.elem == DSA_ELEM_BF16   ? quant_kernel<DSA_ELEM_BF16, N>
                  : a.elem == DSA_ELEM_FP16 ? quant_kernel<DSA_ELEM_FP16, N>
                                            : quant_kernel<DSA_ELEM_FP32, N>;
-  k<<<blocks, 128, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_early(k, blocks, 128, stream, p);
   if (e != cudaSuccess) return cuda_fail(e, "quant_rows: launch", err);
   return DSA_OK;
 }
