@@ -8,16 +8,16 @@
 // is then one number, or two, a thread), while the MMAs fill the other buffer.
 //
 // Wide tiles (prompts): 256 rows x 256 columns by a CTA pair (cta_group::2; each CTA has 128 rows of a, 128 of b
-// and 128 x 256 sums), a ring of five 32-KB stages, one persistent pair per two SMs.  A block's MMAs, 512 cycles at
+// and 128 x 256 sums), a ring of four 32-KB stages, one persistent pair per two SMs.  A block's MMAs, 512 cycles at
 // the nominal rate, are issued and handed over in halves of 128 columns (one scale of b each), which leaves the sums
 // 768 cycles until a buffer is wanted back; a warp's products come from tensor memory a step of 32 columns ahead of its
 // multiply-adds, across blocks.  Two warps multiply the scales, eight blocks at a time.  Rows go out by TMA.
 // Bound: loads and MMAs alone run 4,096 x 7,168 x 16,384 in 250 us (3,850 TFLOP/s, at the power limit: 1,440 MHz
 // after a second of it); the multiply-adds, 256 of a block's cycles on the fp32 pipe, their hand-over and their power
-// make it 325 us (2,960 TFLOP/s; 370 us, 1,620 MHz, after a second).  With 512 columns in all a tile's end, 2,000 cycles,
-// is as long as its sums: 8,192 x 32,768 in 168 us.
-// Measured on the way: waits by suspension or by spinning alike; loads a row a lane of the scales by the sums
-// themselves 430 (each takes 32 lines of L1); halves of 96 columns (256 x 192) 390; sums that spill one register 510.
+// make it 312 us (3,080 TFLOP/s; 360 us, at some 1,650 MHz, after a second).  With 512 columns in all a tile's end (rounding,
+// boxes, TMA) is a third of the time: 8,192 x 32,768 in 163 us, 111 without it.
+// Measured on the way: waits by suspension or by spinning alike; the scales loaded by the sums themselves, a row a lane,
+// 430 (each load takes 32 lines of L1); tiles of 256 x 192 390; sums that spill a few registers 370 to 510.
 //
 // Narrow tiles (few rows): 128 rows x 32 to 128 columns a CTA.  A cluster of up to eight CTAs shares a tile's blocks, and
 // its parts are added in rank order through distributed shared memory: many CTAs stream the weights, the result does not
@@ -611,10 +611,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       if (!go) break;
       tc_fence_after();
       tmem_ld_x32(products(it), r0);
-#pragma unroll 1
-      for (int i = 0;; ++i) {
+#pragma unroll 2
+      for (int i = 0;; ++i) {   // (votes only where a wait has to wait: one more a block took 15 of 328 us)
         const int in = i & (kScaleBlocks - 1);
-        if (in == 0) go = mbar_wait(&ctl->scale_full[set & 1u], (set >> 1) & 1u, abort, p.status);
+        if (in == 0) {
+          go = mbar_wait(&ctl->scale_full[set & 1u], (set >> 1) & 1u, abort, p.status);
+          go = __all_sync(0xffffffffu, go);
+          if (!go) {
+            tmem_ld_wait();
+            break;
+          }
+        }
         const float f = scales[(set & 1u) * (2 * W::kScales) + in * kScalePitch];
         const uint64_t ff = pack2(f, f);
 #pragma unroll
@@ -643,15 +650,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         }
         sums.multiply_add(kSteps - 1, r1, ff);
         if (!ready) {
-          go = mbar_wait(full(it), (it >> 1) & 1u, abort, p.status) && go;
-          __syncwarp();
+          go = mbar_wait(full(it), (it >> 1) & 1u, abort, p.status);
+          go = __all_sync(0xffffffffu, go);
+          if (!go) break;
           tc_fence_after();
           tmem_ld_x32(products(it), r0);
-        }
-        go = __all_sync(0xffffffffu, go);
-        if (!go) {
-          tmem_ld_wait();
-          break;
         }
       }
       if (!go) break;
