@@ -47,7 +47,7 @@ constexpr int kGroupRows = 8;     // wide tiles of a column of tiles that run on
 struct Params {
   int M, N, blocks;
   int elem;
-  int vec;                 // rows of out start 16-byte aligned
+  int vec, even;           // rows of out start 16-byte aligned; on an even element
   int tiles_m, tiles_n;
   int a_box, stages;       // narrow: rows of a that are loaded, stages of the ring
   long long a_scale_stride, b_scale_stride, out_stride;
@@ -81,38 +81,84 @@ DSA_DEV uint32_t pack16(float a, float b) {
 }
 
 // `cols` outputs (at most 128) from column n on of rows m, m + step, ..., `some` of them and R at a time, value(r, c) the
-// c-th of the r-th, by a whole warp, a column a lane: for rows of out that start anywhere.  Bound by instructions: 4
-// bytes a lane, with the lines' ends apart, took 340 us for 4,096 x 20,001 bf16 of 512 columns.
+// c-th of the r-th and the one after it, by a whole warp: for rows of out that do not start 16-byte aligned.  A lane
+// stores a column, or two where rows start on an even element (and n is even).  Bound by instructions: 4 bytes a lane out of
+// rows that start anywhere, with the lines' ends apart, took 340 us for 4,096 x 20,001 bf16 of 512 columns against 141.
 template <int R, class Value>
 DSA_DEV void store_rows(const Params& p, int m, int step, int some, int n, int cols, Value&& value) {
   const int lane = threadIdx.x & 31;
-  auto each = [&](auto* out, auto&& rounded) {
+  const long long apart = (long long)step * p.out_stride;
+  auto singles = [&](auto* out, auto&& rounded) {
     auto* o = out + ((long long)m * p.out_stride + n + lane);
-    const long long apart = (long long)step * p.out_stride;
 #pragma unroll
     for (int c = 0; c < 128; c += 32) {
       if (c + lane >= cols) break;
       float x[R];
 #pragma unroll
-      for (int r = 0; r < R; ++r) x[r] = r < some ? value(r, c + lane) : 0.f;
+      for (int r = 0; r < R; ++r) x[r] = r < some ? value(r, c + lane, false).x : 0.f;
 #pragma unroll
       for (int r = 0; r < R; ++r)
         if (r < some) o[r * apart + c] = rounded(x[r]);
     }
   };
-  if (p.elem == DSA_ELEM_FP32)
-    each(reinterpret_cast<float*>(p.out), [](float x) { return x; });
-  else if (p.elem == DSA_ELEM_BF16)
-    each(reinterpret_cast<__nv_bfloat16*>(p.out), [](float x) { return __float2bfloat16_rn(x); });
-  else
-    each(reinterpret_cast<__half*>(p.out), [](float x) { return __float2half_rn(x); });
+  auto pairs = [&](auto* out, auto&& rounded) {
+    auto* o = out + (((long long)m * p.out_stride + n) / 2 + lane);
+#pragma unroll
+    for (int c = 0; c < 128; c += 64) {
+      if (c + 2 * lane >= cols) break;
+      float2 x[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) x[r] = r < some ? value(r, c + 2 * lane, true) : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r < some) o[r * (apart / 2) + c / 2] = rounded(x[r]);
+    }
+  };
+  if (p.even && (cols & 1) == 0) {
+    if (p.elem == DSA_ELEM_FP32)
+      pairs(reinterpret_cast<float2*>(p.out), [](float2 x) { return x; });
+    else if (p.elem == DSA_ELEM_BF16)
+      pairs(reinterpret_cast<uint32_t*>(p.out), [](float2 x) { return pack16<DSA_ELEM_BF16>(x.x, x.y); });
+    else
+      pairs(reinterpret_cast<uint32_t*>(p.out), [](float2 x) { return pack16<DSA_ELEM_FP16>(x.x, x.y); });
+  } else if (p.elem == DSA_ELEM_FP32) {
+    singles(reinterpret_cast<float*>(p.out), [](float x) { return x; });
+  } else if (p.elem == DSA_ELEM_BF16) {
+    singles(reinterpret_cast<__nv_bfloat16*>(p.out), [](float x) { return __float2bfloat16_rn(x); });
+  } else {
+    singles(reinterpret_cast<__half*>(p.out), [](float x) { return __float2half_rn(x); });
+  }
 }
 
 // Eight rows of 128 sums in shared memory, 16-byte piece i of row r at i ^ r, to rows m .. of out, columns n on.
 __device__ __noinline__ void store_eight(const Params& p, const uint8_t* rows, int m, int n) {
-  store_rows<8>(p, m, 1, p.M - m, n, min(128, p.N - n), [&](int r, int c) {
-    return *reinterpret_cast<const float*>(rows + r * 512 + (((c >> 2) ^ r) << 4) + (c & 3) * 4);
+  store_rows<8>(p, m, 1, p.M - m, n, min(128, p.N - n), [&](int r, int c, bool two) {
+    const float* x = reinterpret_cast<const float*>(rows + r * 512 + (((c >> 2) ^ r) << 4) + (c & 3) * 4);
+    return two ? *reinterpret_cast<const float2*>(x) : make_float2(*x, 0.f);
   });
+}
+
+// The share of CTA `rank` of a narrow tile's rows, from `cols` columns of the parts [128][pitch] of `splits` CTAs.
+__device__ __noinline__ void store_parts(const Params& p, const float* part, int pitch, int splits, int rank, int m0, int n0,
+                                         int cols) {
+  const int rows = min(kRows, p.M - m0), step = kThreads / 32 * splits;
+  for (int row = (int)(threadIdx.x >> 5) * splits + rank; row < rows; row += 4 * step)
+    store_rows<4>(p, m0 + row, step, (rows - row + step - 1) / step, n0, cols, [&](int r, int c, bool two) {
+      const float* from = part + (row + r * step) * pitch + c;
+      if (splits == 1) return make_float2(from[0], two ? from[1] : 0.f);
+      uint2 u[kMostSplits];
+#pragma unroll
+      for (int s = 0; s < kMostSplits; ++s)
+        if (s < splits) {
+          const uint32_t at = map_cluster(from, (uint32_t)s);
+          u[s] = two ? ld_cluster_v2(at) : make_uint2(ld_cluster_u32(at), 0u);
+        }
+      float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int s = 0; s < kMostSplits; ++s)
+        if (s < splits) v = add2(v, make_float2(__uint_as_float(u[s].x), __uint_as_float(u[s].y)));
+      return v;
+    });
 }
 
 // N values to element `at` of out on, `left` columns from the end of its row.
@@ -396,21 +442,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         store<4>(p, (long long)(m0 + row) * p.out_stride + n0 + col, p.N - n0 - col, &v.x);
       }
     } else {       // a share of the rows
-      const int cols = min(BN, p.N - n0), step = kThreads / 32 * splits;
-      for (int row = warp * splits + rank; row < rows; row += 4 * step)
-        store_rows<4>(p, m0 + row, step, (rows - row + step - 1) / step, n0, cols, [&](int r, int c) {
-          const float* from = part + (row + r * step) * kPitch + c;
-          if (splits == 1) return *from;
-          uint32_t u[kMostSplits];
-#pragma unroll
-          for (int s = 0; s < kMostSplits; ++s)
-            if (s < splits) u[s] = ld_cluster_u32(map_cluster(from, (uint32_t)s));
-          float v = 0.f;
-#pragma unroll
-          for (int s = 0; s < kMostSplits; ++s)
-            if (s < splits) v += __uint_as_float(u[s]);
-          return v;
-        });
+      store_parts(p, part, kPitch, splits, rank, m0, n0, min(BN, p.N - n0));
     }
   }
   drain(ctl);
@@ -800,6 +832,7 @@ dsa_status launch_matmul_fp8(const dsa_matmul_fp8_args& a, cudaStream_t stream, 
   p.elem = a.elem;
   const int size = a.elem == DSA_ELEM_FP32 ? 4 : 2;
   p.vec = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && (a.M == 1 || a.out_stride * size % 16 == 0);
+  p.even = (reinterpret_cast<uintptr_t>(a.out) & (2 * size - 1)) == 0 && (a.M == 1 || a.out_stride % 2 == 0);
   p.a_scale_stride = a.a_scale_stride;
   p.b_scale_stride = a.b_scale_stride;
   p.out_stride = a.out_stride;
@@ -839,6 +872,8 @@ dsa_status launch_matmul_fp8(const dsa_matmul_fp8_args& a, cudaStream_t stream, 
   cudaLaunchConfig_t cfg = {};
   CUtensorMap tm_out;
   if (w.wide) {
+    // (a TMA store writes 16 bytes where the row ends inside them)
+    p.vec = p.vec && (long long)a.N * size % 16 == 0;
     if (p.vec && !encode_tmap_2d(&tm_out, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, a.out,
                                  (uint64_t)a.N, (uint64_t)a.M, a.M == 1 ? ((uint64_t)a.N * size + 15) / 16 * 16 : (uint64_t)a.out_stride * size, 64 / size, 32,
                                  CU_TENSOR_MAP_SWIZZLE_64B, err))

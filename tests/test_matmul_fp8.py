@@ -422,3 +422,19 @@ def test_wide_and_narrow_calls_at_once(cuda_lib):
                 got.append(dsa.matmul_fp8(*c))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want[i % 4]) for i, o in enumerate(got))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(2300, 2562, 400), (2300, 2566, 272), (100, 7166, 272), (9, 2110, 7168), (33, 258, 640)])
+def test_rows_of_out_that_start_on_even_elements(cuda_lib, m, n, k):
+    """Rows that are not 16-byte aligned, with an even and with an odd number of columns inside an even stride."""
+    a, a_scale, b, b_scale = whole(m, n, k, gen(m, n))
+    want = definition(a, a_scale, b, b_scale)[0].float()
+    for dtype in TYPES:
+        for cols in (n, n - 1):
+            for left in (0, 2, 1):
+                out = torch.full((m, n + 2 + (n & 1)), 5.0, dtype=dtype, device="cuda")
+                dsa.matmul_fp8(a, a_scale, b[:cols], b_scale[:-(-cols // 128)], out=out[:, left:left + cols])
+                assert torch.equal(out[:, left:left + cols], want[:, :cols].to(dtype)), (dtype, cols, left)
+                out[:, left:left + cols] = 5.0
+                assert torch.all(out == 5.0)
