@@ -9,8 +9,13 @@
 //
 // Every byte moves once: a row stays in registers between the sum and the quantisation.  A lane has a unit of 32 columns,
 // four pieces of eight 32 apart, so that a group is four lanes: its maximum, scale and reciprocal are paid once for 32
-// columns.  A row of up to 1,024 columns is 4 to 32 lanes of a warp, a longer one a block; its warps' sums meet in shared
-// memory, where one warp makes r of them for all.
+// columns (sixteen a lane: 240 us for 16,384 rows of 7,168 bf16 with residual, 54 for 4,095 rows of 16,384).  A row of up to
+// 1,024 columns is 4 to 32 lanes of a warp, a longer one a block; its warps' sums meet in shared memory, where one warp
+// makes r of them for all.
+//
+// Bound by HBM with a residual (16,384 rows of 7,168 bf16 in 123 us in a run of calls, 6.7 TB/s) and with 32-bit rows
+// (4,095 of 16,384 in 49 us, 6.9 TB/s); by instruction issue without one (16,384 of 7,168 bf16 in 89 us, 4.0 TB/s; rows as
+// they are, 4,095 of 16,384 bf16, in 34 us, 5.9 TB/s): a conversion takes two roundings of every value (see quant.cuh).
 #include "dsa_internal.h"
 #include "quant.cuh"
 
