@@ -39,9 +39,9 @@ constexpr int kWideThreads = 384; // of a wide one: 10 and 11 multiply the scale
 constexpr int kScaleBlocks = 8;   // blocks whose scales are multiplied at a time
 constexpr int kScalePitch = kRows + 4;   // floats from one block's to the next
 constexpr int kBlock = 128;       // columns of a scale block: a row of a stage
-constexpr int kMostStages = 16;
+constexpr int kMostStages = 32;
 constexpr int kMostSplits = 8;    // CTAs of a portable cluster
-constexpr int kRing = 96 * 1024;  // of a narrow CTA
+constexpr int kRing = 96 * 1024;  // of a narrow CTA that shares its SM, and half of one's that has it alone
 constexpr int kGroupRows = 8;     // wide tiles of a column of tiles that run one after the other
 
 struct Params {
@@ -49,7 +49,7 @@ struct Params {
   int elem;
   int vec, even;           // rows of out start 16-byte aligned; on an even element
   int tiles_m, tiles_n;
-  int a_box, stages;       // narrow: rows of a that are loaded, stages of the ring
+  int a_box, stages, ring; // narrow: rows of a that are loaded, stages and bytes of the ring
   long long a_scale_stride, b_scale_stride, out_stride;
   const float* a_scale;
   const float* b_scale;
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   static_assert(kRows * kPitch * 4 <= kRing, "parts of a tile");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  Ctl* ctl = reinterpret_cast<Ctl*>(smem + kRing);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + p.ring);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   volatile int* abort = &ctl->abort;
   const int splits = (int)cluster_nrank(), rank = (int)cluster_rank();
@@ -848,7 +848,10 @@ dsa_status launch_matmul_fp8(const dsa_matmul_fp8_args& a, cudaStream_t stream, 
   p.tiles_m = (int)(((long long)a.M + rows - 1) / rows);
   p.tiles_n = (int)(((long long)a.N + w.bn - 1) / w.bn);
   p.a_box = w.wide ? kRows : std::min(kRows, (a.M + 7) / 8 * 8);
-  p.stages = w.wide ? 0 : std::min(kMostStages, kRing / ((p.a_box + w.bn) * kBlock));
+  // (128 x 7,168 x 7,168, 150 CTAs: 16.7 -> 15.6 us; clusters of eight, of which an SM's group holds two with one CTA an SM:
+  // 17 of them 9.5 -> 12.5 us, so not with more than two splits)
+  p.ring = w.splits <= 2 && (long long)p.tiles_m * p.tiles_n * w.splits <= dev.sm_count ? 2 * kRing : kRing;
+  p.stages = w.wide ? 0 : std::min(kMostStages, p.ring / ((p.a_box + w.bn) * kBlock));
   CUtensorMap tm_a, tm_b;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
@@ -862,9 +865,9 @@ dsa_status launch_matmul_fp8(const dsa_matmul_fp8_args& a, cudaStream_t stream, 
                               : w.bn == 96 ? narrow_kernel<3>
                                            : narrow_kernel<4>;
   const void* k = w.wide ? reinterpret_cast<const void*>(wide_kernel) : reinterpret_cast<const void*>(narrow);
-  const int smem = w.wide ? Wide::total + 1024 : kRing + 1024 + 1024;
+  const int smem = w.wide ? Wide::total + 1024 : p.ring + 1024 + 1024;
   static std::atomic<uint64_t> done[5];
-  cudaError_t e = allow_smem(k, smem, dev.device, done[w.wide ? 0 : w.bn / 32]);
+  cudaError_t e = allow_smem(k, w.wide ? smem : 2 * kRing + 1024 + 1024, dev.device, done[w.wide ? 0 : w.bn / 32]);
   if (e != cudaSuccess) return cuda_fail(e, "matmul_fp8: set shared memory size", err);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

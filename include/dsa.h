@@ -373,7 +373,8 @@ typedef struct {
 
 dsa_status dsa_rms_norm_quant(const dsa_rms_norm_quant_args* args, dsa_stream_t stream);
 
-/* Rows as they are into 8-bit rows.  Supported: dim a multiple of 8; rows of x 16-byte, of codes 8-byte aligned. */
+/* Rows as they are into 8-bit rows.  Supported: dim a multiple of 8; rows of x 16-byte, of codes 8-byte aligned; n_rows
+ * times ceil(dim / 128) below 2^29. */
 typedef struct {
   int n_rows;
   int dim;

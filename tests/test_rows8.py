@@ -352,3 +352,9 @@ def test_rows_on_another_stream_and_in_a_graph(cuda_lib):
         graph.replay()
         c, s, total = dsa.rms_norm_quant(x, w, residual=total)
         assert torch.equal(r, total) and torch.equal(codes.view(torch.uint8), c.view(torch.uint8)) and torch.equal(scale, s)
+
+
+def test_more_groups_than_a_launch_numbers_are_refused():
+    lib = dsa.load()
+    a = _rows(n_rows=1 << 27, dim=576)
+    assert lib.dsa_quant_rows(ctypes.byref(a), None) == dsa.DSA_ERR_UNSUPPORTED and "2^29" in dsa.last_error()
