@@ -193,15 +193,6 @@ DSA_DEV bool mbar_wait_fast(uint64_t* bar, uint32_t parity, volatile int* abort,
   return mbar_test(bar, parity) || mbar_wait_slow(bar, parity, abort, status);
 }
 
-// As mbar_wait_fast, with up to 32 tests before the call: for hand-overs of some hundred cycles that the wake-up
-// of a suspended thread would lengthen.
-DSA_DEV bool mbar_spin(uint64_t* bar, uint32_t parity) {
-#pragma unroll 1
-  for (int i = 0; i < 32; ++i)
-    if (mbar_test(bar, parity)) return true;
-  return false;
-}
-
 // Bounded wait of a whole warp, which is converged again after it.
 DSA_DEV void warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
   mbar_wait_fast(bar, parity, abort, status);
