@@ -413,13 +413,17 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   }
+  drain(ctl);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  // Tensor memory goes before any other CTA is waited for: a CTA that holds some never waits for one that may itself
+  // wait for some, on an SM that it shares with another kernel's cluster.
+  if (warp == 8) tmem_dealloc(tmem, 2 * kBuf);
   __syncwarp();
   if (!direct) {
     // ---------------- the parts of a tile: each CTA adds up those of its share, in rank order
-    if (splits > 1)
-      cluster_sync();
-    else
-      __syncthreads();
+    if (splits > 1) cluster_sync();
     const int rows = min(kRows, p.M - m0);
     if (p.vec) {   // a share of the columns, four at a time
       const int quads = BN / 4 / splits, items = rows * quads;
@@ -445,12 +449,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       store_parts(p, part, kPitch, splits, rank, m0, n0, min(BN, p.N - n0));
     }
   }
-  drain(ctl);
   __syncwarp();
-  tc_fence_before();
-  __syncthreads();
   if (splits > 1) cluster_sync();   // no CTA's parts go before all have read them
-  if (warp == 8) tmem_dealloc(tmem, 2 * kBuf);
 }
 
 // ---------------------------------------------------------------- wide tiles

@@ -438,3 +438,26 @@ def test_rows_of_out_that_start_on_even_elements(cuda_lib, m, n, k):
                 assert torch.equal(out[:, left:left + cols], want[:, :cols].to(dtype)), (dtype, cols, left)
                 out[:, left:left + cols] = 5.0
                 assert torch.all(out == 5.0)
+
+
+@pytest.mark.gpu
+def test_products_beside_the_indexer(cuda_lib):
+    """Narrow products, whose CTAs share SMs, and the indexer, whose clusters hold tensor memory too, on two streams."""
+    import dsa_inputs as di
+    wl = di.small("decode_32k_fp8", seq_lens=[2000] * 24, n_new=[4] * 24)
+    inp = di.to_device(di.generate(wl), "cuda")
+    li = lambda: dsa.li_topk(inp["q_li"], inp["w"], inp["k_pool"], inp["pt_k"], inp["seq_lens"], inp["q_start"], wl.K,
+                             q_scale=inp["q_scale"], k_scale=inp["k_scale"], max_seq_len=2000, max_q_per_seq=4)[0]
+    case = whole(9, 2112, 7168, gen(1))
+    idx, out = li(), dsa.matmul_fp8(*case)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(30):
+        with torch.cuda.stream(streams[0]):
+            a = li()
+        with torch.cuda.stream(streams[1]):
+            b = dsa.matmul_fp8(*case)
+        got.append((a, b))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, idx) and torch.equal(b, out) for a, b in got)
