@@ -673,14 +673,20 @@ def _row_stride(name, t, dtype, rows, cols, device):
 
 
 def _rows_in(x):
-    """(rows, columns, element type) of rows that are quantised, on the current device."""
-    if x.dim() != 2:
-        raise ValueError("x must have shape [n, dim] (got %s)" % (tuple(x.shape),))
+    """(rows, columns, element type, elements from row to row, device) of rows that are quantised, on the current
+    device."""
     elem = _ELEM.get(x.dtype)
     if elem is None:
         raise ValueError("x must be bf16, fp16 or fp32 (got %s)" % x.dtype)
-    _on_current(x.device)
-    return x.shape[0], x.shape[1], elem
+    shape, device = x.shape, x.device
+    if len(shape) != 2:
+        raise ValueError("x must have shape [n, dim] (got %s)" % (tuple(shape),))
+    _on_current(device)
+    n, dim = shape
+    stride, step = x.stride()
+    if n > 1 and stride < dim or dim > 1 and n > 0 and step != 1:
+        raise ValueError("the columns of x must be adjacent, and its rows apart")
+    return n, dim, elem, stride if n > 1 else dim, device
 
 
 def _on_current(device):
@@ -690,21 +696,20 @@ def _on_current(device):
         raise ValueError("tensors are on %s, the current device is cuda:%d" % (device, torch.cuda.current_device()))
 
 
-def _rows8_out(a, codes, scale, n, dim, device, stream):
-    """The 8-bit rows that a call writes, new ones where None is given; their addresses and strides go into ``a``.
-    (What is new needs no checks, which take 2 us a tensor.)"""
+def _rows8_out(codes, scale, n, dim, device, stream):
+    """(codes, their stride, scale, its stride) of the 8-bit rows that a call writes, new ones where None is given.
+    (What is new needs no checks.)"""
     groups = (dim + 127) // 128
-    a.codes_stride, a.scale_stride = dim, groups
+    codes_stride, scale_stride = dim, groups
     if codes is None:
         codes = _empty(stream, (n, dim), torch.float8_e4m3fn, device)
     else:
-        a.codes_stride = _row_stride("codes", codes, torch.float8_e4m3fn, n, dim, device)
+        codes_stride = _row_stride("codes", codes, torch.float8_e4m3fn, n, dim, device)
     if scale is None:
         scale = _empty(stream, (n, groups), torch.float32, device)
     else:
-        a.scale_stride = _row_stride("scale", scale, torch.float32, n, groups, device)
-    a.codes, a.scale = codes.data_ptr(), scale.data_ptr()
-    return codes, scale
+        scale_stride = _row_stride("scale", scale, torch.float32, n, groups, device)
+    return codes, codes_stride, scale, scale_stride
 
 
 def rms_norm_quant(x, weight, *, eps=1e-6, residual=None, residual_out=None, codes=None, scale=None, y=None,
@@ -715,29 +720,30 @@ def rms_norm_quant(x, weight, *, eps=1e-6, residual=None, residual_out=None, cod
     ``weight`` [dim] has x's type or is fp32; ``y`` [n, dim] takes the normed rows in x's type too.  All rows may be
     strided, their columns adjacent.  ``codes`` and ``scale`` are what matmul_fp8 takes."""
     lib = load()
-    n, dim, elem = _rows_in(x)
-    device, dtype = x.device, x.dtype
+    n, dim, elem, x_stride, device = _rows_in(x)
+    dtype = x.dtype
     if weight.dtype is not dtype and weight.dtype is not torch.float32:
         raise ValueError("weight must be %s or fp32 (got %s)" % (dtype, weight.dtype))
     if weight.shape != (dim,) or weight.get_device() != device.index or not weight.is_contiguous():
         raise ValueError("weight must be contiguous, on %s and have shape (%d,)" % (device, dim))
-    if residual is None and residual_out is not None:
-        raise ValueError("residual_out goes with residual")
-    a = RmsNormQuantArgs()
-    a.n_rows, a.dim, a.elem, a.weight_elem, a.eps = n, dim, elem, _ELEM[weight.dtype], float(eps)
-    a.x_stride, a.x, a.weight = _row_stride("x", x, dtype, n, dim, device), x.data_ptr(), weight.data_ptr()
-    codes, scale = _rows8_out(a, codes, scale, n, dim, device, stream)
+    codes, codes_stride, scale, scale_stride = _rows8_out(codes, scale, n, dim, device, stream)
+    residual_stride = sum_stride = y_stride = dim
     if residual is not None:
-        a.residual_stride, a.residual = _row_stride("residual", residual, dtype, n, dim, device), residual.data_ptr()
-        a.sum_stride = dim
+        residual_stride = _row_stride("residual", residual, dtype, n, dim, device)
         if residual_out is None:
             residual_out = _empty(stream, (n, dim), dtype, device)
         else:
-            a.sum_stride = _row_stride("residual_out", residual_out, dtype, n, dim, device)
-        a.sum = residual_out.data_ptr()
+            sum_stride = _row_stride("residual_out", residual_out, dtype, n, dim, device)
+    elif residual_out is not None:
+        raise ValueError("residual_out goes with residual")
     if y is not None:
-        a.y_stride, a.y = _row_stride("y", y, dtype, n, dim, device), y.data_ptr()
-    _check(lib.dsa_rms_norm_quant(ctypes.byref(a), _launch_stream(stream, device)), "dsa_rms_norm_quant")
+        y_stride = _row_stride("y", y, dtype, n, dim, device)
+    a = RmsNormQuantArgs(n, dim, elem, _ELEM[weight.dtype], float(eps), x_stride, residual_stride, sum_stride, y_stride,
+                         codes_stride, scale_stride, x.data_ptr(), weight.data_ptr(), _addr(residual),
+                         _addr(residual_out), _addr(y), codes.data_ptr(), scale.data_ptr())
+    code = lib.dsa_rms_norm_quant(ctypes.byref(a), _launch_stream(stream, device))
+    if code:
+        _check(code, "dsa_rms_norm_quant")
     return (codes, scale) if residual is None else (codes, scale, residual_out)
 
 
@@ -745,13 +751,13 @@ def quant_rows(x, *, codes=None, scale=None, stream=None):
     """Rows x [n, dim] (bf16, fp16 or fp32; they may be strided, their columns adjacent) into 8-bit rows: (codes
     [n, dim] e4m3, scale [n, ceil(dim / 128)] fp32), what matmul_fp8 takes."""
     lib = load()
-    n, dim, elem = _rows_in(x)
-    device = x.device
-    a = QuantRowsArgs()
-    a.n_rows, a.dim, a.elem = n, dim, elem
-    a.x_stride, a.x = _row_stride("x", x, x.dtype, n, dim, device), x.data_ptr()
-    codes, scale = _rows8_out(a, codes, scale, n, dim, device, stream)
-    _check(lib.dsa_quant_rows(ctypes.byref(a), _launch_stream(stream, device)), "dsa_quant_rows")
+    n, dim, elem, x_stride, device = _rows_in(x)
+    codes, codes_stride, scale, scale_stride = _rows8_out(codes, scale, n, dim, device, stream)
+    a = QuantRowsArgs(n, dim, elem, x_stride, codes_stride, scale_stride, x.data_ptr(), codes.data_ptr(),
+                      scale.data_ptr())
+    code = lib.dsa_quant_rows(ctypes.byref(a), _launch_stream(stream, device))
+    if code:
+        _check(code, "dsa_quant_rows")
     return codes, scale
 
 
@@ -761,10 +767,11 @@ def matmul_fp8(a, a_scale, b, b_scale, *, out=None, dtype=torch.bfloat16, status
     ``dtype``.  K is a multiple of 16.  All rows may be strided, their columns adjacent: ``a`` and ``a_scale`` can be
     views of the rows of an FP8 latent cache."""
     lib = load()
-    if a.dim() != 2 or b.dim() != 2:
+    a_shape, b_shape = a.shape, b.shape
+    if len(a_shape) != 2 or len(b_shape) != 2:
         raise ValueError("a is [M, K], b is [N, K]")
-    M, K = a.shape
-    N, blocks = b.shape[0], (K + 127) // 128
+    M, K = a_shape
+    N, blocks = b_shape[0], (K + 127) // 128
     device = a.device
     _on_current(device)
     elem = _ELEM.get(dtype if out is None else out.dtype)
@@ -772,20 +779,19 @@ def matmul_fp8(a, a_scale, b, b_scale, *, out=None, dtype=torch.bfloat16, status
         raise ValueError("out must be bf16, fp16 or fp32 (got %s)" % (dtype if out is None else out.dtype))
     if status is not None:
         _fits(device, ("status", status, torch.int32, None))
-    g = MatmulFp8Args()
-    g.M, g.N, g.K, g.elem = M, N, K, elem
-    g.a_stride, g.a = _row_stride("a", a, torch.float8_e4m3fn, M, K, device), a.data_ptr()
-    g.a_scale_stride, g.a_scale = _row_stride("a_scale", a_scale, torch.float32, M, blocks, device), a_scale.data_ptr()
-    g.b_stride, g.b = _row_stride("b", b, torch.float8_e4m3fn, N, K, device), b.data_ptr()
-    g.b_scale_stride = _row_stride("b_scale", b_scale, torch.float32, (N + 127) // 128, blocks, device)
-    g.b_scale = b_scale.data_ptr()
+    a_stride = _row_stride("a", a, torch.float8_e4m3fn, M, K, device)
+    a_scale_stride = _row_stride("a_scale", a_scale, torch.float32, M, blocks, device)
+    b_stride = _row_stride("b", b, torch.float8_e4m3fn, N, K, device)
+    b_scale_stride = _row_stride("b_scale", b_scale, torch.float32, (N + 127) // 128, blocks, device)
     if out is None:
-        out, g.out_stride = _empty(stream, (M, N), dtype, device), N
+        out, out_stride = _empty(stream, (M, N), dtype, device), N
     else:
-        g.out_stride = _row_stride("out", out, out.dtype, M, N, device)
-    g.out = out.data_ptr()
-    g.status = _addr(status)
-    _check(lib.dsa_matmul_fp8(ctypes.byref(g), _launch_stream(stream, device)), "dsa_matmul_fp8")
+        out_stride = _row_stride("out", out, out.dtype, M, N, device)
+    g = MatmulFp8Args(M, N, K, elem, a_stride, a_scale_stride, b_stride, b_scale_stride, out_stride, a.data_ptr(),
+                      a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr(), _addr(status))
+    code = lib.dsa_matmul_fp8(ctypes.byref(g), _launch_stream(stream, device))
+    if code:
+        _check(code, "dsa_matmul_fp8")
     return out
 
 
