@@ -665,7 +665,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         }
         tmem_ld_wait_for<32>(r1);
         tc_fence_before();
-        mbar_arrive_pair_by(sum_free + (it & 1u) * 16, lane == 0);   // (the loads' wait is the whole warp's)
+        __syncwarp();   // (lane 0 arrives for all: after their reads of the products and of the scales)
+        mbar_arrive_pair_by(sum_free + (it & 1u) * 16, lane == 0);
         if (in == kScaleBlocks - 1 || i + 1 == p.blocks) {
           if (lane == 0) mbar_arrive(&ctl->scale_free[set & 1u]);
           ++set;

@@ -461,3 +461,15 @@ def test_products_beside_the_indexer(cuda_lib):
         got.append((a, b))
     torch.cuda.synchronize()
     assert all(torch.equal(a, idx) and torch.equal(b, out) for a, b in got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(2300, 2560, 9232), (700, 7000, 16384)])
+def test_scales_of_long_rows_in_wide_tiles(cuda_lib, m, n, k):
+    """Many sets of eight blocks' scales, each in the place of one that all warps must have read; again and again.
+    (Terms are multiples of 2^-2 and at most 9 * 4, so sums of 16,384 are below 2^24 of them: exact.)"""
+    assert dsa.load_testhooks().dsa_test_matmul_plan(m, n, k, 152) == 0
+    case = whole(m, n, k, gen(m, n, k))
+    want = definition(*case)[0].float()
+    for _ in range(10):
+        assert torch.equal(dsa.matmul_fp8(*case, dtype=torch.float32), want)
