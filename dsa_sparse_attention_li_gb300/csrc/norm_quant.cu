@@ -225,7 +225,20 @@ __global__ void __launch_bounds__(kMost, kMost == kFew<DSA_ELEM_BF16> ? 2 : 1) n
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[4 * k + i] = mul2(h[4 * k + i], f[i]);
   }
-  const float a = group_max(h), top = a * r.x;
+  float a = group_max(h), top = a * r.x;
+  // v is beyond fp32 where h w is not: the largest of the others.  (By the whole warp: groups alone cost registers.)
+  if (__any_sync(0xffffffffu, top == INFINITY)) {
+    a = 0.f;
+#pragma unroll
+    for (int i = 0; i < kUnit / 2; ++i) {
+      const float2 two = unpack2(h[i]);
+      a = fmaxf(a, fabsf(two.x) * r.x < INFINITY ? fabsf(two.x) : 0.f);
+      a = fmaxf(a, fabsf(two.y) * r.x < INFINITY ? fabsf(two.y) : 0.f);
+    }
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    top = a * r.x;
+  }
   float s = 1.f;
   if (top > 0.f) {
     const float q = __fdiv_rn(top, 448.f), e = fmaf(a, r.x, -top) + a * r.y;

@@ -347,7 +347,10 @@ typedef enum { DSA_ELEM_BF16 = 0, DSA_ELEM_FP16 = 1, DSA_ELEM_FP32 = 2 } dsa_ele
  *   h = T(x + residual)  (h = x without a residual),   stored to sum
  *   r = 1 / sqrt(mean(h^2) + eps),   v[d] = h[d] * weight[d] * r   -> codes, scale, and T(v) -> y
  * mean(h^2) and r are held in fp32: a row whose sum of squares is beyond fp32 has r = 0, one with a NaN is all
- * NaN.  h * weight is rounded to fp32 (exact for 16-bit types); v itself is not rounded before it is quantised.
+ * NaN; squares below 2^-126 keep fewer bits and those below 2^-150 none, so that without eps a row that has no other
+ * is taken as a row of zeros, r = infinity.  h * weight is rounded to fp32 (exact for 16-bit types within its normal
+ * range); v itself is not rounded before it is quantised, but counts as infinite where it is beyond fp32 (it
+ * saturates, and its group's scale is that of the others) and is rounded below fp32's normal range.
  *
  * sum and y may be x or residual themselves (same address and stride); outputs overlap nothing else.  Supported:
  * dim a multiple of 8, up to 32768; weight of T or fp32; rows of x, residual, sum, y and weight 16-byte aligned,

@@ -358,3 +358,74 @@ def test_more_groups_than_a_launch_numbers_are_refused():
     lib = dsa.load()
     a = _rows(n_rows=1 << 27, dim=576)
     assert lib.dsa_quant_rows(ctypes.byref(a), None) == dsa.DSA_ERR_UNSUPPORTED and "2^29" in dsa.last_error()
+
+
+LARGEST = torch.finfo(torch.float32).max
+
+
+def check_beyond_fp32(x, w, eps, codes, scale, y, off=OFF):
+    """Codes and scales where some values are beyond fp32: they count as infinite, saturate and leave the others of
+    their group alone.  `off`: what the scale may be off by, beside OFF of the quotients."""
+    h, d = x.double(), x.shape[1]
+    v = h * w.double() / torch.sqrt((h * h).mean(1, keepdim=True) + eps)
+    assert torch.all((v.abs() / LARGEST - 1).abs() > 2.0 ** -16)   # (none that a rounding could take across)
+    beyond = v.abs() > LARGEST
+    v = torch.where(beyond, torch.copysign(torch.full_like(v, math.inf), v), v)
+    want = group_scales(v).double()
+    assert torch.all((scale.double() - want).abs() <= want * off)
+    q = v / columns(want, d)
+    low, sign = nearest_code(torch.copysign((q.abs() * (1 - OFF)).clamp(min=0), q))
+    high, _ = nearest_code(q.abs() * (1 + OFF))
+    raw = codes.view(torch.uint8).long()
+    assert torch.all(((raw & 127) >= low) & ((raw & 127) <= high) & ((raw >> 7) == sign.long()))
+    assert torch.all(y.isinf()[beyond]) and not y.isnan().any()
+    return beyond
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [256, 4096])
+@pytest.mark.parametrize("dtype,wtype", [(torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32),
+                                         (torch.float16, torch.float32), (torch.float32, torch.float32)], ids=str)
+def test_norm_of_values_beyond_fp32(cuda_lib, dtype, wtype, d):
+    """Weights near fp32's largest value, whose products with h are finite and whose products with h r are not: in some
+    columns of a group, in all of them, and in none."""
+    g = torch.Generator().manual_seed(d)
+    x = (0.25 * torch.randn((7, d), generator=g)).to(dtype)
+    x[3, :128] = 0.5            # (r is some 3.7 there)
+    x[3, 64:128] = -0.5
+    w = torch.ones(d)
+    w[:128] = 3.2e38            # |h| below 1: h w is finite
+    w[128:192:3] = 1e38
+    w = w.to(wtype)
+    x[:, :192] = x[:, :192].clamp(-0.96875, 0.96875)
+    y = torch.empty_like(x, device="cuda")
+    codes, scale = dsa.rms_norm_quant(x.cuda(), w.cuda(), eps=1e-6, y=y)
+    beyond = check_beyond_fp32(x, w, 1e-6, codes.cpu(), scale.cpu(), y.cpu())
+    assert beyond[3, :128].all() and beyond[0, :128].any() and not beyond[0, :128].all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [256, 4096])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+def test_norm_without_epsilon_of_rows_whose_squares_are_below_fp32(cuda_lib, dtype, d):
+    """Squares of 2^-200 and 2^-152 .. 2^-150 round to 0: r is infinite, as of a row of zeros, so every value is infinite,
+    or NaN in a column of zeros.  Squares of 2^-140 keep some bits: d of them, each off by 2^-150 at most, the mean by as
+    much again twice over, so that 1 / sqrt is off by half of 3 * 2^-10 and a scale by less than 2^-9; r is one for the row,
+    so the quotients are as close as ever."""
+    g = torch.Generator().manual_seed(d + 2)
+    ones = torch.ones(d).to(dtype)
+    sign = torch.where(torch.rand((4, d), generator=g) < 0.5, -1.0, 1.0)
+    mantissa = (1 + torch.randint(0, 125, (4, d), generator=g) / 128).double()
+    x = sign * mantissa * torch.tensor([2.0 ** -100, 2.0 ** -76, 2.0 ** -70, 1.0], dtype=torch.float64)[:, None]
+    x = x.to(dtype)
+    x[0, 5], x[1, 200] = 0.0, -0.0
+    y = torch.empty_like(x, device="cuda")
+    codes, scale = (t.cpu() for t in dsa.rms_norm_quant(x.cuda(), ones.cuda(), eps=0.0, y=y))
+    y, raw = y.cpu(), codes.view(torch.uint8).long()
+    zero = x[:2] == 0
+    assert torch.all(scale[:2] == 1.0)
+    assert torch.all((raw[:2] & 127) == torch.where(zero, 127, 126)) and torch.equal(y[:2].isnan(), zero)
+    assert torch.all((raw[:2] >> 7 == torch.signbit(x[:2]).long()) | zero) and torch.all(y[:2].isinf() | zero)
+    for row, off in ((2, 2.0 ** -9), (3, OFF)):
+        at = slice(row, row + 1)
+        assert not check_beyond_fp32(x[at], ones, 0.0, codes[at], scale[at], y[at], off).any()
