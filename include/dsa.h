@@ -396,8 +396,9 @@ dsa_status dsa_quant_rows(const dsa_quant_rows_args* args, dsa_stream_t stream);
  * Product of 8-bit rows with e4m3 weights that have one fp32 scale per block of 128 rows and 128 columns:
  *   out[m][n] = sum_i fp32(a_scale[m][i] * b_scale[n / 128][i]) * sum_{k in columns of block i} a[m][k] * b[n][k]
  * for i < ceil(K / 128).  A block's products are added by the tensor cores with fp32 accumulators, the blocks'
- * sums with fp32 multiply-adds, and the result is rounded once to the type of out.  A NaN or an infinity in a row
- * of either operand (or in its scales) reaches the outputs of that row alone.
+ * sums with fp32 multiply-adds, and the result is rounded once to the type of out.  A NaN in a row of either operand,
+ * or a NaN or an infinity in a scale, reaches the outputs of the rows that it belongs to alone: one row of out for a
+ * row of a, one column for a row of b, the 128 columns of its block for a scale of b.
  *
  * a may be the rows of an FP8 latent cache as they lie there (a_stride 608, a_scale 576 bytes on, a_scale_stride
  * 152): the up-projection of dsa_mla_prefill's keys and values reads no converted copy.

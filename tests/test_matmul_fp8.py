@@ -473,3 +473,14 @@ def test_scales_of_long_rows_in_wide_tiles(cuda_lib, m, n, k):
     want = definition(*case)[0].float()
     for _ in range(10):
         assert torch.equal(dsa.matmul_fp8(*case, dtype=torch.float32), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(1, 300, 400), (130, 2112, 1040), (2300, 2560, 896)])
+def test_a_scale_of_b_that_is_not_finite_reaches_its_128_columns(cuda_lib, m, n, k):
+    a, a_scale, b, b_scale = whole(m, n, k, gen(m, n))
+    clean = dsa.matmul_fp8(a, a_scale, b, b_scale, dtype=torch.float32)
+    b_scale[1, 2] = math.nan
+    got = dsa.matmul_fp8(a, a_scale, b, b_scale, dtype=torch.float32)
+    assert torch.all(got[:, 128:256].isnan())
+    assert torch.equal(got[:, :128], clean[:, :128]) and torch.equal(got[:, 256:], clean[:, 256:])
