@@ -352,9 +352,10 @@ typedef enum { DSA_ELEM_BF16 = 0, DSA_ELEM_FP16 = 1, DSA_ELEM_FP32 = 2 } dsa_ele
  * range); v itself is not rounded before it is quantised, but counts as infinite where it is beyond fp32 (it
  * saturates, and its group's scale is that of the others) and is rounded below fp32's normal range.
  *
- * sum and y may be x or residual themselves (same address and stride); outputs overlap nothing else.  Supported:
- * dim a multiple of 8, up to 32768; weight of T or fp32; rows of x, residual, sum, y and weight 16-byte aligned,
- * those of codes 8-byte aligned.
+ * sum and y may be x or residual themselves (same address and stride); outputs overlap nothing else.  Launched as a
+ * programmatic dependent, as dsa_sfa_decode is (see above).  Supported: dim a multiple of 8, up to 32768; weight of T
+ * or fp32; rows of x, residual, sum, y and weight 16-byte aligned, those of codes 8-byte aligned; strides (of more than
+ * one row) from the row's length up to 2^40.
  */
 typedef struct {
   int n_rows;
@@ -376,8 +377,9 @@ typedef struct {
 
 dsa_status dsa_rms_norm_quant(const dsa_rms_norm_quant_args* args, dsa_stream_t stream);
 
-/* Rows as they are into 8-bit rows.  Supported: dim a multiple of 8; rows of x 16-byte, of codes 8-byte aligned; n_rows
- * times ceil(dim / 128) below 2^29. */
+/* Rows as they are into 8-bit rows.  Launched as a programmatic dependent, as dsa_sfa_decode is (see above).  Supported:
+ * dim a multiple of 8, up to 2^30; rows of x 16-byte, of codes 8-byte aligned; n_rows times ceil(dim / 128) below 2^29;
+ * strides as above. */
 typedef struct {
   int n_rows;
   int dim;
@@ -404,10 +406,12 @@ dsa_status dsa_quant_rows(const dsa_quant_rows_args* args, dsa_stream_t stream);
  * 152): the up-projection of dsa_mla_prefill's keys and values reads no converted copy.
  *
  * Few rows stream the weights, many run on tiles of 256 x 256; each output is added up in an order that
- * depends on the sizes alone, so that a call gives the same bits every time.  Rows of out that start 16-byte
+ * depends on the sizes and the GPU's number of SMs alone, so that a call gives the same bits every time.  Rows of out that start 16-byte
  * aligned are stored fastest.  Launched as a programmatic dependent, as dsa_sfa_decode is (see above).
  *
- * Supported: K a multiple of 16; any M and N; rows of a and b 16-byte aligned; out overlaps no input.
+ * Supported: K a multiple of 16; M, N and K up to 2^31 - 256, and M times N in no more than 0x70000000 tiles of
+ * 256 x 256; rows of a and b 16-byte aligned; rows (of more than one) at least their length and less than 2^40 bytes
+ * apart; out overlaps no input.
  */
 typedef struct {
   int M, N, K;

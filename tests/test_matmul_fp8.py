@@ -484,3 +484,10 @@ def test_a_scale_of_b_that_is_not_finite_reaches_its_128_columns(cuda_lib, m, n,
     got = dsa.matmul_fp8(a, a_scale, b, b_scale, dtype=torch.float32)
     assert torch.all(got[:, 128:256].isnan())
     assert torch.equal(got[:, :128], clean[:, :128]) and torch.equal(got[:, 256:], clean[:, 256:])
+
+
+@pytest.mark.parametrize("over", [{"N": 2 ** 31 - 255}, {"K": 2 ** 31 - 128}])
+def test_limits_of_the_header_are_refused(over):
+    """(More tiles than a launch numbers are refused after the device is asked, so not here.)"""
+    a = _args(a_stride=2 ** 39, b_stride=2 ** 39, out_stride=2 ** 37, **over)
+    assert dsa.load().dsa_matmul_fp8(ctypes.byref(a), None) == dsa.DSA_ERR_UNSUPPORTED and "2^31" in dsa.last_error()

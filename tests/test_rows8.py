@@ -429,3 +429,14 @@ def test_norm_without_epsilon_of_rows_whose_squares_are_below_fp32(cuda_lib, dty
     for row, off in ((2, 2.0 ** -9), (3, OFF)):
         at = slice(row, row + 1)
         assert not check_beyond_fp32(x[at], ones, 0.0, codes[at], scale[at], y[at], off).any()
+
+
+@pytest.mark.parametrize("call,args,code", [
+    ("dsa_quant_rows", lambda: _rows(n_rows=1, dim=2 ** 30 + 8), dsa.DSA_ERR_UNSUPPORTED),
+    ("dsa_quant_rows", lambda: _rows(x_stride=2 ** 40 + 8), dsa.DSA_ERR_INVALID_ARG),
+    ("dsa_quant_rows", lambda: _rows(scale_stride=2 ** 40 + 1), dsa.DSA_ERR_INVALID_ARG),
+    ("dsa_rms_norm_quant", lambda: _norm(sum_stride=2 ** 40 + 8), dsa.DSA_ERR_INVALID_ARG),
+    ("dsa_rms_norm_quant", lambda: _norm(codes_stride=2 ** 40 + 8), dsa.DSA_ERR_INVALID_ARG),
+])
+def test_limits_of_the_header_are_refused(call, args, code):
+    assert getattr(dsa.load(), call)(ctypes.byref(args()), None) == code and dsa.last_error()
