@@ -491,3 +491,42 @@ def test_limits_of_the_header_are_refused(over):
     """(More tiles than a launch numbers are refused after the device is asked, so not here.)"""
     a = _args(a_stride=2 ** 39, b_stride=2 ** 39, out_stride=2 ** 37, **over)
     assert dsa.load().dsa_matmul_fp8(ctypes.byref(a), None) == dsa.DSA_ERR_UNSUPPORTED and "2^31" in dsa.last_error()
+
+
+# Every width of narrow tiles with every number of CTAs that share a tile's blocks, one row of tiles (where the plan gives
+# it) and several
+PAIRS = {(32, 1): [(5, 33, 144), (137, 34, 144)], (32, 2): [(95, 1226, 1760), (2442, 33, 2080)],
+         (32, 4): [(5, 34, 784), (1187, 33, 1296)], (32, 8): [(5, 33, 1104), (134, 35, 1248)],
+         (64, 1): [(71, 8998, 144), (130, 2889, 144)], (64, 2): [(5, 7733, 1200), (132, 1879, 3488)],
+         (64, 4): [(5, 2361, 832), (131, 711, 2560)], (64, 8): [(5, 1025, 1056), (1449, 33, 4816)],
+         (96, 1): [(129, 5583, 160)], (96, 2): [(5, 7279, 1440), (129, 2698, 4224)],
+         (96, 4): [(5, 3235, 928), (140, 1247, 2960)], (96, 8): [(5, 1223, 1072), (139, 642, 3680)],
+         (128, 1): [(133, 7755, 144)], (128, 2): [(87, 7857, 4256), (129, 4093, 6048)],
+         (128, 4): [(5, 4745, 992), (129, 1901, 4528)], (128, 8): [(5, 2092, 1040), (130, 871, 10400)]}
+
+
+def test_the_pairs_are_what_the_plan_gives():
+    plan = dsa.load_testhooks().dsa_test_matmul_plan
+    assert set(PAIRS) == {(bn, s) for bn in (32, 64, 96, 128) for s in (1, 2, 4, 8)}
+    for pair, sizes in PAIRS.items():
+        assert all(divmod(plan(*s, 152), 16) == pair for s in sizes)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [s for sizes in PAIRS.values() for s in sizes])
+def test_every_pair_of_width_and_splits_is_exact(cuda_lib, m, n, k):
+    """Rows of out that start 16-byte aligned, on an even element and on an odd one, with an odd number of columns and
+    with an even one; what lies around them stays."""
+    a, a_scale, b, b_scale = whole(m, n, k, gen(m, n, k))
+    want = definition(a, a_scale, b, b_scale)[0].float()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    wide = (n + 23) // 8 * 8
+    for dtype in TYPES:
+        for cols in (n, n - 1):
+            for left, apart in ((0, wide), (8, wide), (2, wide), (1, wide), (0, wide + 1), (0, wide + 2)):
+                out = torch.full((m, apart), 5.0, dtype=dtype, device="cuda")
+                dsa.matmul_fp8(a, a_scale, b[:cols], b_scale[:-(-cols // 128)], out=out[:, left:left + cols], status=status)
+                assert torch.equal(out[:, left:left + cols], want[:, :cols].to(dtype)), (dtype, cols, left, apart)
+                out[:, left:left + cols] = 5.0
+                assert torch.all(out == 5.0)
+    assert int(status) == 0
