@@ -440,3 +440,53 @@ def test_norm_without_epsilon_of_rows_whose_squares_are_below_fp32(cuda_lib, dty
 ])
 def test_limits_of_the_header_are_refused(call, args, code):
     assert getattr(dsa.load(), call)(ctypes.byref(args()), None) == code and dsa.last_error()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("n,d", [(3, 64), (5, 264), (9, 1024), (4, 1536), (3, 7168), (2, 16392)])
+def test_norm_with_rows_of_every_tensor_apart(cuda_lib, n, d, dtype):
+    """Each tensor with a padding of its own, which stays as it is; then in place."""
+    g = torch.Generator().manual_seed(n * 3 + d)
+    x, r = ((1 + i) * torch.randn((n, d), generator=g) for i in range(2))
+    x, r, w = x.to(dtype), r.to(dtype), (1 + 0.3 * torch.randn(d, generator=g)).to(dtype)
+    groups = -(-d // 128)
+    e4m3 = torch.float8_e4m3fn
+    new = lambda cols, pad, kind: strided(torch.zeros((n, cols), device="cuda").to(kind), pad)
+    total, y, codes, scale = new(d, 40, dtype), new(d, 24, dtype), new(d, 56, e4m3), new(groups, 3, torch.float32)
+    xs, rs = strided(x.cuda(), 8), strided(r.cuda(), 16)
+    got = dsa.rms_norm_quant(xs, w.cuda(), eps=1e-6, residual=rs, residual_out=total, codes=codes, scale=scale, y=y)
+    assert got[0] is codes and got[1] is scale and got[2] is total
+    check_norm(x, w, r, 1e-6, codes.cpu().contiguous(), scale.cpu(), total.cpu(), y.cpu())
+    for t, pad in ((xs, 8), (rs, 16), (total, 40), (y, 24), (codes, 56), (scale, 3)):
+        cols = t.shape[1]
+        assert torch.all(t.as_strided((n, pad), (t.stride(0), 1), cols).float() == 3.0)
+    c2, s2 = new(d, 8, e4m3), new(groups, 1, torch.float32)
+    dsa.rms_norm_quant(xs, w.cuda(), eps=1e-6, residual=rs, residual_out=rs, codes=c2, scale=s2, y=xs)
+    assert torch.equal(rs, total) and torch.equal(xs, y) and torch.equal(s2, scale)
+    assert torch.equal(c2.contiguous().view(torch.uint8), codes.contiguous().view(torch.uint8))
+    for t, pad in ((xs, 8), (rs, 16), (c2, 8), (s2, 1)):
+        assert torch.all(t.as_strided((n, pad), (t.stride(0), 1), t.shape[1]).float() == 3.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [576, 2048])
+def test_norm_with_rows_of_every_tensor_far_apart(cuda_lib, d):
+    """Rows 4 GB apart in every tensor, one buffer: offsets beyond 32 bits in bytes and in elements."""
+    g = torch.Generator().manual_seed(d)
+    x, r = (torch.randn((3, d), generator=g).bfloat16().cuda() for _ in range(2))
+    w = torch.rand(d, generator=g).cuda()
+    y = torch.empty_like(x)
+    want = (*dsa.rms_norm_quant(x, w, residual=r, y=y), y)
+    raw = torch.zeros(2 * 2 ** 32 + 7 * 65536, dtype=torch.uint8, device="cuda")
+    def far(like, place):
+        size = like.element_size()
+        return raw.view(like.dtype)[place * 65536 // size:].as_strided(like.shape, (2 ** 32 // size, 1))
+    fx, fr, codes, scale, total, fy = (far(t, i) for i, t in enumerate((x, r, *want)))
+    fx.copy_(x), fr.copy_(r)
+    dsa.rms_norm_quant(fx, w, residual=fr, residual_out=total, codes=codes, scale=scale, y=fy)
+    for a, b in zip((codes, scale, total, fy), want):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.view(torch.uint8))
+    dsa.quant_rows(x, codes=codes, scale=scale)
+    for a, b in zip((codes, scale), dsa.quant_rows(x)):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.view(torch.uint8))
