@@ -890,12 +890,7 @@ dsa_status launch_matmul_fp8(const dsa_matmul_fp8_args& a, cudaStream_t stream, 
     cfg.gridDim = dim3((unsigned)std::min<long long>(tiles, std::max(1, dev.sm_count / 2)) * 2);
     cfg.numAttrs = 1;
   } else {
-    const long long grid = (long long)p.tiles_n * w.splits;
-    if (grid > 0x7fffffffLL) {
-      err = "matmul_fp8: too many columns for one launch";
-      return DSA_ERR_UNSUPPORTED;
-    }
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)p.tiles_m);
+    cfg.gridDim = dim3((unsigned)p.tiles_n * w.splits, (unsigned)p.tiles_m);   // (at most 2^26 * 8)
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = (unsigned)w.splits;
     attr[1].val.clusterDim.y = 1;

@@ -124,7 +124,9 @@ DSA_DEV float e4m3_value(uint32_t code) {
   return __half2float(*reinterpret_cast<const __half*>(&h));
 }
 
-// The quotient lies between x inv kDown and x inv kUp, where inv is off by 2^-23 and x by 2^-24 of itself.
+// The quotient lies between x inv kDown and x inv kUp: inv is off by 2^-23 of itself and the two products by 2^-24 each;
+// x is exact, or after a norm off by 2^-23 (its product with 1 / sqrt as one float, and what that float leaves).  3 * 2^-23
+// in all, of 4.
 constexpr float kDown = 1.f - 0x1p-21f, kUp = 1.f + 0x1p-21f;
 
 // The code of x / s between its neighbours `lo` (toward zero) and `hi`, which differ by one: by the sign
