@@ -14,8 +14,8 @@
 // multiply-adds, across blocks.  Two warps multiply the scales, eight blocks at a time.  Rows go out by TMA.
 // Bound: loads and MMAs alone run 4,096 x 7,168 x 16,384 in 250 us (3,850 TFLOP/s, at the power limit: 1,440 MHz
 // after a second of it); the multiply-adds, 256 of a block's cycles on the fp32 pipe, their hand-over and their power
-// make it 312 us (3,080 TFLOP/s; 360 us, at some 1,650 MHz, after a second).  With 512 columns in all a tile's end (rounding,
-// boxes, TMA) is a third of the time: 8,192 x 32,768 in 163 us, 111 without it.
+// make it 317 us (3,040 TFLOP/s; 355 to 367 us, at some 1,650 MHz, after a second).  With 512 columns in all a tile's end
+// (rounding, boxes, TMA) is a third of the time: 8,192 x 32,768 in 166 to 176 us, 111 without it.
 // Measured on the way: waits by suspension or by spinning alike; the scales loaded by the sums themselves, a row a lane,
 // 430 (each load takes 32 lines of L1); tiles of 256 x 192 390; sums that spill a few registers 370 to 510.
 //
@@ -23,7 +23,7 @@
 // its parts are added in rank order through distributed shared memory: many CTAs stream the weights, the result does not
 // depend on their timing, and there is no workspace.  Two CTAs an SM, so that one's start and end run under the
 // other's stream.  Bound: HBM with long rows (32 x 7,168 x 16,384 in 25 us, 4.8 TB/s of weights), else launch, a
-// tile's chain of blocks (0.25 to 0.38 us each) and the parts' exchange (1 x 2,112 x 7,168 in 9 us).
+// tile's chain of blocks (0.25 to 0.38 us each) and the parts' exchange (1 x 2,112 x 7,168 in 9.6 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -83,7 +83,8 @@ DSA_DEV uint32_t pack16(float a, float b) {
 // `cols` outputs (at most 128) from column n on of rows m, m + step, ..., `some` of them and R at a time, value(r, c) the
 // c-th of the r-th and the one after it, by a whole warp: for rows of out that do not start 16-byte aligned.  A lane
 // stores a column, or two where rows start on an even element (and n is even).  Bound by instructions: 4 bytes a lane out of
-// rows that start anywhere, with the lines' ends apart, took 340 us for 4,096 x 20,001 bf16 of 512 columns against 141.
+// rows that start anywhere, with the lines' ends apart, took 340 us for 4,096 x 20,001 bf16 of 512 columns against 128
+// (aligned rows of 20,000 columns 57, on even elements 110).
 template <int R, class Value>
 DSA_DEV void store_rows(const Params& p, int m, int step, int some, int n, int cols, Value&& value) {
   const int lane = threadIdx.x & 31;
@@ -849,8 +850,9 @@ dsa_status launch_matmul_fp8(const dsa_matmul_fp8_args& a, cudaStream_t stream, 
   p.tiles_m = (int)(((long long)a.M + rows - 1) / rows);
   p.tiles_n = (int)(((long long)a.N + w.bn - 1) / w.bn);
   p.a_box = w.wide ? kRows : std::min(kRows, (a.M + 7) / 8 * 8);
-  // (128 x 7,168 x 7,168, 150 CTAs: 16.7 -> 15.6 us; clusters of eight, of which an SM's group holds two with one CTA an SM:
-  // 17 of them 9.5 -> 12.5 us, so not with more than two splits)
+  // All of an SM's shared memory where every CTA has its SM alone, in clusters of up to two: 1,269 x 640 x 9,328 29.3 -> 25.2
+  // us, 1,875 x 432 x 5,312 21.1 -> 19.1, 1,666 x 936 x 2,176 17.0 -> 15.0, others alike.  One CTA an SM leaves room for
+  // few clusters of more: 1 x 4,632 x 15,056 (four) 27 -> 36 us, 688 x 72 x 13,232 (eight) 17 -> 23.
   p.ring = w.splits <= 2 && (long long)p.tiles_m * p.tiles_n * w.splits <= dev.sm_count ? 2 * kRing : kRing;
   p.stages = w.wide ? 0 : std::min(kMostStages, p.ring / ((p.a_box + w.bn) * kBlock));
   CUtensorMap tm_a, tm_b;

@@ -13,9 +13,12 @@
 // 1,024 columns is 4 to 32 lanes of a warp, a longer one a block; its warps' sums meet in shared memory, where one warp
 // makes r of them for all.
 //
-// Bound by HBM with a residual (16,384 rows of 7,168 bf16 in 123 us in a run of calls, 6.7 TB/s) and with 32-bit rows
-// (4,095 of 16,384 in 49 us, 6.9 TB/s); by instruction issue without one (16,384 of 7,168 bf16 in 89 us, 4.0 TB/s; rows as
-// they are, 4,095 of 16,384 bf16, in 34 us, 5.9 TB/s): a conversion takes two roundings of every value (see quant.cuh).
+// Bound by HBM with a residual (16,384 rows of 7,168 bf16 in 122 us in a run of calls, 6.8 TB/s) and for 32-bit rows as they
+// are (4,095 of 16,384 in 48 us, 6.9 TB/s, above the rate of a copy as four of five bytes are read); 16-bit rows as they are
+// are near both HBM's and the issue's limit (4,095 of 16,384 bf16 in 33.5 us, 6.0 TB/s; 67% of the issue slots): a conversion
+// takes two roundings of every value (see quant.cuh).  A norm without a residual fills neither (16,384 of 7,168 bf16 in 88 us,
+// 4.0 TB/s; 56% of the issue slots): a row's loads, two barriers and conversion follow one another in its block, and nothing
+// of the next row is on its way meanwhile.
 #include "dsa_internal.h"
 #include "quant.cuh"
 
@@ -128,8 +131,12 @@ DSA_DEV float2 root_of(float total, float lost, int dim, float eps) {
   return r;
 }
 
-// Most threads of a block of the variant with registers for four (16-bit rows of 7,168: 72 of them; with 64, which spill,
-// 131 us against 126, with 76, three blocks, 162) or as many as it wants; the other has a block of up to 1,024.
+// Most threads of a block of the variant with registers for two such blocks (16-bit rows, 72 of them; four blocks of 7,168
+// columns) or as many as it wants (32-bit rows, 90).  A longer row's block, of up to 1,024 threads, leaves each 64 at most,
+// which spill, and fits an SM once: 8,192 rows of 14,344 bf16 with residual take 155 us against 131 of 14,336, 4,096 of 16,392
+// fp32 227 against 146 of 16,384 (floors 121 and 129), 2,048 of 32,768 fp32 211.  The same variant for shorter rows: 16,384 of
+// 7,168 bf16 with residual 134 against 122, without 96 against 88, 11,969 of 1,536 fp32 45 against 31.  (76 registers, three
+// blocks of 7,168 columns: 162.)
 template <int E>
 constexpr int kFew = E == DSA_ELEM_FP32 ? 512 : 448;
 
